@@ -1,5 +1,6 @@
-"""ctypes binding of libflashattn.so: the C ABI of include/flash_attn.h under
-the same names, plus thin helpers that take torch tensors.
+"""ctypes binding of libflashattn.so: the C ABI of include/flash_attn.h,
+flash_attn_cache.h and standard_attn.h under the same names, plus thin helpers
+that take torch tensors.
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels behind the C ABI. There is no CPU or PyTorch fallback; if the shared
@@ -22,13 +23,14 @@ STATUS_NAMES = {
 FA_ERR_SCRATCH_LIMIT = 7
 BWD_NOALLOC_SCRATCH_BYTES = 64 << 20
 
-# every symbol include/flash_attn.h and include/standard_attn.h declare
+# every symbol the headers in include/ declare
 EXPORTS = [
     "flash_attn_fwd", "flash_attn_fwd_ex", "flash_attn_bwd_workspace_size", "flash_attn_bwd",
     "flash_attn_bwd_ex", "flash_attn_bwd_noalloc",
     "flash_attn_tile_map",
     "flash_attn_get_device_error", "flash_attn_set_profile_events", "flash_attn_status_string",
     "flash_attn_version",
+    "flash_attn_kv_cache_write", "flash_attn_cached_workspace_size", "flash_attn_cached_fwd",
     "standard_attn_workspace_size", "standard_attn_fwd", "standard_attn_bwd",
 ]
 
@@ -90,6 +92,14 @@ def load(path=LIB_PATH):
     lib.flash_attn_status_string.restype = ctypes.c_char_p
     lib.flash_attn_version.argtypes = []
     lib.flash_attn_version.restype = i32
+    i64 = ctypes.c_int64
+    lib.flash_attn_kv_cache_write.argtypes = [vp, vp, i64, i64, i64, i64, vp, i32, i32, i32, vp, vp, vp, vp, i32, i32,
+                                              i32, opt_p, vp]
+    lib.flash_attn_kv_cache_write.restype = i32
+    lib.flash_attn_cached_workspace_size.argtypes = [i32] * 5
+    lib.flash_attn_cached_workspace_size.restype = sz
+    lib.flash_attn_cached_fwd.argtypes = [vp, i64] + [vp] * 8 + [i32] * 8 + [f32, i32, opt_p, vp, sz, vp]
+    lib.flash_attn_cached_fwd.restype = i32
     lib.standard_attn_workspace_size.argtypes = [i32, i32, i32]
     lib.standard_attn_workspace_size.restype = sz
     lib.standard_attn_fwd.argtypes = [vp] * 5 + [i32, i32, i32, i32, f32, i32, vp, vp, opt_p, i32, vp, sz, vp]
@@ -158,6 +168,26 @@ def flash_attn_status_string(status):
 
 def flash_attn_version():
     return load().flash_attn_version()
+
+
+def flash_attn_kv_cache_write(K, V, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots, T, Hk, d,
+                              k_cache, v_cache, k_scale, v_scale, num_pages, page_size, cache_type, options, stream):
+    return load().flash_attn_kv_cache_write(K, V, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots,
+                                            T, Hk, d, k_cache, v_cache, k_scale, v_scale, num_pages, page_size,
+                                            cache_type, None if options is None else ctypes.byref(options), stream)
+
+
+def flash_attn_cached_workspace_size(B, Nq, Hq, Hk, d):
+    return load().flash_attn_cached_workspace_size(B, Nq, Hq, Hk, d)
+
+
+def flash_attn_cached_fwd(Q, q_token_stride, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, O, LSE, B, Nq,
+                          Hq, Hk, d, num_pages, page_size, max_pages, scale, cache_type, options, workspace,
+                          workspace_bytes, stream):
+    return load().flash_attn_cached_fwd(Q, q_token_stride, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, O,
+                                        LSE, B, Nq, Hq, Hk, d, num_pages, page_size, max_pages, scale, cache_type,
+                                        None if options is None else ctypes.byref(options), workspace,
+                                        workspace_bytes, stream)
 
 
 def standard_attn_workspace_size(B, H, N):
@@ -342,3 +372,143 @@ def standard_attention_bwd(q, k, v, do, workspace, scale, stream=None, s16=False
                            _stream(stream))
     _check(st, "standard_attn_bwd")
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------
+# serving from a paged key/value cache
+# ---------------------------------------------------------------------------
+
+FA_CACHE_16BIT, FA_CACHE_E4M3 = 0, 1
+
+
+def _rows16(t, name, heads, d, dtype, device):
+    """Checks a 16-bit tensor [tokens, heads, d] whose rows may be strided
+    (views of a fused projection): d elements in one piece, token and head
+    strides multiples of 8 elements, 16-byte aligned."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor [tokens, {heads}, {d}] on {device}")
+    st = t.stride()
+    if st[2] != 1 or st[0] % 8 or st[1] % 8:
+        raise ValueError(f"{name}: rows must be contiguous, with token and head strides that are multiples of 8")
+
+
+def _cache_args(k_cache, v_cache, k_scale, v_scale, dtype, device):
+    """Checks the tensors of a paged cache; returns the cache type."""
+    import torch
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache must share one shape [num_pages, Hk, page_size, d] and one dtype")
+    e4m3 = k_cache.dtype == torch.float8_e4m3fn
+    if not e4m3 and k_cache.dtype != dtype:
+        raise ValueError("the cache must hold the 16-bit type of the other tensors, or float8_e4m3fn")
+    for t in (k_cache, v_cache):
+        if t.device != device or not t.is_contiguous():
+            raise ValueError("k_cache and v_cache must be contiguous and on the device of the other tensors")
+    for t in (k_scale, v_scale):
+        if e4m3 != (t is not None):
+            raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache")
+        if e4m3 and (t.shape != k_cache.shape[:3] or t.dtype != torch.float32 or t.device != device
+                     or not t.is_contiguous()):
+            raise ValueError("k_scale and v_scale must be contiguous float32 [num_pages, Hk, page_size]")
+    return FA_CACHE_E4M3 if e4m3 else FA_CACHE_16BIT
+
+
+def _on(stream, device):
+    """The stream to launch on and the context to allocate and launch in."""
+    import contextlib
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+        if device.index == torch.cuda.current_device():
+            return stream, contextlib.nullcontext()
+    return stream, torch.cuda.stream(stream)   # (also makes the stream's device the current one)
+
+
+def _dtype16(t, name):
+    import torch
+    if not t.is_cuda or t.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"{name} must be a bfloat16 or float16 CUDA tensor")
+    return FA_DTYPE_F16 if t.dtype == torch.float16 else FA_DTYPE_BF16
+
+
+def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, stream=None):
+    """Writes keys and values k, v [T, Hk, d] (bf16 or fp16, rows may be
+    strided) into a paged cache k_cache, v_cache [num_pages, Hk, page_size, d]:
+    token t into place slots[t] % page_size of page slots[t] // page_size
+    (int64; a slot outside the cache, -1 for instance, skips its token). A
+    cache of the tokens' dtype takes them as they are; a float8_e4m3fn cache
+    takes them quantised, with one power-of-two scale per row in k_scale,
+    v_scale (float32 [num_pages, Hk, page_size])."""
+    import torch
+    opts = fa_options(_dtype16(k, "k"))
+    if k.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("k must be [T, Hk, d] and k_cache [num_pages, Hk, page_size, d]")
+    T, Hk, d = k.shape
+    dev = k.device
+    _rows16(k, "k", k_cache.shape[1], k_cache.shape[3], k.dtype, dev)
+    _rows16(v, "v", Hk, d, k.dtype, dev)
+    if v.shape[0] != T or slots.shape != (T,) or slots.dtype != torch.int64 or slots.device != dev \
+            or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous int64 tensor with one entry per token of k and v")
+    kind = _cache_args(k_cache, v_cache, k_scale, v_scale, k.dtype, dev)
+    stream, ctx = _on(stream, dev)
+    with ctx:
+        st = flash_attn_kv_cache_write(_ptr(k), _ptr(v), k.stride(0), k.stride(1), v.stride(0), v.stride(1), _ptr(slots),
+                                       T, Hk, d, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                       k_cache.shape[0], k_cache.shape[2], kind, opts, _stream(stream))
+    _check(st, "flash_attn_kv_cache_write")
+
+
+def attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_scale=None, v_scale=None, out=None,
+                         lse=None, workspace=None, stream=None, wait_limit_us=0, test_stall=0):
+    """O, LSE of the newest Nq tokens of B sequences against their keys and
+    values in a paged cache. q: bf16 or fp16 [B, Nq, Hq, d] (a token's heads
+    contiguous, tokens may be strided); the cache, its scales and the slots'
+    meaning as in kv_cache_write; block_table int32 [B, max_pages]; seq_lens
+    int32 [B] counts each sequence's tokens, the newest Nq included. Token i of
+    the Nq sees seq_lens - (Nq - 1 - i) keys; query head h reads key/value head
+    h // (Hq // Hk). Returns O like q (contiguous) and LSE float32 [B, Hq, Nq]."""
+    import torch
+    opts = fa_options(_dtype16(q, "q"), wait_limit_us=wait_limit_us, test_stall=test_stall)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Nq, Hq, d]")
+    B, Nq, Hq, d = q.shape
+    dev = q.device
+    kind = _cache_args(k_cache, v_cache, k_scale, v_scale, q.dtype, dev)
+    pages, Hk, page_size, dk = k_cache.shape
+    if dk != d:
+        raise ValueError("q and the cache must have one head dimension")
+    st = q.stride()
+    if st[3] != 1 or (Hq > 1 and st[2] != d) or (B > 1 and Nq > 1 and st[0] != Nq * st[1]):
+        raise ValueError("q: a token's heads must be contiguous and the tokens evenly spaced")
+    tok = st[1] if Nq > 1 else (st[0] if B > 1 else Hq * d)
+    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.shape != (B,):
+        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
+    for t in (block_table, seq_lens):
+        if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous():
+            raise ValueError("block_table and seq_lens must be contiguous int32 tensors on q's device")
+    need = flash_attn_cached_workspace_size(B, Nq, Hq, Hk, d)
+    stream, ctx = _on(stream, dev)
+    with ctx:
+        o = torch.empty((B, Nq, Hq, d), dtype=q.dtype, device=dev) if out is None else out
+        l = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if lse is None else lse
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        _like(o, "out", (B, Nq, Hq, d), q.dtype, dev)
+        _like(l, "lse", (B, Hq, Nq), torch.float32, dev)
+        _workspace_on(workspace, dev)
+        st = flash_attn_cached_fwd(_ptr(q), tok, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                   _ptr(block_table), _ptr(seq_lens), _ptr(o), _ptr(l), B, Nq, Hq, Hk, d, pages, page_size,
+                                   block_table.shape[1], float(scale), kind, opts, _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "flash_attn_cached_fwd")
+    return o, l
+
+
+def _like(t, name, shape, dtype, device):
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+
+
+def _workspace_on(t, device):
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on {device}")

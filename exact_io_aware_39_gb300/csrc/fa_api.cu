@@ -192,6 +192,33 @@ int internal_read_options(const void* options, bool* f16, bool* flash_only) {
   return st;
 }
 
+int internal_read_check_options(const void* options, bool* f16, bool* record, uint32_t* wait_us, uint32_t* stall) {
+  Options o;
+  const fa_status st = read_options(static_cast<const fa_options*>(options), &o);
+  if (st == FA_OK) {
+    *f16 = o.f16;
+    *record = o.drop.t != 0u || o.chk.rec != nullptr;
+    *wait_us = o.chk.wait_us;
+    *stall = o.chk.stall;
+  }
+  return st;
+}
+
+int internal_tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
+                        const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
+  cuuint64_t d[5], st[4];
+  cuuint32_t bx[5], es[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    es[i] = 1;
+    if (i + 1 < rank) st[i] = strides[i];
+  }
+  return g_encode(m, type, (cuuint32_t)rank, const_cast<void*>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? 0 : 1;
+}
+
 int internal_bwd_validate(const BwdArgs& a, const void* options) {
   fa_status st = check_shape(a.B, a.H, a.N, a.d, a.scale, a.causal);
   if (st != FA_OK) return st;

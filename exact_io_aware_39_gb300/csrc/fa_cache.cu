@@ -1,0 +1,989 @@
+// Serving from a paged key/value cache, for sm_103a: the writer (16-bit copy
+// or quantisation to e4m3 with one scale per row) and the attention of the
+// newest tokens against the cache. Declarations and the contract of the calls
+// are in flash_attn_cache.h.
+//
+// Attention of the newest tokens. Per sequence and key/value head there are
+// Nq * G query rows (G = Hq / Hk; 1 to 16 as a rule) against thousands of
+// keys, so the work is reading the cache: 2 d elements per key for 4 d Nq G
+// operations, far under the 280 operations per byte where the tensor cores
+// would bound it. The design keeps the memory system busy and little else:
+//   * the unit of work is a tile of kKT keys of one (sequence, key/value head,
+//     16 query rows); all units of the call are numbered in that order and cut
+//     into equal ranges, one for each of the 8 x 152 warps of the grid, so
+//     that ragged lengths leave no warp without work;
+//   * each warp is a pipeline of its own: it loads the tiles of its range by
+//     TMA into its own shared-memory ring (24 KB, three to six tiles ahead,
+//     across sequence boundaries), so an SM keeps up to 192 KB in flight
+//     (measured need: 6.8 TB/s x 1 us / 152 = 45 KB), and no warp waits for
+//     another;
+//   * the products are mma.sync m16n8k16: the 16 rows fill it, where a
+//     tcgen05 product of 128 rows would be an eighth full or less, and the
+//     operands come from registers (Q, P, and with e4m3 the converted K and V);
+//   * a warp that finishes a (sequence, head) whole writes O and the LSE; one
+//     that holds a part of it writes O unnormalised with the row's reference
+//     and sum, and a second kernel joins the parts (in a fixed order, so the
+//     result does not change from call to call).
+//
+// e4m3: with q8, k8, v8 the payloads and ks, vs the scales of key j,
+//   S_j = ks_j (q . k8_j),  O = sum_j P_j vs_j v8_j.
+// The payloads are converted exactly to fp16; Q is brought into fp16's range
+// by a power of two per row. The weights w_j = P_j vs_j that go to fp16 for
+// the second product are formed as 2^(s_j + log2 vs_j - m) with m the running
+// maximum of s_j + log2 vs_j, so they are at most 2^8 and lose nothing to
+// fp16's range however the scales differ; the row sum adds w_j / vs_j in fp32.
+#include "flash_attn_cache.h"
+#include "fa_common.cuh"
+#include "fa_ptx.cuh"
+
+#include <cmath>
+
+namespace fa {
+
+namespace {
+
+// --------------------------------------------------------------------------
+// writer
+// --------------------------------------------------------------------------
+
+struct WriteParams {
+  const uint16_t* src[2];      // K, V
+  int64_t tok[2], head[2];     // strides in elements
+  const int64_t* slots;
+  void* cache[2];
+  float* scale[2];
+  uint32_t rows;               // 2 T Hk
+  int T, Hk, d;
+  int ps_log2;
+  int64_t places;              // num_pages * page_size
+};
+
+__device__ __forceinline__ uint16_t cvt_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A row (tensor, token, head) is handled by LANES neighbouring threads of 8
+// elements each; rows are numbered heads first, then tokens, then K / V, so
+// that a token's row of heads is read in one piece.
+template <int LANES, bool E4M3, bool F16>
+__global__ void __launch_bounds__(256) kv_cache_write_kernel(const WriteParams p) {
+  const uint32_t gid = blockIdx.x * 256u + threadIdx.x;
+  const uint32_t row = gid / LANES;
+  const int part = (int)(gid % LANES);
+  const bool mine = row < p.rows && 8 * part < p.d;
+  const uint32_t per = (uint32_t)p.T * (uint32_t)p.Hk;
+  const int kv = row >= per ? 1 : 0;
+  const uint32_t rr = row - (kv ? per : 0u);
+  const int t = (int)(rr / (uint32_t)p.Hk), h = (int)(rr % (uint32_t)p.Hk);
+  uint4 x = make_uint4(0u, 0u, 0u, 0u);
+  int64_t slot = -1;
+  if (mine) {
+    slot = p.slots[t];
+    x = *reinterpret_cast<const uint4*>(p.src[kv] + t * p.tok[kv] + h * p.head[kv] + 8 * part);
+  }
+  const bool put = mine && slot >= 0 && slot < p.places;
+  const int64_t place = ((slot >> p.ps_log2) * p.Hk + h) * ((int64_t)1 << p.ps_log2) +
+                        (slot & (((int64_t)1 << p.ps_log2) - 1));   // row of the cache
+  if constexpr (!E4M3) {
+    if (put) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.cache[kv]) + place * p.d + 8 * part) = x;
+  } else {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float f[8];
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = unpack2<F16>(w[i]);
+      f[2 * i] = a.x;
+      f[2 * i + 1] = a.y;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = fabsf(f[i]);
+      if (a < INFINITY)
+        top = fmaxf(top, a);
+      else
+        f[i] = __int_as_float(0x7FC00000);   // infinities and NaN: stored as NaN
+    }
+#pragma unroll
+    for (int off = LANES / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+    // top = (1 + m) 2^k: the smallest e with top <= 448 2^e = 1.75 2^(8 + e) is
+    // k - 8, or one more where 1 + m > 1.75 (subnormal tops are under the floor)
+    const uint32_t bits = __float_as_uint(top);
+    int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    e = e < -64 ? -64 : e;
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e, exact
+    if (put) {
+      uint32_t o[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        o[i] = (uint32_t)cvt_e4m3x2(f[4 * i] * inv, f[4 * i + 1] * inv) |
+               ((uint32_t)cvt_e4m3x2(f[4 * i + 2] * inv, f[4 * i + 3] * inv) << 16);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.cache[kv]) + place * p.d + 8 * part) = make_uint2(o[0], o[1]);
+      if (part == 0) p.scale[kv][place] = __uint_as_float((uint32_t)(127 + e) << 23);
+    }
+  }
+}
+
+template <int LANES>
+cudaError_t launch_write(const WriteParams& p, bool e4m3, bool f16, cudaStream_t s) {
+  const uint64_t threads = (uint64_t)p.rows * LANES;
+  const dim3 grid((unsigned)((threads + 255) / 256));
+  if (!e4m3)
+    kv_cache_write_kernel<LANES, false, false><<<grid, 256, 0, s>>>(p);
+  else if (f16)
+    kv_cache_write_kernel<LANES, true, true><<<grid, 256, 0, s>>>(p);
+  else
+    kv_cache_write_kernel<LANES, true, false><<<grid, 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+// --------------------------------------------------------------------------
+// attention against the cache
+// --------------------------------------------------------------------------
+
+constexpr int kWarps = 8;
+constexpr int kMaxCtas = 152;
+constexpr int kMaxWorkers = kWarps * kMaxCtas;
+constexpr int kRows = 16;                 // query rows of a unit
+constexpr float kMoveThreshold = 8.0f;    // log2 units: the reference moves only past it
+
+// Shared-memory layout of one warp's ring. A tile is kKT keys: K, then V, each
+// as the TMA writes it (16-bit: 64-column atoms of 128-byte rows; e4m3: one
+// atom of D-byte rows), 128- or 64-byte swizzled, then with e4m3 the scales of
+// K and of V (each 16 keys at a pitch of 64 or, one page each, 128 bytes).
+template <int D, bool E4M3>
+struct CachedLayout {
+  static constexpr int kKT = (!E4M3 && D == 128) ? 16 : 32;
+  static constexpr int kRowBytes = E4M3 ? D : 128;              // of a swizzle atom
+  static constexpr int kAtoms = E4M3 ? 1 : D / 64;
+  static constexpr int kAtomBytes = kKT * kRowBytes;
+  static constexpr int kTileBytes = kAtoms * kAtomBytes;        // K or V
+  static constexpr int kScaleBytes = E4M3 ? 256 : 0;            // K or V
+  // stages start at multiples of 1024 bytes; the scales of all stages follow
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStages = kStageBytes >= 8192 ? 3 : 6;
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+  static constexpr int kScale = kWarps * kWarpBytes;
+  static constexpr int kBar = kScale + kWarps * kStages * 2 * kScaleBytes;
+  static constexpr int kMisc = kBar + 8 * kWarps * kStages;     // abort flag, -, wait limit, -
+  static constexpr int kScan = kMisc + 16;                      // int64 [kWarps] totals, int64 [kWarps] starts, int [kWarps]
+  static constexpr int kSmemBytes = kScan + kWarps * 20;
+  static constexpr uint32_t kTxBytes = 2u * kTileBytes + (E4M3 ? 2u * kKT * 4u : 0u);
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+struct CachedParams {
+  const uint16_t* q;
+  int64_t q_tok;
+  const int32_t* table;
+  const int32_t* lens;
+  uint16_t* o;
+  float* lse;
+  float* part_o;       // [kMaxWorkers][2][kRows][D]
+  float2* part_ml;     // [kMaxWorkers][2][kRows]: reference (log2), sum
+  int2* info;          // [B Hk RT]: first and last worker of a (sequence, head, row tile) held in parts, or -1
+  unsigned int* err;
+  int B, Nq, Hq, Hk, G, d, R, RT;
+  int num_pages, page_size, ps_log2, max_pages;
+  float scale_log2;
+  uint32_t wait_us, stall;
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16) mma_f16(c, a, b0, b1);
+  else mma_bf16(c, a, b0, b1);
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// two e4m3 values (16 bits) -> fp16x2, exact
+__device__ __forceinline__ uint32_t e4m3_to_f16(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+
+// byte offset of 16-byte chunk c of row r in a swizzled atom
+template <int ROWB>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  if constexpr (ROWB == 128) return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
+  return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1) : "memory");
+}
+
+// Walks the units of a range: tile j of n of (sequence b, sub = head * RT + row tile).
+struct Walk {
+  int b, sub, j, n, len;
+};
+
+template <int D, bool E4M3, bool F16>
+__global__ void __launch_bounds__(32 * kWarps, 1)
+fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                 const __grid_constant__ CUtensorMap tks, const __grid_constant__ CUtensorMap tvs,
+                 const CachedParams p) {
+  using L = CachedLayout<D, E4M3>;
+  constexpr int KT = L::kKT;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile uint32_t* abort_flag = misc;
+  Ctl ctl{p.err, abort_flag};
+  if ((sbase & 1023u) != 0u) {   // uniform across the CTA: nothing has started yet
+    if (tid == 0) {
+      uint32_t dummy = 0;
+      Ctl c0{p.err, &dummy};
+      report_error(c0, kErrSmemAlign, 200);
+    }
+    return;
+  }
+  auto bar = [&](int s) -> uint32_t { return sbase + L::kBar + 8u * (uint32_t)(warp * L::kStages + s); };
+  if (lane == 0)
+    for (int s = 0; s < L::kStages; ++s) mbar_init(bar(s), 1u);
+  if (tid == 0) {
+    misc[0] = 0u;
+    misc[2] = p.wait_us;
+  }
+  fence_mbar_init();
+
+  // ---- this warp's range of units
+  const int SUB = p.Hk * p.RT;
+  const int cap = p.max_pages << p.ps_log2;
+  auto seq_len = [&](int b) -> int {
+    const int n = p.lens[b];
+    return n < 0 ? 0 : (n > cap ? cap : n);
+  };
+  auto tiles_of = [&](int len) -> int { return len > 0 ? (len + KT - 1) / KT : 1; };   // an empty sequence is one empty tile
+  long long* tot = reinterpret_cast<long long*>(smem + L::kScan);
+  long long* start_cum = tot + kWarps;
+  int* start_b = reinterpret_cast<int*>(start_cum + kWarps);
+  const int per = (p.B + 32 * kWarps - 1) / (32 * kWarps);
+  const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(seq_len(b));
+  long long incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+    if (lane >= off) incl += o;
+  }
+  if (lane == 31) tot[warp] = incl;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += tot[w];
+    all += tot[w];
+  }
+  const long long total = all * SUB;
+  const int workers = (int)min((long long)(kWarps * gridDim.x), total);
+  // neighbouring ranges go to different SMs, so that a small call spreads out
+  auto worker_id = [&](int w) -> int { return w * (int)gridDim.x + (int)blockIdx.x; };
+  auto range_start = [&](int w) -> long long { return total * w / workers; };
+  {
+    long long cum = before + incl - mine;   // tiles of the sequences before b_lo
+    for (int b = b_lo; b < b_hi; ++b) {
+      const long long next = cum + tiles_of(seq_len(b));
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (worker_id(w) >= workers) break;
+        const long long t0 = range_start(worker_id(w));
+        if (t0 >= cum * SUB && t0 < next * SUB) {
+          start_b[w] = b;
+          start_cum[w] = cum;
+        }
+      }
+      cum = next;
+    }
+  }
+  __syncthreads();
+  const int me = worker_id(warp);
+  if (me >= workers) {
+    grid_dep_launch();
+    return;
+  }
+  const long long t0 = range_start(me), t1 = range_start(me + 1);
+  Walk w0;
+  w0.b = start_b[warp];
+  w0.len = seq_len(w0.b);
+  w0.n = tiles_of(w0.len);
+  {
+    const long long rem = t0 - start_cum[warp] * SUB;
+    w0.sub = (int)(rem / w0.n);
+    w0.j = (int)(rem % w0.n);
+  }
+  grid_dep_launch();   // the joining kernel may be scheduled (it waits for this one's end)
+  auto advance = [&](Walk& w) {
+    if (++w.j < w.n) return;
+    w.j = 0;
+    if (++w.sub < SUB) return;
+    w.sub = 0;
+    if (++w.b < p.B) {
+      w.len = seq_len(w.b);
+      w.n = tiles_of(w.len);
+    }
+  };
+
+  // ---- loads (lane 0): piece i of a tile is one page's share of it
+  const uint32_t ring = sbase + (uint32_t)(warp * L::kWarpBytes);
+  const uint32_t sring = sbase + L::kScale + (uint32_t)(warp * L::kStages * 2 * L::kScaleBytes);
+  const int box = p.page_size < KT ? p.page_size : KT;     // keys of a piece
+  const int pieces = KT / box;
+  const int nowhere = p.num_pages * p.Hk;                  // a coordinate past the cache: reads as zeros
+  int issued = 0;
+  auto issue = [&](const Walk& w) {
+    const int s = issued % L::kStages;
+    ++issued;
+    if (lane != 0) return;
+    const int hk = w.sub / p.RT;
+    mbar_arrive_expect_tx(bar(s), L::kTxBytes);
+    for (int i = 0; i < pieces; ++i) {
+      const int key = w.j * KT + i * box;
+      int z = nowhere;
+      if (key < w.len) {
+        const int page = p.table[(int64_t)w.b * p.max_pages + (key >> p.ps_log2)];
+        if (page >= 0 && page < p.num_pages) z = page * p.Hk + hk;
+      }
+      const int y = key & (p.page_size - 1);
+      const uint32_t dst = ring + (uint32_t)(s * L::kStageBytes + i * box * L::kRowBytes);
+#pragma unroll
+      for (int a = 0; a < L::kAtoms; ++a) tma_load_3d(dst + a * L::kAtomBytes, &tk, bar(s), 64 * a, y, z);
+#pragma unroll
+      for (int a = 0; a < L::kAtoms; ++a)
+        tma_load_3d(dst + L::kTileBytes + a * L::kAtomBytes, &tv, bar(s), 64 * a, y, z);
+      if constexpr (E4M3) {
+        const uint32_t sd = sring + (uint32_t)(s * 2 * L::kScaleBytes + i * 128);
+        tma_load_2d(sd, &tks, bar(s), y, z);
+        tma_load_2d(sd + L::kScaleBytes, &tvs, bar(s), y, z);
+      }
+    }
+  };
+
+  const long long todo = t1 - t0;
+  Walk wi = w0;
+  for (int s = 0; s < L::kStages && s < todo; ++s) {
+    if (p.stall != 0u && s >= 1) break;   // test of the timeout path: tile 1 never comes
+    issue(wi);
+    advance(wi);
+  }
+
+  // ---- the tiles of the range
+  const int g = lane >> 2, t4 = lane & 3;
+  constexpr int kSteps = D / 16;
+  uint32_t qf[kSteps][4];
+  float o[D / 8][4];
+  float m[2], l[2], qs[2];
+  Walk w = w0;
+  bool fresh = true;              // the next tile starts a (sequence, head, row tile) for this warp
+  bool from_start = false;        // ... and is its first
+  bool ok = true;
+  for (long long u = 0; u < todo; ++u) {
+    const int hk = w.sub / p.RT, rt = w.sub % p.RT;
+    if (fresh) {
+      fresh = false;
+      from_start = w.j == 0;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+      m[0] = m[1] = -INFINITY;
+      l[0] = l[1] = 0.f;
+      qs[0] = qs[1] = 1.f;
+      const uint16_t* qp[2];
+      bool live[2];
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int r = rt * kRows + g + 8 * hh;
+        live[hh] = r < p.R;
+        const int i = r / p.G;
+        qp[hh] = p.q + ((int64_t)w.b * p.Nq + i) * p.q_tok + (hk * p.G + r % p.G) * p.d;
+      }
+      // A fragments: 16-bit, K step ks holds dims 16 ks + {2t, 2t+1, 2t+8, 2t+9};
+      // e4m3, dims 16 ks + {4t .. 4t+3} (the order K's bytes come in)
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int hh = i & 1, hi = i >> 1;
+          const int c = 16 * ks + (E4M3 ? 4 * t4 + 2 * hi : 2 * t4 + 8 * hi);
+          qf[ks][i] = live[hh] && c < p.d ? *reinterpret_cast<const uint32_t*>(qp[hh] + c) : 0u;
+        }
+      if constexpr (E4M3 && !F16) {
+        // bf16 -> fp16: each row is divided by a power of two that puts its
+        // largest magnitude in [2^7, 2^8); what then lies under fp16's smallest
+        // step is under 2^-31 of that largest magnitude
+        float top[2] = {0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 a = unpack2<false>(qf[ks][i]);
+            top[i & 1] = fmaxf(top[i & 1], fmaxf(fabsf(a.x), fabsf(a.y)));
+          }
+        float inv[2];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          top[hh] = fmaxf(top[hh], __shfl_xor_sync(0xFFFFFFFFu, top[hh], 1));
+          top[hh] = fmaxf(top[hh], __shfl_xor_sync(0xFFFFFFFFu, top[hh], 2));
+          int k = (int)(__float_as_uint(top[hh]) >> 23) - 127 - 7;
+          k = k < -100 ? -100 : (k > 112 ? 112 : k);
+          inv[hh] = __uint_as_float((uint32_t)(127 - k) << 23);
+          qs[hh] = __uint_as_float((uint32_t)(127 + k) << 23);
+        }
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 a = unpack2<false>(qf[ks][i]);
+            qf[ks][i] = pack_f16x2(a.x * inv[i & 1], a.y * inv[i & 1]);
+          }
+      }
+    }
+    const int s = (int)(u % L::kStages);
+    ok = mbar_wait_warp(bar(s), (uint32_t)(u / L::kStages) & 1u, ctl, 201);
+    if (!ok) break;
+    const uint32_t sk = ring + (uint32_t)(s * L::kStageBytes), sv = sk + L::kTileBytes;
+    const int left = w.len - w.j * KT;      // keys of the sequence from this tile on
+    if (left < KT) {
+      // rows of V past the sequence: whatever the page holds there (NaN times a
+      // weight of zero is NaN) becomes zeros
+      const int first = left < 0 ? 0 : left;
+      constexpr int kChunks = L::kRowBytes / 16;
+      uint8_t* vt = smem + (sv - sbase);
+      for (int c = lane; c < (KT - first) * kChunks * L::kAtoms; c += 32) {
+        const int row = first + (c / kChunks) % (KT - first);
+        const int a = c / (kChunks * (KT - first));
+        *reinterpret_cast<uint4*>(vt + a * L::kAtomBytes + row * L::kRowBytes + 16 * (c % kChunks)) =
+            make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();   // the ring slot is written by TMA again later
+      __syncwarp();
+    }
+
+    // S = Q K^T: sc[2 n + i] of key 8 n + 2 t4 + (i & 1), rows g (i < 2) and g + 8
+    float sc[KT / 8][4];
+#pragma unroll
+    for (int n = 0; n < KT / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[n][i] = 0.f;
+    if constexpr (!E4M3) {
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+        for (int kk = 0; kk < KT / 16; ++kk) {
+          // four 8 x 8 matrices: keys 0-7 / 8-15 of the 16, dims 0-7 / 8-15 of the step
+          uint32_t b[4];
+          const int row = 16 * kk + (lane & 7) + 8 * (lane >> 4);
+          const int chunk = 2 * (ks & 3) + ((lane >> 3) & 1);
+          ldsm4(b, sk + (uint32_t)((ks >> 2) * L::kAtomBytes) + swz<L::kRowBytes>(row, chunk));
+          mma16<F16>(sc[2 * kk], qf[ks], b[0], b[1]);
+          mma16<F16>(sc[2 * kk + 1], qf[ks], b[2], b[3]);
+        }
+    } else {
+#pragma unroll
+      for (int c4 = 0; c4 < kSteps / 4; ++c4)
+#pragma unroll
+        for (int n = 0; n < KT / 8; ++n) {
+          // four 16-dim chunks of 8 keys; a lane gets 4 payloads of each
+          uint32_t b[4];
+          ldsm4(b, sk + swz<L::kRowBytes>(8 * n + (lane & 7), 4 * c4 + (lane >> 3)));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma_f16(sc[n], qf[4 * c4 + i], e4m3_to_f16(b[i] & 0xFFFFu), e4m3_to_f16(b[i] >> 16));
+        }
+    }
+    // scores in log2 units; with e4m3 plus log2 of the value's scale
+    float ivs[KT / 8][2];
+    if constexpr (E4M3) {
+      const uint8_t* ss = smem + (sring - sbase) + s * 2 * L::kScaleBytes;
+#pragma unroll
+      for (int n = 0; n < KT / 8; ++n) {
+        const int key = 8 * n + 2 * t4;
+        const int off = (box == 16 ? (key >> 4) * 128 + (key & 15) * 4 : key * 4);
+        const float2 ks2 = *reinterpret_cast<const float2*>(ss + off);
+        float2 vs2 = *reinterpret_cast<const float2*>(ss + L::kScaleBytes + off);
+        if (key >= left) vs2.x = 1.f;       // past the sequence: any scale, the weight is zero
+        if (key + 1 >= left) vs2.y = 1.f;
+        ivs[n][0] = __fdividef(1.f, vs2.x);
+        ivs[n][1] = __fdividef(1.f, vs2.y);
+        const float lv0 = __log2f(vs2.x), lv1 = __log2f(vs2.y);
+        const float a0 = ks2.x * p.scale_log2, a1 = ks2.y * p.scale_log2;
+        sc[n][0] = fmaf(sc[n][0] * qs[0], a0, lv0);
+        sc[n][1] = fmaf(sc[n][1] * qs[0], a1, lv1);
+        sc[n][2] = fmaf(sc[n][2] * qs[1], a0, lv0);
+        sc[n][3] = fmaf(sc[n][3] * qs[1], a1, lv1);
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < KT / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[n][i] *= p.scale_log2;
+    }
+    if (left - (p.Nq - 1) < KT) {
+      // token i sees the first left - (Nq - 1 - i) keys from here
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int lim = left - (p.Nq - 1) + (rt * kRows + g + 8 * hh) / p.G;
+#pragma unroll
+        for (int n = 0; n < KT / 8; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (8 * n + 2 * t4 + i >= min(lim, left)) sc[n][2 * hh + i] = -INFINITY;
+      }
+    }
+    // running reference: moved when a row's maximum passes it by more than 2^8
+    float alpha[2] = {1.f, 1.f};
+    bool move = false;
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < KT / 8; ++n) mx = fmaxf(mx, fmaxf(sc[n][2 * hh], sc[n][2 * hh + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+      if (mx > m[hh] + kMoveThreshold || (m[hh] == -INFINITY && mx > -INFINITY)) {
+        alpha[hh] = m[hh] == -INFINITY ? 0.f : ex2(m[hh] - mx);
+        m[hh] = mx;
+        l[hh] *= alpha[hh];
+        move = true;
+      }
+    }
+    if (__any_sync(0xFFFFFFFFu, move)) {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[n][i] *= alpha[i >> 1];
+    }
+    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+    for (int n = 0; n < KT / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sc[n][i] = ex2(sc[n][i] - ref[i >> 1]);
+        l[i >> 1] += E4M3 ? sc[n][i] * ivs[n][i & 1] : sc[n][i];
+      }
+    // O += P V, 16 keys at a time; P goes to 16 bits (of the inputs' type, or
+    // fp16 with e4m3: weights of at most 2^8 lose 2^-12 of themselves at most,
+    // or 2^-25 next to a largest one of about 1)
+#pragma unroll
+    for (int kk = 0; kk < KT / 16; ++kk) {
+      constexpr bool PF16 = E4M3 || F16;
+      uint32_t a[4];
+      a[0] = pack2<PF16>(sc[2 * kk][0], sc[2 * kk][1]);
+      a[1] = pack2<PF16>(sc[2 * kk][2], sc[2 * kk][3]);
+      a[2] = pack2<PF16>(sc[2 * kk + 1][0], sc[2 * kk + 1][1]);
+      a[3] = pack2<PF16>(sc[2 * kk + 1][2], sc[2 * kk + 1][3]);
+      const int row = 16 * kk + (lane & 15);
+#pragma unroll
+      for (int c = 0; c < kSteps; ++c) {
+        // !E4M3: dims 16 c .. 16 c + 15 as two 8-dim chunks; E4M3: one 16-dim
+        // chunk per matrix pair, so every second c loads two
+        uint32_t b[4];
+        if constexpr (!E4M3) {
+          const int chunk = 2 * (c & 3) + (lane >> 4);
+          ldsm4_t(b, sv + (uint32_t)((c >> 2) * L::kAtomBytes) + swz<L::kRowBytes>(row, chunk));
+          mma16<F16>(o[2 * c], a, b[0], b[1]);
+          mma16<F16>(o[2 * c + 1], a, b[2], b[3]);
+        } else if ((c & 1) == 0) {
+          ldsm4_t(b, sv + swz<L::kRowBytes>(row, c + (lane >> 4)));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // a word: payloads (key 2t, dims 2n and 2n + 1), (key 2t + 1, the same dims)
+            const uint32_t lo = prmt(b[2 * i], 0u, 0x3120u), hi = prmt(b[2 * i + 1], 0u, 0x3120u);
+            mma_f16(o[2 * (c + i)], a, e4m3_to_f16(lo & 0xFFFFu), e4m3_to_f16(hi & 0xFFFFu));        // even dims
+            mma_f16(o[2 * (c + i) + 1], a, e4m3_to_f16(lo >> 16), e4m3_to_f16(hi >> 16));            // odd dims
+          }
+        }
+      }
+    }
+    __syncwarp();   // every lane has read the tile: its place may be loaded again
+    if (issued < todo && p.stall == 0u) {
+      issue(wi);
+      advance(wi);
+    }
+
+    if (w.j == w.n - 1 || u == todo - 1) {
+      // the end of a (sequence, head, row tile), or of what this warp has of it
+      fresh = true;
+      const bool whole = from_start && w.j == w.n - 1;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        l[hh] += __shfl_xor_sync(0xFFFFFFFFu, l[hh], 1);
+        l[hh] += __shfl_xor_sync(0xFFFFFFFFu, l[hh], 2);
+      }
+      if (from_start && lane == 0) {
+        int2 f = make_int2(-1, -1);
+        if (!whole) {
+          // this warp's range starts it; the last unit belongs to the last worker
+          // whose range starts at or before it
+          const long long last = t0 + u + (w.n - 1 - w.j);
+          f = make_int2(me, (int)(((last + 1) * workers + total - 1) / total) - 1);
+        }
+        p.info[(int64_t)w.b * SUB + w.sub] = f;
+      }
+      const int slot = 2 * me + (from_start ? 1 : 0);
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int rr = g + 8 * hh, r = rt * kRows + rr;
+        if (r >= p.R) continue;
+        if (whole) {
+          const int i = r / p.G, h = hk * p.G + r % p.G;
+          const float inv = l[hh] > 0.f ? 1.f / l[hh] : (l[hh] == 0.f ? 0.f : l[hh]);
+          uint16_t* op = p.o + (((int64_t)w.b * p.Nq + i) * p.Hq + h) * p.d;
+          if constexpr (!E4M3) {
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+              if (8 * n < p.d)
+                *reinterpret_cast<uint32_t*>(op + 8 * n + 2 * t4) = pack2<F16>(o[n][2 * hh] * inv, o[n][2 * hh + 1] * inv);
+          } else {
+#pragma unroll
+            for (int c = 0; c < kSteps; ++c)
+              if (16 * c < p.d)
+                *reinterpret_cast<uint2*>(op + 16 * c + 4 * t4) =
+                    make_uint2(pack2<F16>(o[2 * c][2 * hh] * inv, o[2 * c + 1][2 * hh] * inv),
+                               pack2<F16>(o[2 * c][2 * hh + 1] * inv, o[2 * c + 1][2 * hh + 1] * inv));
+          }
+          if (t4 == 0)
+            p.lse[((int64_t)w.b * p.Hq + h) * p.Nq + i] =
+                l[hh] == 0.f ? -INFINITY : (m[hh] + log2f(l[hh])) * 0.69314718055994531f;
+        } else {
+          float* po = p.part_o + ((int64_t)slot * kRows + rr) * D;
+          if constexpr (!E4M3) {
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+              *reinterpret_cast<float2*>(po + 8 * n + 2 * t4) = make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < kSteps; ++c)
+              *reinterpret_cast<float4*>(po + 16 * c + 4 * t4) =
+                  make_float4(o[2 * c][2 * hh], o[2 * c + 1][2 * hh], o[2 * c][2 * hh + 1], o[2 * c + 1][2 * hh + 1]);
+          }
+          if (t4 == 0) p.part_ml[(int64_t)slot * kRows + rr] = make_float2(m[hh], l[hh]);
+        }
+      }
+    }
+    advance(w);
+  }
+  // every load issued has landed before the warp leaves (after a timeout)
+  if (!ok && lane == 0)
+    for (int s = 0; s < L::kStages && s < issued; ++s)
+      drain_wait(bar(s), (uint32_t)((issued - 1 - s) / L::kStages) & 1u);
+}
+
+// Joins the parts of a (sequence, head, row tile): one block of 4 warps per
+// query row, the parts shared out over the warps, a lane holding D / 32
+// columns. m is the row's reference, l its sum:
+//   O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k,  M = max m_k.
+template <int D, bool F16>
+__global__ void __launch_bounds__(128) fa_cached_join_kernel(const CachedParams p) {
+  constexpr int C = D / 32;
+  __shared__ float sm_o[4][D];
+  __shared__ float sm_ml[4][2];
+  grid_dep_wait();   // the parts are complete
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per_b = p.Hq * p.Nq;
+  const int b = (int)(blockIdx.x / (unsigned)per_b), x = (int)(blockIdx.x % (unsigned)per_b);
+  const int h = x / p.Nq, i = x % p.Nq;
+  const int hk = h / p.G, r = i * p.G + h % p.G;
+  const int2 f = p.info[((int64_t)b * p.Hk + hk) * p.RT + r / kRows];
+  // -1: written whole (or, after a timeout, nothing to join)
+  if (f.x < 0 || f.y <= f.x || f.y >= kMaxWorkers) return;
+  const int rr = r % kRows, parts = f.y - f.x + 1;
+  auto at = [&](int k) -> int64_t { return (int64_t)(2 * (f.x + k) + (k == 0 ? 1 : 0)) * kRows + rr; };
+  float mx = -INFINITY;
+  for (int k = lane; k < parts; k += 32) mx = fmaxf(mx, p.part_ml[at(k)].x);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  float acc[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = 0.f;
+  float l = 0.f;
+#pragma unroll 4
+  for (int k = warp; k < parts; k += 4) {
+    const float2 ml = p.part_ml[at(k)];
+    const float f2 = ex2(ml.x - ref);
+    l = fmaf(f2, ml.y, l);
+    const float* po = p.part_o + at(k) * D + C * lane;
+#pragma unroll
+    for (int c = 0; c < C; c += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(po + c);
+      acc[c] = fmaf(f2, v.x, acc[c]);
+      acc[c + 1] = fmaf(f2, v.y, acc[c + 1]);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) sm_o[warp][C * lane + c] = acc[c];
+  if (lane == 0) sm_ml[warp][0] = l;
+  __syncthreads();
+  l = (sm_ml[0][0] + sm_ml[1][0]) + (sm_ml[2][0] + sm_ml[3][0]);
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  uint16_t* op = p.o + (((int64_t)b * p.Nq + i) * p.Hq + h) * p.d;
+  if (2 * tid < p.d) {
+    const int c = 2 * tid;
+    const float a0 = (sm_o[0][c] + sm_o[1][c]) + (sm_o[2][c] + sm_o[3][c]);
+    const float a1 = (sm_o[0][c + 1] + sm_o[1][c + 1]) + (sm_o[2][c + 1] + sm_o[3][c + 1]);
+    *reinterpret_cast<uint32_t*>(op + c) = pack2<F16>(a0 * inv, a1 * inv);
+  }
+  if (tid == 0)
+    p.lse[((int64_t)b * p.Hq + h) * p.Nq + i] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
+}
+
+struct CachedWorkspace {
+  size_t o_off, ml_off, info_off, total;
+};
+
+CachedWorkspace cached_workspace_layout(int B, int Nq, int Hq, int Hk, int d) {
+  auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const size_t D = d <= 64 ? 64 : 128;
+  const size_t RT = ((size_t)Nq * (Hq / Hk) + kRows - 1) / kRows;
+  CachedWorkspace w;
+  w.o_off = 0;
+  w.ml_off = al((size_t)kMaxWorkers * 2 * kRows * D * sizeof(float));
+  w.info_off = al(w.ml_off + (size_t)kMaxWorkers * 2 * kRows * sizeof(float2));
+  w.total = al(w.info_off + (size_t)B * Hk * RT * sizeof(int2));
+  return w;
+}
+
+fa_status check_cached_shape(int B, int Nq, int Hq, int Hk, int d) {
+  if (B < 1 || Nq < 1 || Hk < 1 || Hq < 1 || Hq % Hk != 0) return FA_ERR_INVALID_ARG;
+  if (d < 8 || d > 128 || d % 8 != 0) return FA_ERR_UNSUPPORTED;
+  const double units = (double)B * Nq * Hq;
+  if (units > 1073741824.0) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+// page sizes the kernels take: 16 .. 256, powers of two; the exponent, or -1
+int page_log2(int page_size) {
+  for (int k = 4; k <= 8; ++k)
+    if (page_size == (1 << k)) return k;
+  return -1;
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+template <int D, bool E4M3, bool F16>
+cudaError_t launch_cached_d(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tks,
+                            const CUtensorMap& tvs, const CachedParams& p, cudaStream_t s) {
+  using L = CachedLayout<D, E4M3>;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static PerDeviceOnce smem_set;
+  e = once_per_device(smem_set, dev, [] {
+    return cudaFuncSetAttribute(fa_cached_kernel<D, E4M3, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                L::kSmemBytes);
+  });
+  if (e != cudaSuccess) return e;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // one CTA per SM, fewer when even full sequences have fewer units
+  const double most = (double)p.B * p.Hk * p.RT * (((double)p.max_pages * p.page_size + L::kKT - 1) / L::kKT);
+  int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  if (most < ctas) ctas = most < 1.0 ? 1 : (int)most;
+  e = launch_pdl(false, fa_cached_kernel<D, E4M3, F16>, dim3((unsigned)ctas), dim3(32 * kWarps), L::kSmemBytes, s, tk, tv,
+                 tks, tvs, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(true, fa_cached_join_kernel<D, F16>, dim3((unsigned)(p.B * p.Hq * p.Nq)), dim3(128), 0, s, p);
+}
+
+}  // namespace
+
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+fa_status flash_attn_kv_cache_write(const void* K, const void* V, int64_t k_token_stride, int64_t k_head_stride,
+                                    int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots, int T,
+                                    int Hk, int d, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                    int num_pages, int page_size, int cache_type, const fa_options* options,
+                                    void* stream) {
+  const bool e4m3 = cache_type == FA_CACHE_E4M3;
+  if (T < 0 || Hk < 1 || num_pages < 1) return FA_ERR_INVALID_ARG;
+  if (!e4m3 && cache_type != FA_CACHE_16BIT) return FA_ERR_UNSUPPORTED;
+  if (d < 8 || d > 128 || d % (e4m3 ? 16 : 8) != 0) return FA_ERR_UNSUPPORTED;
+  const int pl = page_log2(page_size);
+  if (pl < 0) return FA_ERR_UNSUPPORTED;
+  if ((double)T * Hk > 67108864.0) return FA_ERR_UNSUPPORTED;   // 2^26 rows: thread indices stay under 2^31
+  bool f16 = false, flash_only = false;
+  int st = internal_read_options(options, &f16, &flash_only);
+  if (st != FA_OK) return static_cast<fa_status>(st);
+  if (flash_only) return FA_ERR_UNSUPPORTED;
+  if (k_cache == nullptr || v_cache == nullptr || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return FA_ERR_INVALID_ARG;
+  if (e4m3 ? (k_scale == nullptr || v_scale == nullptr || !aligned(k_scale, 16) || !aligned(v_scale, 16))
+           : (k_scale != nullptr || v_scale != nullptr))
+    return FA_ERR_INVALID_ARG;
+  if (T == 0) return FA_OK;
+  if (K == nullptr || V == nullptr || slots == nullptr || !aligned(K, 16) || !aligned(V, 16) || !aligned(slots, 8) ||
+      ((k_token_stride | k_head_stride | v_token_stride | v_head_stride) & 7) != 0)
+    return FA_ERR_INVALID_ARG;
+  unsigned int* err = nullptr;
+  if ((st = internal_device_error_word(&err)) != FA_OK) return static_cast<fa_status>(st);
+  WriteParams p{};
+  p.src[0] = static_cast<const uint16_t*>(K);
+  p.src[1] = static_cast<const uint16_t*>(V);
+  p.tok[0] = k_token_stride;
+  p.tok[1] = v_token_stride;
+  p.head[0] = k_head_stride;
+  p.head[1] = v_head_stride;
+  p.slots = slots;
+  p.cache[0] = k_cache;
+  p.cache[1] = v_cache;
+  p.scale[0] = k_scale;
+  p.scale[1] = v_scale;
+  p.rows = 2u * (uint32_t)T * (uint32_t)Hk;
+  p.T = T;
+  p.Hk = Hk;
+  p.d = d;
+  p.ps_log2 = pl;
+  p.places = (int64_t)num_pages * page_size;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int lanes = d / 8;
+  const cudaError_t e = lanes <= 1   ? launch_write<1>(p, e4m3, f16, s)
+                        : lanes <= 2 ? launch_write<2>(p, e4m3, f16, s)
+                        : lanes <= 4 ? launch_write<4>(p, e4m3, f16, s)
+                        : lanes <= 8 ? launch_write<8>(p, e4m3, f16, s)
+                                     : launch_write<16>(p, e4m3, f16, s);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t flash_attn_cached_workspace_size(int B, int Nq, int Hq, int Hk, int d) {
+  if (check_cached_shape(B, Nq, Hq, Hk, d) != FA_OK) return 0;
+  return cached_workspace_layout(B, Nq, Hq, Hk, d).total;
+}
+
+fa_status flash_attn_cached_fwd(const void* Q, int64_t q_token_stride, const void* k_cache, const void* v_cache,
+                                const float* k_scale, const float* v_scale, const int32_t* block_table,
+                                const int32_t* seq_lens, void* O, float* LSE, int B, int Nq, int Hq, int Hk, int d,
+                                int num_pages, int page_size, int max_pages, float scale, int cache_type,
+                                const fa_options* options, void* workspace, size_t workspace_bytes, void* stream) {
+  const bool e4m3 = cache_type == FA_CACHE_E4M3;
+  fa_status st = check_cached_shape(B, Nq, Hq, Hk, d);
+  if (st != FA_OK) return st;
+  if (num_pages < 1 || max_pages < 1 || !std::isfinite(scale) || scale <= 0.f) return FA_ERR_INVALID_ARG;
+  if (!e4m3 && cache_type != FA_CACHE_16BIT) return FA_ERR_UNSUPPORTED;
+  if (e4m3 && d % 16 != 0) return FA_ERR_UNSUPPORTED;
+  const int pl = page_log2(page_size);
+  if (pl < 0) return FA_ERR_UNSUPPORTED;
+  // page * Hk is a TMA coordinate, lengths and key numbers are 32-bit
+  if ((double)num_pages * Hk > 2147480000.0 || (double)max_pages * page_size > 1073741824.0) return FA_ERR_UNSUPPORTED;
+  bool f16 = false, record = false;
+  uint32_t wait_us = 0, stall = 0;
+  int sr = internal_read_check_options(options, &f16, &record, &wait_us, &stall);
+  if (sr != FA_OK) return static_cast<fa_status>(sr);
+  if (record) return FA_ERR_UNSUPPORTED;
+  const void* ptrs[] = {Q, k_cache, v_cache, O, LSE, block_table, seq_lens};
+  for (const void* x : ptrs)
+    if (x == nullptr) return FA_ERR_INVALID_ARG;
+  if (!aligned(Q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(O, 16) || !aligned(LSE, 4) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4))
+    return FA_ERR_INVALID_ARG;
+  if ((q_token_stride & 7) != 0 || q_token_stride < (int64_t)Hq * d) return FA_ERR_INVALID_ARG;
+  if (e4m3 ? (k_scale == nullptr || v_scale == nullptr || !aligned(k_scale, 16) || !aligned(v_scale, 16))
+           : (k_scale != nullptr || v_scale != nullptr))
+    return FA_ERR_INVALID_ARG;
+  const CachedWorkspace w = cached_workspace_layout(B, Nq, Hq, Hk, d);
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < w.total) return FA_ERR_WORKSPACE;
+  unsigned int* err = nullptr;
+  if ((sr = internal_device_error_word(&err)) != FA_OK) return static_cast<fa_status>(sr);
+
+  const int D = d <= 64 ? 64 : 128;
+  const int KT = (!e4m3 && D == 128) ? 16 : 32;
+  const uint32_t box_keys = (uint32_t)(page_size < KT ? page_size : KT);
+  CUtensorMap tk, tv, tks, tvs;
+  {
+    const uint64_t es = e4m3 ? 1 : 2;
+    const uint64_t dims[3] = {(uint64_t)d, (uint64_t)page_size, (uint64_t)num_pages * Hk};
+    const uint64_t strides[2] = {d * es, (uint64_t)page_size * d * es};
+    const uint32_t box[3] = {(uint32_t)(e4m3 ? D : 64), box_keys, 1};
+    const CUtensorMapDataType ty = e4m3  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                         : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapSwizzle sw = e4m3 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    if (internal_tensor_map(&tk, ty, 3, k_cache, dims, strides, box, sw) ||
+        internal_tensor_map(&tv, ty, 3, v_cache, dims, strides, box, sw))
+      return FA_ERR_CUDA;
+    const uint64_t sdims[2] = {(uint64_t)page_size, (uint64_t)num_pages * Hk};
+    const uint64_t sstr[1] = {(uint64_t)page_size * 4};
+    const uint32_t sbox[2] = {box_keys, 1};
+    tks = tk;
+    tvs = tv;
+    if (e4m3 &&
+        (internal_tensor_map(&tks, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, k_scale, sdims, sstr, sbox,
+                             CU_TENSOR_MAP_SWIZZLE_NONE) ||
+         internal_tensor_map(&tvs, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, v_scale, sdims, sstr, sbox,
+                             CU_TENSOR_MAP_SWIZZLE_NONE)))
+      return FA_ERR_CUDA;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  CachedParams p{};
+  p.q = static_cast<const uint16_t*>(Q);
+  p.q_tok = q_token_stride;
+  p.table = block_table;
+  p.lens = seq_lens;
+  p.o = static_cast<uint16_t*>(O);
+  p.lse = LSE;
+  p.part_o = reinterpret_cast<float*>(ws + w.o_off);
+  p.part_ml = reinterpret_cast<float2*>(ws + w.ml_off);
+  p.info = reinterpret_cast<int2*>(ws + w.info_off);
+  p.err = err;
+  p.B = B;
+  p.Nq = Nq;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.G = Hq / Hk;
+  p.d = d;
+  p.R = Nq * p.G;
+  p.RT = (p.R + kRows - 1) / kRows;
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.ps_log2 = pl;
+  p.max_pages = max_pages;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.wait_us = wait_us;
+  p.stall = stall;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaErrorInvalidValue;
+#define FA_CACHED_CASE(DD, EE, FF) \
+  if (D == DD && e4m3 == EE && f16 == FF) e = launch_cached_d<DD, EE, FF>(tk, tv, tks, tvs, p, s);
+  FA_CACHED_CASE(64, false, false)
+  FA_CACHED_CASE(64, false, true)
+  FA_CACHED_CASE(64, true, false)
+  FA_CACHED_CASE(64, true, true)
+  FA_CACHED_CASE(128, false, false)
+  FA_CACHED_CASE(128, false, true)
+  FA_CACHED_CASE(128, true, false)
+  FA_CACHED_CASE(128, true, true)
+#undef FA_CACHED_CASE
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -226,6 +226,13 @@ int internal_device_error_word(unsigned int** err);   // current device; runs it
 // options: const fa_options* or null. flash_only: an option only the flash
 // kernels implement is set (dropout, tile record, test stall).
 int internal_read_options(const void* options, bool* f16, bool* flash_only);
+// The same for calls that have bounded waits but no dropout and no tile record
+// (record: one of the two is set).
+int internal_read_check_options(const void* options, bool* f16, bool* record, uint32_t* wait_us, uint32_t* stall);
+// Tiled tensor map of the given rank (element strides 1, no interleave, zero
+// fill, 256-byte L2 promotion); nonzero on failure. After internal_device_error_word.
+int internal_tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
+                        const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
 
 // Arguments of a backward call (the flash_attn_bwd signature without the
 // workspace and the stream).
