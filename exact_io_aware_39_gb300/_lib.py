@@ -1,5 +1,5 @@
 """ctypes binding of libflashattn.so: the C ABI of include/flash_attn.h,
-flash_attn_cache.h and standard_attn.h under the same names, plus thin helpers
+flash_attn_packed.h, flash_attn_cache.h and standard_attn.h under the same names, plus thin helpers
 that take torch tensors.
 
 Argument marshalling only: every step of the computation runs in the CUDA
@@ -30,6 +30,7 @@ EXPORTS = [
     "flash_attn_tile_map",
     "flash_attn_get_device_error", "flash_attn_set_profile_events", "flash_attn_status_string",
     "flash_attn_version",
+    "flash_attn_packed_workspace_size", "flash_attn_packed_fwd", "flash_attn_packed_bwd",
     "flash_attn_kv_cache_write", "flash_attn_cached_workspace_size", "flash_attn_cached_fwd",
     "standard_attn_workspace_size", "standard_attn_fwd", "standard_attn_bwd",
 ]
@@ -93,6 +94,12 @@ def load(path=LIB_PATH):
     lib.flash_attn_version.argtypes = []
     lib.flash_attn_version.restype = i32
     i64 = ctypes.c_int64
+    lib.flash_attn_packed_workspace_size.argtypes = [i32] * 6
+    lib.flash_attn_packed_workspace_size.restype = sz
+    lib.flash_attn_packed_fwd.argtypes = [vp] * 6 + [i32] * 5 + [vp, f32, i32, opt_p, vp, sz, vp]
+    lib.flash_attn_packed_fwd.restype = i32
+    lib.flash_attn_packed_bwd.argtypes = [vp] * 10 + [i32] * 5 + [vp, f32, i32, opt_p, vp, sz, vp]
+    lib.flash_attn_packed_bwd.restype = i32
     lib.flash_attn_kv_cache_write.argtypes = [vp, vp, i64, i64, i64, i64, vp, i32, i32, i32, vp, vp, vp, vp, i32, i32,
                                               i32, opt_p, vp]
     lib.flash_attn_kv_cache_write.restype = i32
@@ -168,6 +175,24 @@ def flash_attn_status_string(status):
 
 def flash_attn_version():
     return load().flash_attn_version()
+
+
+def flash_attn_packed_workspace_size(B, total, Hq, Hk, d, backward):
+    return load().flash_attn_packed_workspace_size(B, total, Hq, Hk, d, backward)
+
+
+def flash_attn_packed_fwd(Q, K, V, O, LSE, cu_seqlens, B, total, Hq, Hk, d, strides, scale, causal, options, workspace,
+                          workspace_bytes, stream):
+    return load().flash_attn_packed_fwd(Q, K, V, O, LSE, cu_seqlens, B, total, Hq, Hk, d, strides, scale, causal,
+                                        None if options is None else ctypes.byref(options), workspace,
+                                        workspace_bytes, stream)
+
+
+def flash_attn_packed_bwd(Q, K, V, O, dO, LSE, dQ, dK, dV, cu_seqlens, B, total, Hq, Hk, d, strides, scale, causal,
+                          options, workspace, workspace_bytes, stream):
+    return load().flash_attn_packed_bwd(Q, K, V, O, dO, LSE, dQ, dK, dV, cu_seqlens, B, total, Hq, Hk, d, strides, scale,
+                                        causal, None if options is None else ctypes.byref(options), workspace,
+                                        workspace_bytes, stream)
 
 
 def flash_attn_kv_cache_write(K, V, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots, T, Hk, d,
@@ -375,21 +400,101 @@ def standard_attention_bwd(q, k, v, do, workspace, scale, stream=None, s16=False
 
 
 # ---------------------------------------------------------------------------
+# packed sequences with grouped heads
+# ---------------------------------------------------------------------------
+
+def _rows16(t, name, tokens, heads, d, dtype, device):
+    """Checks a 16-bit tensor [tokens, heads, d] whose rows may be strided
+    (views of a fused projection): d elements in one piece, token and head
+    strides positive multiples of 8 elements. Returns the two strides."""
+    if t.shape != (tokens, heads, d) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor {[tokens, heads, d]} on {device}")
+    tok, head, one = t.stride()
+    if tokens <= 1:
+        tok = heads * d        # (the stride of a single token, or of none, says nothing)
+    if heads == 1:
+        head = d
+    if (one != 1 and d > 1) or tok <= 0 or head <= 0 or tok % 8 or head % 8:
+        raise ValueError(f"{name}: rows must be contiguous, with token and head strides that are positive multiples of 8")
+    return tok, head
+
+
+def _packed_args(q, k, v, cu_seqlens):
+    import torch
+    dt = _dtype16(q, "q")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [tokens, Hq, d] and k, v [tokens, Hk, d]")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or cu_seqlens.dtype != torch.int32 \
+            or cu_seqlens.device != q.device or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous int32 tensor [B + 1] on q's device")
+    return dt
+
+
+def attention_packed_fwd(q, k, v, cu_seqlens, scale, causal=True, out=None, lse=None, workspace=None, stream=None,
+                         wait_limit_us=0, test_stall=0):
+    """O, LSE of attention within each sequence of a packed batch. q: bf16 or
+    fp16 [tokens, Hq, d]; k, v: [tokens, Hk, d], Hq a multiple of Hk (query
+    head h reads key/value head h // (Hq // Hk)); rows may be strided, as views
+    of a fused projection are. cu_seqlens: int32 [B + 1], sequence b is rows
+    cu_seqlens[b] .. cu_seqlens[b + 1] - 1. Returns O like q and LSE float32
+    [Hq, tokens]; rows of no sequence are left as they are in `out` and `lse`."""
+    import torch
+    opts = fa_options(_packed_args(q, k, v, cu_seqlens), wait_limit_us=wait_limit_us, test_stall=test_stall)
+    T, Hq, d = q.shape
+    Hk, B, dev = k.shape[1], cu_seqlens.numel() - 1, q.device
+    stream, ctx = _on(stream, dev)
+    with ctx:
+        o = torch.empty((T, Hq, d), dtype=q.dtype, device=dev) if out is None else out
+        l = torch.empty((Hq, T), dtype=torch.float32, device=dev) if lse is None else lse
+        _like(l, "lse", (Hq, T), torch.float32, dev)
+        st = (ctypes.c_int64 * 8)(*_rows16(q, "q", T, Hq, d, q.dtype, dev), *_rows16(k, "k", T, Hk, d, q.dtype, dev),
+                                  *_rows16(v, "v", T, Hk, d, q.dtype, dev), *_rows16(o, "out", T, Hq, d, q.dtype, dev))
+        if workspace is None:
+            workspace = torch.empty(flash_attn_packed_workspace_size(B, T, Hq, Hk, d, 0), dtype=torch.uint8, device=dev)
+        _workspace_on(workspace, dev)
+        rc = flash_attn_packed_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(l), _ptr(cu_seqlens), B, T, Hq, Hk, d, st,
+                                   float(scale), int(bool(causal)), opts, _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "flash_attn_packed_fwd")
+    return o, l
+
+
+def attention_packed_bwd(q, k, v, o, do, lse, cu_seqlens, scale, causal=True, workspace=None, dq=None, dk=None, dv=None,
+                         stream=None, wait_limit_us=0, test_stall=0):
+    """dQ, dK, dV of attention_packed_fwd from its inputs, its O and LSE and the
+    output gradient do (like q); dK and dV are summed over the query heads that
+    share a key/value head. Rows of no sequence are left as they are in dq, dk,
+    dv (which may be strided like q, k, v)."""
+    import torch
+    opts = fa_options(_packed_args(q, k, v, cu_seqlens), wait_limit_us=wait_limit_us, test_stall=test_stall)
+    T, Hq, d = q.shape
+    Hk, B, dev, dt = k.shape[1], cu_seqlens.numel() - 1, q.device, q.dtype
+    stream, ctx = _on(stream, dev)
+    with ctx:
+        dq = torch.empty((T, Hq, d), dtype=dt, device=dev) if dq is None else dq
+        dk = torch.empty((T, Hk, d), dtype=dt, device=dev) if dk is None else dk
+        dv = torch.empty((T, Hk, d), dtype=dt, device=dev) if dv is None else dv
+        _like(lse, "lse", (Hq, T), torch.float32, dev)
+        st = []
+        for t, name, h in ((q, "q", Hq), (k, "k", Hk), (v, "v", Hk), (o, "o", Hq), (do, "do", Hq), (dq, "dq", Hq),
+                           (dk, "dk", Hk), (dv, "dv", Hk)):
+            st += _rows16(t, name, T, h, d, dt, dev)
+        if workspace is None:
+            workspace = torch.empty(flash_attn_packed_workspace_size(B, T, Hq, Hk, d, 1), dtype=torch.uint8, device=dev)
+        _workspace_on(workspace, dev)
+        rc = flash_attn_packed_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+                                   _ptr(cu_seqlens), B, T, Hq, Hk, d, (ctypes.c_int64 * 16)(*st), float(scale),
+                                   int(bool(causal)), opts, _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "flash_attn_packed_bwd")
+    return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------
 # serving from a paged key/value cache
 # ---------------------------------------------------------------------------
 
 FA_CACHE_16BIT, FA_CACHE_E4M3 = 0, 1
-
-
-def _rows16(t, name, heads, d, dtype, device):
-    """Checks a 16-bit tensor [tokens, heads, d] whose rows may be strided
-    (views of a fused projection): d elements in one piece, token and head
-    strides multiples of 8 elements, 16-byte aligned."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor [tokens, {heads}, {d}] on {device}")
-    st = t.stride()
-    if st[2] != 1 or st[0] % 8 or st[1] % 8:
-        raise ValueError(f"{name}: rows must be contiguous, with token and head strides that are multiples of 8")
 
 
 def _cache_args(k_cache, v_cache, k_scale, v_scale, dtype, device):
@@ -444,15 +549,15 @@ def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, st
         raise ValueError("k must be [T, Hk, d] and k_cache [num_pages, Hk, page_size, d]")
     T, Hk, d = k.shape
     dev = k.device
-    _rows16(k, "k", k_cache.shape[1], k_cache.shape[3], k.dtype, dev)
-    _rows16(v, "v", Hk, d, k.dtype, dev)
-    if v.shape[0] != T or slots.shape != (T,) or slots.dtype != torch.int64 or slots.device != dev \
+    k_st = _rows16(k, "k", T, k_cache.shape[1], k_cache.shape[3], k.dtype, dev)
+    v_st = _rows16(v, "v", T, Hk, d, k.dtype, dev)
+    if slots.shape != (T,) or slots.dtype != torch.int64 or slots.device != dev \
             or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous int64 tensor with one entry per token of k and v")
     kind = _cache_args(k_cache, v_cache, k_scale, v_scale, k.dtype, dev)
     stream, ctx = _on(stream, dev)
     with ctx:
-        st = flash_attn_kv_cache_write(_ptr(k), _ptr(v), k.stride(0), k.stride(1), v.stride(0), v.stride(1), _ptr(slots),
+        st = flash_attn_kv_cache_write(_ptr(k), _ptr(v), *k_st, *v_st, _ptr(slots),
                                        T, Hk, d, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
                                        k_cache.shape[0], k_cache.shape[2], kind, opts, _stream(stream))
     _check(st, "flash_attn_kv_cache_write")

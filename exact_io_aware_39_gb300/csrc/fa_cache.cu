@@ -843,7 +843,8 @@ fa_status flash_attn_kv_cache_write(const void* K, const void* V, int64_t k_toke
     return FA_ERR_INVALID_ARG;
   if (T == 0) return FA_OK;
   if (K == nullptr || V == nullptr || slots == nullptr || !aligned(K, 16) || !aligned(V, 16) || !aligned(slots, 8) ||
-      ((k_token_stride | k_head_stride | v_token_stride | v_head_stride) & 7) != 0)
+      ((k_token_stride | k_head_stride | v_token_stride | v_head_stride) & 7) != 0 || k_token_stride <= 0 ||
+      k_head_stride <= 0 || v_token_stride <= 0 || v_head_stride <= 0)
     return FA_ERR_INVALID_ARG;
   unsigned int* err = nullptr;
   if ((st = internal_device_error_word(&err)) != FA_OK) return static_cast<fa_status>(st);

@@ -1,0 +1,829 @@
+// Backward pass over packed sequences with grouped heads, by recomputation, for
+// sm_103a. The computation of one (128-key tile, 128-query tile) pair is that of
+// fa_bwd.cu (five tcgen05 products, P and dS recomputed by two warpgroups, the
+// dQ partial drained by a third and added into an fp32 accumulator with TMA
+// reduce-add). What is different:
+//   * a work item is a key tile of one (sequence, key/value head). A CTA loops
+//     over the G query heads of that head and their live query tiles, so dK and
+//     dV of a shared head are summed in TMEM, in a fixed order, and written
+//     once; nothing of them is added through memory;
+//   * items come from the list that the plan kernel makes on the device,
+//     heaviest first, through a counter;
+//   * tiles are boxes of the strided [token, head, d] tensors and may run into
+//     the next sequence: the MMA warp zeroes the rows past the end in shared
+//     memory (K and V once per item, Q and dO at a head's last query tile)
+//     before the products that read them, so what lies there (NaN included)
+//     reaches no sum;
+//   * the row statistics and the dQ accumulator are kept over sequences padded
+//     to whole tiles, where the 128-row copies need no bounds; rows of dK, dV
+//     past a sequence's end are not stored.
+//
+// Launches (after the plan): the pre-pass (D = rowsum(dO * O), LSE * log2 e,
+// zeroed accumulator), the main kernel, and dQ = 16-bit(scale * accumulator).
+#include "fa_packed.cuh"
+
+namespace fa {
+
+namespace {
+
+// Warp roles: 0-3 and 4-7 recompute P and dS for query columns 0-63 and 64-127
+// (thread = key row), 8-11 drain dQ (thread = query row), 12 TMA producer,
+// 13 MMA, 14-15 idle (their warpgroup hands its registers to the others).
+constexpr int kGroups = 2;
+constexpr int kCols = kTile / kGroups;
+constexpr int kBwdThreads = 128 * (kGroups + 2);
+constexpr int kDrainWarp0 = 4 * kGroups;
+constexpr int kProducerWarp = kDrainWarp0 + 4;
+constexpr int kMmaWarp = kProducerWarp + 1;
+constexpr int kComputeRegs = 160, kDrainRegs = 96, kOtherRegs = 96;
+static_assert(128 * (kGroups * kComputeRegs + kDrainRegs + kOtherRegs) == kBwdThreads * 128,
+              "the reallocated registers must add up to the launch allocation");
+
+template <int D>
+struct PackedBwdLayout {
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kHalves = D / 64;
+  static constexpr int kStages = (D == 64) ? 3 : 2;   // Q/dO ring depth (smem-limited at d = 128)
+  static constexpr int kKV = (D == 64) ? 2 : 1;        // K/V buffers (a second one fits at d = 64)
+  static constexpr int kKVBytes = 2 * kTileBytes;
+  static constexpr int kK = 0;                                // [kKV] buffers of K then V
+  static constexpr int kV = kK + kTileBytes;
+  static constexpr int kQ = kKV * kKVBytes;                   // [stages]
+  static constexpr int kdO = kQ + kStages * kTileBytes;       // [stages]
+  static constexpr int kdS = kdO + kStages * kTileBytes;      // 128 x 128 bf16
+  static constexpr int kRow = kdS + kTile * kTile * 2;        // [stages] x (LSE2[128], D[128])
+  static constexpr int kBar = kRow + kStages * 2 * kTile * 4;
+  static constexpr int bKV = 0;                            // [kKV]
+  static constexpr int bQFull = bKV + kKV;
+  static constexpr int bQEmpty = bQFull + kStages;
+  static constexpr int bdOFull = bQEmpty + kStages;        // [stages]
+  static constexpr int bdOFree = bdOFull + kStages;        // [stages]: dQ staging read by TMA (1 arrival, 4 per warp at d = 128)
+  static constexpr int bSFull = bdOFree + kStages;
+  static constexpr int bPFull = bSFull + 1;
+  static constexpr int bdPFull = bPFull + 1;
+  static constexpr int bdSFull = bdPFull + 1;
+  static constexpr int bdSEmpty = bdSFull + 1;
+  static constexpr int bdQFull = bdSEmpty + 1;
+  static constexpr int bdQFree = bdQFull + 1;
+  static constexpr int bFinal = bdQFree + 1;
+  static constexpr int bDrain = bFinal + 1;
+  static constexpr int bKVFree = bDrain + 1;   // [kKV]: the epilogue's staging has been read (2 arrivals)
+  // work items reach the other roles through a ring filled by the producer
+  static constexpr int kItemRing = 4;
+  static constexpr int bItemFull = bKVFree + kKV;            // [kItemRing]
+  static constexpr int bItemEmpty = bItemFull + kItemRing;   // [kItemRing]: MMA warp, compute and drain warps
+  static constexpr int bdSHalf = bItemEmpty + kItemRing;     // the first 32 dS^T columns of each warpgroup
+  static constexpr int kNumBars = bdSHalf + 1;
+  static constexpr int kMisc = kBar + 8 * kNumBars;   // tmem slot, abort flag, -, wait limit
+  static constexpr int kRing = kMisc + 16;                    // [kItemRing] x {key tile, head, first row, length, first padded tile, -, -, -}
+  static constexpr int kSmemBytes = kRing + 32 * kItemRing;
+  // the dQ partial is drained per warp (each warp adds its own 32 rows) at
+  // d = 128 and by the four warps together (whole 128-row boxes) at d = 64:
+  // measured, each is the faster one at its width
+  static constexpr bool kGroupDrain = (D == 64);
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+                   const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv,
+                   const __grid_constant__ CUtensorMap tdq, const PackedBwdParams p) {
+  using L = PackedBwdLayout<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+
+  // An item: key tile kj of the sequence of rows start .. start + len - 1, for
+  // key/value head hk; its query tiles i0 .. nT - 1 of each of the G query
+  // heads, a head after the other; slot0 is the sequence's first padded tile.
+  struct Item {
+    int kj, hk, start, len, slot0;
+    int i0, nT;
+    __device__ __forceinline__ int tail() const { return len & (kTile - 1); }
+  };
+  auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * (uint32_t)i; };
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile uint32_t* abort_flag = misc + 1;
+  Ctl ctl{p.err, abort_flag};
+  volatile int* ring = reinterpret_cast<volatile int*>(smem + L::kRing);
+  // item k of this CTA from the ring; kj < 0 when none is left or a wait
+  // failed (then ok is false too)
+  auto take_item = [&](int k, bool& ok) -> Item {
+    const int rs = k % L::kItemRing;
+    const uint32_t ph = (uint32_t)(k / L::kItemRing) & 1u;
+    ok = mbar_wait_warp(bar(L::bItemFull + rs), ph, ctl, 355);
+    Item w{-1, 0, 0, 0, 0, 0, 0};
+    if (!ok) return w;
+    w.kj = ring[8 * rs];
+    w.hk = ring[8 * rs + 1];
+    w.start = ring[8 * rs + 2];
+    w.len = ring[8 * rs + 3];
+    w.slot0 = ring[8 * rs + 4];
+    w.nT = (w.len + kTile - 1) / kTile;
+    w.i0 = p.causal ? w.kj : 0;
+    mbar_arrive_warp(bar(L::bItemEmpty + rs));
+    return w;
+  };
+
+  if ((sbase & 1023u) != 0u) {   // uniform across the CTA: nothing has started yet
+    if (tid == 0) {
+      uint32_t dummy = 0;   // report_error writes only the abort flag
+      Ctl c0{p.err, &dummy};
+      report_error(c0, kErrSmemAlign, 350);
+    }
+    return;
+  }
+
+  if (tid == 0) {
+    for (int i = 0; i < L::kNumBars; ++i)
+      mbar_init(bar(i), (i == L::bPFull || i == L::bdSFull || i == L::bdSHalf) ? (uint32_t)(4 * kGroups)
+                        : i == L::bdQFree ? 4u                                       // the four drain warps
+                        : (i >= L::bKVFree && i < L::bKVFree + L::kKV) ? (uint32_t)kGroups   // one thread per compute group
+                        : (!L::kGroupDrain && i >= L::bdOFree && i < L::bdOFree + L::kStages) ? 4u   // the drain warps
+                        : (i >= L::bItemEmpty && i < L::bItemEmpty + L::kItemRing)
+                            ? (uint32_t)(1 + 4 * kGroups + 4) : 1u);   // arrivals: MMA, compute and drain warps
+    abort_flag[0] = 0u;
+    abort_flag[2] = p.wait_us;   // the wait limit, read by the slow path of every wait
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(misc), 512);
+    tmem_relinquish();
+  }
+  // global memory is read and written only from here on: what the pre-pass
+  // wrote (row statistics, zeroed accumulator and work counter) is visible
+  grid_dep_wait();
+  grid_dep_launch();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  const uint32_t tmem = misc[0];
+  const uint32_t tdV = tmem;
+  const uint32_t tdK = tmem + (uint32_t)D;
+  const uint32_t tS = tmem + 2u * D;
+  const uint32_t tP = tmem + 2u * D + 128u;   // dP^T (and at d = 128 then the dQ partial)
+  // At d = 64 the dQ partial has 64 columns of its own (2d + 256 + d <= 512),
+  // which allows a schedule where nothing waits for its drain (see the MMA
+  // issuer); at d = 128 it reuses the dP^T columns.
+  constexpr bool kOwnDQ = (D == 64);
+  constexpr bool kSplitDS = (D == 128);   // dS^T handed to dK in two halves
+  const uint32_t tQ = kOwnDQ ? tmem + 2u * D + 256u : tP;
+  // S^T of the next tile right behind dV (before dK) at d = 64; at d = 128
+  // behind dQ, which leaves its Q load the longest window
+  constexpr bool kEarlyS = kOwnDQ;
+  // dS^T for dK: packed over the consumed dP^T columns when the next S^T is
+  // issued before dK (dQ, which reuses those columns at d = 128, is issued
+  // after dK, and the tensor pipe runs in issue order), else into the S
+  // columns next to P^T
+  const uint32_t tDS = kEarlyS ? tP : tS + (uint32_t)(kCols / 2);
+  // TMEM column of K step ks (16 queries) of the packed P^T / dS^T: each
+  // warpgroup packs its kCols queries into the first kCols / 2 of its own
+  // kCols S (or dP^T) columns
+  auto packed_col = [](int ks) -> uint32_t {
+    constexpr int kSteps = kCols / 16;   // K steps per warpgroup
+    return (uint32_t)(kCols * (ks / kSteps) + 8 * (ks % kSteps));
+  };
+
+  // Every role walks the same items in the same order and counts the query
+  // tiles it has passed over all of them (g): ring slots and barrier phases
+  // follow g, so the pipeline runs on across item boundaries. Work items walk
+  // groups of p.group key/value heads (whose Q, dO and dQ accumulator fit in L2
+  // together), within a group the list's order (heaviest first), and for each
+  // entry the heads of the group.
+  const int n_items = p.plan->items;
+  const int total = n_items * p.Hk;
+  const size_t Np = (size_t)p.cap_tiles * kTile;
+  if (warp >= kProducerWarp) regs_dec<kOtherRegs>();
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_map(&tq);
+      tma_prefetch_map(&tk);
+      tma_prefetch_map(&tv);
+      tma_prefetch_map(&tdo);
+      int nq = 0, nd = 0, nkv = 0;
+      // K and V of item k into buffer k % kKV, once the epilogue of the item
+      // that used the buffer before has been read out of it
+      auto load_kv = [&](int k, const Item& w) -> bool {
+        const int kb = k % L::kKV;
+        if (k >= L::kKV && !mbar_wait(bar(L::bKVFree + kb), (uint32_t)(k / L::kKV - 1) & 1u, ctl, 353)) return false;
+        mbar_arrive_expect_tx(bar(L::bKV + kb), 2u * L::kTileBytes);
+        for (int h = 0; h < L::kHalves; ++h) {
+          tma_load_3d(sbase + L::kK + kb * L::kKVBytes + h * 16384, &tk, bar(L::bKV + kb), 64 * h, w.hk,
+                      w.start + kTile * w.kj);
+          tma_load_3d(sbase + L::kV + kb * L::kKVBytes + h * 16384, &tv, bar(L::bKV + kb), 64 * h, w.hk,
+                      w.start + kTile * w.kj);
+        }
+        ++nkv;
+        return true;
+      };
+      bool ok = true;
+      int g = 0;
+      for (int k = 0; ok; ++k) {
+        // claim the next item and hand it to the other roles
+        const int rs = k % L::kItemRing;
+        if (k >= L::kItemRing &&
+            !(ok = mbar_wait(bar(L::bItemEmpty + rs), (uint32_t)(k / L::kItemRing - 1) & 1u, ctl, 354)))
+          break;
+        Item w{-1, 0, 0, 0, 0, 0, 0};
+        for (bool first = k == 0;; first = false) {
+          const int item = first ? (int)blockIdx.x : (int)gridDim.x + (int)atomicAdd(&p.plan->sched, 1u);
+          if (item >= total) break;
+          const PackedItem pi = p.items[split_grouped(item, p.group, n_items, p.Hk, &w.hk)];
+          if (pi.len <= 0) continue;   // left out by the plan
+          w.kj = pi.c;
+          w.start = pi.start;
+          w.len = pi.len;
+          w.slot0 = pi.slot0;
+          w.nT = (w.len + kTile - 1) / kTile;
+          w.i0 = p.causal ? w.kj : 0;
+          break;
+        }
+        ring[8 * rs] = w.kj;
+        ring[8 * rs + 1] = w.hk;
+        ring[8 * rs + 2] = w.start;
+        ring[8 * rs + 3] = w.len;
+        ring[8 * rs + 4] = w.slot0;
+        mbar_arrive(bar(L::bItemFull + rs));   // (release: the ring entry is visible to the waiters)
+        if (w.kj < 0) break;
+        for (int it = 0, i = w.i0, hq = w.hk * p.G; it < p.G * (w.nT - w.i0); ++it, ++g) {
+          if (p.stall != 0u && g >= 1) { ok = false; break; }   // test of the timeout path: Q of tile 1 never comes
+          const int s = g % L::kStages;
+          const uint32_t n = (uint32_t)(g / L::kStages);
+          // Q and the row statistics once dK has read the slot's Q; dO once the
+          // dQ partial staged in the slot's dO buffer has been read
+          if (g >= L::kStages && !(ok = mbar_wait(bar(L::bQEmpty + s), (n - 1) & 1u, ctl, 351))) break;
+          mbar_arrive_expect_tx(bar(L::bQFull + s), L::kTileBytes + 2u * kTile * 4u);
+          for (int h = 0; h < L::kHalves; ++h)
+            tma_load_3d(sbase + L::kQ + s * L::kTileBytes + h * 16384, &tq, bar(L::bQFull + s),
+                        64 * h, hq, w.start + kTile * i);
+          const size_t roff = (size_t)hq * Np + (size_t)kTile * (w.slot0 + i);
+          bulk_load(sbase + L::kRow + s * 1024, p.lse2 + roff, kTile * 4, bar(L::bQFull + s));
+          bulk_load(sbase + L::kRow + s * 1024 + 512, p.delta + roff, kTile * 4, bar(L::bQFull + s));
+          ++nq;
+          if (g >= L::kStages && !(ok = mbar_wait(bar(L::bdOFree + s), (n - 1) & 1u, ctl, 352))) break;
+          mbar_arrive_expect_tx(bar(L::bdOFull + s), L::kTileBytes);
+          for (int h = 0; h < L::kHalves; ++h)
+            tma_load_3d(sbase + L::kdO + s * L::kTileBytes + h * 16384, &tdo, bar(L::bdOFull + s),
+                        64 * h, hq, w.start + kTile * i);
+          ++nd;
+          // K and V behind the first query tile of the item, whose loads only
+          // wait for ring slots of the previous item
+          if (it == 0 && !(ok = load_kv(k, w))) break;
+          if (++i == w.nT) {
+            i = w.i0;
+            ++hq;
+          }
+        }
+      }
+      // every load issued has landed before the CTA exits
+      for (int kb = 0; kb < L::kKV && kb < nkv; ++kb)
+        drain_wait(bar(L::bKV + kb), (uint32_t)((nkv - 1 - kb) / L::kKV) & 1u);
+      for (int s = 0; s < L::kStages; ++s) {
+        if (s < nq) drain_wait(bar(L::bQFull + s), (uint32_t)((nq - 1 - s) / L::kStages) & 1u);
+        if (s < nd) drain_wait(bar(L::bdOFull + s), (uint32_t)((nd - 1 - s) / L::kStages) & 1u);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    // the whole warp runs the schedule and one elected lane issues each MMA and
+    // commit; all lanes take part when the rows past a sequence are zeroed
+    {
+      constexpr uint32_t idSP = idesc_16<F16>(128, 128, false, false);
+      constexpr uint32_t idV = idesc_16<F16>(128, D, false, true);
+      constexpr uint32_t idK = idesc_16<F16>(128, D, false, true);
+      constexpr uint32_t idQ = idesc_16<F16>(128, D, true, true);
+      const uint32_t sdS = sbase + L::kdS;
+      bool ok = true;
+      int g = 0;
+      // Shared-memory descriptors are built as a base plus a constant step per
+      // K step wherever that keeps within the MMA thread's registers, so that
+      // issuing an MMA costs the thread one 64-bit add.
+      // S^T = K Q^T of running query tile g1 (tail: its first row past the
+      // sequence, or 0)
+      auto issue_s = [&](uint32_t sK, int g1, int tail) -> bool {
+        const int s1 = g1 % L::kStages;
+        if (!mbar_wait_warp(bar(L::bQFull + s1), (uint32_t)(g1 / L::kStages) & 1u, ctl, 364)) return false;
+        if (tail != 0) zero_tail_rows<D>(smem + L::kQ + s1 * L::kTileBytes, tail);
+        tc_fence_after();
+        const uint64_t dK0 = desc_kmajor(sK, 0), dQ0 = desc_kmajor(sbase + L::kQ + s1 * L::kTileBytes, 0);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          mma_ss_w(tS, dK0 + kmajor_step(ks), dQ0 + kmajor_step(ks), idSP, ks > 0 ? 1u : 0u);
+        mma_commit_w(bar(L::bSFull));
+        return true;
+      };
+      for (int k = 0; ok; ++k) {
+        const Item w = take_item(k, ok);
+        if (w.kj < 0) break;
+        int i = w.i0;
+        const int tail = w.tail(), steps = p.G * (w.nT - w.i0);
+        const int kb = k % L::kKV;
+        const uint32_t sK = sbase + L::kK + kb * L::kKVBytes, sV = sbase + L::kV + kb * L::kKVBytes;
+        const uint64_t mK = desc_mnmajor(sK, 0);
+        if (!(ok = mbar_wait_warp(bar(L::bKV + kb), (uint32_t)(k / L::kKV) & 1u, ctl, 360))) break;
+        if (tail != 0 && w.kj == w.nT - 1) {
+          zero_tail_rows<D>(smem + L::kK + kb * L::kKVBytes, tail);
+          zero_tail_rows<D>(smem + L::kV + kb * L::kKVBytes, tail);
+        }
+        if (!(ok = issue_s(sK, g, i == w.nT - 1 ? tail : 0))) break;
+        for (int it = 0; it < steps; ++it, ++g) {
+          const bool more = it + 1 < steps;
+          const int inext = i + 1 < w.nT ? i + 1 : w.i0;
+          const int tail_next = inext == w.nT - 1 ? tail : 0;
+          const int s = g % L::kStages;
+          const uint32_t sQ = sbase + L::kQ + s * L::kTileBytes;
+          const uint32_t sdO = sbase + L::kdO + s * L::kTileBytes;
+          // dP^T = V dO^T (at d = 128 the dQ partial of the previous tile must
+          // have been read out of these columns)
+          if (!kOwnDQ && g > 0 && !(ok = mbar_wait_warp(bar(L::bdQFree), (uint32_t)(g - 1) & 1u, ctl, 362))) break;
+          if (!(ok = mbar_wait_warp(bar(L::bdOFull + s), (uint32_t)(g / L::kStages) & 1u, ctl, 366))) break;
+          if (tail != 0 && i == w.nT - 1) zero_tail_rows<D>(smem + L::kdO + s * L::kTileBytes, tail);
+          tc_fence_after();
+          const uint64_t kdV = desc_kmajor(sV, 0), kdO = desc_kmajor(sdO, 0);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_ss_w(tP, kdV + kmajor_step(ks), kdO + kmajor_step(ks), idSP, ks > 0 ? 1u : 0u);
+          mma_commit_w(bar(L::bdPFull));
+          // dV += P^T dO (at it == 0 over the previous item's dV and dK, which
+          // the compute warps have read out of TMEM before arriving on this P)
+          if (!(ok = mbar_wait_warp(bar(L::bPFull), (uint32_t)g & 1u, ctl, 363))) break;
+          tc_fence_after();
+          const uint64_t mdO = desc_mnmajor(sdO, 0);
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            // P of each warpgroup's queries packed in the first half of its own S columns
+            mma_ts_w(tdV, tS + packed_col(ks), mdO + mnmajor_step(ks), idV,
+                   (it > 0 || ks > 0) ? 1u : 0u);
+          // next S^T of this item: early, right behind dV (the tensor pipe
+          // runs in issue order, so dV has read P first), so that P of the
+          // next tile is recomputed while dK, dQ and the next dP run; else
+          // after dQ, which leaves the next Q load the longest window
+          if (kEarlyS && more && !(ok = issue_s(sK, g + 1, tail_next))) break;
+          // dK += dS^T Q ; dQ_i = dS K. dS^T is packed like P (packed_col) from
+          // tDS on; at d = 128 each warpgroup hands over its first 32 queries
+          // (K steps 0, 1 and 4, 5) before the rest (2, 3 and 6, 7), so half of
+          // dK runs while dS is finished
+          const uint64_t mQ = desc_mnmajor(sQ, 0);
+          // dQ_i = dS K: with dS^T handed over in halves, dQ goes right after
+          // dS is complete, in front of the second half of dK, so that its
+          // drain overlaps that half
+          auto issue_dq = [&]() {
+#pragma unroll
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              mma_ss_w(tQ, desc_mnmajor(sdS, ks), mK + mnmajor_step(ks), idQ, ks > 0 ? 1u : 0u);
+            mma_commit_w(bar(L::bdQFull));
+          };
+#pragma unroll
+          for (int half = kSplitDS ? 0 : 1; half < 2; ++half) {
+            if (!(ok = mbar_wait_warp(bar(half == 0 ? L::bdSHalf : L::bdSFull), (uint32_t)g & 1u, ctl, 365)))
+              break;
+            tc_fence_after();
+            if (kSplitDS && half == 1) issue_dq();
+#pragma unroll
+            for (int k4 = 0; k4 < (kSplitDS ? 4 : 8); ++k4) {
+              const int ks = kSplitDS ? 2 * half + (k4 & 1) + 4 * (k4 >> 1) : k4;
+              mma_ts_w(tdK, tDS + packed_col(ks), mQ + mnmajor_step(ks), idK,
+                           (it > 0 || ks > 0) ? 1u : 0u);
+            }
+          }
+          if (!ok) break;
+          mma_commit_w(bar(L::bQEmpty + s));   // the slot's Q has been read for the last time
+          if (!kSplitDS) {
+            // at d = 64 the previous dQ partial must have been read out of its columns
+            if (kOwnDQ && g > 0 && !(ok = mbar_wait_warp(bar(L::bdQFree), (uint32_t)(g - 1) & 1u, ctl, 362))) break;
+            tc_fence_after();
+            issue_dq();
+          }
+          mma_commit_w(bar(L::bdSEmpty));      // dK and dQ have read dS
+          if (!kEarlyS && more && !(ok = issue_s(sK, g + 1, tail_next))) break;
+          i = inext;
+        }
+        if (ok) mma_commit_w(bar(L::bFinal));   // dV and dK of the item are complete
+      }
+      mma_commit_w(bar(L::bDrain));
+      drain_wait(bar(L::bDrain), 0);
+    }
+  } else if (warp < kDrainWarp0) {
+    // ------------------------------------------------------------ P and dS (thread = key row)
+    // warpgroup cw handles query columns kC cw .. kC cw + kC - 1 of each tile
+    regs_inc<kComputeRegs>();
+    constexpr int kC = kCols;
+    const int cw = warp >> 2;
+    const int cb = kC * cw;
+    const int r = tid & 127;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const float sl2 = p.scale_log2;
+    bool ok = true;
+    int g = 0, nf = 0;
+    int pending = -1;   // K/V buffer whose epilogue store has not been waited for yet (thread r == 0)
+    // the store out of buffer `pending` has read its staging: the buffer goes
+    // back to the producer
+    auto release_kv = [&]() {
+      if (pending >= 0) {
+        if (r == 0) {
+          bulk_wait_group_read_all();
+          mbar_arrive(bar(L::bKVFree + pending));
+        }
+        pending = -1;
+      }
+    };
+    // The four warps of a group meet at a named barrier in each item's
+    // epilogue; before it, and wherever one of them may have stopped (a wait
+    // that ran out or saw the abort flag), they agree with group_all, so that
+    // all of them take the same branch and none waits for one that has left.
+    const uint32_t gbar = 1u + (uint32_t)cw;
+    constexpr uint32_t kGThreads = 128u;
+    for (int k = 0; ok; ++k) {
+      const Item w = take_item(k, ok);
+      ok = group_all(gbar, kGThreads, ok);
+      if (!ok || w.kj < 0) break;
+      const int krow = kTile * w.kj + r;
+      const int steps = p.G * (w.nT - w.i0);
+      for (int it = 0, i = w.i0; it < steps; ++it, ++g, i = i + 1 < w.nT ? i + 1 : w.i0) {
+        const bool partial = (p.causal && i == w.kj) || (w.kj + 1) * kTile > w.len;
+        const int s = g % L::kStages;
+        if (!(ok = mbar_wait_warp(bar(L::bQFull + s), (uint32_t)(g / L::kStages) & 1u, ctl, 370))) break;
+        if (!(ok = mbar_wait_warp(bar(L::bSFull), (uint32_t)g & 1u, ctl, 371))) break;
+        tc_fence_after();
+        const float* lse2 = reinterpret_cast<const float*>(smem + L::kRow + s * 1024) + cb;
+        const float* dlt = lse2 + kTile;
+        float x[kC];
+        {
+          uint32_t u0[32], u1[32];
+          tmem_ld32(tS + lane_off + (uint32_t)cb, u0);
+          tmem_ld32(tS + lane_off + (uint32_t)cb + 32u, u1);
+          tmem_ld_wait(u0);
+          tmem_ld_wait(u1);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            x[c] = __uint_as_float(u0[c]);
+            x[32 + c] = __uint_as_float(u1[c]);
+          }
+        }
+        // P^T row: p[c] = exp2(s * scale * log2e - LSE2[query c])
+#pragma unroll
+        for (int c4 = 0; c4 < kC / 4; ++c4) {
+          const float4 l = reinterpret_cast<const float4*>(lse2)[c4];   // one broadcast load per 4 queries
+          x[4 * c4] = ex2(fmaf(x[4 * c4], sl2, -l.x));
+          x[4 * c4 + 1] = ex2(fmaf(x[4 * c4 + 1], sl2, -l.y));
+          x[4 * c4 + 2] = ex2(fmaf(x[4 * c4 + 2], sl2, -l.z));
+          x[4 * c4 + 3] = ex2(fmaf(x[4 * c4 + 3], sl2, -l.w));
+        }
+        if (partial) {
+          // key row krow is masked for query q0 + c when it lies past the
+          // query (causal: c < krow - q0) or at or past the key length (every c)
+          const int lim = krow >= w.len ? kC : (p.causal ? krow - (kTile * i + cb) : 0);
+#pragma unroll
+          for (int c = 0; c < kC; ++c)
+            if (c < lim) x[c] = 0.f;
+        }
+        // the dV operand is P packed two queries per TMEM column into the first
+        // half of this warpgroup's own S columns (the other warpgroup may still
+        // be reading its half)
+        {
+          uint32_t pk[kC / 2];
+#pragma unroll
+          for (int c = 0; c < kC / 2; ++c) pk[c] = pack2<F16>(x[2 * c], x[2 * c + 1]);
+          tmem_st32(tS + lane_off + (uint32_t)cb, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(bar(L::bPFull));
+        if (it == 0) release_kv();   // the previous item's store has had this tile's time to read its staging
+
+        // dS^T row: ds[c] = p[c] * (dP[c] - D[query c]) -> 16-bit -> swizzled smem
+        if (!(ok = mbar_wait_warp(bar(L::bdPFull), (uint32_t)g & 1u, ctl, 372))) break;
+        if (g > 0 && !(ok = mbar_wait_warp(bar(L::bdSEmpty), (uint32_t)(g - 1) & 1u, ctl, 373))) break;
+        tc_fence_after();
+        // at d = 128 both 32-column halves of this warpgroup's dP^T are loaded
+        // before the first wait, so their TMEM latencies overlap (at d = 64 the
+        // 32 extra live registers would spill)
+        constexpr bool kBothHalves = (D == 128);
+        uint32_t ud[kC / 32][32];
+        if constexpr (kBothHalves) {
+#pragma unroll
+          for (int cc = 0; cc < kC / 32; ++cc) tmem_ld32(tP + lane_off + (uint32_t)cb + 32u * cc, ud[cc]);
+#pragma unroll
+          for (int cc = 0; cc < kC / 32; ++cc) tmem_ld_wait(ud[cc]);
+        }
+#pragma unroll
+        for (int cc = 0; cc < kC / 32; ++cc) {
+          if constexpr (!kBothHalves) {
+            tmem_ld32(tP + lane_off + (uint32_t)cb + 32u * cc, ud[cc]);
+            tmem_ld_wait(ud[cc]);
+          }
+          const uint32_t* u = ud[cc];
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const int c0 = 32 * cc + 2 * c;
+            const float g0 = __uint_as_float(u[2 * c]), g1 = __uint_as_float(u[2 * c + 1]);
+            const float2 dl = reinterpret_cast<const float2*>(dlt)[c0 >> 1];
+            const float d0 = x[c0] * (g0 - dl.x), d1 = x[c0 + 1] * (g1 - dl.y);
+            pk[c] = pack2<F16>(d0, d1);
+          }
+          // dS^T also goes to TMEM (the A operand of dK), packed (tDS): over
+          // this warpgroup's dP columns, which it has already read, or into the
+          // second half of its S columns, after its P
+          tmem_st16(tDS + lane_off + (uint32_t)cb + 16u * cc, pk);
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4) {
+            uint8_t* dst = smem + L::kdS + tile_chunk(r, (cb >> 3) + 4 * cc + k4);
+            *reinterpret_cast<uint4*>(dst) =
+                make_uint4(pk[4 * k4], pk[4 * k4 + 1], pk[4 * k4 + 2], pk[4 * k4 + 3]);
+          }
+          if (kSplitDS && cc == 0) {   // the first 32 queries' dS^T is in TMEM: dK may start on them
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive_warp(bar(L::bdSHalf));
+          }
+        }
+        tmem_st_wait();
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive_warp(bar(L::bdSFull));
+      }
+
+      // epilogue: the first warpgroup stores dV, the second scale * dK, staged
+      // in the item's V or K buffer once every MMA has read it: whole tiles by
+      // TMA, a sequence's last rows one by one
+      ok = group_all(gbar, kGThreads, ok);
+      if (!ok) break;
+      const int kb = k % L::kKV;
+      ok = mbar_wait_warp(bar(L::bKV + kb), (uint32_t)(k / L::kKV) & 1u, ctl, 374);
+      if (ok) ok = mbar_wait_warp(bar(L::bFinal), (uint32_t)nf & 1u, ctl, 375);
+      ok = group_all(gbar, kGThreads, ok);
+      if (!ok) break;
+      ++nf;
+      tc_fence_after();
+      const bool is_v = cw == 0;
+      const uint32_t tacc = (is_v ? tdV : tdK) + lane_off;
+      const float mul = is_v ? 1.f : p.scale;
+      const int stage_off = (is_v ? L::kV : L::kK) + kb * L::kKVBytes;
+      uint8_t* stage = smem + stage_off;
+#pragma unroll
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t u[32];
+        tmem_ld32(tacc + 32u * cc, u);
+        tmem_ld_wait(u);
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          pk[c] = pack2<F16>(__uint_as_float(u[2 * c]) * mul, __uint_as_float(u[2 * c + 1]) * mul);
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4)
+          *reinterpret_cast<uint4*>(stage + tile_chunk(r, 4 * cc + k4)) =
+              make_uint4(pk[4 * k4], pk[4 * k4 + 1], pk[4 * k4 + 2], pk[4 * k4 + 3]);
+      }
+      tc_fence_before();
+      fence_proxy_async_smem();
+      named_bar_sync(gbar, kGThreads);
+      const int rows = w.len - kTile * w.kj;
+      if (rows >= kTile) {
+        if (r == 0) {
+          for (int h = 0; h < L::kHalves; ++h)
+            tma_store_3d(is_v ? &tdv : &tdk, sbase + stage_off + h * 16384, 64 * h, w.hk, w.start + kTile * w.kj);
+          bulk_commit_group();
+        }
+      } else {
+        const int64_t tok = is_v ? p.dv_tok : p.dk_tok;
+        uint16_t* op = (is_v ? p.dv : p.dk) + (int64_t)(w.start + kTile * w.kj) * tok +
+                       w.hk * (is_v ? p.dv_head : p.dk_head);
+        const int chunks = p.d >> 3;
+        for (int i = r; i < rows * chunks; i += 128) {
+          const int rr = i / chunks, ch = i % chunks;
+          *reinterpret_cast<uint4*>(op + rr * tok + 8 * ch) = *reinterpret_cast<const uint4*>(stage + tile_chunk(rr, ch));
+        }
+        fence_proxy_async_smem();
+        named_bar_sync(gbar, kGThreads);   // every row is read before the buffer goes back to the producer
+      }
+      pending = kb;
+      // with one K/V buffer the next item's K and V wait for this store
+      if (L::kKV == 1) release_kv();
+    }
+    if (r == 0) bulk_wait_group_read_all();   // the stores have read the staging; the grid's end makes them visible
+  } else if (warp < kProducerWarp) {
+    // ------------------------------------------------------------ dQ drain (thread = query row)
+    // TMEM -> fp32 rows staged in this iteration's dO ring slot (dead once dQ
+    // has completed) in two rounds of 32-column boxes, 128-byte swizzled ->
+    // TMA reduce-add into the accumulator. The TMEM columns are released as
+    // soon as they are all in registers or staged; the slot goes back to the
+    // producer when its last round has been read.
+    //   d = 128: each warp stages and adds its own 32 query rows (boxes of 32
+    //            rows) and synchronises only within itself.
+    //   d = 64:  the four warps stage whole 128-row boxes that one thread adds,
+    //            meeting at named barriers; after each wait that one of them
+    //            may fail they agree with group_all, so that they always take
+    //            the same branch and none waits at a barrier another has left.
+    regs_dec<kDrainRegs>();
+    constexpr uint32_t kDrainBar = 1u + kGroups;   // named barrier of the drain warps (d = 64)
+    constexpr int kBoxesPerRound = L::kTileBytes / 16384;    // 1 (d = 64) or 2 (d = 128)
+    constexpr int kRounds = D / 32 / kBoxesPerRound;
+    const int r = tid - 32 * kDrainWarp0;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t sw = (uint32_t)((r >> 3) * 1024 + (r & 7) * 128);
+    const uint32_t wrow = L::kGroupDrain ? 0u : 4096u * (uint32_t)(warp & 3);   // this warp's rows in a box
+    bool ok = true;
+    int g = 0;
+    for (int k = 0; ok; ++k) {
+      const Item w = take_item(k, ok);
+      if constexpr (L::kGroupDrain) ok = group_all(kDrainBar, 128, ok);
+      if (!ok || w.kj < 0) break;
+      const int steps = p.G * (w.nT - w.i0);
+      for (int it = 0, i = w.i0, hq = w.hk * p.G; it < steps; ++it, ++g) {
+        const int s = g % L::kStages;
+        const uint32_t stage = (uint32_t)(L::kdO + s * L::kTileBytes);
+        ok = mbar_wait_warp(bar(L::bdQFull), (uint32_t)g & 1u, ctl, 380);
+        if constexpr (L::kGroupDrain) ok = group_all(kDrainBar, 128, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t u[kBoxesPerRound][32];
+#pragma unroll
+        for (int b = 0; b < kBoxesPerRound; ++b) tmem_ld32(tQ + lane_off + 32u * b, u[b]);
+#pragma unroll
+        for (int b = 0; b < kBoxesPerRound; ++b) tmem_ld_wait(u[b]);
+#pragma unroll
+        for (int round = 0; round < kRounds; ++round) {
+          if (round == kRounds - 1) {
+            tc_fence_before();
+            mbar_arrive_warp(bar(L::bdQFree));   // every dQ column is in registers or staged
+          }
+          if (round > 0) {              // the previous round has been read out of the slot
+            if constexpr (L::kGroupDrain) {
+              if (r == 0) bulk_wait_group_read_all();
+              named_bar_sync(kDrainBar, 128);
+            } else {
+              if (lane == 0) bulk_wait_group_read_all();
+              __syncwarp();
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < kBoxesPerRound; ++b)
+#pragma unroll
+            for (int k8 = 0; k8 < 8; ++k8) {    // 8 chunks of 4 fp32 per 32-column box
+              const uint32_t o = sw + (uint32_t)((k8 ^ (r & 7)) << 4);
+              *reinterpret_cast<uint4*>(smem + stage + 16384 * b + o) =
+                  make_uint4(u[b][4 * k8], u[b][4 * k8 + 1], u[b][4 * k8 + 2], u[b][4 * k8 + 3]);
+            }
+          fence_proxy_async_smem();
+          if constexpr (L::kGroupDrain)
+            named_bar_sync(kDrainBar, 128);
+          else
+            __syncwarp();
+          if (L::kGroupDrain ? r == 0 : lane == 0) {
+            const int row0 = kTile * (w.slot0 + i) + (L::kGroupDrain ? 0 : 32 * (warp & 3));
+#pragma unroll
+            for (int b = 0; b < kBoxesPerRound; ++b)
+              if (32 * (round * kBoxesPerRound + b) < p.d)   // boxes wholly past the head dimension hold zeros
+                tma_reduce_add_3d(&tdq, sbase + stage + 16384u * b + wrow, 32 * (round * kBoxesPerRound + b),
+                                  row0, hq);
+            bulk_commit_group();
+          }
+          if (round + 1 < kRounds) {    // the next columns into registers while the round is read
+#pragma unroll
+            for (int b = 0; b < kBoxesPerRound; ++b)
+              tmem_ld32(tQ + lane_off + 32u * ((round + 1) * kBoxesPerRound + b), u[b]);
+#pragma unroll
+            for (int b = 0; b < kBoxesPerRound; ++b) tmem_ld_wait(u[b]);
+          }
+        }
+        if (L::kGroupDrain ? r == 0 : lane == 0) {
+          bulk_wait_group_read_all();
+          mbar_arrive(bar(L::bdOFree + s));
+        }
+        if (++i == w.nT) {
+          i = w.i0;
+          ++hq;
+        }
+      }
+    }
+    if (L::kGroupDrain ? r == 0 : lane == 0) bulk_wait_group_all();     // reductions complete before exit
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Per padded tile and query head: D = rowsum(dO * O) and LSE * log2(e) of its
+// rows (0 and +inf past the sequence), and the dQ accumulator's tile zeroed.
+// LANES neighbouring threads take a row, 8 columns each.
+template <int LANES, bool F16>
+__global__ void __launch_bounds__(256) packed_bwd_pre_kernel(const PackedBwdParams p) {
+  grid_dep_launch();
+  const int tile = (int)(blockIdx.x / (unsigned)p.Hq), h = (int)(blockIdx.x % (unsigned)p.Hq);
+  if (tile >= p.plan->tiles) return;
+  const PackedItem it = p.tiles[tile];
+  const size_t row_off = ((size_t)h * p.cap_tiles + tile) * kTile;
+  const int part = (int)threadIdx.x % LANES;
+  const bool cols = 8 * part < p.d;
+  for (int r = (int)threadIdx.x / LANES; r < kTile; r += 256 / LANES) {
+    const int n = kTile * it.c + r;       // token of the sequence
+    float acc = 0.f;
+    if (n < it.len && cols) {
+      const int64_t t = (int64_t)it.start + n;
+      const uint4 a = *reinterpret_cast<const uint4*>(p.o + t * p.o_tok + h * p.o_head + 8 * part);
+      const uint4 g = *reinterpret_cast<const uint4*>(p.dout + t * p.do_tok + h * p.do_head + 8 * part);
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 af = unpack2<F16>(aw[k]);
+        const float2 gf = unpack2<F16>(gw[k]);
+        acc = fmaf(af.x, gf.x, acc);
+        acc = fmaf(af.y, gf.y, acc);
+      }
+    }
+#pragma unroll
+    for (int off = LANES / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, off);
+    if (cols) {
+      float4* z = reinterpret_cast<float4*>(p.dq_acc + (row_off + r) * p.d + 8 * part);
+      z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+      z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (part == 0) {
+      p.delta[row_off + r] = acc;
+      p.lse2[row_off + r] =
+          n < it.len ? p.lse[(size_t)h * p.total + it.start + n] * 1.4426950408889634f : INFINITY;
+    }
+  }
+}
+
+// dQ = 16-bit(scale * accumulator), one thread per 8 columns of a row.
+template <bool F16>
+__global__ void __launch_bounds__(256) packed_bwd_dq_kernel(const PackedBwdParams p) {
+  grid_dep_wait();   // every partial of the main kernel has been added
+  const int tile = (int)(blockIdx.x / (unsigned)p.Hq), h = (int)(blockIdx.x % (unsigned)p.Hq);
+  if (tile >= p.plan->tiles) return;
+  const PackedItem it = p.tiles[tile];
+  const size_t row_off = ((size_t)h * p.cap_tiles + tile) * kTile;
+  const int parts = p.d / 8;
+  const int rows = min(kTile, it.len - kTile * it.c);
+  for (int i = (int)threadIdx.x; i < rows * parts; i += 256) {
+    const int r = i / parts, part = i % parts;
+    const float4* src = reinterpret_cast<const float4*>(p.dq_acc + (row_off + r) * p.d + 8 * part);
+    const float4 a = src[0], c = src[1];
+    uint4 out;
+    out.x = pack2<F16>(a.x * p.scale, a.y * p.scale);
+    out.y = pack2<F16>(a.z * p.scale, a.w * p.scale);
+    out.z = pack2<F16>(c.x * p.scale, c.y * p.scale);
+    out.w = pack2<F16>(c.z * p.scale, c.w * p.scale);
+    const int64_t t = (int64_t)it.start + kTile * it.c + r;
+    *reinterpret_cast<uint4*>(p.dq + t * p.dq_tok + h * p.dq_head + 8 * part) = out;
+  }
+}
+
+template <int D, bool F16>
+cudaError_t launch_packed_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv,
+                                const CUtensorMap& tdq, const PackedBwdParams& p, cudaStream_t s) {
+  using L = PackedBwdLayout<D>;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static PerDeviceOnce smem_set;
+  e = once_per_device(smem_set, dev, [] {
+    return cudaFuncSetAttribute(fa_packed_bwd_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                L::kSmemBytes);
+  });
+  if (e != cudaSuccess) return e;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  PackedBwdParams q = p;
+  // Q and dO (16-bit) and the fp32 dQ accumulator of a key/value head's G query
+  // heads are re-read by all of its key tiles
+  q.group = l2_head_group(8.0 * p.total * p.d * p.G, p.Hk);
+  const dim3 tiles((unsigned)p.cap_tiles * (unsigned)p.Hq);
+  // 16 lanes cover d <= 128, 8 cover d <= 64
+  e = launch_pdl(false, packed_bwd_pre_kernel<D / 8, F16>, tiles, dim3(256), 0, s, q);
+  if (e != cudaSuccess) return e;
+  // persistent: at most one CTA per SM (the kernel holds all of TMEM)
+  const long long most = (long long)p.cap_tiles * p.Hk;
+  e = launch_pdl(true, fa_packed_bwd_kernel<D, F16>, dim3((unsigned)(most < sms ? most : sms)), dim3(kBwdThreads),
+                 L::kSmemBytes, s, tq, tk, tv, tdo, tdk, tdv, tdq, q);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(false, packed_bwd_dq_kernel<F16>, tiles, dim3(256), 0, s, q);
+}
+
+}  // namespace
+
+cudaError_t launch_packed_bwd(bool f16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv,
+                              const CUtensorMap& tdq, const PackedBwdParams& p, cudaStream_t s) {
+  if (p.d <= 64)
+    return f16 ? launch_packed_bwd_d<64, true>(tq, tk, tv, tdo, tdk, tdv, tdq, p, s)
+               : launch_packed_bwd_d<64, false>(tq, tk, tv, tdo, tdk, tdv, tdq, p, s);
+  return f16 ? launch_packed_bwd_d<128, true>(tq, tk, tv, tdo, tdk, tdv, tdq, p, s)
+             : launch_packed_bwd_d<128, false>(tq, tk, tv, tdo, tdk, tdv, tdq, p, s);
+}
+
+}  // namespace fa

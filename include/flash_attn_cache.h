@@ -42,8 +42,8 @@ typedef enum { FA_CACHE_16BIT = 0, FA_CACHE_E4M3 = 1 } fa_cache_type;
  * Writes the keys and values of T tokens into the cache.
  *   K, V  : in, 16-bit; row (t, h) starts at element t * token_stride +
  *           h * head_stride of its tensor and holds d elements. Strides are
- *           multiples of 8 elements (any sign or order; rows may be views of
- *           a fused projection).
+ *           positive multiples of 8 elements (rows may be views of a fused
+ *           projection).
  *   slots : in, int64 [T] (8-byte aligned): token t goes to place
  *           slots[t] mod page_size of page slots[t] / page_size. A slot that
  *           is negative or past the cache is skipped (padding tokens). Slots

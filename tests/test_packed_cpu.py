@@ -1,0 +1,111 @@
+"""Refusals of the packed calls, decided on the host before any launch."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def L():
+    from exact_io_aware_39_gb300 import build as b
+    import exact_io_aware_39_gb300._lib as lib
+    lib.load(b.build())
+    return lib
+
+
+P = ctypes.c_void_p(1 << 20)
+ODD = ctypes.c_void_p((1 << 20) + 8)
+
+
+def _strides(n, bad=None, value=None):
+    s = [1024, 128] * n
+    if bad is not None:
+        s[bad] = value
+    return (ctypes.c_int64 * (2 * n))(*s)
+
+
+def _fwd(L, Q=P, K=P, V=P, O=P, LSE=P, cu=P, B=2, total=300, Hq=8, Hk=2, d=128, st=None, scale=0.1, causal=1, opts=None,
+         ws=P, nbytes=None):
+    if nbytes is None:
+        nbytes = L.flash_attn_packed_workspace_size(2, 300, 8, 2, 128, 0)
+    return L.flash_attn_packed_fwd(Q, K, V, O, LSE, cu, B, total, Hq, Hk, d, st, scale, causal, opts, ws, nbytes, None)
+
+
+def _bwd(L, ptrs=None, LSE=P, cu=P, B=2, total=300, Hq=8, Hk=2, d=128, st=None, scale=0.1, causal=1, opts=None, ws=P,
+         nbytes=None):
+    q, k, v, o, do, dq, dk, dv = ptrs or [P] * 8
+    if nbytes is None:
+        nbytes = L.flash_attn_packed_workspace_size(2, 300, 8, 2, 128, 1)
+    return L.flash_attn_packed_bwd(q, k, v, o, do, LSE, dq, dk, dv, cu, B, total, Hq, Hk, d, st, scale, causal, opts, ws,
+                                   nbytes, None)
+
+
+SHAPES = [
+    (dict(B=-1), 1), (dict(total=-1), 1), (dict(Hk=0), 1), (dict(Hq=0), 1), (dict(Hq=9), 1), (dict(d=0), 2),
+    (dict(d=12), 2), (dict(d=136), 2), (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1),
+    (dict(scale=float("inf")), 1), (dict(causal=2), 1), (dict(total=1 << 30, Hq=64), 2), (dict(B=1 << 30), 2),
+    (dict(LSE=None), 1), (dict(cu=None), 1), (dict(cu=ctypes.c_void_p((1 << 20) + 2)), 1),
+    (dict(ws=None), 3), (dict(ws=ctypes.c_void_p((1 << 20) + 16)), 3), (dict(nbytes=100), 3),
+]
+
+
+@pytest.mark.parametrize("kw,want", SHAPES)
+def test_refusals(L, kw, want):
+    assert _fwd(L, **kw) == want
+    assert _bwd(L, **kw) == want
+
+
+def test_pointers_and_strides(L):
+    for name in "QKVO":
+        assert _fwd(L, **{name: None}) == 1 and _fwd(L, **{name: ODD}) == 1
+    for i in range(8):
+        for x in (None, ODD):
+            ptrs = [P] * 8
+            ptrs[i] = x
+            assert _bwd(L, ptrs) == 1
+    for i in range(8):
+        for v in (0, -128, 12, 1 << 36):
+            assert _fwd(L, st=_strides(4, i, v)) == 1
+    for i in range(16):
+        for v in (0, -128, 12, 1 << 36):
+            assert _bwd(L, st=_strides(8, i, v)) == 1
+
+
+def test_nothing_to_do(L):
+    for kw in (dict(B=0), dict(total=0)):
+        assert _fwd(L, Q=None, K=None, V=None, O=None, LSE=None, cu=None, ws=None, nbytes=0, **kw) == 0
+        assert _bwd(L, [None] * 8, LSE=None, cu=None, ws=None, nbytes=0, **kw) == 0
+
+
+def test_options(L):
+    for call in (_fwd, _bwd):
+        assert call(L, opts=L.fa_options(7)) == 2
+        assert call(L, opts=L.fa_options(p_drop=0.1)) == 2
+        assert call(L, opts=L.fa_options(tile_record=1 << 20)) == 2
+        assert call(L, opts=L.fa_options(test_stall=2)) == 1
+
+
+def test_workspace_size(L):
+    def al(x):
+        return (x + 255) // 256 * 256
+    B, total, Hq, d = 5, 1000, 8, 96
+    items, tiles = total // 256 + B, total // 128 + B
+    want = al(al(al(256) + 4 * B) + 16 * items)
+    assert L.flash_attn_packed_workspace_size(B, total, Hq, 2, d, 0) == want
+    want = al(al(al(256) + 4 * B) + 16 * tiles)
+    want = al(want + 16 * tiles)
+    rows = Hq * tiles * 128
+    want = al(want + rows * d * 4)
+    want = al(al(want + rows * 4) + rows * 4)
+    assert L.flash_attn_packed_workspace_size(B, total, Hq, 2, d, 1) == want
+    for bad in ((-1, 1, 1, 1, 64), (1, 1, 3, 2, 64), (1, 1, 1, 1, 256), (1, 1, 1, 1, 4)):
+        assert L.flash_attn_packed_workspace_size(*bad, 0) == 0
+
+
+def test_helpers_refuse_cpu_tensors(L):
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(ValueError):
+        L.attention_packed_fwd(q, q, q, cu, 0.1)
+    with pytest.raises(ValueError):
+        L.attention_packed_bwd(q, q, q, q, q, torch.zeros(2, 4), cu, 0.1)
