@@ -16,15 +16,15 @@ constexpr int kMaxUnits = kMaxN / kTile;   // most tiles of a sequence: 1024
 // The plan: which (sequence, tile) pairs there are, heaviest first, so that
 // the persistent kernels end together. cu_seqlens lives on the device, so the
 // list is made there, by one block. Sequences are sorted by their unit count
-// (a counting sort; a unit is a pair of query tiles in the forward pass, a key
-// tile in the backward). Causal: a unit with c units before it in the forward
+// (a counting sort; a unit is a query tile or a pair of them in the forward pass,
+// a key tile in the backward). Causal: a unit with c units before it in the forward
 // (or behind it in the backward) costs c + 1 tile pairs, so units are listed
 // by c, descending: those of rank c are held by the first sequences of the
 // sorted order, which gives every unit its place without a search. Not causal:
 // a unit costs its sequence's length, so the units follow the sorted order.
 __global__ void __launch_bounds__(kPlanThreads)
-packed_plan_kernel(const int32_t* __restrict__ cu, int B, int total, int causal, int backward, PackedPlan* plan,
-                   int* sorted, PackedItem* items, int cap_items, PackedItem* tiles, int cap_tiles,
+packed_plan_kernel(const int32_t* __restrict__ cu, int B, int total, int rows, int causal, int backward,
+                   PackedPlan* plan, int* sorted, PackedItem* items, int cap_items, PackedItem* tiles, int cap_tiles,
                    unsigned int* err) {
   __shared__ int hist[kMaxUnits + 1];      // sequences with that many units; then the next free rank
   __shared__ int off[kMaxUnits + 1];       // first list place of the units with c units before them
@@ -32,14 +32,7 @@ packed_plan_kernel(const int32_t* __restrict__ cu, int B, int total, int causal,
   __shared__ int carry[2];
   grid_dep_launch();   // the main kernel may set itself up (it waits for this one's end)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rows = backward ? kTile : 2 * kTile;
-  // Sequence b, or an empty one where its bounds are not valid.
-  auto seq = [&](int b, int& start, bool& bad) -> int {
-    const int s = cu[b], e = cu[b + 1];
-    bad = s < 0 || e < s || e > total || e - s > kMaxN;
-    start = s;
-    return bad ? 0 : e - s;
-  };
+  auto seq = [&](int b, int& start, bool& bad) -> int { return seq_bounds(cu, b, total, start, bad); };
   auto units = [&](int len) -> int { return (len + rows - 1) / rows; };
 
   for (int i = tid; i <= kMaxUnits; i += kPlanThreads) hist[i] = 0;
@@ -49,11 +42,7 @@ packed_plan_kernel(const int32_t* __restrict__ cu, int B, int total, int causal,
     int start;
     bool bad;
     const int len = seq(b, start, bad);
-    if (bad && atomicCAS(err, 0u, (unsigned)kErrInternal) == 0u) {
-      err[1] = 300u;
-      err[2] = 0u;
-      err[3] = (unsigned)b;
-    }
+    if (bad) report_bounds(err, b);
     if (len > 0) atomicAdd(&hist[units(len)], 1);
   }
   __syncthreads();
@@ -179,11 +168,11 @@ fa_status packed_options(const fa_options* options, PackedOptions* o) {
 
 }  // namespace
 
-cudaError_t launch_packed_plan(const int32_t* cu, int B, int total, int causal, bool backward, PackedPlan* plan,
-                               int* sorted, PackedItem* items, int cap_items, PackedItem* tiles, int cap_tiles,
-                               unsigned int* err, cudaStream_t s) {
-  packed_plan_kernel<<<1, kPlanThreads, 0, s>>>(cu, B, total, causal, backward ? 1 : 0, plan, sorted, items, cap_items,
-                                                tiles, cap_tiles, err);
+cudaError_t launch_packed_plan(const int32_t* cu, int B, int total, int rows, int causal, bool backward,
+                               PackedPlan* plan, int* sorted, PackedItem* items, int cap_items, PackedItem* tiles,
+                               int cap_tiles, unsigned int* err, cudaStream_t s) {
+  packed_plan_kernel<<<1, kPlanThreads, 0, s>>>(cu, B, total, rows, causal, backward ? 1 : 0, plan, sorted, items,
+                                                cap_items, tiles, cap_tiles, err);
   return cudaGetLastError();
 }
 
@@ -221,9 +210,9 @@ fa_status flash_attn_packed_fwd(const void* Q, const void* K, const void* V, voi
   unsigned int* err = nullptr;
   const int e = internal_device_error_word(&err);
   if (e != FA_OK) return static_cast<fa_status>(e);
-  CUtensorMap tq, tk, tv, to;
+  CUtensorMap tq, tk, tv;
   if (packed_map(&tq, Q, o.f16, total, Hq, d, sq, kTile) || packed_map(&tk, K, o.f16, total, Hk, d, sk, kTile) ||
-      packed_map(&tv, V, o.f16, total, Hk, d, sv, kTile) || packed_map(&to, O, o.f16, total, Hq, d, so, 32))
+      packed_map(&tv, V, o.f16, total, Hk, d, sv, kTile))
     return FA_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -243,11 +232,17 @@ fa_status flash_attn_packed_fwd(const void* Q, const void* K, const void* V, voi
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_us = o.wait_us;
   p.stall = o.stall;
+  p.cu = cu_seqlens;
+  p.B = B;
   p.cap_items = w.cap_items;
-  if (launch_packed_plan(cu_seqlens, B, total, causal, false, p.plan, reinterpret_cast<int*>(ws + w.sorted_off),
-                         reinterpret_cast<PackedItem*>(ws + w.item_off), w.cap_items, nullptr, 0, err, s) != cudaSuccess)
+  p.pair_heads = packed_pair_heads(Hq, Hk);
+  p.heads = p.pair_heads ? Hq / 2 : Hq;
+  if (B > kDirect &&
+      launch_packed_plan(cu_seqlens, B, total, p.pair_heads ? kTile : 2 * kTile, causal, false, p.plan,
+                         reinterpret_cast<int*>(ws + w.sorted_off), reinterpret_cast<PackedItem*>(ws + w.item_off),
+                         w.cap_items, nullptr, 0, err, s) != cudaSuccess)
     return FA_ERR_CUDA;
-  return launch_packed_fwd(o.f16, tq, tk, tv, to, p, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_packed_fwd(o.f16, tq, tk, tv, p, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 fa_status flash_attn_packed_bwd(const void* Q, const void* K, const void* V, const void* O, const void* dO,
@@ -326,7 +321,7 @@ fa_status flash_attn_packed_bwd(const void* Q, const void* K, const void* V, con
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_us = o.wait_us;
   p.stall = o.stall;
-  if (launch_packed_plan(cu_seqlens, B, total, causal, true, p.plan, reinterpret_cast<int*>(ws + w.sorted_off),
+  if (launch_packed_plan(cu_seqlens, B, total, kTile, causal, true, p.plan, reinterpret_cast<int*>(ws + w.sorted_off),
                          reinterpret_cast<PackedItem*>(ws + w.item_off), w.cap_items,
                          reinterpret_cast<PackedItem*>(ws + w.tile_off), w.cap_tiles, err, s) != cudaSuccess)
     return FA_ERR_CUDA;

@@ -30,14 +30,17 @@ struct PackedWorkspace {
   bool ok;   // the counts fit 32-bit work indices
 };
 
+// The forward's work item is one query tile of two neighbouring query heads of
+// a key/value head where there are such pairs, else two query tiles of a head.
+inline bool packed_pair_heads(int Hq, int Hk) { return (Hq / Hk) % 2 == 0; }
+
 inline PackedWorkspace packed_workspace_layout(int B, int total, int Hq, int Hk, int d, bool backward) {
   auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
   PackedWorkspace w;
   const long long tiles = (long long)total / kTile + B;
-  const long long items = backward ? tiles : (long long)total / (2 * kTile) + B;
   w.ok = tiles * Hq < 0x7FFFFFFFll / kTile;
   w.cap_tiles = w.ok ? (int)tiles : 0;
-  w.cap_items = w.ok ? (int)items : 0;
+  w.cap_items = !w.ok ? 0 : (int)(backward || packed_pair_heads(Hq, Hk) ? tiles : (long long)total / (2 * kTile) + B);
   w.plan_off = 0;
   w.sorted_off = al(sizeof(PackedPlan));
   w.item_off = al(w.sorted_off + (size_t)B * sizeof(int));
@@ -50,8 +53,14 @@ inline PackedWorkspace packed_workspace_layout(int B, int total, int Hq, int Hk,
   return w;
 }
 
+// Up to kDirect sequences: no plan kernel runs, every warp that needs the work
+// list makes it from the bounds, a lane per sequence (DirectList).
+constexpr int kDirect = 32;
+
 struct PackedFwdParams {
-  const PackedItem* items;
+  const int32_t* cu;          // [B + 1]
+  int B;
+  const PackedItem* items;    // B > kDirect
   PackedPlan* plan;
   uint16_t* o;
   int64_t o_tok, o_head;
@@ -61,7 +70,9 @@ struct PackedFwdParams {
   float scale_log2;
   uint32_t wait_us, stall;
   int cap_items;
-  int group;                  // query heads per group of the work order
+  int pair_heads;             // an item's two query tiles: one tile of two heads, or two tiles of one head
+  int heads;                  // Hq, or with pair_heads Hq / 2
+  int group;                  // of those, per group of the work order
 };
 
 struct PackedBwdParams {
@@ -81,6 +92,83 @@ struct PackedBwdParams {
   float scale, scale_log2;
   uint32_t wait_us, stall;
   int group;                  // key/value heads per group of the work order
+};
+
+// Rows [start, start + len) of sequence b; an empty one (bad set) where its
+// bounds decrease, leave [0, total] or span more than kMaxN tokens.
+__device__ __forceinline__ int seq_bounds(const int32_t* cu, int b, int total, int& start, bool& bad) {
+  const int s = cu[b], e = cu[b + 1];
+  bad = s < 0 || e < s || e > total || e - s > kMaxN;
+  start = s;
+  return bad ? 0 : e - s;
+}
+
+__device__ __forceinline__ void report_bounds(unsigned int* err, int b) {
+  if (atomicCAS(err, 0u, (unsigned)kErrInternal) == 0u) {
+    err[1] = 300u;
+    err[2] = blockIdx.x;
+    err[3] = (unsigned)b;
+  }
+}
+
+// The work list of up to 32 sequences, held by a warp: lane b has sequence b
+// and its n units of `rows` rows. Units are listed as the plan kernel lists
+// them: causal, by the number c of units before them, descending, and for each
+// c the sequences that have one; not causal, sequence by sequence, the longest
+// first. All lanes call the members together.
+struct DirectList {
+  int start, len, n, items;
+  int c, off;        // causal: items with more than c units before them, and how many
+  int rank, first;   // not causal: place of this lane's sequence by length, and of its first unit
+  __device__ __forceinline__ void init(const int32_t* cu, int B, int total, int rows, bool causal, unsigned int* err) {
+    const int lane = threadIdx.x & 31;
+    start = len = 0;
+    if (lane < B) {
+      bool bad;
+      len = seq_bounds(cu, lane, total, start, bad);
+      if (bad) report_bounds(err, lane);
+    }
+    n = (len + rows - 1) / rows;
+    items = __reduce_add_sync(0xFFFFFFFFu, n);
+    c = __reduce_max_sync(0xFFFFFFFFu, n) - 1;
+    off = 0;
+    rank = first = 0;
+    if (!causal)
+      for (int l = 0; l < 32; ++l) {
+        const int o = __shfl_sync(0xFFFFFFFFu, n, l);
+        if (o > n || (o == n && l < lane)) {
+          ++rank;
+          first += o;
+        }
+      }
+  }
+  __device__ __forceinline__ PackedItem at(int idx, bool causal) {
+    int b;
+    PackedItem it;
+    if (causal) {
+      if (idx < off) {     // the order starts again for another group of heads
+        c = __reduce_max_sync(0xFFFFFFFFu, n) - 1;
+        off = 0;
+      }
+      uint32_t has = __ballot_sync(0xFFFFFFFFu, n > c);
+      while (c > 0 && idx >= off + __popc(has)) {
+        off += __popc(has);
+        --c;
+        has = __ballot_sync(0xFFFFFFFFu, n > c);
+      }
+      for (int r = idx - off; r > 0; --r) has &= has - 1;
+      b = __ffs(has) - 1;
+      it.c = c;
+    } else {
+      const uint32_t mine = __ballot_sync(0xFFFFFFFFu, n > 0 && idx >= first && idx < first + n);
+      b = __ffs(mine) - 1;
+      it.c = idx - __shfl_sync(0xFFFFFFFFu, first, b);
+    }
+    it.start = __shfl_sync(0xFFFFFFFFu, start, b);
+    it.len = __shfl_sync(0xFFFFFFFFu, len, b);
+    it.slot0 = 0;
+    return it;
+  }
 };
 
 // Zeroes rows r0 .. 127 of a 128-row tile (64-column atoms of 16 KB, D / 64 of
@@ -105,12 +193,13 @@ __device__ __forceinline__ uint32_t tile_chunk(int r, int c) {
   return (uint32_t)((c >> 3) * 16384 + (r >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-cudaError_t launch_packed_plan(const int32_t* cu, int B, int total, int causal, bool backward, PackedPlan* plan,
-                               int* sorted, PackedItem* items, int cap_items, PackedItem* tiles, int cap_tiles,
+// rows: rows of a unit (a work item's share of a sequence).
+cudaError_t launch_packed_plan(const int32_t* cu, int B, int total, int rows, int causal, bool backward,
+                               PackedPlan* plan, int* sorted, PackedItem* items, int cap_items, PackedItem* tiles, int cap_tiles,
                                unsigned int* err, cudaStream_t s);
 
 cudaError_t launch_packed_fwd(bool f16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                              const CUtensorMap& to, const PackedFwdParams& p, cudaStream_t s);
+                              const PackedFwdParams& p, cudaStream_t s);
 
 cudaError_t launch_packed_bwd(bool f16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv,

@@ -1,27 +1,37 @@
 // Forward pass over packed sequences with grouped heads, for sm_103a
 // (tcgen05 tensor cores, TMEM accumulators, TMA staging).
 //
-// The computation of one pair of 128-row query tiles is that of fa_fwd.cu: a
-// persistent CTA per SM with two softmax warpgroups (one per query tile), a TMA
-// producer each for Q / K and for V, and one warp that runs the MMA schedule;
-// S_t = Q_t K_j^T and O_t in TMEM, P_t packed to 16 bits into TMEM for the
-// second product, the reference maximum moved only past 2^8. What is different:
-//   * a work item is a pair of query tiles of one (sequence, query head). The
-//     items of a call come from a list that the plan kernel makes on the device
-//     (the lengths are there), heaviest first, and are taken from a counter;
-//   * the tensors are [token, head, d] with any strides: a tile is a 3-D TMA
-//     box of one head and 128 tokens. It may run into the next sequence: keys
-//     past the end are masked in S, their rows of V are zeroed in shared memory
-//     before the product (a zero weight times a NaN that lies there would be
-//     NaN), and rows of O past the end are not stored (full groups of 32 rows
-//     go out by TMA, the last one row by row);
-//   * query head h reads key/value head h / G; neighbouring query heads run at
-//     the same time, so a group's K and V come from L2 after their first read;
-//   * the live key tiles of an item are a range, so no list is built.
+// The arithmetic of a 128-row query tile is that of fa_fwd.cu: S = Q K_j^T in
+// TMEM, one softmax warpgroup per query tile (thread = row) that writes P packed
+// to 16 bits into TMEM, O += P V_j in TMEM, the reference maximum moved only
+// past 2^8. What is different:
+//   * a work item is two query tiles that share their K and V loads: the same
+//     tile of two neighbouring query heads of one key/value head where the group
+//     size is even (both then end at the same key tile, and a sequence of one
+//     tile still fills both softmax groups), else two neighbouring tiles of a
+//     head;
+//   * the items of a call are listed on the device (the lengths are there),
+//     heaviest first: for up to 32 sequences by every producer warp for itself
+//     (DirectList), for more by a plan kernel. A CTA takes its own item, then,
+//     as it gets ready for one, the next of a counter that the plan kernel zeroed
+//     or, without one, a CTA of the grid that has not started, cancelled through
+//     cluster launch control (dealing the sorted list out in a fixed snake was
+//     12 % slower on one sequence of 16384 tokens, 32 heads, d = 128);
+//   * no role waits for another at the end of an item. Items pass through a
+//     ring, every barrier phase runs on across them, and a query tile's
+//     Q buffer goes back to the producer behind its last S, so the next item's
+//     loads and first S products run while this one's O is read out (measured
+//     against a barrier of all roles around each item: see kItemRing);
+//   * O goes from registers to global memory, four lanes writing 64 bytes of a
+//     row (a transpose across the lane quad), which needs no staging buffer and
+//     ends at a sequence's end without a second path;
+//   * tensors are [token, head, d] with any strides: a tile is a 3-D TMA box of
+//     one head and 128 tokens. It may run into the next sequence: keys past the
+//     end are masked in S, and their rows of V are zeroed in shared memory before
+//     the product (a zero weight times a NaN that lies there would be NaN).
 //
-// Bound: 4 d operations per visible pair on the tensor cores. At d = 128 each
-// S tile costs a warpgroup 128 exponentials per row; the two query tiles
-// alternate so that the products of one hide the softmax of the other.
+// Bound: 4 d operations per visible pair on the tensor cores, and one
+// exponential per pair, which at d = 64 takes as long (16 per clock and SM).
 #include "fa_packed.cuh"
 
 namespace fa {
@@ -42,59 +52,62 @@ struct PackedFwdLayout {
   // that read K come first
   static constexpr int kStagesK = (D == 64) ? 5 : 3;
   static constexpr int kStagesV = (D == 64) ? 4 : 2;
-  // Q buffers (each the two Q tiles of an item, and then the item's O
-  // staging): at d = 64 two, so that the next item's Q and first K tiles are
-  // loaded while this item runs; at d = 128 the shared memory holds one.
-  // At d = 64, S_0, S_1 (128 columns each) and O_0, O_1 (64 each) leave 128
-  // TMEM columns, which give each Q tile's P columns of their own: S_t is then
-  // free as soon as its softmax group has read it into registers, and the
-  // next S_t is computed while that group works on this one. At d = 128 the
-  // four regions fill TMEM and P is packed over S in place.
+  // Q buffers of each query tile: at d = 64 two, at d = 128 the shared memory
+  // holds one. At d = 64, S_0, S_1 (128 columns each) and O_0, O_1 (64 each)
+  // leave 128 TMEM columns, which give each Q tile's P columns of their own:
+  // S_t is then free as soon as its softmax group has read it into registers,
+  // and the next S_t is computed while that group works on this one. At d = 128
+  // the four regions fill TMEM and P is packed over S in place.
   static constexpr bool kOwnP = (D == 64);
   static constexpr int kQBuf = (D == 64) ? 2 : 1;
-  static constexpr int kQ = 0;
-  static constexpr int kK = kQ + kQBuf * 2 * kTileBytes;
+  static constexpr int kItemRing = 4;
+  static constexpr int kQ = 0;                              // [2][kQBuf] tiles
+  static constexpr int kK = kQ + 2 * kQBuf * kTileBytes;
   static constexpr int kV = kK + kStagesK * kTileBytes;
   static constexpr int kBar = kV + kStagesV * kTileBytes;   // 8-byte mbarriers
   // barrier slots
-  static constexpr int bQFull = 0;                    // [kQBuf]
-  static constexpr int bKFull = bQFull + kQBuf;
+  static constexpr int bQFull = 0;                    // [2][kQBuf]
+  static constexpr int bQEmpty = bQFull + 2 * kQBuf;  // [2][kQBuf]: the tile's last S is complete
+  static constexpr int bKFull = bQEmpty + 2 * kQBuf;
   static constexpr int bKEmpty = bKFull + kStagesK;
   static constexpr int bVFull = bKEmpty + kStagesK;
   static constexpr int bVEmpty = bVFull + kStagesV;
   static constexpr int bSFull = bVEmpty + kStagesV;   // [2]
-  static constexpr int bPFull = bSFull + 2;           // [2]
+  static constexpr int bPFull = bSFull + 2;           // [2], 4 arrivals (warps)
   static constexpr int bOFinal = bPFull + 2;          // [2]
-  static constexpr int bSFree = bOFinal + 2;          // [2] S_t read into registers (own P columns only)
+  static constexpr int bSFree = bOFinal + 2;          // [2], 4: S_t read into registers (own P columns only)
   static constexpr int bPVDone = bSFree + 2;          // [2] O_t += P_t V complete (own P columns only)
-  static constexpr int bPHalf = bPVDone + 2;          // [2] P_t of the first 64 keys is in TMEM (P over S only)
-  static constexpr int bDrain = bPHalf + 2;
+  static constexpr int bPHalf = bPVDone + 2;          // [2], 4: P_t of the first 64 keys is in TMEM (P over S only)
+  static constexpr int bItemFull = bPHalf + 2;        // [kItemRing]
+  static constexpr int bItemEmpty = bItemFull + kItemRing;   // [kItemRing], 10: V producer, MMA and softmax warps
+  static constexpr int bClc = bItemEmpty + kItemRing;        // the next item's cancellation answer has arrived
+  static constexpr int bDrain = bClc + 1;
   static constexpr int kNumBars = bDrain + 1;
-  // 32-bit words: tmem slot, abort flag, -, wait limit, -, -, next item, -;
-  // then per Q buffer b at 8 + 4 b the item: first row, length, pair, query head
-  static constexpr int kMisc = kBar + 8 * kNumBars;
-  static constexpr int kSmemBytes = kMisc + 4 * (8 + 4 * kQBuf);
+  static constexpr int kMisc = (kBar + 8 * kNumBars + 15) & ~15;   // tmem slot, abort flag, -, wait limit
+  static constexpr int kRing = kMisc + 16;            // [kItemRing] x {first row, length, unit or -1, head}
+  static constexpr int kClc = kRing + 16 * kItemRing;   // 16-byte answer of a launch cancellation
+  static constexpr int kSmemBytes = kClc + 16;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
-// What the roles need of an item: its query tiles qi0 and qi0 + 1 (the second
-// one may be missing), the key tiles 0 .. n - 1 live for either, the last one
-// live for each, and per (key tile, query tile) whether it is live and masked.
+// An item as the roles see it: its two query tiles, and the key tiles 0 .. n - 1
+// live for either.
 struct Pair {
-  int start, len, qi0, h;
-  int n;
-  bool two, causal;
-  __device__ __forceinline__ Pair(const volatile uint32_t* m, int causal_)
-      : start((int)m[0]), len((int)m[1]), qi0(2 * (int)m[2]), h((int)m[3]), causal(causal_ != 0) {
-    const int nT = (len + kTile - 1) / kTile;
-    two = qi0 + 1 < nT;
-    n = causal ? min(nT, qi0 + 2) : nT;
+  int start, len, c, head;      // c < 0: no item
+  int nT, n;
+  bool pair_heads, causal;
+  __device__ __forceinline__ void finish(const PackedFwdParams& p) {
+    pair_heads = p.pair_heads != 0;
+    causal = p.causal != 0;
+    nT = (len + kTile - 1) / kTile;
+    n = causal ? last(has(1) ? 1 : 0) + 1 : nT;
   }
-  __device__ __forceinline__ int last(int t) const { return t == 0 ? (causal ? qi0 : n - 1) : (two ? n - 1 : -1); }
-  __device__ __forceinline__ bool live(int e, int t) const { return t == 0 ? (!causal || e <= qi0) : two; }
-  __device__ __forceinline__ bool partial(int e, int t) const {
-    return (causal && e == qi0 + t) || (e + 1) * kTile > len;
-  }
+  __device__ __forceinline__ bool has(int t) const { return t == 0 || pair_heads || 2 * c + 1 < nT; }
+  __device__ __forceinline__ int qi(int t) const { return pair_heads ? c : 2 * c + t; }
+  __device__ __forceinline__ int hq(int t) const { return pair_heads ? 2 * head + t : head; }
+  __device__ __forceinline__ int last(int t) const { return causal ? qi(t) : nT - 1; }   // last key tile live for t
+  __device__ __forceinline__ bool live(int e, int t) const { return has(t) && e <= last(t); }
+  __device__ __forceinline__ bool partial(int e, int q) const { return (causal && e == q) || (e + 1) * kTile > len; }
   // valid rows of the last key tile when it is not full, else 0
   __device__ __forceinline__ int tail() const { return len & (kTile - 1); }
 };
@@ -102,8 +115,7 @@ struct Pair {
 template <int D, bool F16>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-              const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
-              const PackedFwdParams p) {
+                     const __grid_constant__ CUtensorMap tv, const PackedFwdParams p) {
   using L = PackedFwdLayout<D>;
   // With P over S (d = 128), P of a tile's first 64 keys goes to the tensor
   // core before the rest is formed, and its half of P V runs meanwhile; the
@@ -120,6 +132,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * (uint32_t)i; };
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile uint32_t* abort_flag = misc + 1;
+  volatile int* ring = reinterpret_cast<volatile int*>(smem + L::kRing);
   Ctl ctl{p.err, abort_flag};
 
   if ((sbase & 1023u) != 0u) {   // uniform across the CTA: nothing has started yet
@@ -132,9 +145,13 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   }
 
   if (tid == 0) {
-    for (int i = 0; i < L::kNumBars; ++i)
-      mbar_init(bar(i), (i == L::bPFull || i == L::bPFull + 1 || i == L::bSFree || i == L::bSFree + 1 ||
-                         i == L::bPHalf || i == L::bPHalf + 1) ? 4u : 1u);   // 4 = warps
+    auto arrivals = [](int i) -> uint32_t {
+      if ((i >= L::bPFull && i < L::bPFull + 2) || (i >= L::bSFree && i < L::bSFree + 2) ||
+          (i >= L::bPHalf && i < L::bPHalf + 2))
+        return 4u;
+      return i >= L::bItemEmpty && i < L::bItemEmpty + L::kItemRing ? 10u : 1u;
+    };
+    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), arrivals(i));
     abort_flag[0] = 0u;
     abort_flag[2] = p.wait_us;   // the wait limit, read by the slow path of every wait
     fence_mbar_init();
@@ -152,330 +169,328 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   grid_dep_wait();
   grid_dep_launch();
 
-  // Persistent over items: the first is this CTA's own, each further one the
-  // next of a counter that the plan kernel zeroed. The work order walks groups
-  // of p.group query heads whose K and V fit in L2 together, within a group
-  // the items heaviest first, and for each item the heads of the group. Every
-  // ring and barrier phase runs on across items: eK / eV count the K / V ring
-  // entries of the items before this one, and each role keeps its own counts.
-  const int n_items = p.plan->items;
-  const int total = n_items * p.Hq;
-  int eK = 0, eV = 0;
-  int nk = 0, nv = 0;                     // K / V loads issued (producer threads)
-  uint32_t ns[2] = {0u, 0u}, npv[2] = {0u, 0u};   // S and PV groups issued per Q tile (MMA warp)
-  uint32_t nS = 0u, nOF = 0u;             // S tiles and final O read by this softmax group
-  int item = (int)blockIdx.x;
-  uint32_t kq = 0u;                       // items started: the phase of the Q barrier
-  // The roles meet at a named barrier before each item (its description is in
-  // shared memory) and after it (its O is stored, its products read out).
-  auto item_sync = [&]() {
-    tc_fence_before();
-    named_bar_sync(1, kFwdThreads);
-    tc_fence_after();
+  // Item k of this CTA from the ring; w.c < 0 when none is left or a wait
+  // failed (then ok is false too). Executed by whole warps.
+  auto take_item = [&](int k, Pair& w) -> bool {
+    const int rs = k % L::kItemRing;
+    w.c = -1;
+    if (!mbar_wait_warp(bar(L::bItemFull + rs), (uint32_t)(k / L::kItemRing) & 1u, ctl, 319)) return false;
+    w.start = ring[4 * rs];
+    w.len = ring[4 * rs + 1];
+    w.c = ring[4 * rs + 2];
+    w.head = ring[4 * rs + 3];
+    w.finish(p);
+    mbar_arrive_warp(bar(L::bItemEmpty + rs));
+    return true;
   };
-  // after an item: the next one, or none (then every role leaves its loop)
-  auto next_item = [&]() -> int {
-    const int next = (int)misc[6];
-    return abort_flag[0] != 0u ? -1 : next;
-  };
-  if (item >= total) {
-    // nothing for this CTA (uniform)
-  } else if (warp == 8) {
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ items, Q and K producer
     regs_dec<kOtherRegs>();
-    uint32_t nq[2] = {0u, 0u};   // Q loads issued into each buffer (lane 0)
-    // K of key tile e of item w into ring entry n, once the MMAs of the entry
-    // that used the slot before (of this item or an earlier one) have read it
-    auto load_k = [&](const Pair& w, int e, int n) -> bool {
-      const int sk = n % L::kStagesK;
-      if (n >= L::kStagesK && !mbar_wait(bar(L::bKEmpty + sk), (uint32_t)(n / L::kStagesK - 1) & 1u, ctl, 311))
-        return false;
-      mbar_arrive_expect_tx(bar(L::bKFull + sk), L::kTileBytes);
-      for (int h = 0; h < L::kHalves; ++h)
-        tma_load_3d(sbase + L::kK + sk * L::kTileBytes + h * 16384, &tk, bar(L::bKFull + sk), 64 * h, w.h / p.G,
-                    w.start + kTile * e);
-      ++nk;
-      return true;
-    };
-    // Sets item `it` up in buffer qb (lane 0): its description is written down,
-    // its Q tiles are loaded, and the first ring's worth of its K tiles (ring
-    // entries base, base + 1, ...). Returns the K loads issued.
-    auto setup = [&](int it, int qb, int base) -> int {
-      int kpre = 0;
-      if (lane == 0) {
-        int h = 0;
-        const PackedItem pi = p.items[split_grouped(it, p.group, n_items, p.Hq, &h)];
-        uint32_t* m = misc + 8 + 4 * qb;
-        m[0] = (uint32_t)pi.start;
-        m[1] = (uint32_t)pi.len;
-        m[2] = (uint32_t)pi.c;
-        m[3] = (uint32_t)h;
-        const Pair w(m, p.causal);
-        mbar_arrive_expect_tx(bar(L::bQFull + qb), (w.two ? 2u : 1u) * L::kTileBytes);
-        for (int t = 0; t < (w.two ? 2 : 1); ++t)
-          for (int a = 0; a < L::kHalves; ++a)
-            tma_load_3d(sbase + L::kQ + (2 * qb + t) * L::kTileBytes + a * 16384, &tq, bar(L::bQFull + qb), 64 * a, h,
-                        w.start + kTile * (w.qi0 + t));
-        ++nq[qb];
-        for (; kpre < w.n && kpre < L::kStagesK; ++kpre) {
-          if (p.stall != 0u && kpre >= 1) break;   // test of the timeout path: K of entry 1 never comes
-          if (!load_k(w, kpre, base + kpre)) break;
-        }
-      }
-      return kpre;
-    };
     if (lane == 0) {
       tma_prefetch_map(&tq);
       tma_prefetch_map(&tk);
     }
-    int kpre = setup(item, 0, 0);   // K loads of the current item issued during its set-up (lane 0)
-    for (;; ++kq) {
-      const int qb = (int)(kq % L::kQBuf);
-      item_sync();
-      // ------------------------------------------------------------ Q and K producer
-      const Pair w(misc + 8 + 4 * qb, p.causal);
-      int next = -1;
-      if (lane == 0) {
-        bool ok = true;
-        for (int e = kpre; e < w.n && ok; ++e) {
-          if (p.stall != 0u && e >= 1) ok = false;   // test of the timeout path: K of entry 1 never comes
-          else ok = load_k(w, e, eK + e);
-        }
-        // every K load of the item is issued: take the next item
-        if (ok) {
-          next = (int)gridDim.x + (int)atomicAdd(&p.plan->sched, 1u);
-          if (next >= total) next = -1;
-        }
-        misc[6] = (uint32_t)next;
-      }
-      // with two buffers the next item is set up while this one runs (the
-      // other buffer's item has been stored: every role has passed the barrier
-      // after it)
-      next = __shfl_sync(0xFFFFFFFFu, next, 0);
-      if (L::kQBuf == 2 && next >= 0) kpre = setup(next, qb ^ 1, eK + w.n);
-      item_sync();
-      item = next_item();
-      if (item < 0) break;
-      eK += w.n;
-      if (L::kQBuf == 1) kpre = setup(item, 0, eK);
+    // The work order walks groups of p.group heads whose K and V fit in L2
+    // together, within a group the list heaviest first, and for each unit the
+    // heads of the group.
+    const bool direct = p.B <= kDirect;
+    DirectList dl;
+    int n_items = 0;
+    if (direct) {
+      dl.init(p.cu, p.B, p.total, p.pair_heads ? kTile : 2 * kTile, p.causal != 0, p.err);
+      n_items = dl.items;
+    } else {
+      n_items = p.plan->items;
     }
-    // every load issued has completed before the CTA exits; loads were issued
-    // in ring order, so the last load into slot
-    // s was number s + S * floor((n - 1 - s) / S)
+    const int total = n_items * p.heads;
+    int nk = 0;                  // K loads issued
+    int nq[2] = {0, 0};          // Q loads issued per query tile
+    bool clc_out = false;        // a cancellation answer is outstanding
+    uint32_t clc = 0u;           // answers received
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const int rs = k % L::kItemRing;
+      if (k >= L::kItemRing &&
+          !(ok = mbar_wait_warp(bar(L::bItemEmpty + rs), (uint32_t)(k / L::kItemRing - 1) & 1u, ctl, 313)))
+        break;
+      int item = (int)blockIdx.x;
+      if (k > 0 && !direct) {
+        item = (int)gridDim.x + __shfl_sync(0xFFFFFFFFu, lane == 0 ? (int)atomicAdd(&p.plan->sched, 1u) : 0, 0);
+      } else if (k > 0) {
+        // (the grid is sized for the most items these bounds can have: CTAs past
+        // the list are cancelled too, until none is left)
+        do {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(L::bClc), 16u);
+            clc_try_cancel(sbase + L::kClc, bar(L::bClc));
+          }
+          __syncwarp();
+          clc_out = true;
+          if (!(ok = mbar_wait_warp(bar(L::bClc), clc & 1u, ctl, 309))) break;
+          clc_out = false;
+          ++clc;
+          item = clc_first_ctaid_x(sbase + L::kClc);
+        } while (item >= total);
+        if (!ok) break;
+        if (item < 0) item = total;
+      }
+      Pair w;
+      w.c = -1;
+      if (item < total) {
+        int head = 0;
+        const int idx = split_grouped(item, p.group, n_items, p.heads, &head);
+        const PackedItem pi = direct ? dl.at(idx, p.causal != 0) : p.items[idx];
+        w.start = pi.start;
+        w.len = pi.len;
+        w.c = pi.c;
+        w.head = head;
+        w.finish(p);
+      }
+      if (lane == 0) {
+        ring[4 * rs] = w.start;
+        ring[4 * rs + 1] = w.len;
+        ring[4 * rs + 2] = w.c;
+        ring[4 * rs + 3] = w.head;
+        mbar_arrive(bar(L::bItemFull + rs));   // (release: the ring entry is visible to the waiters)
+      }
+      if (w.c < 0) break;
+      if (lane == 0) {
+        const int hk = w.hq(0) / p.G;
+        for (int e = 0; e < w.n && ok; ++e) {
+          if (p.stall != 0u && e >= 1) { ok = false; break; }   // test of the timeout path: K of entry 1 never comes
+          // K of key tile e, once the MMAs of the entry that used the slot
+          // before (of this item or an earlier one) have read it
+          const int sk = nk % L::kStagesK;
+          if (nk >= L::kStagesK &&
+              !(ok = mbar_wait(bar(L::bKEmpty + sk), (uint32_t)(nk / L::kStagesK - 1) & 1u, ctl, 311)))
+            break;
+          mbar_arrive_expect_tx(bar(L::bKFull + sk), L::kTileBytes);
+          for (int a = 0; a < L::kHalves; ++a)
+            tma_load_3d(sbase + L::kK + sk * L::kTileBytes + a * 16384, &tk, bar(L::bKFull + sk), 64 * a, hk,
+                        w.start + kTile * e);
+          ++nk;
+          // the item's Q tiles behind its first K, which seldom waits; a tile's
+          // buffer is free once the last S of the item before has read it
+          for (int t = 0; e == 0 && t < 2 && ok; ++t) {
+            if (!w.has(t)) continue;
+            const int qb = nq[t] % L::kQBuf, slot = t * L::kQBuf + qb;
+            if (nq[t] >= L::kQBuf &&
+                !(ok = mbar_wait(bar(L::bQEmpty + slot), (uint32_t)(nq[t] / L::kQBuf - 1) & 1u, ctl, 310)))
+              break;
+            mbar_arrive_expect_tx(bar(L::bQFull + slot), L::kTileBytes);
+            for (int a = 0; a < L::kHalves; ++a)
+              tma_load_3d(sbase + L::kQ + slot * L::kTileBytes + a * 16384, &tq, bar(L::bQFull + slot), 64 * a, w.hq(t),
+                          w.start + kTile * w.qi(t));
+            ++nq[t];
+          }
+        }
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+    }
+    // every load and cancellation request issued has completed before the CTA
+    // exits; loads were issued in ring order, so the last load into slot s was
+    // number s + S * floor((n - 1 - s) / S)
     if (lane == 0) {
-      for (int b = 0; b < L::kQBuf; ++b)
-        if (nq[b] > 0u) drain_wait(bar(L::bQFull + b), (nq[b] - 1u) & 1u);
+      if (clc_out) drain_wait(bar(L::bClc), clc & 1u);
+      for (int t = 0; t < 2; ++t)
+        for (int b = 0; b < L::kQBuf && b < nq[t]; ++b)
+          drain_wait(bar(L::bQFull + t * L::kQBuf + b), (uint32_t)((nq[t] - 1 - b) / L::kQBuf) & 1u);
       for (int s = 0; s < L::kStagesK && s < nk; ++s)
         drain_wait(bar(L::bKFull + s), (uint32_t)((nk - 1 - s) / L::kStagesK) & 1u);
     }
   } else if (warp == 10) {
+    // ------------------------------------------------------------ V producer
+    // (its own warp, so that the K ring can run ahead of the V ring)
     regs_dec<kOtherRegs>();
-    for (;; ++kq) {
-      const int qb = (int)(kq % L::kQBuf);
-      item_sync();
-      const Pair w(misc + 8 + 4 * qb, p.causal);
-      // ------------------------------------------------------------ V producer
-      // (its own thread, so that the K ring can run ahead of the V ring)
+    if (lane == 0) tma_prefetch_map(&tv);
+    int nv = 0;
+    Pair w;
+    bool ok = true;
+    for (int k = 0; ok && take_item(k, w) && w.c >= 0; ++k) {
       if (lane == 0) {
-        if (kq == 0u) tma_prefetch_map(&tv);
+        const int hk = w.hq(0) / p.G;
         for (int e = 0; e < w.n; ++e) {
-          const int n = eV + e;
-          const int sv = n % L::kStagesV;
-          if (n >= L::kStagesV && !mbar_wait(bar(L::bVEmpty + sv), (uint32_t)(n / L::kStagesV - 1) & 1u, ctl, 312))
+          const int sv = nv % L::kStagesV;
+          if (nv >= L::kStagesV &&
+              !(ok = mbar_wait(bar(L::bVEmpty + sv), (uint32_t)(nv / L::kStagesV - 1) & 1u, ctl, 312)))
             break;
           mbar_arrive_expect_tx(bar(L::bVFull + sv), L::kTileBytes);
-          for (int h = 0; h < L::kHalves; ++h)
-            tma_load_3d(sbase + L::kV + sv * L::kTileBytes + h * 16384, &tv, bar(L::bVFull + sv),
-                        64 * h, w.h / p.G, w.start + kTile * e);
+          for (int a = 0; a < L::kHalves; ++a)
+            tma_load_3d(sbase + L::kV + sv * L::kTileBytes + a * 16384, &tv, bar(L::bVFull + sv), 64 * a, hk,
+                        w.start + kTile * e);
           ++nv;
         }
       }
-      item_sync();
-      item = next_item();
-      if (item < 0) break;
-      eV += w.n;
+      ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
     }
     if (lane == 0)
       for (int s = 0; s < L::kStagesV && s < nv; ++s)
         drain_wait(bar(L::bVFull + s), (uint32_t)((nv - 1 - s) / L::kStagesV) & 1u);
   } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp runs the schedule; one elected lane issues each MMA and
+    // commit. At entry e, for each Q tile t, first the pending O_t += P_t V of
+    // t's previous entry (waiting for P_t), then S_t = Q_t K_e^T. For dense rows
+    // this is
+    //   PV0(e-1), S0(e), PV1(e-1), S1(e), PV0(e), ...
+    // so that while one softmax group works the tensor core runs the other
+    // tile's products; with P columns of their own both S of an entry come
+    // before both PV, so S_t(e+1) is computed while group t still works on
+    // S_t(e). The last PVs of an item stay pending into the next one, unless
+    // its first loads are not there yet.
     regs_dec<kOtherRegs>();
-    for (;; ++kq) {
-      const int qb = (int)(kq % L::kQBuf);
-      item_sync();
-      const Pair w(misc + 8 + 4 * qb, p.causal);
-      const int len = w.n;
-      // ------------------------------------------------------------ MMA issuer
-      // Fixed schedule over the live key tiles: at entry e, for each Q tile t, first
-      // the pending O_t += P_t V of t's previous live entry (waiting for P_t),
-      // then S_t = Q_t K_e^T if t is live at e. For dense rows this is
-      //   PV0(e-1), S0(e), PV1(e-1), S1(e), PV0(e), ...
-      // so that while one softmax group works the tensor core runs the other
-      // tile's products. A pending PV is issued at the very next entry, so each
-      // V slot is released one entry after its load and the K slot of entry e
-      // right after its S products.
-      {   // the whole warp runs the schedule; one elected lane issues each MMA and commit
-        constexpr uint32_t idS = idesc_16<F16>(128, 128, false, false);
-        constexpr uint32_t idO = idesc_16<F16>(128, D, false, true);
-        const uint32_t tS[2] = {tmem + 0u, tmem + 128u};
-        const uint32_t tO[2] = {tmem + 256u, tmem + 256u + (uint32_t)D};
-        // P_t: over S_t, or in columns of its own (after O_1)
-        const uint32_t tP[2] = {L::kOwnP ? tmem + 256u + 2u * D : tS[0], L::kOwnP ? tmem + 320u + 2u * D : tS[1]};
-        const uint64_t dQ[2] = {desc_kmajor(sbase + L::kQ + 2 * qb * L::kTileBytes, 0),
-                                desc_kmajor(sbase + L::kQ + (2 * qb + 1) * L::kTileBytes, 0)};
-        const uint64_t dK0 = desc_kmajor(sbase + L::kK, 0);
-        const uint64_t dV0 = desc_mnmajor(sbase + L::kV, 0);
-        constexpr uint64_t kSlotStep = (uint64_t)(L::kTileBytes >> 4);
-        int prev[2] = {-1, -1};       // entry of the pending PV of each Q tile
-        // the last entry live for each Q tile: its PV completes O_t, which the
-        // softmax group may then read out while the other tile's products run
-        const int lastE[2] = {w.last(0), w.last(1)};
-        uint32_t npv_item[2] = {0u, 0u};   // PV groups of this item per Q tile
-        // the rows of V behind the sequence's end are zeroed once, before the
-        // first product that reads the last key tile
-        int tail_entry = w.tail() != 0 ? (w.len + kTile - 1) / kTile - 1 : -1;
-        bool ok = mbar_wait_warp(bar(L::bQFull + qb), (kq / L::kQBuf) & 1u, ctl, 314);
-        tc_fence_after();
-
-        // O_t += P_t V_{entry pe}
-        auto issue_pv = [&](int t, int pe) -> bool {
-          const int nvp = eV + pe;
-          const int sv = nvp % L::kStagesV;
-          if (!mbar_wait_warp(bar((kHalfP ? L::bPHalf : L::bPFull) + t), npv[t] & 1u, ctl, 315)) return false;
-          if (!mbar_wait_warp(bar(L::bVFull + sv), (uint32_t)(nvp / L::kStagesV) & 1u, ctl, 316)) return false;
-          if (pe == tail_entry) {
-            zero_tail_rows<D>(smem + L::kV + sv * L::kTileBytes, w.tail());
-            tail_entry = -1;
-          }
-          tc_fence_after();
-          const uint64_t dV = dV0 + (uint64_t)sv * kSlotStep;
-          const uint32_t acc0 = npv_item[t] > 0 ? 1u : 0u;
+    constexpr uint32_t idS = idesc_16<F16>(128, 128, false, false);
+    constexpr uint32_t idO = idesc_16<F16>(128, D, false, true);
+    const uint32_t tS[2] = {tmem + 0u, tmem + 128u};
+    const uint32_t tO[2] = {tmem + 256u, tmem + 256u + (uint32_t)D};
+    // P_t: over S_t, or in columns of its own (after O_1)
+    const uint32_t tP[2] = {L::kOwnP ? tmem + 256u + 2u * D : tS[0], L::kOwnP ? tmem + 320u + 2u * D : tS[1]};
+    const uint64_t dQ0 = desc_kmajor(sbase + L::kQ, 0);
+    const uint64_t dK0 = desc_kmajor(sbase + L::kK, 0);
+    const uint64_t dV0 = desc_mnmajor(sbase + L::kV, 0);
+    constexpr uint64_t kSlotStep = (uint64_t)(L::kTileBytes >> 4);
+    int nk = 0, nv = 0;              // K and V ring entries of the entries before this one
+    int nq[2] = {0, 0};              // items with query tile t so far
+    uint32_t ns[2] = {0u, 0u}, npv[2] = {0u, 0u};   // S and PV groups issued per Q tile
+    // the pending PV of each Q tile: its V ring entry or -1, whether it is the
+    // item's first (overwrites O_t) and last, and the valid rows of a V tile
+    // that the sequence ends in (else 0)
+    int pend[2] = {-1, -1};
+    bool pfirst[2] = {false, false}, plast[2] = {false, false};
+    int ptail[2] = {0, 0};
+    int zeroed = -1;                 // last V ring entry whose rows past the sequence were zeroed
+    auto issue_pv = [&](int t) -> bool {
+      const int v = pend[t], sv = v % L::kStagesV;
+      pend[t] = -1;
+      if (!mbar_wait_warp(bar((kHalfP ? L::bPHalf : L::bPFull) + t), npv[t] & 1u, ctl, 315)) return false;
+      if (!mbar_wait_warp(bar(L::bVFull + sv), (uint32_t)(v / L::kStagesV) & 1u, ctl, 316)) return false;
+      if (ptail[t] != 0 && zeroed != v) {
+        zero_tail_rows<D>(smem + L::kV + sv * L::kTileBytes, ptail[t]);
+        zeroed = v;
+      }
+      tc_fence_after();
+      const uint64_t dV = dV0 + (uint64_t)sv * kSlotStep;
 #pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks) {
-            if (kHalfP && ks == kTile / 32) {   // the second half of P
-              if (!mbar_wait_warp(bar(L::bPFull + t), npv[t] & 1u, ctl, 315)) return false;
-              tc_fence_after();
-            }
-            mma_ts_w(tO[t], tP[t] + (uint32_t)ks * 8u, dV + mnmajor_step(ks), idO, ks > 0 ? 1u : acc0);
-          }
-          if constexpr (L::kOwnP) mma_commit_w(bar(L::bPVDone + t));   // P_t may be rewritten, O_t rescaled
-          if (pe == lastE[t]) mma_commit_w(bar(L::bOFinal + t));       // O_t is complete
-          ++npv[t];
-          ++npv_item[t];
+      for (int ks = 0; ks < kTile / 16; ++ks) {
+        if (kHalfP && ks == kTile / 32) {   // the second half of P
+          if (!mbar_wait_warp(bar(L::bPFull + t), npv[t] & 1u, ctl, 315)) return false;
+          tc_fence_after();
+        }
+        mma_ts_w(tO[t], tP[t] + (uint32_t)ks * 8u, dV + mnmajor_step(ks), idO, ks > 0 || !pfirst[t] ? 1u : 0u);
+      }
+      if constexpr (L::kOwnP) mma_commit_w(bar(L::bPVDone + t));   // P_t may be rewritten, O_t rescaled
+      if (plast[t]) mma_commit_w(bar(L::bOFinal + t));             // O_t is complete
+      ++npv[t];
+      return true;
+    };
+    bool open = false;               // V ring entry nv - 1 has not gone back to the producer
+    auto release_v = [&]() {
+      if (open) mma_commit_w(bar(L::bVEmpty + (nv - 1) % L::kStagesV));
+      open = false;
+    };
+    auto flush = [&]() -> bool {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (pend[t] >= 0 && !issue_pv(t)) return false;
+      release_v();
+      return true;
+    };
+    bool ok = true;
+    Pair w;
+    for (int k = 0; ok; ++k) {
+      if (!(ok = take_item(k, w))) break;
+      if (w.c < 0) {
+        ok = flush();
+        break;
+      }
+      const int tail = w.tail();
+      // Q_t of this item: its buffer and phase
+      auto q_slot = [&](int t) -> int { return t * L::kQBuf + nq[t] % L::kQBuf; };
+      auto q_phase = [&](int t) -> uint32_t { return (uint32_t)(nq[t] / L::kQBuf) & 1u; };
+      if (pend[0] >= 0 || pend[1] >= 0) {
+        const bool there = mbar_test(bar(L::bQFull + q_slot(0)), q_phase(0)) &&
+                           mbar_test(bar(L::bKFull + nk % L::kStagesK), (uint32_t)(nk / L::kStagesK) & 1u);
+        if (!__all_sync(0xFFFFFFFFu, there) && !(ok = flush())) break;
+      }
+      for (int e = 0; e < w.n && ok; ++e) {
+        const int sk = nk % L::kStagesK;
+        bool k_ready = false;
+        auto issue_s = [&](int t) -> bool {
+          if (L::kOwnP && ns[t] > 0 && !mbar_wait_warp(bar(L::bSFree + t), (ns[t] - 1u) & 1u, ctl, 318)) return false;
+          if (e == 0 && !mbar_wait_warp(bar(L::bQFull + q_slot(t)), q_phase(t), ctl, 314)) return false;
+          if (!k_ready && !mbar_wait_warp(bar(L::bKFull + sk), (uint32_t)(nk / L::kStagesK) & 1u, ctl, 317)) return false;
+          k_ready = true;
+          tc_fence_after();
+          const uint64_t dQ = dQ0 + (uint64_t)q_slot(t) * kSlotStep, dK = dK0 + (uint64_t)sk * kSlotStep;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_ss_w(tS[t], dQ + kmajor_step(ks), dK + kmajor_step(ks), idS, ks > 0 ? 1u : 0u);
+          mma_commit_w(bar(L::bSFull + t));
+          if (e == w.last(t)) mma_commit_w(bar(L::bQEmpty + q_slot(t)));   // Q_t is no longer needed
+          ++ns[t];
           return true;
         };
-
+        // the entry's PV, once issue_s has put its S on the way
+        auto set_pending = [&](int t) {
+          pend[t] = nv;
+          pfirst[t] = e == 0;
+          plast[t] = e == w.last(t);
+          ptail[t] = e == w.nT - 1 ? tail : 0;
+        };
         if constexpr (L::kOwnP) {
-          // Own P columns: at entry e, first S_t(e) for each live tile, each as
-          // soon as group t has read its previous S_t into registers, then the
-          // PVs of entry e - 1. For dense rows:
-          //   S0(e), S1(e), PV0(e-1), PV1(e-1), S0(e+1), ...
-          // so S_t(e+1) is computed while group t still works on S_t(e).
-          for (int e = 0; e < len && ok; ++e) {
-            const int sk = (eK + e) % L::kStagesK;
-            bool k_ready = false;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (!ok || !w.live(e, t)) continue;
-              if (ns[t] > 0 && !(ok = mbar_wait_warp(bar(L::bSFree + t), (ns[t] - 1u) & 1u, ctl, 318))) break;
-              if (!k_ready) {
-                ok = mbar_wait_warp(bar(L::bKFull + sk), (uint32_t)((eK + e) / L::kStagesK) & 1u, ctl, 317);
-                if (!ok) break;
-                tc_fence_after();
-                k_ready = true;
-              }
-              const uint64_t dK = dK0 + (uint64_t)sk * kSlotStep;
+          for (int t = 0; t < 2; ++t)
+            if (ok && w.live(e, t)) ok = issue_s(t);
+          if (!ok) break;
+          mma_commit_w(bar(L::bKEmpty + sk));   // K_e is no longer needed
+          if (!(ok = flush())) break;
 #pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks)
-                mma_ss_w(tS[t], dQ[t] + kmajor_step(ks), dK + kmajor_step(ks), idS, ks > 0 ? 1u : 0u);
-              mma_commit_w(bar(L::bSFull + t));
-              ++ns[t];
-            }
-            if (!ok) break;
-            mma_commit_w(bar(L::bKEmpty + sk));   // K_e is no longer needed
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (ok && prev[t] >= 0) ok = issue_pv(t, prev[t]);
-              prev[t] = w.live(e, t) ? e : -1;
-            }
-            if (!ok) break;
-            if (e > 0) mma_commit_w(bar(L::bVEmpty + (eV + e - 1) % L::kStagesV));   // both PVs of entry e-1 issued
-          }
+          for (int t = 0; t < 2; ++t)
+            if (w.live(e, t)) set_pending(t);
         } else {
-          for (int e = 0; e < len && ok; ++e) {
-            const int sk = (eK + e) % L::kStagesK;
-            bool k_ready = false;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (!ok) break;
-              if (prev[t] >= 0) {
-                ok = issue_pv(t, prev[t]);
-                prev[t] = -1;
-                if (!ok) break;
-              }
-              if (w.live(e, t)) {
-                if (!k_ready) {
-                  ok = mbar_wait_warp(bar(L::bKFull + sk), (uint32_t)((eK + e) / L::kStagesK) & 1u, ctl, 317);
-                  if (!ok) break;
-                  tc_fence_after();
-                  k_ready = true;
-                }
-                const uint64_t dK = dK0 + (uint64_t)sk * kSlotStep;
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                  mma_ss_w(tS[t], dQ[t] + kmajor_step(ks), dK + kmajor_step(ks), idS, ks > 0 ? 1u : 0u);
-                mma_commit_w(bar(L::bSFull + t));
-                prev[t] = e;
-              }
-            }
-            if (!ok) break;
-            mma_commit_w(bar(L::bKEmpty + sk));                       // K_e is no longer needed
-            if (e > 0) mma_commit_w(bar(L::bVEmpty + (eV + e - 1) % L::kStagesV));   // both PVs of entry e-1 issued
-          }
-        }
-        if (ok) {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (ok && prev[t] >= 0) ok = issue_pv(t, prev[t]);   // (commits O_t's completion)
+            if (ok && pend[t] >= 0) ok = issue_pv(t);
+            if (ok && w.live(e, t) && (ok = issue_s(t))) set_pending(t);
           }
-          // the last entry's V slot goes back to the producer
-          if (ok && len > 0) mma_commit_w(bar(L::bVEmpty + (eV + len - 1) % L::kStagesV));
+          if (!ok) break;
+          mma_commit_w(bar(L::bKEmpty + sk));   // K_e is no longer needed
+          release_v();                          // both PVs of the entry before are issued
         }
+        open = true;
+        ++nk;
+        ++nv;
       }
-      item_sync();
-      item = next_item();
-      if (item < 0) break;
-      eK += len;
-      eV += len;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (w.has(t)) ++nq[t];
     }
     // every MMA issued has completed before TMEM is freed
     mma_commit_w(bar(L::bDrain));
     drain_wait(bar(L::bDrain), 0);
   } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax groups
     regs_inc<kSoftmaxRegs>();
-    for (;; ++kq) {
-      item_sync();
-      const int qb = (int)(kq % L::kQBuf);
-      const Pair w(misc + 8 + 4 * qb, p.causal);
-      const int len = w.n, qi0 = w.qi0;
-      // ------------------------------------------------------------ softmax groups
-      const int t = warp >> 2;                 // Q tile of this warpgroup
-      const int r = tid & 127;                 // row within the tile = TMEM lane
-      const int qi = qi0 + t;
-      const int row = kTile * qi + r;          // query index within the sequence
-      const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t tS = tmem + (uint32_t)(t * 128) + lane_off;
-      const uint32_t tO = tmem + 256u + (uint32_t)(t * D) + lane_off;
-      const uint32_t tP = L::kOwnP ? tmem + 256u + 2u * D + 64u * (uint32_t)t + lane_off : tS;
-      const float sl2 = p.scale_log2;
-
+    const int t = warp >> 2;                 // Q tile of this warpgroup
+    const int r = tid & 127;                 // row within the tile = TMEM lane
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + (uint32_t)(t * 128) + lane_off;
+    const uint32_t tO = tmem + 256u + (uint32_t)(t * D) + lane_off;
+    const uint32_t tP = L::kOwnP ? tmem + 256u + 2u * D + 64u * (uint32_t)t + lane_off : tS;
+    const float sl2 = p.scale_log2;
+    uint32_t nS = 0u, nO = 0u;               // S tiles and final O read by this group
+    bool ok = true;
+    Pair w;
+    for (int k = 0; ok && take_item(k, w) && w.c >= 0; ++k) {
+      if (!w.has(t)) continue;
+      const int qi = w.qi(t), last = w.last(t);
+      const int row = kTile * qi + r;        // query index within the sequence
       float m_ref = -INFINITY;
       float l = 0.f;
-      uint32_t n = 0;   // S tiles of this item (nS: of all items)
-      const bool has = t == 0 || w.two;        // this query tile exists
-      bool ok = has;
-      for (int e = 0; e < len && ok; ++e) {
-        if (!w.live(e, t)) continue;
-        if (!mbar_wait_warp(bar(L::bSFull + t), nS & 1u, ctl, 320 + t)) { ok = false; break; }
+      for (int e = 0; e <= last; ++e) {
+        const uint32_t n = (uint32_t)e;      // S tiles of this item before this one
+        if (!(ok = mbar_wait_warp(bar(L::bSFull + t), nS & 1u, ctl, 320 + t))) break;
         tc_fence_after();
         float x[128];
         {
@@ -500,7 +515,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           tc_fence_before();
           mbar_arrive_warp(bar(L::bSFree + t));
         }
-        if (w.partial(e, t)) {
+        if (w.partial(e, qi)) {
           // a key is masked when it lies past the row (causal) or past the
           // sequence: key >= min(row + 1, length), i.e. column i >= lim (never
           // all of a row's columns; rows past the sequence are not stored)
@@ -600,85 +615,46 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         l += s_row;
         tc_fence_before();
         mbar_arrive_warp(bar(L::bPFull + t));
-        ++n;
         ++nS;
       }
-
-      if (has) {
-        // all MMAs that read Q_t have completed (or never ran); make sure the
-        // Q load itself has landed before its buffer is reused for staging O
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (ok) ok = mbar_wait_warp(bar(L::bQFull + qb), (kq / L::kQBuf) & 1u, ctl, 322 + t);
-        if (ok && n > 0) ok = mbar_wait_warp(bar(L::bOFinal + t), nOF & 1u, ctl, 324 + t);
-        if (n > 0) ++nOF;
-        if (!ok) drain_wait(bar(L::bQFull + qb), (kq / L::kQBuf) & 1u);   // after an abort: the Q load (always issued) lands before its buffer is rewritten
-        tc_fence_after();
-        uint8_t* stage = smem + L::kQ + (2 * qb + t) * L::kTileBytes;
-        const float inv_l = n > 0 ? 1.f / l : 0.f;
-        const bool have_o = ok && n > 0;
+      // O / l and the LSE, once the last PV has completed. A lane holds 32
+      // columns of its row at a time, as four 16-byte chunks; transposed across
+      // its quad it holds one chunk of four rows, and a quad writes 64 bytes of
+      // each.
+      if (ok) ok = mbar_wait_warp(bar(L::bOFinal + t), nO & 1u, ctl, 324 + t);
+      if (!ok) break;
+      ++nO;
+      tc_fence_after();
+      const float inv_l = 1.f / l;
+      const int s4 = lane & 3;
+      const int row0 = kTile * qi + 32 * (warp & 3) + (lane & ~3);   // the quad's first row
+      uint16_t* op = p.o + (int64_t)(w.start + row0) * p.o_tok + w.hq(t) * p.o_head + 8 * s4;
 #pragma unroll
-        for (int cc = 0; cc < D / 32; ++cc) {
-          uint32_t u[32];
-          if (have_o) {
-            tmem_ld32(tO + 32u * cc, u);
-            tmem_ld_wait(u);
-          } else {
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t u[32];
+        tmem_ld32(tO + 32u * cc, u);
+        tmem_ld_wait(u);
+        uint32_t x[4][4];   // [word of a chunk][chunk of this row, then row of the quad]
 #pragma unroll
-            for (int i = 0; i < 32; ++i) u[i] = 0u;
-          }
-          uint32_t pk[16];
+        for (int wd = 0; wd < 4; ++wd) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            pk[i] = pack2<F16>(__uint_as_float(u[2 * i]) * inv_l, __uint_as_float(u[2 * i + 1]) * inv_l);
-          // 32 columns = 4 chunks of 16 bytes, 128B-swizzled rows
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int col = 32 * cc + 8 * k;           // first column of the chunk
-            const int h = col >> 6;                    // 64-column half
-            const int chunk = (col & 63) >> 3;         // chunk within the 128-byte row
-            uint8_t* dst = stage + h * 16384 + (r >> 3) * 1024 + (r & 7) * 128 + ((chunk ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4*>(dst) = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
-          }
+          for (int j = 0; j < 4; ++j)
+            x[wd][j] = pack2<F16>(__uint_as_float(u[8 * j + 2 * wd]) * inv_l, __uint_as_float(u[8 * j + 2 * wd + 1]) * inv_l);
+          quad_transpose(x[wd], (uint32_t)s4);
         }
-        if (row < w.len)
-          p.lse[(size_t)w.h * p.total + w.start + row] = (m_ref + log2f(l)) * 0.69314718055994531f;
-        // each warp stores its own 32 rows, so that no warp ever waits for
-        // another at a group-wide barrier: all 32 by TMA, or, where the sequence
-        // ends among them, the rows up to its end
-        fence_proxy_async_smem();
-        __syncwarp();
-        const int row0 = kTile * qi + 32 * (warp & 3);
-        const int rows = min(32, w.len - row0);
-        if (rows == 32) {
-          if (lane == 0) {
-            for (int h = 0; h < L::kHalves; ++h)
-              tma_store_3d(&to, smem_u32(stage) + h * 16384 + 4096 * (warp & 3), 64 * h, w.h, w.start + row0);
-            bulk_commit_group();
-            bulk_wait_group_read_all();   // the store has read the staging; the grid's end makes it visible
-          }
-        } else if (rows > 0) {
-          uint16_t* op = p.o + (int64_t)(w.start + row0) * p.o_tok + w.h * p.o_head;
-          const int chunks = p.d >> 3;
-          for (int i = lane; i < rows * chunks; i += 32) {
-            const int rr = i / chunks, ch = i % chunks;
-            *reinterpret_cast<uint4*>(op + rr * p.o_tok + 8 * ch) =
-                *reinterpret_cast<const uint4*>(stage + tile_chunk(32 * (warp & 3) + rr, ch));
-          }
-          fence_proxy_async_smem();   // read before TMA writes the buffer again
+        if (32 * cc + 8 * s4 < p.d) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (row0 + j < w.len)
+              *reinterpret_cast<uint4*>(op + j * p.o_tok + 32 * cc) = make_uint4(x[0][j], x[1][j], x[2][j], x[3][j]);
         }
       }
-      item_sync();
-      item = next_item();
-      if (item < 0) break;
+      if (row < w.len)
+        p.lse[(size_t)w.hq(t) * p.total + w.start + row] = (m_ref + log2f(l)) * 0.69314718055994531f;
+      tc_fence_before();   // (the next PV of this tile waits for this group's next P)
     }
   } else {
-    regs_dec<kOtherRegs>();   // warp 11: no role of its own, it only keeps the item barriers
-    for (;; ++kq) {
-      item_sync();
-      item_sync();
-      item = next_item();
-      if (item < 0) break;
-    }
+    regs_dec<kOtherRegs>();   // warp 11: no role
   }
   tc_fence_before();
   __syncthreads();
@@ -690,7 +666,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
 
 template <int D, bool F16>
 cudaError_t launch_packed_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                const CUtensorMap& to, const PackedFwdParams& p, cudaStream_t s) {
+                                const PackedFwdParams& p, cudaStream_t s) {
   using L = PackedFwdLayout<D>;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -706,19 +682,20 @@ cudaError_t launch_packed_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
   PackedFwdParams q = p;
   // K and V of a key/value head (2 total d 16-bit elements) are re-read by the
   // items of its G query heads
-  q.group = p.G * l2_head_group(4.0 * p.total * p.d, p.Hq / p.G);
-  const long long most = (long long)p.cap_items * p.Hq;
-  return launch_pdl(true, fa_packed_fwd_kernel<D, F16>, dim3((unsigned)(most < sms ? most : sms)), dim3(kFwdThreads),
-                    L::kSmemBytes, s, tq, tk, tv, to, q);
+  q.group = p.G / (p.Hq / p.heads) * l2_head_group(4.0 * p.total * p.d, p.Hq / p.G);
+  // a CTA per item where items are taken by cancelling CTAs, else one per SM
+  const long long most = (long long)p.cap_items * p.heads;
+  return launch_pdl(true, fa_packed_fwd_kernel<D, F16>, dim3((unsigned)(p.B <= kDirect || most < sms ? most : sms)),
+                    dim3(kFwdThreads), L::kSmemBytes, s, tq, tk, tv, q);
 }
 
 }  // namespace
 
 cudaError_t launch_packed_fwd(bool f16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                              const CUtensorMap& to, const PackedFwdParams& p, cudaStream_t s) {
+                              const PackedFwdParams& p, cudaStream_t s) {
   if (p.d <= 64)
-    return f16 ? launch_packed_fwd_d<64, true>(tq, tk, tv, to, p, s) : launch_packed_fwd_d<64, false>(tq, tk, tv, to, p, s);
-  return f16 ? launch_packed_fwd_d<128, true>(tq, tk, tv, to, p, s) : launch_packed_fwd_d<128, false>(tq, tk, tv, to, p, s);
+    return f16 ? launch_packed_fwd_d<64, true>(tq, tk, tv, p, s) : launch_packed_fwd_d<64, false>(tq, tk, tv, p, s);
+  return f16 ? launch_packed_fwd_d<128, true>(tq, tk, tv, p, s) : launch_packed_fwd_d<128, false>(tq, tk, tv, p, s);
 }
 
 }  // namespace fa

@@ -89,9 +89,11 @@ def test_workspace_size(L):
     def al(x):
         return (x + 255) // 256 * 256
     B, total, Hq, d = 5, 1000, 8, 96
-    items, tiles = total // 256 + B, total // 128 + B
-    want = al(al(al(256) + 4 * B) + 16 * items)
+    tiles = total // 128 + B
+    want = al(al(al(256) + 4 * B) + 16 * tiles)
     assert L.flash_attn_packed_workspace_size(B, total, Hq, 2, d, 0) == want
+    # an odd group: two query tiles to an item
+    assert L.flash_attn_packed_workspace_size(B, total, Hq, Hq, d, 0) == al(al(al(256) + 4 * B) + 16 * (total // 256 + B))
     want = al(al(al(256) + 4 * B) + 16 * tiles)
     want = al(want + 16 * tiles)
     rows = Hq * tiles * 128
