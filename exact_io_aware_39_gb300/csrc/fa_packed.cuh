@@ -134,6 +134,7 @@ struct DirectList {
     off = 0;
     rank = first = 0;
     if (!causal)
+#pragma unroll 1
       for (int l = 0; l < 32; ++l) {
         const int o = __shfl_sync(0xFFFFFFFFu, n, l);
         if (o > n || (o == n && l < lane)) {
@@ -151,11 +152,13 @@ struct DirectList {
         off = 0;
       }
       uint32_t has = __ballot_sync(0xFFFFFFFFu, n > c);
+#pragma unroll 1
       while (c > 0 && idx >= off + __popc(has)) {
         off += __popc(has);
         --c;
         has = __ballot_sync(0xFFFFFFFFu, n > c);
       }
+#pragma unroll 1
       for (int r = idx - off; r > 0; --r) has &= has - 1;
       b = __ffs(has) - 1;
       it.c = c;
@@ -171,6 +174,35 @@ struct DirectList {
   }
 };
 
+// Bounded waits of little code: these kernels wait at some thirty places, and
+// one that inlines the report of a timeout at each of them no longer fits the
+// instruction cache. A wait that runs out leaves its site in the abort word;
+// report_aborted, once at the end of the kernel, records it.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Ctl& c, uint32_t site) {
+  if (mbar_try(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  do {
+    if (mbar_try(bar, parity)) return true;
+    if (globaltimer() - t0 > 1000ull * c.abort[2] && *c.abort == 0u) *c.abort = site;
+  } while (*c.abort == 0u);
+  return false;
+}
+__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, const Ctl& c, uint32_t site) {
+  const bool ok = bar_wait(bar, parity, c, site);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+// by one thread, behind a barrier of the whole CTA
+__device__ __forceinline__ void report_aborted(const Ctl& c) {
+  const uint32_t site = *c.abort;
+  if (site != 0u) report_error(c, kErrTimeout, site);
+}
+
+// Brings a tile box into L2 (same coordinates as the load).
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* m, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
+               :: "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2) : "memory");
+}
+
 // Zeroes rows r0 .. 127 of a 128-row tile (64-column atoms of 16 KB, D / 64 of
 // them), executed by a whole warp on a tile that TMA has written: the rows
 // behind a sequence's end hold other sequences' data or none, and a zero
@@ -179,10 +211,10 @@ struct DirectList {
 template <int D>
 __device__ __forceinline__ void zero_tail_rows(uint8_t* tile, int r0) {
   const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int i = 8 * r0 + lane; i < 8 * kTile; i += 32)
 #pragma unroll
-  for (int h = 0; h < D / 64; ++h)
-    for (int i = 8 * r0 + lane; i < 8 * kTile; i += 32)
-      *reinterpret_cast<uint4*>(tile + h * 16384 + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+    for (int h = 0; h < D / 64; ++h) *reinterpret_cast<uint4*>(tile + h * 16384 + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   __syncwarp();
 }

@@ -116,7 +116,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   auto take_item = [&](int k, bool& ok) -> Item {
     const int rs = k % L::kItemRing;
     const uint32_t ph = (uint32_t)(k / L::kItemRing) & 1u;
-    ok = mbar_wait_warp(bar(L::bItemFull + rs), ph, ctl, 355);
+    ok = bar_wait_warp(bar(L::bItemFull + rs), ph, ctl, 355);
     Item w{-1, 0, 0, 0, 0, 0, 0};
     if (!ok) return w;
     w.kj = ring[8 * rs];
@@ -212,7 +212,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       // that used the buffer before has been read out of it
       auto load_kv = [&](int k, const Item& w) -> bool {
         const int kb = k % L::kKV;
-        if (k >= L::kKV && !mbar_wait(bar(L::bKVFree + kb), (uint32_t)(k / L::kKV - 1) & 1u, ctl, 353)) return false;
+        if (k >= L::kKV && !bar_wait(bar(L::bKVFree + kb), (uint32_t)(k / L::kKV - 1) & 1u, ctl, 353)) return false;
         mbar_arrive_expect_tx(bar(L::bKV + kb), 2u * L::kTileBytes);
         for (int h = 0; h < L::kHalves; ++h) {
           tma_load_3d(sbase + L::kK + kb * L::kKVBytes + h * 16384, &tk, bar(L::bKV + kb), 64 * h, w.hk,
@@ -229,7 +229,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         // claim the next item and hand it to the other roles
         const int rs = k % L::kItemRing;
         if (k >= L::kItemRing &&
-            !(ok = mbar_wait(bar(L::bItemEmpty + rs), (uint32_t)(k / L::kItemRing - 1) & 1u, ctl, 354)))
+            !(ok = bar_wait(bar(L::bItemEmpty + rs), (uint32_t)(k / L::kItemRing - 1) & 1u, ctl, 354)))
           break;
         Item w{-1, 0, 0, 0, 0, 0, 0};
         for (bool first = k == 0;; first = false) {
@@ -258,7 +258,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           const uint32_t n = (uint32_t)(g / L::kStages);
           // Q and the row statistics once dK has read the slot's Q; dO once the
           // dQ partial staged in the slot's dO buffer has been read
-          if (g >= L::kStages && !(ok = mbar_wait(bar(L::bQEmpty + s), (n - 1) & 1u, ctl, 351))) break;
+          if (g >= L::kStages && !(ok = bar_wait(bar(L::bQEmpty + s), (n - 1) & 1u, ctl, 351))) break;
           mbar_arrive_expect_tx(bar(L::bQFull + s), L::kTileBytes + 2u * kTile * 4u);
           for (int h = 0; h < L::kHalves; ++h)
             tma_load_3d(sbase + L::kQ + s * L::kTileBytes + h * 16384, &tq, bar(L::bQFull + s),
@@ -267,7 +267,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           bulk_load(sbase + L::kRow + s * 1024, p.lse2 + roff, kTile * 4, bar(L::bQFull + s));
           bulk_load(sbase + L::kRow + s * 1024 + 512, p.delta + roff, kTile * 4, bar(L::bQFull + s));
           ++nq;
-          if (g >= L::kStages && !(ok = mbar_wait(bar(L::bdOFree + s), (n - 1) & 1u, ctl, 352))) break;
+          if (g >= L::kStages && !(ok = bar_wait(bar(L::bdOFree + s), (n - 1) & 1u, ctl, 352))) break;
           mbar_arrive_expect_tx(bar(L::bdOFull + s), L::kTileBytes);
           for (int h = 0; h < L::kHalves; ++h)
             tma_load_3d(sbase + L::kdO + s * L::kTileBytes + h * 16384, &tdo, bar(L::bdOFull + s),
@@ -309,7 +309,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       // sequence, or 0)
       auto issue_s = [&](uint32_t sK, int g1, int tail) -> bool {
         const int s1 = g1 % L::kStages;
-        if (!mbar_wait_warp(bar(L::bQFull + s1), (uint32_t)(g1 / L::kStages) & 1u, ctl, 364)) return false;
+        if (!bar_wait_warp(bar(L::bQFull + s1), (uint32_t)(g1 / L::kStages) & 1u, ctl, 364)) return false;
         if (tail != 0) zero_tail_rows<D>(smem + L::kQ + s1 * L::kTileBytes, tail);
         tc_fence_after();
         const uint64_t dK0 = desc_kmajor(sK, 0), dQ0 = desc_kmajor(sbase + L::kQ + s1 * L::kTileBytes, 0);
@@ -327,7 +327,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         const int kb = k % L::kKV;
         const uint32_t sK = sbase + L::kK + kb * L::kKVBytes, sV = sbase + L::kV + kb * L::kKVBytes;
         const uint64_t mK = desc_mnmajor(sK, 0);
-        if (!(ok = mbar_wait_warp(bar(L::bKV + kb), (uint32_t)(k / L::kKV) & 1u, ctl, 360))) break;
+        if (!(ok = bar_wait_warp(bar(L::bKV + kb), (uint32_t)(k / L::kKV) & 1u, ctl, 360))) break;
         if (tail != 0 && w.kj == w.nT - 1) {
           zero_tail_rows<D>(smem + L::kK + kb * L::kKVBytes, tail);
           zero_tail_rows<D>(smem + L::kV + kb * L::kKVBytes, tail);
@@ -342,8 +342,8 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           const uint32_t sdO = sbase + L::kdO + s * L::kTileBytes;
           // dP^T = V dO^T (at d = 128 the dQ partial of the previous tile must
           // have been read out of these columns)
-          if (!kOwnDQ && g > 0 && !(ok = mbar_wait_warp(bar(L::bdQFree), (uint32_t)(g - 1) & 1u, ctl, 362))) break;
-          if (!(ok = mbar_wait_warp(bar(L::bdOFull + s), (uint32_t)(g / L::kStages) & 1u, ctl, 366))) break;
+          if (!kOwnDQ && g > 0 && !(ok = bar_wait_warp(bar(L::bdQFree), (uint32_t)(g - 1) & 1u, ctl, 362))) break;
+          if (!(ok = bar_wait_warp(bar(L::bdOFull + s), (uint32_t)(g / L::kStages) & 1u, ctl, 366))) break;
           if (tail != 0 && i == w.nT - 1) zero_tail_rows<D>(smem + L::kdO + s * L::kTileBytes, tail);
           tc_fence_after();
           const uint64_t kdV = desc_kmajor(sV, 0), kdO = desc_kmajor(sdO, 0);
@@ -353,7 +353,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           mma_commit_w(bar(L::bdPFull));
           // dV += P^T dO (at it == 0 over the previous item's dV and dK, which
           // the compute warps have read out of TMEM before arriving on this P)
-          if (!(ok = mbar_wait_warp(bar(L::bPFull), (uint32_t)g & 1u, ctl, 363))) break;
+          if (!(ok = bar_wait_warp(bar(L::bPFull), (uint32_t)g & 1u, ctl, 363))) break;
           tc_fence_after();
           const uint64_t mdO = desc_mnmajor(sdO, 0);
 #pragma unroll
@@ -382,7 +382,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           };
 #pragma unroll
           for (int half = kSplitDS ? 0 : 1; half < 2; ++half) {
-            if (!(ok = mbar_wait_warp(bar(half == 0 ? L::bdSHalf : L::bdSFull), (uint32_t)g & 1u, ctl, 365)))
+            if (!(ok = bar_wait_warp(bar(half == 0 ? L::bdSHalf : L::bdSFull), (uint32_t)g & 1u, ctl, 365)))
               break;
             tc_fence_after();
             if (kSplitDS && half == 1) issue_dq();
@@ -397,7 +397,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           mma_commit_w(bar(L::bQEmpty + s));   // the slot's Q has been read for the last time
           if (!kSplitDS) {
             // at d = 64 the previous dQ partial must have been read out of its columns
-            if (kOwnDQ && g > 0 && !(ok = mbar_wait_warp(bar(L::bdQFree), (uint32_t)(g - 1) & 1u, ctl, 362))) break;
+            if (kOwnDQ && g > 0 && !(ok = bar_wait_warp(bar(L::bdQFree), (uint32_t)(g - 1) & 1u, ctl, 362))) break;
             tc_fence_after();
             issue_dq();
           }
@@ -449,8 +449,8 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       for (int it = 0, i = w.i0; it < steps; ++it, ++g, i = i + 1 < w.nT ? i + 1 : w.i0) {
         const bool partial = (p.causal && i == w.kj) || (w.kj + 1) * kTile > w.len;
         const int s = g % L::kStages;
-        if (!(ok = mbar_wait_warp(bar(L::bQFull + s), (uint32_t)(g / L::kStages) & 1u, ctl, 370))) break;
-        if (!(ok = mbar_wait_warp(bar(L::bSFull), (uint32_t)g & 1u, ctl, 371))) break;
+        if (!(ok = bar_wait_warp(bar(L::bQFull + s), (uint32_t)(g / L::kStages) & 1u, ctl, 370))) break;
+        if (!(ok = bar_wait_warp(bar(L::bSFull), (uint32_t)g & 1u, ctl, 371))) break;
         tc_fence_after();
         const float* lse2 = reinterpret_cast<const float*>(smem + L::kRow + s * 1024) + cb;
         const float* dlt = lse2 + kTile;
@@ -499,8 +499,8 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         if (it == 0) release_kv();   // the previous item's store has had this tile's time to read its staging
 
         // dS^T row: ds[c] = p[c] * (dP[c] - D[query c]) -> 16-bit -> swizzled smem
-        if (!(ok = mbar_wait_warp(bar(L::bdPFull), (uint32_t)g & 1u, ctl, 372))) break;
-        if (g > 0 && !(ok = mbar_wait_warp(bar(L::bdSEmpty), (uint32_t)(g - 1) & 1u, ctl, 373))) break;
+        if (!(ok = bar_wait_warp(bar(L::bdPFull), (uint32_t)g & 1u, ctl, 372))) break;
+        if (g > 0 && !(ok = bar_wait_warp(bar(L::bdSEmpty), (uint32_t)(g - 1) & 1u, ctl, 373))) break;
         tc_fence_after();
         // at d = 128 both 32-column halves of this warpgroup's dP^T are loaded
         // before the first wait, so their TMEM latencies overlap (at d = 64 the
@@ -557,8 +557,8 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       ok = group_all(gbar, kGThreads, ok);
       if (!ok) break;
       const int kb = k % L::kKV;
-      ok = mbar_wait_warp(bar(L::bKV + kb), (uint32_t)(k / L::kKV) & 1u, ctl, 374);
-      if (ok) ok = mbar_wait_warp(bar(L::bFinal), (uint32_t)nf & 1u, ctl, 375);
+      ok = bar_wait_warp(bar(L::bKV + kb), (uint32_t)(k / L::kKV) & 1u, ctl, 374);
+      if (ok) ok = bar_wait_warp(bar(L::bFinal), (uint32_t)nf & 1u, ctl, 375);
       ok = group_all(gbar, kGThreads, ok);
       if (!ok) break;
       ++nf;
@@ -640,7 +640,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       for (int it = 0, i = w.i0, hq = w.hk * p.G; it < steps; ++it, ++g) {
         const int s = g % L::kStages;
         const uint32_t stage = (uint32_t)(L::kdO + s * L::kTileBytes);
-        ok = mbar_wait_warp(bar(L::bdQFull), (uint32_t)g & 1u, ctl, 380);
+        ok = bar_wait_warp(bar(L::bdQFull), (uint32_t)g & 1u, ctl, 380);
         if constexpr (L::kGroupDrain) ok = group_all(kDrainBar, 128, ok);
         if (!ok) break;
         tc_fence_after();
@@ -709,6 +709,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
 
   tc_fence_before();
   __syncthreads();
+  if (tid == 0) report_aborted(ctl);
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

@@ -106,7 +106,6 @@ struct Pair {
   __device__ __forceinline__ int qi(int t) const { return pair_heads ? c : 2 * c + t; }
   __device__ __forceinline__ int hq(int t) const { return pair_heads ? 2 * head + t : head; }
   __device__ __forceinline__ int last(int t) const { return causal ? qi(t) : nT - 1; }   // last key tile live for t
-  __device__ __forceinline__ bool live(int e, int t) const { return has(t) && e <= last(t); }
   __device__ __forceinline__ bool partial(int e, int q) const { return (causal && e == q) || (e + 1) * kTile > len; }
   // valid rows of the last key tile when it is not full, else 0
   __device__ __forceinline__ int tail() const { return len & (kTile - 1); }
@@ -174,7 +173,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   auto take_item = [&](int k, Pair& w) -> bool {
     const int rs = k % L::kItemRing;
     w.c = -1;
-    if (!mbar_wait_warp(bar(L::bItemFull + rs), (uint32_t)(k / L::kItemRing) & 1u, ctl, 319)) return false;
+    if (!bar_wait_warp(bar(L::bItemFull + rs), (uint32_t)(k / L::kItemRing) & 1u, ctl, 319)) return false;
     w.start = ring[4 * rs];
     w.len = ring[4 * rs + 1];
     w.c = ring[4 * rs + 2];
@@ -205,14 +204,14 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     }
     const int total = n_items * p.heads;
     int nk = 0;                  // K loads issued
-    int nq[2] = {0, 0};          // Q loads issued per query tile
+    int nq0 = 0, nq1 = 0;        // Q loads issued per query tile
     bool clc_out = false;        // a cancellation answer is outstanding
     uint32_t clc = 0u;           // answers received
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const int rs = k % L::kItemRing;
       if (k >= L::kItemRing &&
-          !(ok = mbar_wait_warp(bar(L::bItemEmpty + rs), (uint32_t)(k / L::kItemRing - 1) & 1u, ctl, 313)))
+          !(ok = bar_wait_warp(bar(L::bItemEmpty + rs), (uint32_t)(k / L::kItemRing - 1) & 1u, ctl, 313)))
         break;
       int item = (int)blockIdx.x;
       if (k > 0 && !direct) {
@@ -227,7 +226,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           }
           __syncwarp();
           clc_out = true;
-          if (!(ok = mbar_wait_warp(bar(L::bClc), clc & 1u, ctl, 309))) break;
+          if (!(ok = bar_wait_warp(bar(L::bClc), clc & 1u, ctl, 309))) break;
           clc_out = false;
           ++clc;
           item = clc_first_ctaid_x(sbase + L::kClc);
@@ -257,13 +256,21 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       if (w.c < 0) break;
       if (lane == 0) {
         const int hk = w.hq(0) / p.G;
+        // Q can only be loaded behind the last S of the item before: it is
+        // brought into L2 until then
+        if (k >= L::kQBuf)
+#pragma unroll 1
+          for (int t = 0; t < 2; ++t)
+            for (int a = 0; w.has(t) && a < L::kHalves; ++a)
+              tma_prefetch_3d(&tq, 64 * a, w.hq(t), w.start + kTile * w.qi(t));
+#pragma unroll 1
         for (int e = 0; e < w.n && ok; ++e) {
           if (p.stall != 0u && e >= 1) { ok = false; break; }   // test of the timeout path: K of entry 1 never comes
           // K of key tile e, once the MMAs of the entry that used the slot
           // before (of this item or an earlier one) have read it
           const int sk = nk % L::kStagesK;
           if (nk >= L::kStagesK &&
-              !(ok = mbar_wait(bar(L::bKEmpty + sk), (uint32_t)(nk / L::kStagesK - 1) & 1u, ctl, 311)))
+              !(ok = bar_wait(bar(L::bKEmpty + sk), (uint32_t)(nk / L::kStagesK - 1) & 1u, ctl, 311)))
             break;
           mbar_arrive_expect_tx(bar(L::bKFull + sk), L::kTileBytes);
           for (int a = 0; a < L::kHalves; ++a)
@@ -272,17 +279,17 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           ++nk;
           // the item's Q tiles behind its first K, which seldom waits; a tile's
           // buffer is free once the last S of the item before has read it
+#pragma unroll 1
           for (int t = 0; e == 0 && t < 2 && ok; ++t) {
             if (!w.has(t)) continue;
-            const int qb = nq[t] % L::kQBuf, slot = t * L::kQBuf + qb;
-            if (nq[t] >= L::kQBuf &&
-                !(ok = mbar_wait(bar(L::bQEmpty + slot), (uint32_t)(nq[t] / L::kQBuf - 1) & 1u, ctl, 310)))
+            const int nt = t ? nq1 : nq0, slot = t * L::kQBuf + nt % L::kQBuf;
+            if (nt >= L::kQBuf && !(ok = bar_wait(bar(L::bQEmpty + slot), (uint32_t)(nt / L::kQBuf - 1) & 1u, ctl, 310)))
               break;
             mbar_arrive_expect_tx(bar(L::bQFull + slot), L::kTileBytes);
             for (int a = 0; a < L::kHalves; ++a)
               tma_load_3d(sbase + L::kQ + slot * L::kTileBytes + a * 16384, &tq, bar(L::bQFull + slot), 64 * a, w.hq(t),
                           w.start + kTile * w.qi(t));
-            ++nq[t];
+            (t ? nq1 : nq0) += 1;
           }
         }
       }
@@ -293,9 +300,12 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     // number s + S * floor((n - 1 - s) / S)
     if (lane == 0) {
       if (clc_out) drain_wait(bar(L::bClc), clc & 1u);
-      for (int t = 0; t < 2; ++t)
-        for (int b = 0; b < L::kQBuf && b < nq[t]; ++b)
-          drain_wait(bar(L::bQFull + t * L::kQBuf + b), (uint32_t)((nq[t] - 1 - b) / L::kQBuf) & 1u);
+#pragma unroll 1
+      for (int i = 0; i < 2 * L::kQBuf; ++i) {
+        const int nt = i < L::kQBuf ? nq0 : nq1, b = i % L::kQBuf;
+        if (b < nt) drain_wait(bar(L::bQFull + i), (uint32_t)((nt - 1 - b) / L::kQBuf) & 1u);
+      }
+#pragma unroll 1
       for (int s = 0; s < L::kStagesK && s < nk; ++s)
         drain_wait(bar(L::bKFull + s), (uint32_t)((nk - 1 - s) / L::kStagesK) & 1u);
     }
@@ -310,10 +320,11 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     for (int k = 0; ok && take_item(k, w) && w.c >= 0; ++k) {
       if (lane == 0) {
         const int hk = w.hq(0) / p.G;
+#pragma unroll 1
         for (int e = 0; e < w.n; ++e) {
           const int sv = nv % L::kStagesV;
           if (nv >= L::kStagesV &&
-              !(ok = mbar_wait(bar(L::bVEmpty + sv), (uint32_t)(nv / L::kStagesV - 1) & 1u, ctl, 312)))
+              !(ok = bar_wait(bar(L::bVEmpty + sv), (uint32_t)(nv / L::kStagesV - 1) & 1u, ctl, 312)))
             break;
           mbar_arrive_expect_tx(bar(L::bVFull + sv), L::kTileBytes);
           for (int a = 0; a < L::kHalves; ++a)
@@ -325,6 +336,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
     }
     if (lane == 0)
+#pragma unroll 1
       for (int s = 0; s < L::kStagesV && s < nv; ++s)
         drain_wait(bar(L::bVFull + s), (uint32_t)((nv - 1 - s) / L::kStagesV) & 1u);
   } else if (warp == 9) {
@@ -360,66 +372,39 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     bool pfirst[2] = {false, false}, plast[2] = {false, false};
     int ptail[2] = {0, 0};
     int zeroed = -1;                 // last V ring entry whose rows past the sequence were zeroed
-    auto issue_pv = [&](int t) -> bool {
-      const int v = pend[t], sv = v % L::kStagesV;
-      pend[t] = -1;
-      if (!mbar_wait_warp(bar((kHalfP ? L::bPHalf : L::bPFull) + t), npv[t] & 1u, ctl, 315)) return false;
-      if (!mbar_wait_warp(bar(L::bVFull + sv), (uint32_t)(v / L::kStagesV) & 1u, ctl, 316)) return false;
-      if (ptail[t] != 0 && zeroed != v) {
-        zero_tail_rows<D>(smem + L::kV + sv * L::kTileBytes, ptail[t]);
-        zeroed = v;
-      }
-      tc_fence_after();
-      const uint64_t dV = dV0 + (uint64_t)sv * kSlotStep;
-#pragma unroll
-      for (int ks = 0; ks < kTile / 16; ++ks) {
-        if (kHalfP && ks == kTile / 32) {   // the second half of P
-          if (!mbar_wait_warp(bar(L::bPFull + t), npv[t] & 1u, ctl, 315)) return false;
-          tc_fence_after();
-        }
-        mma_ts_w(tO[t], tP[t] + (uint32_t)ks * 8u, dV + mnmajor_step(ks), idO, ks > 0 || !pfirst[t] ? 1u : 0u);
-      }
-      if constexpr (L::kOwnP) mma_commit_w(bar(L::bPVDone + t));   // P_t may be rewritten, O_t rescaled
-      if (plast[t]) mma_commit_w(bar(L::bOFinal + t));             // O_t is complete
-      ++npv[t];
-      return true;
-    };
     bool open = false;               // V ring entry nv - 1 has not gone back to the producer
-    auto release_v = [&]() {
-      if (open) mma_commit_w(bar(L::bVEmpty + (nv - 1) % L::kStagesV));
-      open = false;
-    };
-    auto flush = [&]() -> bool {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (pend[t] >= 0 && !issue_pv(t)) return false;
-      release_v();
-      return true;
-    };
-    bool ok = true;
+    bool ok = true, more = true;
     Pair w;
-    for (int k = 0; ok; ++k) {
+    for (int k = 0; ok && more; ++k) {
       if (!(ok = take_item(k, w))) break;
-      if (w.c < 0) {
-        ok = flush();
-        break;
-      }
+      more = w.c >= 0;
+      const int n = more ? w.n : 0;
       const int tail = w.tail();
+      const int last[2] = {w.last(0), w.has(1) ? w.last(1) : -1};   // t is live at entries 0 .. last
       // Q_t of this item: its buffer and phase
       auto q_slot = [&](int t) -> int { return t * L::kQBuf + nq[t] % L::kQBuf; };
       auto q_phase = [&](int t) -> uint32_t { return (uint32_t)(nq[t] / L::kQBuf) & 1u; };
-      if (pend[0] >= 0 || pend[1] >= 0) {
+      // Where this item's first loads are not there yet, its pending PVs go
+      // before its first S, as an entry -1 without an S of its own. (The loop
+      // holds each product's code once per query tile: an item passes through
+      // every line of the kernel, and a larger one misses the instruction cache;
+      // with copies of its own for the end of an item, items of one key tile
+      // took 4.9 us instead of 4.2.)
+      bool first = !more;
+      if (more) {
         const bool there = mbar_test(bar(L::bQFull + q_slot(0)), q_phase(0)) &&
                            mbar_test(bar(L::bKFull + nk % L::kStagesK), (uint32_t)(nk / L::kStagesK) & 1u);
-        if (!__all_sync(0xFFFFFFFFu, there) && !(ok = flush())) break;
+        first = !__all_sync(0xFFFFFFFFu, there);
       }
-      for (int e = 0; e < w.n && ok; ++e) {
+#pragma unroll 1
+      for (int e = first ? -1 : 0; e < n && ok; ++e) {
         const int sk = nk % L::kStagesK;
         bool k_ready = false;
+        // S_t = Q_t K_e^T
         auto issue_s = [&](int t) -> bool {
-          if (L::kOwnP && ns[t] > 0 && !mbar_wait_warp(bar(L::bSFree + t), (ns[t] - 1u) & 1u, ctl, 318)) return false;
-          if (e == 0 && !mbar_wait_warp(bar(L::bQFull + q_slot(t)), q_phase(t), ctl, 314)) return false;
-          if (!k_ready && !mbar_wait_warp(bar(L::bKFull + sk), (uint32_t)(nk / L::kStagesK) & 1u, ctl, 317)) return false;
+          if (L::kOwnP && ns[t] > 0 && !bar_wait_warp(bar(L::bSFree + t), (ns[t] - 1u) & 1u, ctl, 318)) return false;
+          if (e == 0 && !bar_wait_warp(bar(L::bQFull + q_slot(t)), q_phase(t), ctl, 314)) return false;
+          if (!k_ready && !bar_wait_warp(bar(L::bKFull + sk), (uint32_t)(nk / L::kStagesK) & 1u, ctl, 317)) return false;
           k_ready = true;
           tc_fence_after();
           const uint64_t dQ = dQ0 + (uint64_t)q_slot(t) * kSlotStep, dK = dK0 + (uint64_t)sk * kSlotStep;
@@ -427,44 +412,74 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           for (int ks = 0; ks < D / 16; ++ks)
             mma_ss_w(tS[t], dQ + kmajor_step(ks), dK + kmajor_step(ks), idS, ks > 0 ? 1u : 0u);
           mma_commit_w(bar(L::bSFull + t));
-          if (e == w.last(t)) mma_commit_w(bar(L::bQEmpty + q_slot(t)));   // Q_t is no longer needed
+          if (e == last[t]) mma_commit_w(bar(L::bQEmpty + q_slot(t)));   // Q_t is no longer needed
           ++ns[t];
           return true;
         };
-        // the entry's PV, once issue_s has put its S on the way
+        // O_t += P_t V of the pending entry
+        auto issue_pv = [&](int t) -> bool {
+          const int v = pend[t], sv = v % L::kStagesV;
+          pend[t] = -1;
+          if (!bar_wait_warp(bar((kHalfP ? L::bPHalf : L::bPFull) + t), npv[t] & 1u, ctl, 315)) return false;
+          if (!bar_wait_warp(bar(L::bVFull + sv), (uint32_t)(v / L::kStagesV) & 1u, ctl, 316)) return false;
+          if (ptail[t] != 0 && zeroed != v) {
+            zero_tail_rows<D>(smem + L::kV + sv * L::kTileBytes, ptail[t]);
+            zeroed = v;
+          }
+          tc_fence_after();
+          const uint64_t dV = dV0 + (uint64_t)sv * kSlotStep;
+          const uint32_t acc0 = pfirst[t] ? 0u : 1u;
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks) {
+            if (kHalfP && ks == kTile / 32) {   // the second half of P
+              if (!bar_wait_warp(bar(L::bPFull + t), npv[t] & 1u, ctl, 315)) return false;
+              tc_fence_after();
+            }
+            mma_ts_w(tO[t], tP[t] + (uint32_t)ks * 8u, dV + mnmajor_step(ks), idO, ks > 0 ? 1u : acc0);
+          }
+          if constexpr (L::kOwnP) mma_commit_w(bar(L::bPVDone + t));   // P_t may be rewritten, O_t rescaled
+          if (plast[t]) mma_commit_w(bar(L::bOFinal + t));             // O_t is complete
+          ++npv[t];
+          return true;
+        };
+        // the entry's PV becomes the pending one once the one before it is on its way
         auto set_pending = [&](int t) {
           pend[t] = nv;
           pfirst[t] = e == 0;
-          plast[t] = e == w.last(t);
+          plast[t] = e == last[t];
           ptail[t] = e == w.nT - 1 ? tail : 0;
         };
         if constexpr (L::kOwnP) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
-            if (ok && w.live(e, t)) ok = issue_s(t);
+            if (ok && e >= 0 && e <= last[t]) ok = issue_s(t);
           if (!ok) break;
-          mma_commit_w(bar(L::bKEmpty + sk));   // K_e is no longer needed
-          if (!(ok = flush())) break;
+          if (e >= 0) mma_commit_w(bar(L::bKEmpty + sk));   // K_e is no longer needed
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (w.live(e, t)) set_pending(t);
+          for (int t = 0; t < 2; ++t) {
+            if (ok && pend[t] >= 0) ok = issue_pv(t);
+            if (e >= 0 && e <= last[t]) set_pending(t);
+          }
         } else {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (ok && pend[t] >= 0) ok = issue_pv(t);
-            if (ok && w.live(e, t) && (ok = issue_s(t))) set_pending(t);
+            if (ok && e >= 0 && e <= last[t] && (ok = issue_s(t))) set_pending(t);
           }
-          if (!ok) break;
-          mma_commit_w(bar(L::bKEmpty + sk));   // K_e is no longer needed
-          release_v();                          // both PVs of the entry before are issued
+          if (ok && e >= 0) mma_commit_w(bar(L::bKEmpty + sk));   // K_e is no longer needed
         }
-        open = true;
-        ++nk;
-        ++nv;
+        if (!ok) break;
+        if (open) mma_commit_w(bar(L::bVEmpty + (nv - 1) % L::kStagesV));   // both PVs of the entry before are issued
+        open = e >= 0;
+        if (e >= 0) {
+          ++nk;
+          ++nv;
+        }
       }
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (w.has(t)) ++nq[t];
+      if (more) {
+        ++nq[0];
+        nq[1] += w.has(1) ? 1 : 0;
+      }
     }
     // every MMA issued has completed before TMEM is freed
     mma_commit_w(bar(L::bDrain));
@@ -490,7 +505,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       float l = 0.f;
       for (int e = 0; e <= last; ++e) {
         const uint32_t n = (uint32_t)e;      // S tiles of this item before this one
-        if (!(ok = mbar_wait_warp(bar(L::bSFull + t), nS & 1u, ctl, 320 + t))) break;
+        if (!(ok = bar_wait_warp(bar(L::bSFull + t), nS & 1u, ctl, 320 + t))) break;
         tc_fence_after();
         float x[128];
         {
@@ -527,7 +542,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         if (L::kOwnP && nS > 0) {
           // the previous O_t += P_t V has completed (of this item or the last
           // one): O_t may be rescaled and the P_t columns rewritten
-          if (!mbar_wait_warp(bar(L::bPVDone + t), (nS - 1u) & 1u, ctl, 326 + t)) { ok = false; break; }
+          if (!bar_wait_warp(bar(L::bPVDone + t), (nS - 1u) & 1u, ctl, 326 + t)) { ok = false; break; }
           tc_fence_after();
         }
         // Two passes at most (at d = 64; at d = 128 only pass 1).
@@ -541,6 +556,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         // warp-collective). This saves the row max on most tiles.
         float s_row = 0.f;
         // (when half of P goes ahead: always the row max)
+#pragma unroll 1
         for (int pass = (n == 0 || kHalfP) ? 1 : 0; pass < 2; ++pass) {
           if (pass == 1) {
             // row max with three-input max: 8 independent chains over 128 scores
@@ -621,7 +637,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       // columns of its row at a time, as four 16-byte chunks; transposed across
       // its quad it holds one chunk of four rows, and a quad writes 64 bytes of
       // each.
-      if (ok) ok = mbar_wait_warp(bar(L::bOFinal + t), nO & 1u, ctl, 324 + t);
+      if (ok) ok = bar_wait_warp(bar(L::bOFinal + t), nO & 1u, ctl, 324 + t);
       if (!ok) break;
       ++nO;
       tc_fence_after();
@@ -629,7 +645,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       const int s4 = lane & 3;
       const int row0 = kTile * qi + 32 * (warp & 3) + (lane & ~3);   // the quad's first row
       uint16_t* op = p.o + (int64_t)(w.start + row0) * p.o_tok + w.hq(t) * p.o_head + 8 * s4;
-#pragma unroll
+#pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t u[32];
         tmem_ld32(tO + 32u * cc, u);
@@ -658,6 +674,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0) report_aborted(ctl);
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
