@@ -95,7 +95,10 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   const uint32_t sbase = smem_u32(smem);
 
   const int tid = threadIdx.x;
-  const int warp = tid >> 5;
+  // (from a shuffle, so that the compiler knows it to be the same in all lanes:
+  // the operands of an MMA are uniform registers, and in a branch that it takes
+  // for divergent each MMA costs some 40 instructions more)
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const int lane = tid & 31;
 
   // An item: key tile kj of the sequence of rows start .. start + len - 1, for
@@ -119,11 +122,11 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     ok = bar_wait_warp(bar(L::bItemFull + rs), ph, ctl, 355);
     Item w{-1, 0, 0, 0, 0, 0, 0};
     if (!ok) return w;
-    w.kj = ring[8 * rs];
-    w.hk = ring[8 * rs + 1];
-    w.start = ring[8 * rs + 2];
-    w.len = ring[8 * rs + 3];
-    w.slot0 = ring[8 * rs + 4];
+    w.kj = __shfl_sync(0xFFFFFFFFu, ring[8 * rs], 0);   // (the same in all lanes, as the compiler then knows)
+    w.hk = __shfl_sync(0xFFFFFFFFu, ring[8 * rs + 1], 0);
+    w.start = __shfl_sync(0xFFFFFFFFu, ring[8 * rs + 2], 0);
+    w.len = __shfl_sync(0xFFFFFFFFu, ring[8 * rs + 3], 0);
+    w.slot0 = __shfl_sync(0xFFFFFFFFu, ring[8 * rs + 4], 0);
     w.nT = (w.len + kTile - 1) / kTile;
     w.i0 = p.causal ? w.kj : 0;
     mbar_arrive_warp(bar(L::bItemEmpty + rs));
@@ -201,90 +204,97 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   const size_t Np = (size_t)p.cap_tiles * kTile;
   if (warp >= kProducerWarp) regs_dec<kOtherRegs>();
   if (warp == kProducerWarp) {
-    // ------------------------------------------------------------ producer
+    // ------------------------------------------------------------ producer (warp-wide)
     if (lane == 0) {
       tma_prefetch_map(&tq);
       tma_prefetch_map(&tk);
       tma_prefetch_map(&tv);
       tma_prefetch_map(&tdo);
-      int nq = 0, nd = 0, nkv = 0;
-      // K and V of item k into buffer k % kKV, once the epilogue of the item
-      // that used the buffer before has been read out of it
-      auto load_kv = [&](int k, const Item& w) -> bool {
-        const int kb = k % L::kKV;
-        if (k >= L::kKV && !bar_wait(bar(L::bKVFree + kb), (uint32_t)(k / L::kKV - 1) & 1u, ctl, 353)) return false;
-        mbar_arrive_expect_tx(bar(L::bKV + kb), 2u * L::kTileBytes);
-        for (int h = 0; h < L::kHalves; ++h) {
-          tma_load_3d(sbase + L::kK + kb * L::kKVBytes + h * 16384, &tk, bar(L::bKV + kb), 64 * h, w.hk,
-                      w.start + kTile * w.kj);
-          tma_load_3d(sbase + L::kV + kb * L::kKVBytes + h * 16384, &tv, bar(L::bKV + kb), 64 * h, w.hk,
-                      w.start + kTile * w.kj);
-        }
-        ++nkv;
-        return true;
-      };
-      bool ok = true;
-      int g = 0;
-      for (int k = 0; ok; ++k) {
-        // claim the next item and hand it to the other roles
-        const int rs = k % L::kItemRing;
-        if (k >= L::kItemRing &&
-            !(ok = bar_wait(bar(L::bItemEmpty + rs), (uint32_t)(k / L::kItemRing - 1) & 1u, ctl, 354)))
-          break;
-        Item w{-1, 0, 0, 0, 0, 0, 0};
-        for (bool first = k == 0;; first = false) {
-          const int item = first ? (int)blockIdx.x : (int)gridDim.x + (int)atomicAdd(&p.plan->sched, 1u);
-          if (item >= total) break;
-          const PackedItem pi = p.items[split_grouped(item, p.group, n_items, p.Hk, &w.hk)];
-          if (pi.len <= 0) continue;   // left out by the plan
-          w.kj = pi.c;
-          w.start = pi.start;
-          w.len = pi.len;
-          w.slot0 = pi.slot0;
-          w.nT = (w.len + kTile - 1) / kTile;
-          w.i0 = p.causal ? w.kj : 0;
-          break;
-        }
+    }
+    int nq = 0, nd = 0, nkv = 0;
+    bool ok = true;
+    int g = 0;
+    for (int k = 0; ok; ++k) {
+      // claim the next item and hand it to the other roles
+      const int rs = k % L::kItemRing;
+      if (k >= L::kItemRing &&
+          !(ok = bar_wait_warp(bar(L::bItemEmpty + rs), (uint32_t)(k / L::kItemRing - 1) & 1u, ctl, 354)))
+        break;
+      Item w{-1, 0, 0, 0, 0, 0, 0};
+      for (bool first = k == 0;; first = false) {
+        int item = (int)blockIdx.x;
+        if (!first)
+          item = (int)gridDim.x + __shfl_sync(0xFFFFFFFFu, lane == 0 ? (int)atomicAdd(&p.plan->sched, 1u) : 0, 0);
+        if (item >= total) break;
+        const PackedItem pi = p.items[split_grouped(item, p.group, n_items, p.Hk, &w.hk)];
+        if (pi.len <= 0) continue;   // left out by the plan
+        w.kj = __shfl_sync(0xFFFFFFFFu, pi.c, 0);
+        w.start = __shfl_sync(0xFFFFFFFFu, pi.start, 0);
+        w.len = __shfl_sync(0xFFFFFFFFu, pi.len, 0);
+        w.slot0 = __shfl_sync(0xFFFFFFFFu, pi.slot0, 0);
+        w.nT = (w.len + kTile - 1) / kTile;
+        w.i0 = p.causal ? w.kj : 0;
+        break;
+      }
+      if (lane == 0) {
         ring[8 * rs] = w.kj;
         ring[8 * rs + 1] = w.hk;
         ring[8 * rs + 2] = w.start;
         ring[8 * rs + 3] = w.len;
         ring[8 * rs + 4] = w.slot0;
         mbar_arrive(bar(L::bItemFull + rs));   // (release: the ring entry is visible to the waiters)
-        if (w.kj < 0) break;
-        for (int it = 0, i = w.i0, hq = w.hk * p.G; it < p.G * (w.nT - w.i0); ++it, ++g) {
-          if (p.stall != 0u && g >= 1) { ok = false; break; }   // test of the timeout path: Q of tile 1 never comes
-          const int s = g % L::kStages;
-          const uint32_t n = (uint32_t)(g / L::kStages);
-          // Q and the row statistics once dK has read the slot's Q; dO once the
-          // dQ partial staged in the slot's dO buffer has been read
-          if (g >= L::kStages && !(ok = bar_wait(bar(L::bQEmpty + s), (n - 1) & 1u, ctl, 351))) break;
-          mbar_arrive_expect_tx(bar(L::bQFull + s), L::kTileBytes + 2u * kTile * 4u);
-          for (int h = 0; h < L::kHalves; ++h)
-            tma_load_3d(sbase + L::kQ + s * L::kTileBytes + h * 16384, &tq, bar(L::bQFull + s),
-                        64 * h, hq, w.start + kTile * i);
-          const size_t roff = (size_t)hq * Np + (size_t)kTile * (w.slot0 + i);
-          bulk_load(sbase + L::kRow + s * 1024, p.lse2 + roff, kTile * 4, bar(L::bQFull + s));
-          bulk_load(sbase + L::kRow + s * 1024 + 512, p.delta + roff, kTile * 4, bar(L::bQFull + s));
-          ++nq;
-          if (g >= L::kStages && !(ok = bar_wait(bar(L::bdOFree + s), (n - 1) & 1u, ctl, 352))) break;
-          mbar_arrive_expect_tx(bar(L::bdOFull + s), L::kTileBytes);
-          for (int h = 0; h < L::kHalves; ++h)
-            tma_load_3d(sbase + L::kdO + s * L::kTileBytes + h * 16384, &tdo, bar(L::bdOFull + s),
-                        64 * h, hq, w.start + kTile * i);
-          ++nd;
-          // K and V behind the first query tile of the item, whose loads only
-          // wait for ring slots of the previous item
-          if (it == 0 && !(ok = load_kv(k, w))) break;
-          if (++i == w.nT) {
-            i = w.i0;
-            ++hq;
+      }
+      if (w.kj < 0) break;
+      const int steps = p.G * (w.nT - w.i0);
+#pragma unroll 1
+      for (int it = 0, i = w.i0, hq = w.hk * p.G; it < steps; ++it, ++g) {
+        if (p.stall != 0u && g >= 1) { ok = false; break; }   // test of the timeout path: Q of tile 1 never comes
+        const int s = g % L::kStages;
+        const uint32_t n = (uint32_t)(g / L::kStages);
+        // Q and the row statistics once dK has read the slot's Q; dO once the
+        // dQ partial staged in the slot's dO buffer has been read
+        if (g >= L::kStages && !(ok = bar_wait_warp(bar(L::bQEmpty + s), (n - 1) & 1u, ctl, 351))) break;
+        mbar_arrive_expect_tx_w(bar(L::bQFull + s), L::kTileBytes + 2u * kTile * 4u);
+        for (int h = 0; h < L::kHalves; ++h)
+          tma_load_3d_w(sbase + L::kQ + s * L::kTileBytes + h * 16384, &tq, bar(L::bQFull + s), 64 * h, hq,
+                        w.start + kTile * i);
+        const size_t roff = (size_t)hq * Np + (size_t)kTile * (w.slot0 + i);
+        bulk_load_w(sbase + L::kRow + s * 1024, p.lse2 + roff, kTile * 4, bar(L::bQFull + s));
+        bulk_load_w(sbase + L::kRow + s * 1024 + 512, p.delta + roff, kTile * 4, bar(L::bQFull + s));
+        ++nq;
+        if (g >= L::kStages && !(ok = bar_wait_warp(bar(L::bdOFree + s), (n - 1) & 1u, ctl, 352))) break;
+        mbar_arrive_expect_tx_w(bar(L::bdOFull + s), L::kTileBytes);
+        for (int h = 0; h < L::kHalves; ++h)
+          tma_load_3d_w(sbase + L::kdO + s * L::kTileBytes + h * 16384, &tdo, bar(L::bdOFull + s), 64 * h, hq,
+                        w.start + kTile * i);
+        ++nd;
+        // K and V behind the first query tile of the item, whose loads only
+        // wait for ring slots of the previous item: into buffer k % kKV, once the
+        // epilogue of the item that used it before has been read out of it
+        if (it == 0) {
+          const int kb = k % L::kKV;
+          if (k >= L::kKV && !(ok = bar_wait_warp(bar(L::bKVFree + kb), (uint32_t)(k / L::kKV - 1) & 1u, ctl, 353))) break;
+          mbar_arrive_expect_tx_w(bar(L::bKV + kb), 2u * L::kTileBytes);
+          for (int h = 0; h < L::kHalves; ++h) {
+            tma_load_3d_w(sbase + L::kK + kb * L::kKVBytes + h * 16384, &tk, bar(L::bKV + kb), 64 * h, w.hk,
+                          w.start + kTile * w.kj);
+            tma_load_3d_w(sbase + L::kV + kb * L::kKVBytes + h * 16384, &tv, bar(L::bKV + kb), 64 * h, w.hk,
+                          w.start + kTile * w.kj);
           }
+          ++nkv;
+        }
+        if (++i == w.nT) {
+          i = w.i0;
+          ++hq;
         }
       }
-      // every load issued has landed before the CTA exits
+    }
+    // every load issued has landed before the CTA exits
+    if (lane == 0) {
+#pragma unroll 1
       for (int kb = 0; kb < L::kKV && kb < nkv; ++kb)
         drain_wait(bar(L::bKV + kb), (uint32_t)((nkv - 1 - kb) / L::kKV) & 1u);
+#pragma unroll 1
       for (int s = 0; s < L::kStages; ++s) {
         if (s < nq) drain_wait(bar(L::bQFull + s), (uint32_t)((nq - 1 - s) / L::kStages) & 1u);
         if (s < nd) drain_wait(bar(L::bdOFull + s), (uint32_t)((nd - 1 - s) / L::kStages) & 1u);
@@ -299,7 +309,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       constexpr uint32_t idV = idesc_16<F16>(128, D, false, true);
       constexpr uint32_t idK = idesc_16<F16>(128, D, false, true);
       constexpr uint32_t idQ = idesc_16<F16>(128, D, true, true);
-      const uint32_t sdS = sbase + L::kdS;
+      const uint32_t dS0 = desc_lo(desc_mnmajor(sbase + L::kdS, 0));
       bool ok = true;
       int g = 0;
       // Shared-memory descriptors are built as a base plus a constant step per
@@ -312,10 +322,10 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         if (!bar_wait_warp(bar(L::bQFull + s1), (uint32_t)(g1 / L::kStages) & 1u, ctl, 364)) return false;
         if (tail != 0) zero_tail_rows<D>(smem + L::kQ + s1 * L::kTileBytes, tail);
         tc_fence_after();
-        const uint64_t dK0 = desc_kmajor(sK, 0), dQ0 = desc_kmajor(sbase + L::kQ + s1 * L::kTileBytes, 0);
+        const uint32_t dK0 = desc_lo(desc_kmajor(sK, 0)), dQ0 = desc_lo(desc_kmajor(sbase + L::kQ + s1 * L::kTileBytes, 0));
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-          mma_ss_w(tS, dK0 + kmajor_step(ks), dQ0 + kmajor_step(ks), idSP, ks > 0 ? 1u : 0u);
+          mma_ss_lo(tS, dK0 + (uint32_t)kmajor_step(ks), dQ0 + (uint32_t)kmajor_step(ks), idSP, ks > 0 ? 1u : 0u);
         mma_commit_w(bar(L::bSFull));
         return true;
       };
@@ -326,7 +336,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         const int tail = w.tail(), steps = p.G * (w.nT - w.i0);
         const int kb = k % L::kKV;
         const uint32_t sK = sbase + L::kK + kb * L::kKVBytes, sV = sbase + L::kV + kb * L::kKVBytes;
-        const uint64_t mK = desc_mnmajor(sK, 0);
+        const uint32_t mK = desc_lo(desc_mnmajor(sK, 0));
         if (!(ok = bar_wait_warp(bar(L::bKV + kb), (uint32_t)(k / L::kKV) & 1u, ctl, 360))) break;
         if (tail != 0 && w.kj == w.nT - 1) {
           zero_tail_rows<D>(smem + L::kK + kb * L::kKVBytes, tail);
@@ -346,20 +356,20 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           if (!(ok = bar_wait_warp(bar(L::bdOFull + s), (uint32_t)(g / L::kStages) & 1u, ctl, 366))) break;
           if (tail != 0 && i == w.nT - 1) zero_tail_rows<D>(smem + L::kdO + s * L::kTileBytes, tail);
           tc_fence_after();
-          const uint64_t kdV = desc_kmajor(sV, 0), kdO = desc_kmajor(sdO, 0);
+          const uint32_t kdV = desc_lo(desc_kmajor(sV, 0)), kdO = desc_lo(desc_kmajor(sdO, 0));
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
-            mma_ss_w(tP, kdV + kmajor_step(ks), kdO + kmajor_step(ks), idSP, ks > 0 ? 1u : 0u);
+            mma_ss_lo(tP, kdV + (uint32_t)kmajor_step(ks), kdO + (uint32_t)kmajor_step(ks), idSP, ks > 0 ? 1u : 0u);
           mma_commit_w(bar(L::bdPFull));
           // dV += P^T dO (at it == 0 over the previous item's dV and dK, which
           // the compute warps have read out of TMEM before arriving on this P)
           if (!(ok = bar_wait_warp(bar(L::bPFull), (uint32_t)g & 1u, ctl, 363))) break;
           tc_fence_after();
-          const uint64_t mdO = desc_mnmajor(sdO, 0);
+          const uint32_t mdO = desc_lo(desc_mnmajor(sdO, 0));
 #pragma unroll
           for (int ks = 0; ks < kTile / 16; ++ks)
             // P of each warpgroup's queries packed in the first half of its own S columns
-            mma_ts_w(tdV, tS + packed_col(ks), mdO + mnmajor_step(ks), idV,
+            mma_ts_lo(tdV, tS + packed_col(ks), mdO + (uint32_t)mnmajor_step(ks), idV,
                    (it > 0 || ks > 0) ? 1u : 0u);
           // next S^T of this item: early, right behind dV (the tensor pipe
           // runs in issue order, so dV has read P first), so that P of the
@@ -370,14 +380,14 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           // tDS on; at d = 128 each warpgroup hands over its first 32 queries
           // (K steps 0, 1 and 4, 5) before the rest (2, 3 and 6, 7), so half of
           // dK runs while dS is finished
-          const uint64_t mQ = desc_mnmajor(sQ, 0);
+          const uint32_t mQ = desc_lo(desc_mnmajor(sQ, 0));
           // dQ_i = dS K: with dS^T handed over in halves, dQ goes right after
           // dS is complete, in front of the second half of dK, so that its
           // drain overlaps that half
           auto issue_dq = [&]() {
 #pragma unroll
             for (int ks = 0; ks < kTile / 16; ++ks)
-              mma_ss_w(tQ, desc_mnmajor(sdS, ks), mK + mnmajor_step(ks), idQ, ks > 0 ? 1u : 0u);
+              mma_ss_lo(tQ, dS0 + (uint32_t)mnmajor_step(ks), mK + (uint32_t)mnmajor_step(ks), idQ, ks > 0 ? 1u : 0u);
             mma_commit_w(bar(L::bdQFull));
           };
 #pragma unroll
@@ -389,7 +399,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
 #pragma unroll
             for (int k4 = 0; k4 < (kSplitDS ? 4 : 8); ++k4) {
               const int ks = kSplitDS ? 2 * half + (k4 & 1) + 4 * (k4 >> 1) : k4;
-              mma_ts_w(tdK, tDS + packed_col(ks), mQ + mnmajor_step(ks), idK,
+              mma_ts_lo(tdK, tDS + packed_col(ks), mQ + (uint32_t)mnmajor_step(ks), idK,
                            (it > 0 || ks > 0) ? 1u : 0u);
             }
           }

@@ -125,7 +125,10 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   const uint32_t sbase = smem_u32(smem);
 
   const int tid = threadIdx.x;
-  const int warp = tid >> 5;
+  // (from a shuffle, so that the compiler knows it to be the same in all lanes:
+  // the operands of an MMA are uniform registers, and in a branch that it takes
+  // for divergent each MMA costs some 40 instructions more)
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const int lane = tid & 31;
 
   auto bar = [&](int i) -> uint32_t { return sbase + L::kBar + 8u * (uint32_t)i; };
@@ -174,10 +177,10 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     const int rs = k % L::kItemRing;
     w.c = -1;
     if (!bar_wait_warp(bar(L::bItemFull + rs), (uint32_t)(k / L::kItemRing) & 1u, ctl, 319)) return false;
-    w.start = ring[4 * rs];
-    w.len = ring[4 * rs + 1];
-    w.c = ring[4 * rs + 2];
-    w.head = ring[4 * rs + 3];
+    w.start = __shfl_sync(0xFFFFFFFFu, ring[4 * rs], 0);   // (the same in all lanes, as the compiler then knows)
+    w.len = __shfl_sync(0xFFFFFFFFu, ring[4 * rs + 1], 0);
+    w.c = __shfl_sync(0xFFFFFFFFu, ring[4 * rs + 2], 0);
+    w.head = __shfl_sync(0xFFFFFFFFu, ring[4 * rs + 3], 0);
     w.finish(p);
     mbar_arrive_warp(bar(L::bItemEmpty + rs));
     return true;
@@ -229,7 +232,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           if (!(ok = bar_wait_warp(bar(L::bClc), clc & 1u, ctl, 309))) break;
           clc_out = false;
           ++clc;
-          item = clc_first_ctaid_x(sbase + L::kClc);
+          item = __shfl_sync(0xFFFFFFFFu, clc_first_ctaid_x(sbase + L::kClc), 0);
         } while (item >= total);
         if (!ok) break;
         if (item < 0) item = total;
@@ -254,46 +257,44 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         mbar_arrive(bar(L::bItemFull + rs));   // (release: the ring entry is visible to the waiters)
       }
       if (w.c < 0) break;
-      if (lane == 0) {
-        const int hk = w.hq(0) / p.G;
-        // Q can only be loaded behind the last S of the item before: it is
-        // brought into L2 until then
-        if (k >= L::kQBuf)
+      const int hk = w.hq(0) / p.G;
+      // Q can only be loaded behind the last S of the item before: it is
+      // brought into L2 until then
+      if (k >= L::kQBuf)
 #pragma unroll 1
-          for (int t = 0; t < 2; ++t)
-            for (int a = 0; w.has(t) && a < L::kHalves; ++a)
-              tma_prefetch_3d(&tq, 64 * a, w.hq(t), w.start + kTile * w.qi(t));
+        for (int t = 0; t < 2; ++t)
+          for (int a = 0; w.has(t) && a < L::kHalves; ++a)
+            tma_prefetch_3d_w(&tq, 64 * a, w.hq(t), w.start + kTile * w.qi(t));
 #pragma unroll 1
-        for (int e = 0; e < w.n && ok; ++e) {
-          if (p.stall != 0u && e >= 1) { ok = false; break; }   // test of the timeout path: K of entry 1 never comes
-          // K of key tile e, once the MMAs of the entry that used the slot
-          // before (of this item or an earlier one) have read it
-          const int sk = nk % L::kStagesK;
-          if (nk >= L::kStagesK &&
-              !(ok = bar_wait(bar(L::bKEmpty + sk), (uint32_t)(nk / L::kStagesK - 1) & 1u, ctl, 311)))
-            break;
-          mbar_arrive_expect_tx(bar(L::bKFull + sk), L::kTileBytes);
-          for (int a = 0; a < L::kHalves; ++a)
-            tma_load_3d(sbase + L::kK + sk * L::kTileBytes + a * 16384, &tk, bar(L::bKFull + sk), 64 * a, hk,
+      for (int e = 0; e < w.n && ok; ++e) {
+        if (p.stall != 0u && e >= 1) { ok = false; break; }   // test of the timeout path: K of entry 1 never comes
+        // K of key tile e, once the MMAs of the entry that used the slot
+        // before (of this item or an earlier one) have read it
+        const int sk = nk % L::kStagesK;
+        if (nk >= L::kStagesK &&
+            !(ok = bar_wait_warp(bar(L::bKEmpty + sk), (uint32_t)(nk / L::kStagesK - 1) & 1u, ctl, 311)))
+          break;
+        mbar_arrive_expect_tx_w(bar(L::bKFull + sk), L::kTileBytes);
+        for (int a = 0; a < L::kHalves; ++a)
+          tma_load_3d_w(sbase + L::kK + sk * L::kTileBytes + a * 16384, &tk, bar(L::bKFull + sk), 64 * a, hk,
                         w.start + kTile * e);
-          ++nk;
-          // the item's Q tiles behind its first K, which seldom waits; a tile's
-          // buffer is free once the last S of the item before has read it
+        ++nk;
+        // the item's Q tiles behind its first K, which seldom waits; a tile's
+        // buffer is free once the last S of the item before has read it
 #pragma unroll 1
-          for (int t = 0; e == 0 && t < 2 && ok; ++t) {
-            if (!w.has(t)) continue;
-            const int nt = t ? nq1 : nq0, slot = t * L::kQBuf + nt % L::kQBuf;
-            if (nt >= L::kQBuf && !(ok = bar_wait(bar(L::bQEmpty + slot), (uint32_t)(nt / L::kQBuf - 1) & 1u, ctl, 310)))
-              break;
-            mbar_arrive_expect_tx(bar(L::bQFull + slot), L::kTileBytes);
-            for (int a = 0; a < L::kHalves; ++a)
-              tma_load_3d(sbase + L::kQ + slot * L::kTileBytes + a * 16384, &tq, bar(L::bQFull + slot), 64 * a, w.hq(t),
+        for (int t = 0; e == 0 && t < 2 && ok; ++t) {
+          if (!w.has(t)) continue;
+          const int nt = t ? nq1 : nq0, slot = t * L::kQBuf + nt % L::kQBuf;
+          if (nt >= L::kQBuf &&
+              !(ok = bar_wait_warp(bar(L::bQEmpty + slot), (uint32_t)(nt / L::kQBuf - 1) & 1u, ctl, 310)))
+            break;
+          mbar_arrive_expect_tx_w(bar(L::bQFull + slot), L::kTileBytes);
+          for (int a = 0; a < L::kHalves; ++a)
+            tma_load_3d_w(sbase + L::kQ + slot * L::kTileBytes + a * 16384, &tq, bar(L::bQFull + slot), 64 * a, w.hq(t),
                           w.start + kTile * w.qi(t));
-            (t ? nq1 : nq0) += 1;
-          }
+          (t ? nq1 : nq0) += 1;
         }
       }
-      ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
     }
     // every load and cancellation request issued has completed before the CTA
     // exits; loads were issued in ring order, so the last load into slot s was
@@ -318,22 +319,19 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     Pair w;
     bool ok = true;
     for (int k = 0; ok && take_item(k, w) && w.c >= 0; ++k) {
-      if (lane == 0) {
-        const int hk = w.hq(0) / p.G;
+      const int hk = w.hq(0) / p.G;
 #pragma unroll 1
-        for (int e = 0; e < w.n; ++e) {
-          const int sv = nv % L::kStagesV;
-          if (nv >= L::kStagesV &&
-              !(ok = bar_wait(bar(L::bVEmpty + sv), (uint32_t)(nv / L::kStagesV - 1) & 1u, ctl, 312)))
-            break;
-          mbar_arrive_expect_tx(bar(L::bVFull + sv), L::kTileBytes);
-          for (int a = 0; a < L::kHalves; ++a)
-            tma_load_3d(sbase + L::kV + sv * L::kTileBytes + a * 16384, &tv, bar(L::bVFull + sv), 64 * a, hk,
+      for (int e = 0; e < w.n; ++e) {
+        const int sv = nv % L::kStagesV;
+        if (nv >= L::kStagesV &&
+            !(ok = bar_wait_warp(bar(L::bVEmpty + sv), (uint32_t)(nv / L::kStagesV - 1) & 1u, ctl, 312)))
+          break;
+        mbar_arrive_expect_tx_w(bar(L::bVFull + sv), L::kTileBytes);
+        for (int a = 0; a < L::kHalves; ++a)
+          tma_load_3d_w(sbase + L::kV + sv * L::kTileBytes + a * 16384, &tv, bar(L::bVFull + sv), 64 * a, hk,
                         w.start + kTile * e);
-          ++nv;
-        }
+        ++nv;
       }
-      ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
     }
     if (lane == 0)
 #pragma unroll 1
@@ -358,10 +356,10 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     const uint32_t tO[2] = {tmem + 256u, tmem + 256u + (uint32_t)D};
     // P_t: over S_t, or in columns of its own (after O_1)
     const uint32_t tP[2] = {L::kOwnP ? tmem + 256u + 2u * D : tS[0], L::kOwnP ? tmem + 320u + 2u * D : tS[1]};
-    const uint64_t dQ0 = desc_kmajor(sbase + L::kQ, 0);
-    const uint64_t dK0 = desc_kmajor(sbase + L::kK, 0);
-    const uint64_t dV0 = desc_mnmajor(sbase + L::kV, 0);
-    constexpr uint64_t kSlotStep = (uint64_t)(L::kTileBytes >> 4);
+    const uint32_t dQ0 = desc_lo(desc_kmajor(sbase + L::kQ, 0));
+    const uint32_t dK0 = desc_lo(desc_kmajor(sbase + L::kK, 0));
+    const uint32_t dV0 = desc_lo(desc_mnmajor(sbase + L::kV, 0));
+    constexpr uint32_t kSlotStep = (uint32_t)(L::kTileBytes >> 4);
     int nk = 0, nv = 0;              // K and V ring entries of the entries before this one
     int nq[2] = {0, 0};              // items with query tile t so far
     uint32_t ns[2] = {0u, 0u}, npv[2] = {0u, 0u};   // S and PV groups issued per Q tile
@@ -407,10 +405,10 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           if (!k_ready && !bar_wait_warp(bar(L::bKFull + sk), (uint32_t)(nk / L::kStagesK) & 1u, ctl, 317)) return false;
           k_ready = true;
           tc_fence_after();
-          const uint64_t dQ = dQ0 + (uint64_t)q_slot(t) * kSlotStep, dK = dK0 + (uint64_t)sk * kSlotStep;
+          const uint32_t dQ = dQ0 + (uint32_t)q_slot(t) * kSlotStep, dK = dK0 + (uint32_t)sk * kSlotStep;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
-            mma_ss_w(tS[t], dQ + kmajor_step(ks), dK + kmajor_step(ks), idS, ks > 0 ? 1u : 0u);
+            mma_ss_lo(tS[t], dQ + (uint32_t)kmajor_step(ks), dK + (uint32_t)kmajor_step(ks), idS, ks > 0 ? 1u : 0u);
           mma_commit_w(bar(L::bSFull + t));
           if (e == last[t]) mma_commit_w(bar(L::bQEmpty + q_slot(t)));   // Q_t is no longer needed
           ++ns[t];
@@ -427,7 +425,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
             zeroed = v;
           }
           tc_fence_after();
-          const uint64_t dV = dV0 + (uint64_t)sv * kSlotStep;
+          const uint32_t dV = dV0 + (uint32_t)sv * kSlotStep;
           const uint32_t acc0 = pfirst[t] ? 0u : 1u;
 #pragma unroll
           for (int ks = 0; ks < kTile / 16; ++ks) {
@@ -435,7 +433,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
               if (!bar_wait_warp(bar(L::bPFull + t), npv[t] & 1u, ctl, 315)) return false;
               tc_fence_after();
             }
-            mma_ts_w(tO[t], tP[t] + (uint32_t)ks * 8u, dV + mnmajor_step(ks), idO, ks > 0 ? 1u : acc0);
+            mma_ts_lo(tO[t], tP[t] + (uint32_t)ks * 8u, dV + (uint32_t)mnmajor_step(ks), idO, ks > 0 ? 1u : acc0);
           }
           if constexpr (L::kOwnP) mma_commit_w(bar(L::bPVDone + t));   // P_t may be rewritten, O_t rescaled
           if (plast[t]) mma_commit_w(bar(L::bOFinal + t));             // O_t is complete
