@@ -400,34 +400,80 @@ def standard_attention_bwd(q, k, v, do, workspace, scale, stream=None, s16=False
 
 
 # ---------------------------------------------------------------------------
-# packed sequences with grouped heads
+# packed sequences with grouped heads, and serving from a paged cache
 # ---------------------------------------------------------------------------
+# These calls can take less time on the GPU than their checks take here, so the
+# helpers look at each tensor once and build nothing twice.
 
-def _rows16(t, name, tokens, heads, d, dtype, device):
+FA_CACHE_16BIT, FA_CACHE_E4M3 = 0, 1
+PACKED_DIRECT = 32           # a forward of so many sequences needs no workspace
+_I64x8, _I64x16 = ctypes.c_int64 * 8, ctypes.c_int64 * 16
+_opts = {}
+
+
+def _options(t, wait_limit_us, test_stall):
+    """(reference to) the fa_options for t's dtype and the checking fields."""
+    import torch
+    if t.dtype not in (torch.bfloat16, torch.float16) or not t.is_cuda:
+        raise ValueError("q (or k) must be a bfloat16 or float16 CUDA tensor")
+    key = (t.dtype, wait_limit_us, test_stall)
+    o = _opts.get(key)
+    if o is None:
+        o = fa_options(FA_DTYPE_F16 if t.dtype == torch.float16 else FA_DTYPE_BF16, wait_limit_us=wait_limit_us,
+                       test_stall=test_stall)
+        o = ctypes.byref(o)
+        if not (wait_limit_us or test_stall):
+            _opts[key] = o
+    return o
+
+
+def _elsewhere(stream, dev):
+    """None when a call launches on the current stream of the current device
+    (dev), else the context to allocate and launch in."""
+    import torch
+    if stream is None:
+        if dev == torch.cuda.current_device():
+            return None
+        return torch.cuda.stream(torch.cuda.current_stream(dev))
+    if stream.device.index != dev:
+        raise ValueError("the stream belongs to another device than the tensors")
+    return torch.cuda.stream(stream)     # (also makes its device the current one)
+
+
+def _current_stream(dev):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _rows16(t, name, shape, dtype, dev):
     """Checks a 16-bit tensor [tokens, heads, d] whose rows may be strided
     (views of a fused projection): d elements in one piece, token and head
     strides positive multiples of 8 elements. Returns the two strides."""
-    if t.shape != (tokens, heads, d) or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor {[tokens, heads, d]} on {device}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} tensor {list(shape)} on cuda:{dev}")
     tok, head, one = t.stride()
-    if tokens <= 1:
-        tok = heads * d        # (the stride of a single token, or of none, says nothing)
-    if heads == 1:
-        head = d
-    if (one != 1 and d > 1) or tok <= 0 or head <= 0 or tok % 8 or head % 8:
+    if shape[0] <= 1:
+        tok = shape[1] * shape[2]        # (the stride of a single token, or of none, says nothing)
+    if shape[1] == 1:
+        head = shape[2]
+    if one != 1 or tok <= 0 or head <= 0 or (tok | head) & 7:
         raise ValueError(f"{name}: rows must be contiguous, with token and head strides that are positive multiples of 8")
     return tok, head
 
 
-def _packed_args(q, k, v, cu_seqlens):
+def _plain(t, name, shape, dtype, dev):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{dev}")
+
+
+def _scratch(workspace, need, dev):
+    """The caller's workspace, or a new one: (tensor, bytes)."""
     import torch
-    dt = _dtype16(q, "q")
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q must be [tokens, Hq, d] and k, v [tokens, Hk, d]")
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or cu_seqlens.dtype != torch.int32 \
-            or cu_seqlens.device != q.device or not cu_seqlens.is_contiguous():
-        raise ValueError("cu_seqlens must be a contiguous int32 tensor [B + 1] on q's device")
-    return dt
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev), need
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on cuda:{dev}")
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def attention_packed_fwd(q, k, v, cu_seqlens, scale, causal=True, out=None, lse=None, workspace=None, stream=None,
@@ -439,24 +485,36 @@ def attention_packed_fwd(q, k, v, cu_seqlens, scale, causal=True, out=None, lse=
     cu_seqlens[b] .. cu_seqlens[b + 1] - 1. Returns O like q and LSE float32
     [Hq, tokens]; rows of no sequence are left as they are in `out` and `lse`."""
     import torch
-    opts = fa_options(_packed_args(q, k, v, cu_seqlens), wait_limit_us=wait_limit_us, test_stall=test_stall)
+    opts = _options(q, wait_limit_us, test_stall)
+    dev = q.get_device()
+    ctx = _elsewhere(stream, dev)
+    if ctx is not None:
+        with ctx:
+            return attention_packed_fwd(q, k, v, cu_seqlens, scale, causal, out, lse, workspace, None, wait_limit_us,
+                                        test_stall)
+    dt = q.dtype
+    if q.dim() != 3 or k.dim() != 3 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("q must be [tokens, Hq, d], k and v [tokens, Hk, d], cu_seqlens [B + 1]")
     T, Hq, d = q.shape
-    Hk, B, dev = k.shape[1], cu_seqlens.numel() - 1, q.device
-    stream, ctx = _on(stream, dev)
-    with ctx:
-        o = torch.empty((T, Hq, d), dtype=q.dtype, device=dev) if out is None else out
-        l = torch.empty((Hq, T), dtype=torch.float32, device=dev) if lse is None else lse
-        _like(l, "lse", (Hq, T), torch.float32, dev)
-        st = (ctypes.c_int64 * 8)(*_rows16(q, "q", T, Hq, d, q.dtype, dev), *_rows16(k, "k", T, Hk, d, q.dtype, dev),
-                                  *_rows16(v, "v", T, Hk, d, q.dtype, dev), *_rows16(o, "out", T, Hq, d, q.dtype, dev))
-        if workspace is None:
-            workspace = torch.empty(flash_attn_packed_workspace_size(B, T, Hq, Hk, d, 0), dtype=torch.uint8, device=dev)
-        _workspace_on(workspace, dev)
-        rc = flash_attn_packed_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(l), _ptr(cu_seqlens), B, T, Hq, Hk, d, st,
-                                   float(scale), int(bool(causal)), opts, _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _stream(stream))
+    Hk, B = k.shape[1], cu_seqlens.numel() - 1
+    _plain(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=dt, device=dev)
+    if lse is None:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+    else:
+        _plain(lse, "lse", (Hq, T), torch.float32, dev)
+    st = _I64x8(*_rows16(q, "q", (T, Hq, d), dt, dev), *_rows16(k, "k", (T, Hk, d), dt, dev),
+                *_rows16(v, "v", (T, Hk, d), dt, dev), *_rows16(out, "out", (T, Hq, d), dt, dev))
+    ws, nbytes = None, 0
+    if B > PACKED_DIRECT or workspace is not None:
+        workspace, nbytes = _scratch(workspace, flash_attn_packed_workspace_size(B, T, Hq, Hk, d, 0), dev)
+        ws = workspace.data_ptr()
+    rc = load().flash_attn_packed_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                      cu_seqlens.data_ptr(), B, T, Hq, Hk, d, st, scale, 1 if causal else 0, opts, ws,
+                                      nbytes, _current_stream(dev))
     _check(rc, "flash_attn_packed_fwd")
-    return o, l
+    return out, lse
 
 
 def attention_packed_bwd(q, k, v, o, do, lse, cu_seqlens, scale, causal=True, workspace=None, dq=None, dk=None, dv=None,
@@ -466,73 +524,57 @@ def attention_packed_bwd(q, k, v, o, do, lse, cu_seqlens, scale, causal=True, wo
     share a key/value head. Rows of no sequence are left as they are in dq, dk,
     dv (which may be strided like q, k, v)."""
     import torch
-    opts = fa_options(_packed_args(q, k, v, cu_seqlens), wait_limit_us=wait_limit_us, test_stall=test_stall)
+    opts = _options(q, wait_limit_us, test_stall)
+    dev = q.get_device()
+    ctx = _elsewhere(stream, dev)
+    if ctx is not None:
+        with ctx:
+            return attention_packed_bwd(q, k, v, o, do, lse, cu_seqlens, scale, causal, workspace, dq, dk, dv, None,
+                                        wait_limit_us, test_stall)
+    dt = q.dtype
+    if q.dim() != 3 or k.dim() != 3 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("q must be [tokens, Hq, d], k and v [tokens, Hk, d], cu_seqlens [B + 1]")
     T, Hq, d = q.shape
-    Hk, B, dev, dt = k.shape[1], cu_seqlens.numel() - 1, q.device, q.dtype
-    stream, ctx = _on(stream, dev)
-    with ctx:
-        dq = torch.empty((T, Hq, d), dtype=dt, device=dev) if dq is None else dq
-        dk = torch.empty((T, Hk, d), dtype=dt, device=dev) if dk is None else dk
-        dv = torch.empty((T, Hk, d), dtype=dt, device=dev) if dv is None else dv
-        _like(lse, "lse", (Hq, T), torch.float32, dev)
-        st = []
-        for t, name, h in ((q, "q", Hq), (k, "k", Hk), (v, "v", Hk), (o, "o", Hq), (do, "do", Hq), (dq, "dq", Hq),
-                           (dk, "dk", Hk), (dv, "dv", Hk)):
-            st += _rows16(t, name, T, h, d, dt, dev)
-        if workspace is None:
-            workspace = torch.empty(flash_attn_packed_workspace_size(B, T, Hq, Hk, d, 1), dtype=torch.uint8, device=dev)
-        _workspace_on(workspace, dev)
-        rc = flash_attn_packed_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
-                                   _ptr(cu_seqlens), B, T, Hq, Hk, d, (ctypes.c_int64 * 16)(*st), float(scale),
-                                   int(bool(causal)), opts, _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _stream(stream))
+    Hk, B = k.shape[1], cu_seqlens.numel() - 1
+    hq, hk = (T, Hq, d), (T, Hk, d)
+    _plain(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
+    _plain(lse, "lse", (Hq, T), torch.float32, dev)
+    if dq is None:
+        dq = torch.empty(hq, dtype=dt, device=dev)
+    if dk is None:
+        dk = torch.empty(hk, dtype=dt, device=dev)
+    if dv is None:
+        dv = torch.empty(hk, dtype=dt, device=dev)
+    st = _I64x16(*_rows16(q, "q", hq, dt, dev), *_rows16(k, "k", hk, dt, dev), *_rows16(v, "v", hk, dt, dev),
+                 *_rows16(o, "o", hq, dt, dev), *_rows16(do, "do", hq, dt, dev), *_rows16(dq, "dq", hq, dt, dev),
+                 *_rows16(dk, "dk", hk, dt, dev), *_rows16(dv, "dv", hk, dt, dev))
+    workspace, nbytes = _scratch(workspace, flash_attn_packed_workspace_size(B, T, Hq, Hk, d, 1), dev)
+    rc = load().flash_attn_packed_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+                                      lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                      cu_seqlens.data_ptr(), B, T, Hq, Hk, d, st, scale, 1 if causal else 0, opts,
+                                      workspace.data_ptr(), nbytes, _current_stream(dev))
     _check(rc, "flash_attn_packed_bwd")
     return dq, dk, dv
 
 
-# ---------------------------------------------------------------------------
-# serving from a paged key/value cache
-# ---------------------------------------------------------------------------
-
-FA_CACHE_16BIT, FA_CACHE_E4M3 = 0, 1
-
-
-def _cache_args(k_cache, v_cache, k_scale, v_scale, dtype, device):
+def _cache_args(k_cache, v_cache, k_scale, v_scale, dtype, dev):
     """Checks the tensors of a paged cache; returns the cache type."""
     import torch
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
-        raise ValueError("k_cache and v_cache must share one shape [num_pages, Hk, page_size, d] and one dtype")
-    e4m3 = k_cache.dtype == torch.float8_e4m3fn
-    if not e4m3 and k_cache.dtype != dtype:
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be [num_pages, Hk, page_size, d]")
+    shape, kind = k_cache.shape, k_cache.dtype
+    e4m3 = kind is torch.float8_e4m3fn
+    if not e4m3 and kind is not dtype:
         raise ValueError("the cache must hold the 16-bit type of the other tensors, or float8_e4m3fn")
-    for t in (k_cache, v_cache):
-        if t.device != device or not t.is_contiguous():
-            raise ValueError("k_cache and v_cache must be contiguous and on the device of the other tensors")
-    for t in (k_scale, v_scale):
-        if e4m3 != (t is not None):
-            raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache")
-        if e4m3 and (t.shape != k_cache.shape[:3] or t.dtype != torch.float32 or t.device != device
-                     or not t.is_contiguous()):
-            raise ValueError("k_scale and v_scale must be contiguous float32 [num_pages, Hk, page_size]")
-    return FA_CACHE_E4M3 if e4m3 else FA_CACHE_16BIT
-
-
-def _on(stream, device):
-    """The stream to launch on and the context to allocate and launch in."""
-    import contextlib
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-        if device.index == torch.cuda.current_device():
-            return stream, contextlib.nullcontext()
-    return stream, torch.cuda.stream(stream)   # (also makes the stream's device the current one)
-
-
-def _dtype16(t, name):
-    import torch
-    if not t.is_cuda or t.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"{name} must be a bfloat16 or float16 CUDA tensor")
-    return FA_DTYPE_F16 if t.dtype == torch.float16 else FA_DTYPE_BF16
+    _plain(k_cache, "k_cache", shape, kind, dev)
+    _plain(v_cache, "v_cache", shape, kind, dev)
+    if (k_scale is not None) != e4m3 or (v_scale is not None) != e4m3:
+        raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache")
+    if e4m3:
+        _plain(k_scale, "k_scale", shape[:3], torch.float32, dev)
+        _plain(v_scale, "v_scale", shape[:3], torch.float32, dev)
+        return FA_CACHE_E4M3
+    return FA_CACHE_16BIT
 
 
 def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, stream=None):
@@ -544,23 +586,25 @@ def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, st
     takes them quantised, with one power-of-two scale per row in k_scale,
     v_scale (float32 [num_pages, Hk, page_size])."""
     import torch
-    opts = fa_options(_dtype16(k, "k"))
-    if k.dim() != 3 or k_cache.dim() != 4:
-        raise ValueError("k must be [T, Hk, d] and k_cache [num_pages, Hk, page_size, d]")
-    T, Hk, d = k.shape
-    dev = k.device
-    k_st = _rows16(k, "k", T, k_cache.shape[1], k_cache.shape[3], k.dtype, dev)
-    v_st = _rows16(v, "v", T, Hk, d, k.dtype, dev)
-    if slots.shape != (T,) or slots.dtype != torch.int64 or slots.device != dev \
-            or not slots.is_contiguous():
-        raise ValueError("slots must be a contiguous int64 tensor with one entry per token of k and v")
-    kind = _cache_args(k_cache, v_cache, k_scale, v_scale, k.dtype, dev)
-    stream, ctx = _on(stream, dev)
-    with ctx:
-        st = flash_attn_kv_cache_write(_ptr(k), _ptr(v), *k_st, *v_st, _ptr(slots),
-                                       T, Hk, d, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                       k_cache.shape[0], k_cache.shape[2], kind, opts, _stream(stream))
-    _check(st, "flash_attn_kv_cache_write")
+    opts = _options(k, 0, 0)
+    dev = k.get_device()
+    ctx = _elsewhere(stream, dev)
+    if ctx is not None:
+        with ctx:
+            return kv_cache_write(k, v, slots, k_cache, v_cache, k_scale, v_scale)
+    dt = k.dtype
+    kind = _cache_args(k_cache, v_cache, k_scale, v_scale, dt, dev)
+    pages, Hk, page, d = k_cache.shape
+    T = k.shape[0] if k.dim() == 3 else -1
+    k_tok, k_head = _rows16(k, "k", (T, Hk, d), dt, dev)
+    v_tok, v_head = _rows16(v, "v", (T, Hk, d), dt, dev)
+    _plain(slots, "slots", (T,), torch.int64, dev)
+    e4m3 = kind == FA_CACHE_E4M3
+    rc = load().flash_attn_kv_cache_write(k.data_ptr(), v.data_ptr(), k_tok, k_head, v_tok, v_head, slots.data_ptr(), T,
+                                          Hk, d, k_cache.data_ptr(), v_cache.data_ptr(),
+                                          k_scale.data_ptr() if e4m3 else None, v_scale.data_ptr() if e4m3 else None,
+                                          pages, page, kind, opts, _current_stream(dev))
+    _check(rc, "flash_attn_kv_cache_write")
 
 
 def attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_scale=None, v_scale=None, out=None,
@@ -573,47 +617,39 @@ def attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_sc
     the Nq sees seq_lens - (Nq - 1 - i) keys; query head h reads key/value head
     h // (Hq // Hk). Returns O like q (contiguous) and LSE float32 [B, Hq, Nq]."""
     import torch
-    opts = fa_options(_dtype16(q, "q"), wait_limit_us=wait_limit_us, test_stall=test_stall)
-    if q.dim() != 4:
-        raise ValueError("q must be [B, Nq, Hq, d]")
-    B, Nq, Hq, d = q.shape
-    dev = q.device
-    kind = _cache_args(k_cache, v_cache, k_scale, v_scale, q.dtype, dev)
-    pages, Hk, page_size, dk = k_cache.shape
-    if dk != d:
-        raise ValueError("q and the cache must have one head dimension")
-    st = q.stride()
-    if st[3] != 1 or (Hq > 1 and st[2] != d) or (B > 1 and Nq > 1 and st[0] != Nq * st[1]):
+    opts = _options(q, wait_limit_us, test_stall)
+    dev = q.get_device()
+    ctx = _elsewhere(stream, dev)
+    if ctx is not None:
+        with ctx:
+            return attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale, out, lse,
+                                        workspace, None, wait_limit_us, test_stall)
+    dt = q.dtype
+    kind = _cache_args(k_cache, v_cache, k_scale, v_scale, dt, dev)
+    pages, Hk, page, d = k_cache.shape
+    if q.dim() != 4 or q.shape[3] != d or block_table.dim() != 2:
+        raise ValueError("q must be [B, Nq, Hq, d] with the cache's d, block_table [B, max_pages]")
+    B, Nq, Hq, _ = q.shape
+    s0, s1, s2, s3 = q.stride()
+    if s3 != 1 or (Hq > 1 and s2 != d) or (B > 1 and Nq > 1 and s0 != Nq * s1):
         raise ValueError("q: a token's heads must be contiguous and the tokens evenly spaced")
-    tok = st[1] if Nq > 1 else (st[0] if B > 1 else Hq * d)
-    if block_table.dim() != 2 or block_table.shape[0] != B or seq_lens.shape != (B,):
-        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
-    for t in (block_table, seq_lens):
-        if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous():
-            raise ValueError("block_table and seq_lens must be contiguous int32 tensors on q's device")
-    need = flash_attn_cached_workspace_size(B, Nq, Hq, Hk, d)
-    stream, ctx = _on(stream, dev)
-    with ctx:
-        o = torch.empty((B, Nq, Hq, d), dtype=q.dtype, device=dev) if out is None else out
-        l = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if lse is None else lse
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        _like(o, "out", (B, Nq, Hq, d), q.dtype, dev)
-        _like(l, "lse", (B, Hq, Nq), torch.float32, dev)
-        _workspace_on(workspace, dev)
-        st = flash_attn_cached_fwd(_ptr(q), tok, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                   _ptr(block_table), _ptr(seq_lens), _ptr(o), _ptr(l), B, Nq, Hq, Hk, d, pages, page_size,
-                                   block_table.shape[1], float(scale), kind, opts, _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "flash_attn_cached_fwd")
-    return o, l
-
-
-def _like(t, name, shape, dtype, device):
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
-
-
-def _workspace_on(t, device):
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"the workspace must be a contiguous tensor on {device}")
+    tok = s1 if Nq > 1 else (s0 if B > 1 else Hq * d)
+    _plain(block_table, "block_table", (B, block_table.shape[1]), torch.int32, dev)
+    _plain(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    if out is None:
+        out = torch.empty((B, Nq, Hq, d), dtype=dt, device=dev)
+    else:
+        _plain(out, "out", (B, Nq, Hq, d), dt, dev)
+    if lse is None:
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
+    else:
+        _plain(lse, "lse", (B, Hq, Nq), torch.float32, dev)
+    workspace, nbytes = _scratch(workspace, flash_attn_cached_workspace_size(B, Nq, Hq, Hk, d), dev)
+    e4m3 = kind == FA_CACHE_E4M3
+    rc = load().flash_attn_cached_fwd(q.data_ptr(), tok, k_cache.data_ptr(), v_cache.data_ptr(),
+                                      k_scale.data_ptr() if e4m3 else None, v_scale.data_ptr() if e4m3 else None,
+                                      block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Nq,
+                                      Hq, Hk, d, pages, page, block_table.shape[1], scale, kind, opts,
+                                      workspace.data_ptr(), nbytes, _current_stream(dev))
+    _check(rc, "flash_attn_cached_fwd")
+    return out, lse

@@ -206,7 +206,9 @@ fa_status flash_attn_packed_fwd(const void* Q, const void* K, const void* V, voi
     if (x == nullptr || !aligned(x, 16)) return FA_ERR_INVALID_ARG;
   if (LSE == nullptr || !aligned(LSE, 4) || cu_seqlens == nullptr || !aligned(cu_seqlens, 4)) return FA_ERR_INVALID_ARG;
   const PackedWorkspace w = packed_workspace_layout(B, total, Hq, Hk, d, false);
-  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < w.total) return FA_ERR_WORKSPACE;
+  if (!(B <= kDirect && workspace == nullptr) &&   // (up to kDirect sequences use none)
+      (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < w.total))
+    return FA_ERR_WORKSPACE;
   unsigned int* err = nullptr;
   const int e = internal_device_error_word(&err);
   if (e != FA_OK) return static_cast<fa_status>(e);
@@ -217,8 +219,10 @@ fa_status flash_attn_packed_fwd(const void* Q, const void* K, const void* V, voi
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   PackedFwdParams p{};
-  p.items = reinterpret_cast<PackedItem*>(ws + w.item_off);
-  p.plan = reinterpret_cast<PackedPlan*>(ws + w.plan_off);
+  if (B > kDirect) {
+    p.items = reinterpret_cast<PackedItem*>(ws + w.item_off);
+    p.plan = reinterpret_cast<PackedPlan*>(ws + w.plan_off);
+  }
   p.o = static_cast<uint16_t*>(O);
   p.o_tok = so.tok;
   p.o_head = so.head;

@@ -35,7 +35,8 @@
  *    be 0 and tile_record NULL (FA_ERR_UNSUPPORTED otherwise).
  *  - workspace: at least flash_attn_packed_workspace_size(...) bytes, 256-byte
  *    aligned; contents on entry do not matter. Calls whose kernels may overlap
- *    need workspaces of their own.
+ *    need workspaces of their own. A forward call of at most 32 sequences uses
+ *    none (workspace may be NULL).
  */
 #ifndef FLASH_ATTN_PACKED_H
 #define FLASH_ATTN_PACKED_H
