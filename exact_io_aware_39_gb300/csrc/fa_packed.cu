@@ -325,7 +325,10 @@ fa_status flash_attn_packed_bwd(const void* Q, const void* K, const void* V, con
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_us = o.wait_us;
   p.stall = o.stall;
-  if (launch_packed_plan(cu_seqlens, B, total, kTile, causal, true, p.plan, reinterpret_cast<int*>(ws + w.sorted_off),
+  p.cu = cu_seqlens;
+  p.B = B;
+  if (B > kDirect &&
+      launch_packed_plan(cu_seqlens, B, total, kTile, causal, true, p.plan, reinterpret_cast<int*>(ws + w.sorted_off),
                          reinterpret_cast<PackedItem*>(ws + w.item_off), w.cap_items,
                          reinterpret_cast<PackedItem*>(ws + w.tile_off), w.cap_tiles, err, s) != cudaSuccess)
     return FA_ERR_CUDA;

@@ -76,6 +76,9 @@ struct PackedFwdParams {
 };
 
 struct PackedBwdParams {
+  const int32_t* cu;          // [B + 1]
+  int B;
+  // B > kDirect:
   const PackedItem* items;    // (sequence, key tile)
   const PackedItem* tiles;    // every tile, in padded order
   PackedPlan* plan;
@@ -112,23 +115,40 @@ __device__ __forceinline__ void report_bounds(unsigned int* err, int b) {
 }
 
 // The work list of up to 32 sequences, held by a warp: lane b has sequence b
-// and its n units of `rows` rows. Units are listed as the plan kernel lists
+// and its n units of `rows` rows, slot0 the units of the sequences before it. A
+// sequence that would end past `cap` units in all (only bounds that overlap can
+// name so many) is left out. Units are listed as the plan kernel lists
 // them: causal, by the number c of units before them, descending, and for each
 // c the sequences that have one; not causal, sequence by sequence, the longest
 // first. All lanes call the members together.
 struct DirectList {
-  int start, len, n, items;
+  int start, len, n, slot0, items;
   int c, off;        // causal: items with more than c units before them, and how many
   int rank, first;   // not causal: place of this lane's sequence by length, and of its first unit
-  __device__ __forceinline__ void init(const int32_t* cu, int B, int total, int rows, bool causal, unsigned int* err) {
+  // the sequences alone (err may be null)
+  __device__ __forceinline__ void read(const int32_t* cu, int B, int total, int rows, int cap, unsigned int* err) {
     const int lane = threadIdx.x & 31;
     start = len = 0;
-    if (lane < B) {
-      bool bad;
-      len = seq_bounds(cu, lane, total, start, bad);
-      if (bad) report_bounds(err, lane);
-    }
+    bool bad = false;
+    if (lane < B) len = seq_bounds(cu, lane, total, start, bad);
     n = (len + rows - 1) / rows;
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    slot0 = upto - n;
+    if (upto > cap) {
+      bad = true;
+      len = n = 0;
+    }
+    if (bad && err != nullptr) report_bounds(err, lane);
+  }
+  __device__ __forceinline__ void init(const int32_t* cu, int B, int total, int rows, int cap, bool causal,
+                                       unsigned int* err) {
+    const int lane = threadIdx.x & 31;
+    read(cu, B, total, rows, cap, err);
     items = __reduce_add_sync(0xFFFFFFFFu, n);
     c = __reduce_max_sync(0xFFFFFFFFu, n) - 1;
     off = 0;
@@ -169,7 +189,19 @@ struct DirectList {
     }
     it.start = __shfl_sync(0xFFFFFFFFu, start, b);
     it.len = __shfl_sync(0xFFFFFFFFu, len, b);
-    it.slot0 = 0;
+    it.slot0 = __shfl_sync(0xFFFFFFFFu, slot0, b);
+    return it;
+  }
+  // the unit at place `slot` of the sequences' order; len 0 where there is none
+  __device__ __forceinline__ PackedItem unit(int slot) const {
+    const uint32_t mine = __ballot_sync(0xFFFFFFFFu, slot >= slot0 && slot < slot0 + n);
+    PackedItem it{0, 0, 0, 0};
+    if (mine == 0u) return it;
+    const int b = __ffs(mine) - 1;
+    it.start = __shfl_sync(0xFFFFFFFFu, start, b);
+    it.len = __shfl_sync(0xFFFFFFFFu, len, b);
+    it.slot0 = __shfl_sync(0xFFFFFFFFu, slot0, b);
+    it.c = slot - it.slot0;
     return it;
   }
 };

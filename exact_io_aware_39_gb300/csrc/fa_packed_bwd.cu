@@ -7,8 +7,8 @@
 //     over the G query heads of that head and their live query tiles, so dK and
 //     dV of a shared head are summed in TMEM, in a fixed order, and written
 //     once; nothing of them is added through memory;
-//   * items come from the list that the plan kernel makes on the device,
-//     heaviest first, through a counter;
+//   * items come from a list made on the device, heaviest first, as in the
+//     forward (fa_packed_fwd.cu);
 //   * tiles are boxes of the strided [token, head, d] tensors and may run into
 //     the next sequence: the MMA warp zeroes the rows past the end in shared
 //     memory (K and V once per item, Q and dO at a head's last query tile)
@@ -18,7 +18,7 @@
 //     to whole tiles, where the 128-row copies need no bounds; rows of dK, dV
 //     past a sequence's end are not stored.
 //
-// Launches (after the plan): the pre-pass (D = rowsum(dO * O), LSE * log2 e,
+// Launches (after the plan, for more than kDirect sequences): the pre-pass (D = rowsum(dO * O), LSE * log2 e,
 // zeroed accumulator), the main kernel, and dQ = 16-bit(scale * accumulator).
 #include "fa_packed.cuh"
 
@@ -73,10 +73,12 @@ struct PackedBwdLayout {
   static constexpr int bItemFull = bKVFree + kKV;            // [kItemRing]
   static constexpr int bItemEmpty = bItemFull + kItemRing;   // [kItemRing]: MMA warp, compute and drain warps
   static constexpr int bdSHalf = bItemEmpty + kItemRing;     // the first 32 dS^T columns of each warpgroup
-  static constexpr int kNumBars = bdSHalf + 1;
-  static constexpr int kMisc = kBar + 8 * kNumBars;   // tmem slot, abort flag, -, wait limit
+  static constexpr int bClc = bdSHalf + 1;                   // the next item's cancellation answer has arrived
+  static constexpr int kNumBars = bClc + 1;
+  static constexpr int kMisc = (kBar + 8 * kNumBars + 15) & ~15;   // tmem slot, abort flag, -, wait limit
   static constexpr int kRing = kMisc + 16;                    // [kItemRing] x {key tile, head, first row, length, first padded tile, -, -, -}
-  static constexpr int kSmemBytes = kRing + 32 * kItemRing;
+  static constexpr int kClc = kRing + 32 * kItemRing;   // 16-byte answer of a launch cancellation
+  static constexpr int kSmemBytes = kClc + 16;
   // the dQ partial is drained per warp (each warp adds its own 32 rows) at
   // d = 128 and by the four warps together (whole 128-row boxes) at d = 64:
   // measured, each is the faster one at its width
@@ -199,8 +201,6 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   // groups of p.group key/value heads (whose Q, dO and dQ accumulator fit in L2
   // together), within a group the list's order (heaviest first), and for each
   // entry the heads of the group.
-  const int n_items = p.plan->items;
-  const int total = n_items * p.Hk;
   const size_t Np = (size_t)p.cap_tiles * kTile;
   if (warp >= kProducerWarp) regs_dec<kOtherRegs>();
   if (warp == kProducerWarp) {
@@ -211,7 +211,21 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       tma_prefetch_map(&tv);
       tma_prefetch_map(&tdo);
     }
+    // up to kDirect sequences: the list is made here and items are taken by
+    // cancelling CTAs of the grid that have not started; else both are the plan's
+    const bool direct = p.B <= kDirect;
+    DirectList dl;
+    int n_items = 0;
+    if (direct) {
+      dl.init(p.cu, p.B, p.total, kTile, p.cap_tiles, p.causal != 0, p.err);
+      n_items = dl.items;
+    } else {
+      n_items = p.plan->items;
+    }
+    const int total = n_items * p.Hk;
     int nq = 0, nd = 0, nkv = 0;
+    bool clc_out = false;        // a cancellation answer is outstanding
+    uint32_t clc = 0u;           // answers received
     bool ok = true;
     int g = 0;
     for (int k = 0; ok; ++k) {
@@ -223,12 +237,36 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       Item w{-1, 0, 0, 0, 0, 0, 0};
       for (bool first = k == 0;; first = false) {
         int item = (int)blockIdx.x;
-        if (!first)
+        if (!first && !direct) {
           item = (int)gridDim.x + __shfl_sync(0xFFFFFFFFu, lane == 0 ? (int)atomicAdd(&p.plan->sched, 1u) : 0, 0);
+        } else if (!first) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(L::bClc), 16u);
+            clc_try_cancel(sbase + L::kClc, bar(L::bClc));
+          }
+          __syncwarp();
+          clc_out = true;
+          if (!(ok = bar_wait_warp(bar(L::bClc), clc & 1u, ctl, 356))) break;
+          clc_out = false;
+          ++clc;
+          item = __shfl_sync(0xFFFFFFFFu, clc_first_ctaid_x(sbase + L::kClc), 0);
+          if (item < 0) break;
+          if (item >= total) continue;   // past the list: cancelled too, until none is left
+        }
         if (item >= total) break;
-        const PackedItem pi = p.items[split_grouped(item, p.group, n_items, p.Hk, &w.hk)];
-        if (pi.len <= 0) continue;   // left out by the plan
+        int hk = 0;
+        const int idx = split_grouped(item, p.group, n_items, p.Hk, &hk);
+        PackedItem pi;
+        if (direct) {
+          pi = dl.at(idx, p.causal != 0);
+          // causal: key tile kj has nT - kj query tiles, the list's c is one less
+          if (p.causal) pi.c = (pi.len + kTile - 1) / kTile - 1 - pi.c;
+        } else {
+          pi = p.items[idx];
+          if (pi.len <= 0) continue;     // left out by the plan
+        }
         w.kj = __shfl_sync(0xFFFFFFFFu, pi.c, 0);
+        w.hk = hk;
         w.start = __shfl_sync(0xFFFFFFFFu, pi.start, 0);
         w.len = __shfl_sync(0xFFFFFFFFu, pi.len, 0);
         w.slot0 = __shfl_sync(0xFFFFFFFFu, pi.slot0, 0);
@@ -236,6 +274,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         w.i0 = p.causal ? w.kj : 0;
         break;
       }
+      if (!ok) break;
       if (lane == 0) {
         ring[8 * rs] = w.kj;
         ring[8 * rs + 1] = w.hk;
@@ -289,8 +328,9 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         }
       }
     }
-    // every load issued has landed before the CTA exits
+    // every load and cancellation request issued has completed before the CTA exits
     if (lane == 0) {
+      if (clc_out) drain_wait(bar(L::bClc), clc & 1u);
 #pragma unroll 1
       for (int kb = 0; kb < L::kKV && kb < nkv; ++kb)
         drain_wait(bar(L::bKV + kb), (uint32_t)((nkv - 1 - kb) / L::kKV) & 1u);
@@ -726,15 +766,26 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   }
 }
 
+// Padded tile `tile`; len 0 where there is none (whole warps call it together).
+__device__ __forceinline__ PackedItem padded_tile(const PackedBwdParams& p, int tile) {
+  if (p.B <= kDirect) {
+    DirectList dl;
+    dl.read(p.cu, p.B, p.total, kTile, p.cap_tiles, nullptr);
+    return dl.unit(tile);
+  }
+  return tile < p.plan->tiles ? p.tiles[tile] : PackedItem{0, 0, 0, 0};
+}
+
 // Per padded tile and query head: D = rowsum(dO * O) and LSE * log2(e) of its
 // rows (0 and +inf past the sequence), and the dQ accumulator's tile zeroed.
 // LANES neighbouring threads take a row, 8 columns each.
 template <int LANES, bool F16>
 __global__ void __launch_bounds__(256) packed_bwd_pre_kernel(const PackedBwdParams p) {
+  grid_dep_wait();   // O, dO and the LSE are complete
   grid_dep_launch();
   const int tile = (int)(blockIdx.x / (unsigned)p.Hq), h = (int)(blockIdx.x % (unsigned)p.Hq);
-  if (tile >= p.plan->tiles) return;
-  const PackedItem it = p.tiles[tile];
+  const PackedItem it = padded_tile(p, tile);
+  if (it.len == 0) return;
   const size_t row_off = ((size_t)h * p.cap_tiles + tile) * kTile;
   const int part = (int)threadIdx.x % LANES;
   const bool cols = 8 * part < p.d;
@@ -773,9 +824,10 @@ __global__ void __launch_bounds__(256) packed_bwd_pre_kernel(const PackedBwdPara
 template <bool F16>
 __global__ void __launch_bounds__(256) packed_bwd_dq_kernel(const PackedBwdParams p) {
   grid_dep_wait();   // every partial of the main kernel has been added
+  grid_dep_launch();
   const int tile = (int)(blockIdx.x / (unsigned)p.Hq), h = (int)(blockIdx.x % (unsigned)p.Hq);
-  if (tile >= p.plan->tiles) return;
-  const PackedItem it = p.tiles[tile];
+  const PackedItem it = padded_tile(p, tile);
+  if (it.len == 0) return;
   const size_t row_off = ((size_t)h * p.cap_tiles + tile) * kTile;
   const int parts = p.d / 8;
   const int rows = min(kTile, it.len - kTile * it.c);
@@ -815,14 +867,14 @@ cudaError_t launch_packed_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
   q.group = l2_head_group(8.0 * p.total * p.d * p.G, p.Hk);
   const dim3 tiles((unsigned)p.cap_tiles * (unsigned)p.Hq);
   // 16 lanes cover d <= 128, 8 cover d <= 64
-  e = launch_pdl(false, packed_bwd_pre_kernel<D / 8, F16>, tiles, dim3(256), 0, s, q);
+  e = launch_pdl(true, packed_bwd_pre_kernel<D / 8, F16>, tiles, dim3(256), 0, s, q);
   if (e != cudaSuccess) return e;
-  // persistent: at most one CTA per SM (the kernel holds all of TMEM)
+  // a CTA per item where items are taken by cancelling CTAs, else one per SM
   const long long most = (long long)p.cap_tiles * p.Hk;
-  e = launch_pdl(true, fa_packed_bwd_kernel<D, F16>, dim3((unsigned)(most < sms ? most : sms)), dim3(kBwdThreads),
-                 L::kSmemBytes, s, tq, tk, tv, tdo, tdk, tdv, tdq, q);
+  e = launch_pdl(true, fa_packed_bwd_kernel<D, F16>, dim3((unsigned)(p.B <= kDirect || most < sms ? most : sms)),
+                 dim3(kBwdThreads), L::kSmemBytes, s, tq, tk, tv, tdo, tdk, tdv, tdq, q);
   if (e != cudaSuccess) return e;
-  return launch_pdl(false, packed_bwd_dq_kernel<F16>, tiles, dim3(256), 0, s, q);
+  return launch_pdl(true, packed_bwd_dq_kernel<F16>, tiles, dim3(256), 0, s, q);
 }
 
 }  // namespace

@@ -200,7 +200,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     DirectList dl;
     int n_items = 0;
     if (direct) {
-      dl.init(p.cu, p.B, p.total, p.pair_heads ? kTile : 2 * kTile, p.causal != 0, p.err);
+      dl.init(p.cu, p.B, p.total, p.pair_heads ? kTile : 2 * kTile, p.cap_items, p.causal != 0, p.err);
       n_items = dl.items;
     } else {
       n_items = p.plan->items;
