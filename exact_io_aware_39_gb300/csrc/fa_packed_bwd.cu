@@ -807,7 +807,8 @@ __global__ void __launch_bounds__(256) packed_bwd_pre_kernel(const PackedBwdPara
     }
 #pragma unroll
     for (int off = LANES / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, off);
-    if (cols) {
+    // (rows past the sequence are added to as well, and never read)
+    if (n < it.len && cols) {
       float4* z = reinterpret_cast<float4*>(p.dq_acc + (row_off + r) * p.d + 8 * part);
       z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
       z[1] = make_float4(0.f, 0.f, 0.f, 0.f);

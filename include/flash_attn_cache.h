@@ -56,7 +56,7 @@ typedef enum { FA_CACHE_16BIT = 0, FA_CACHE_E4M3 = 1 } fa_cache_type;
  * The division is exact, so each element is rounded once: to within 2^-4 of
  * itself, or 2^-10 scale for elements below 2^-6 scale. The maximum is taken
  * over the finite elements; infinities and NaN are stored as NaN.
- *   T >= 0 (0 writes nothing); Hk >= 1; num_pages >= 1.
+ *   T >= 0 (0 writes nothing), T Hk <= 2^26; 1 <= Hk <= 1024; num_pages >= 1.
  */
 fa_status flash_attn_kv_cache_write(const void* K, const void* V, int64_t k_token_stride, int64_t k_head_stride,
                                     int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,

@@ -30,7 +30,7 @@ def _write(L, K=P, V=P, kt=1024, kh=128, vt=1024, vh=128, slots=P, T=4, Hk=8, d=
     (dict(kt=1028), 1), (dict(vh=4), 1), (dict(d=0), 2), (dict(d=60), 2), (dict(d=136), 2), (dict(page=8), 2),
     (dict(page=48), 2), (dict(page=512), 2), (dict(kind=2), 2), (dict(ks=P, vs=P), 1),
     (dict(kind=1), 1), (dict(kind=1, ks=P), 1), (dict(kind=1, ks=P, vs=ODD), 1), (dict(kind=1, ks=P, vs=P, d=72), 2),
-    (dict(T=1 << 24, Hk=8), 2),
+    (dict(T=1 << 24, Hk=8), 2), (dict(Hk=1025), 2),
 ])
 def test_write_refusals(L, kw, want):
     assert _write(L, **kw) == want
