@@ -35,6 +35,7 @@
 #include "flash_attn_cache.h"
 #include "fa_common.cuh"
 #include "fa_ptx.cuh"
+#include "fa_warp.cuh"
 
 #include <cmath>
 
@@ -290,10 +291,12 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
+__device__ __forceinline__ void tma_load_2d_w(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];"
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];\n\t}"
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1) : "memory");
 }
 
@@ -311,7 +314,10 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
   constexpr int KT = L::kKT;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (what is the same in all lanes of a warp comes from a shuffle, so that the
+  // compiler knows it: the copies' operands are uniform registers)
+  auto same = [](int v) -> int { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+  const int tid = threadIdx.x, warp = same(tid >> 5), lane = tid & 31;
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile uint32_t* abort_flag = misc;
   Ctl ctl{p.err, abort_flag};
@@ -388,15 +394,16 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     grid_dep_launch();
     return;
   }
-  const long long t0 = range_start(me), t1 = range_start(me + 1);
+  const long long t0 = range_start(me);
+  const int todo = same((int)(range_start(me + 1) - t0));
   Walk w0;
-  w0.b = start_b[warp];
-  w0.len = seq_len(w0.b);
+  w0.b = same(start_b[warp]);
+  w0.len = same(seq_len(w0.b));
   w0.n = tiles_of(w0.len);
   {
     const long long rem = t0 - start_cum[warp] * SUB;
-    w0.sub = (int)(rem / w0.n);
-    w0.j = (int)(rem % w0.n);
+    w0.sub = same((int)(rem / w0.n));
+    w0.j = same((int)(rem % w0.n));
   }
   grid_dep_launch();   // the joining kernel may be scheduled (it waits for this one's end)
   auto advance = [&](Walk& w) {
@@ -405,52 +412,62 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     if (++w.sub < SUB) return;
     w.sub = 0;
     if (++w.b < p.B) {
-      w.len = seq_len(w.b);
+      w.len = same(seq_len(w.b));
       w.n = tiles_of(w.len);
     }
   };
 
-  // ---- loads (lane 0): piece i of a tile is one page's share of it
+  // ---- loads (warp-wide): piece i of a tile is one page's share of it. The page
+  // numbers of a tile are read when the tile before it is issued.
   const uint32_t ring = sbase + (uint32_t)(warp * L::kWarpBytes);
   const uint32_t sring = sbase + L::kScale + (uint32_t)(warp * L::kStages * 2 * L::kScaleBytes);
   const int box = p.page_size < KT ? p.page_size : KT;     // keys of a piece
-  const int pieces = KT / box;
+  const int pieces = KT / box;                             // 1 or 2
   const int nowhere = p.num_pages * p.Hk;                  // a coordinate past the cache: reads as zeros
   int issued = 0;
-  auto issue = [&](const Walk& w) {
+  // page of lane i's piece of the tile (lanes 0 and 1), or -1
+  auto page_of = [&](const Walk& w) -> int {
+    const int key = w.j * KT + (lane & 1) * box;
+    return w.b < p.B && key < w.len ? p.table[(int64_t)w.b * p.max_pages + (key >> p.ps_log2)] : -1;
+  };
+  auto issue = [&](const Walk& w, int pages) {
     const int s = issued % L::kStages;
     ++issued;
-    if (lane != 0) return;
     const int hk = w.sub / p.RT;
-    mbar_arrive_expect_tx(bar(s), L::kTxBytes);
+    mbar_arrive_expect_tx_w(bar(s), L::kTxBytes);
+#pragma unroll 1
     for (int i = 0; i < pieces; ++i) {
-      const int key = w.j * KT + i * box;
-      int z = nowhere;
-      if (key < w.len) {
-        const int page = p.table[(int64_t)w.b * p.max_pages + (key >> p.ps_log2)];
-        if (page >= 0 && page < p.num_pages) z = page * p.Hk + hk;
-      }
-      const int y = key & (p.page_size - 1);
+      const int page = __shfl_sync(0xFFFFFFFFu, pages, i);
+      const int z = page >= 0 && page < p.num_pages ? page * p.Hk + hk : nowhere;
+      const int y = (w.j * KT + i * box) & (p.page_size - 1);
       const uint32_t dst = ring + (uint32_t)(s * L::kStageBytes + i * box * L::kRowBytes);
 #pragma unroll
-      for (int a = 0; a < L::kAtoms; ++a) tma_load_3d(dst + a * L::kAtomBytes, &tk, bar(s), 64 * a, y, z);
+      for (int a = 0; a < L::kAtoms; ++a) tma_load_3d_w(dst + a * L::kAtomBytes, &tk, bar(s), 64 * a, y, z);
 #pragma unroll
       for (int a = 0; a < L::kAtoms; ++a)
-        tma_load_3d(dst + L::kTileBytes + a * L::kAtomBytes, &tv, bar(s), 64 * a, y, z);
+        tma_load_3d_w(dst + L::kTileBytes + a * L::kAtomBytes, &tv, bar(s), 64 * a, y, z);
       if constexpr (E4M3) {
         const uint32_t sd = sring + (uint32_t)(s * 2 * L::kScaleBytes + i * 128);
-        tma_load_2d(sd, &tks, bar(s), y, z);
-        tma_load_2d(sd + L::kScaleBytes, &tvs, bar(s), y, z);
+        tma_load_2d_w(sd, &tks, bar(s), y, z);
+        tma_load_2d_w(sd + L::kScaleBytes, &tvs, bar(s), y, z);
       }
     }
   };
 
-  const long long todo = t1 - t0;
   Walk wi = w0;
+  int pages = page_of(wi);
+  // the next tile of the range, and the pages of the one after it
+  auto issue_next = [&]() {
+    const Walk w = wi;
+    const int pg = pages;
+    advance(wi);
+    pages = page_of(wi);
+    issue(w, pg);
+  };
+#pragma unroll 1
   for (int s = 0; s < L::kStages && s < todo; ++s) {
     if (p.stall != 0u && s >= 1) break;   // test of the timeout path: tile 1 never comes
-    issue(wi);
-    advance(wi);
+    issue_next();
   }
 
   // ---- the tiles of the range
@@ -463,7 +480,8 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
   bool fresh = true;              // the next tile starts a (sequence, head, row tile) for this warp
   bool from_start = false;        // ... and is its first
   bool ok = true;
-  for (long long u = 0; u < todo; ++u) {
+#pragma unroll 1
+  for (int u = 0; u < todo; ++u) {
     const int hk = w.sub / p.RT, rt = w.sub % p.RT;
     if (fresh) {
       fresh = false;
@@ -525,8 +543,8 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
           }
       }
     }
-    const int s = (int)(u % L::kStages);
-    ok = mbar_wait_warp(bar(s), (uint32_t)(u / L::kStages) & 1u, ctl, 201);
+    const int s = u % L::kStages;
+    ok = bar_wait_warp(bar(s), (uint32_t)(u / L::kStages) & 1u, ctl, 201);
     if (!ok) break;
     const uint32_t sk = ring + (uint32_t)(s * L::kStageBytes), sv = sk + L::kTileBytes;
     const int left = w.len - w.j * KT;      // keys of the sequence from this tile on
@@ -553,6 +571,11 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 #pragma unroll
       for (int i = 0; i < 4; ++i) sc[n][i] = 0.f;
     if constexpr (!E4M3) {
+      float sd[KT / 8][4];   // odd steps' sums: twice as many independent products
+#pragma unroll
+      for (int n = 0; n < KT / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sd[n][i] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
@@ -562,9 +585,13 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
           const int row = 16 * kk + (lane & 7) + 8 * (lane >> 4);
           const int chunk = 2 * (ks & 3) + ((lane >> 3) & 1);
           ldsm4(b, sk + (uint32_t)((ks >> 2) * L::kAtomBytes) + swz<L::kRowBytes>(row, chunk));
-          mma16<F16>(sc[2 * kk], qf[ks], b[0], b[1]);
-          mma16<F16>(sc[2 * kk + 1], qf[ks], b[2], b[3]);
+          mma16<F16>((ks & 1) ? sd[2 * kk] : sc[2 * kk], qf[ks], b[0], b[1]);
+          mma16<F16>((ks & 1) ? sd[2 * kk + 1] : sc[2 * kk + 1], qf[ks], b[2], b[3]);
         }
+#pragma unroll
+      for (int n = 0; n < KT / 8; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[n][i] += sd[n][i];
     } else {
 #pragma unroll
       for (int c4 = 0; c4 < kSteps / 4; ++c4)
@@ -683,10 +710,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
       }
     }
     __syncwarp();   // every lane has read the tile: its place may be loaded again
-    if (issued < todo && p.stall == 0u) {
-      issue(wi);
-      advance(wi);
-    }
+    if (issued < todo && p.stall == 0u) issue_next();
 
     if (w.j == w.n - 1 || u == todo - 1) {
       // the end of a (sequence, head, row tile), or of what this warp has of it
@@ -751,6 +775,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     advance(w);
   }
   // every load issued has landed before the warp leaves (after a timeout)
+  if (!ok && lane == 0) report_aborted(ctl);
   if (!ok && lane == 0)
     for (int s = 0; s < L::kStages && s < issued; ++s)
       drain_wait(bar(s), (uint32_t)((issued - 1 - s) / L::kStages) & 1u);
