@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(256) kv_cache_write_kernel(const WriteParams p
   const bool cols = kE * part < p.d;
   uint4 x[U][kW];
   int64_t place[U];   // row of the cache, or -1
+  grid_dep_wait();
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const uint32_t row = row0 + (uint32_t)u * kGroups;
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(256) kv_cache_write_kernel(const WriteParams p
 template <int LANES, int U, bool E4M3, bool F16>
 cudaError_t launch_write_u(const WriteParams& p, cudaStream_t s) {
   const uint32_t per = 256 / LANES * U;
-  return launch_pdl(false, kv_cache_write_kernel<LANES, U, E4M3, F16>, dim3((p.rows + per - 1) / per, 2), dim3(256), 0, s, p);
+  return launch_pdl(true, kv_cache_write_kernel<LANES, U, E4M3, F16>, dim3((p.rows + per - 1) / per, 2), dim3(256), 0, s, p);
 }
 
 template <bool E4M3, bool F16>
@@ -337,6 +338,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     misc[2] = p.wait_us;
   }
   fence_mbar_init();
+  grid_dep_wait();   // global memory is read and written only from here on
 
   // ---- this warp's range of units
   const int SUB = p.Hk * p.RT;
@@ -781,19 +783,28 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
       drain_wait(bar(s), (uint32_t)((issued - 1 - s) / L::kStages) & 1u);
 }
 
-// Joins the parts of a (sequence, head, row tile): one block of 4 warps per
-// query row, the parts shared out over the warps, a lane holding D / 32
-// columns. m is the row's reference, l its sum:
+// Joins the parts of a query row. m is a part's reference, l its sum:
 //   O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k,  M = max m_k.
-template <int D, bool F16>
-__global__ void __launch_bounds__(128) fa_cached_join_kernel(const CachedParams p) {
+// WARPS warps share a row's parts out (a lane holds D / 32 columns); with
+// WARPS = 1 a block of four warps joins four rows. The rows of one launch have
+// about as many parts each as there are workers to a (sequence, head, row tile);
+// from kManyParts on 16 warps take a row, so that no warp walks a long list (one
+// sequence of 32768 tokens, 152 parts a row: the call takes 33.7 us so, 40.2 with
+// four warps), and below it one (256 sequences of 20-200 tokens: 33.0 us, against
+// 37.4 with a block of four warps for every row).
+constexpr int kManyParts = 8;
+
+template <int D, bool F16, int WARPS>
+__global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) fa_cached_join_kernel(const CachedParams p) {
   constexpr int C = D / 32;
-  __shared__ float sm_o[4][D];
-  __shared__ float sm_ml[4][2];
+  __shared__ float sm_o[WARPS == 1 ? 1 : WARPS][D];
+  __shared__ float2 sm_ml[WARPS];
   grid_dep_wait();   // the parts are complete
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+  const unsigned row = WARPS == 1 ? blockIdx.x * 4u + (unsigned)warp : blockIdx.x;   // over [B][Hq][Nq]
   const int per_b = p.Hq * p.Nq;
-  const int b = (int)(blockIdx.x / (unsigned)per_b), x = (int)(blockIdx.x % (unsigned)per_b);
+  if (row >= (unsigned)(p.B * per_b)) return;
+  const int b = (int)(row / (unsigned)per_b), x = (int)(row % (unsigned)per_b);
   const int h = x / p.Nq, i = x % p.Nq;
   const int hk = h / p.G, r = i * p.G + h % p.G;
   const int2 f = p.info[((int64_t)b * p.Hk + hk) * p.RT + r / kRows];
@@ -801,43 +812,72 @@ __global__ void __launch_bounds__(128) fa_cached_join_kernel(const CachedParams 
   if (f.x < 0 || f.y <= f.x || f.y >= kMaxWorkers) return;
   const int rr = r % kRows, parts = f.y - f.x + 1;
   auto at = [&](int k) -> int64_t { return (int64_t)(2 * (f.x + k) + (k == 0 ? 1 : 0)) * kRows + rr; };
-  float mx = -INFINITY;
-  for (int k = lane; k < parts; k += 32) mx = fmaxf(mx, p.part_ml[at(k)].x);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-  const float ref = mx == -INFINITY ? 0.f : mx;
-  float acc[C];
+  // this warp's parts k0, k0 + step, ..., a lane looking after the weight of one
+  // of 32 of them, four parts' columns on their way at a time
+  const int k0 = WARPS == 1 ? 0 : warp, step = WARPS;
+  const int mine = k0 < parts ? (parts - k0 + step - 1) / step : 0;
+  float M = -INFINITY, l = 0.f, acc[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) acc[c] = 0.f;
-  float l = 0.f;
-#pragma unroll 4
-  for (int k = warp; k < parts; k += 4) {
-    const float2 ml = p.part_ml[at(k)];
-    const float f2 = ex2(ml.x - ref);
-    l = fmaf(f2, ml.y, l);
-    const float* po = p.part_o + at(k) * D + C * lane;
+  for (int base = 0; base < mine; base += 32) {
+    const int n = min(32, mine - base);
+    const float2 ml = lane < n ? p.part_ml[at(k0 + step * (base + lane))] : make_float2(-INFINITY, 0.f);
+    float mx = ml.x;
 #pragma unroll
-    for (int c = 0; c < C; c += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(po + c);
-      acc[c] = fmaf(f2, v.x, acc[c]);
-      acc[c + 1] = fmaf(f2, v.y, acc[c + 1]);
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
+    const float Mn = fmaxf(M, mx), ref = Mn == -INFINITY ? 0.f : Mn;
+    const float old = ex2(M - ref), wt = ex2(ml.x - ref);
+    M = Mn;
+    float ls = wt * ml.y;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, off);
+    l = fmaf(l, old, ls);
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] *= old;
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float* po = p.part_o + at(k0 + step * (base + k)) * D + C * lane;
+      const float w = __shfl_sync(0xFFFFFFFFu, wt, k);
+#pragma unroll
+      for (int c = 0; c < C; c += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(po + c);
+        acc[c] = fmaf(w, v.x, acc[c]);
+        acc[c + 1] = fmaf(w, v.y, acc[c + 1]);
+      }
     }
   }
-#pragma unroll
-  for (int c = 0; c < C; ++c) sm_o[warp][C * lane + c] = acc[c];
-  if (lane == 0) sm_ml[warp][0] = l;
-  __syncthreads();
-  l = (sm_ml[0][0] + sm_ml[1][0]) + (sm_ml[2][0] + sm_ml[3][0]);
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
   uint16_t* op = p.o + (((int64_t)b * p.Nq + i) * p.Hq + h) * p.d;
-  if (2 * tid < p.d) {
-    const int c = 2 * tid;
-    const float a0 = (sm_o[0][c] + sm_o[1][c]) + (sm_o[2][c] + sm_o[3][c]);
-    const float a1 = (sm_o[0][c + 1] + sm_o[1][c + 1]) + (sm_o[2][c + 1] + sm_o[3][c + 1]);
-    *reinterpret_cast<uint32_t*>(op + c) = pack2<F16>(a0 * inv, a1 * inv);
+  float* lp = p.lse + ((int64_t)b * p.Hq + h) * p.Nq + i;
+  if constexpr (WARPS > 1) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) sm_o[warp][C * lane + c] = acc[c];
+    if (lane == 0) sm_ml[warp] = make_float2(M, l);
+    __syncthreads();
+    if (warp > 0) return;
+    float2 ml = lane < WARPS ? sm_ml[lane] : make_float2(-INFINITY, 0.f);
+    M = ml.x;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+    const float wt = ex2(ml.x - (M == -INFINITY ? 0.f : M));
+    l = wt * ml.y;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, off);
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = 0.f;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) {
+      const float w = __shfl_sync(0xFFFFFFFFu, wt, k);
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] = fmaf(w, sm_o[k][C * lane + c], acc[c]);
+    }
   }
-  if (tid == 0)
-    p.lse[((int64_t)b * p.Hq + h) * p.Nq + i] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  if (C * lane < p.d) {
+#pragma unroll
+    for (int c = 0; c < C; c += 2)
+      *reinterpret_cast<uint32_t*>(op + C * lane + c) = pack2<F16>(acc[c] * inv, acc[c + 1] * inv);
+  }
+  if (lane == 0) *lp = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
 }
 
 struct CachedWorkspace {
@@ -892,10 +932,13 @@ cudaError_t launch_cached_d(const CUtensorMap& tk, const CUtensorMap& tv, const 
   const double most = (double)p.B * p.Hk * p.RT * (((double)p.max_pages * p.page_size + L::kKT - 1) / L::kKT);
   int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   if (most < ctas) ctas = most < 1.0 ? 1 : (int)most;
-  e = launch_pdl(false, fa_cached_kernel<D, E4M3, F16>, dim3((unsigned)ctas), dim3(32 * kWarps), L::kSmemBytes, s, tk, tv,
+  e = launch_pdl(true, fa_cached_kernel<D, E4M3, F16>, dim3((unsigned)ctas), dim3(32 * kWarps), L::kSmemBytes, s, tk, tv,
                  tks, tvs, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(true, fa_cached_join_kernel<D, F16>, dim3((unsigned)(p.B * p.Hq * p.Nq)), dim3(128), 0, s, p);
+  const unsigned rows = (unsigned)(p.B * p.Hq * p.Nq);
+  if ((long long)p.B * p.Hk * p.RT * kManyParts <= (long long)kWarps * ctas)
+    return launch_pdl(true, fa_cached_join_kernel<D, F16, 16>, dim3(rows), dim3(512), 0, s, p);
+  return launch_pdl(true, fa_cached_join_kernel<D, F16, 1>, dim3((rows + 3) / 4), dim3(128), 0, s, p);
 }
 
 }  // namespace
