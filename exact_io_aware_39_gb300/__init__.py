@@ -13,7 +13,7 @@ raises if it is missing.
 from ._lib import (FlashAttnError, attention_bwd, attention_cached_fwd, attention_fwd,
                    attention_packed_bwd, attention_packed_fwd, device_error, fa_options,
                    flash_attn_bwd, flash_attn_bwd_ex, flash_attn_bwd_noalloc, flash_attn_fwd_ex, flash_attn_bwd_workspace_size, flash_attn_cached_fwd,
-                   flash_attn_cached_workspace_size, flash_attn_fwd, flash_attn_kv_cache_write,
+                   flash_attn_cached_needs_workspace, flash_attn_cached_workspace_size, flash_attn_fwd, flash_attn_kv_cache_write,
                    flash_attn_get_device_error, flash_attn_packed_bwd, flash_attn_packed_fwd,
                    flash_attn_packed_workspace_size, flash_attn_set_profile_events,
                    flash_attn_status_string, flash_attn_tile_map, flash_attn_version, kv_cache_write, load,
@@ -24,7 +24,8 @@ __all__ = [
     "FlashAttnError", "attention_bwd", "attention_cached_fwd", "attention_fwd",
     "attention_packed_bwd", "attention_packed_fwd", "device_error", "fa_options", "flash_attn_bwd",
     "flash_attn_bwd_ex", "flash_attn_bwd_noalloc", "flash_attn_fwd_ex",
-    "flash_attn_bwd_workspace_size", "flash_attn_cached_fwd", "flash_attn_cached_workspace_size", "flash_attn_fwd",
+    "flash_attn_bwd_workspace_size", "flash_attn_cached_fwd", "flash_attn_cached_needs_workspace",
+    "flash_attn_cached_workspace_size", "flash_attn_fwd",
     "flash_attn_kv_cache_write", "flash_attn_packed_bwd", "flash_attn_packed_fwd", "flash_attn_packed_workspace_size",
     "flash_attn_get_device_error",
     "flash_attn_set_profile_events", "flash_attn_status_string", "flash_attn_tile_map",

@@ -31,7 +31,8 @@ EXPORTS = [
     "flash_attn_get_device_error", "flash_attn_set_profile_events", "flash_attn_status_string",
     "flash_attn_version",
     "flash_attn_packed_workspace_size", "flash_attn_packed_fwd", "flash_attn_packed_bwd",
-    "flash_attn_kv_cache_write", "flash_attn_cached_workspace_size", "flash_attn_cached_fwd",
+    "flash_attn_kv_cache_write", "flash_attn_cached_workspace_size", "flash_attn_cached_needs_workspace",
+    "flash_attn_cached_fwd",
     "standard_attn_workspace_size", "standard_attn_fwd", "standard_attn_bwd",
 ]
 
@@ -105,6 +106,8 @@ def load(path=LIB_PATH):
     lib.flash_attn_kv_cache_write.restype = i32
     lib.flash_attn_cached_workspace_size.argtypes = [i32] * 5
     lib.flash_attn_cached_workspace_size.restype = sz
+    lib.flash_attn_cached_needs_workspace.argtypes = [i32] * 8
+    lib.flash_attn_cached_needs_workspace.restype = i32
     lib.flash_attn_cached_fwd.argtypes = [vp, i64] + [vp] * 8 + [i32] * 8 + [f32, i32, opt_p, vp, sz, vp]
     lib.flash_attn_cached_fwd.restype = i32
     lib.standard_attn_workspace_size.argtypes = [i32, i32, i32]
@@ -204,6 +207,10 @@ def flash_attn_kv_cache_write(K, V, k_token_stride, k_head_stride, v_token_strid
 
 def flash_attn_cached_workspace_size(B, Nq, Hq, Hk, d):
     return load().flash_attn_cached_workspace_size(B, Nq, Hq, Hk, d)
+
+
+def flash_attn_cached_needs_workspace(B, Nq, Hq, Hk, d, page_size, max_pages, cache_type):
+    return load().flash_attn_cached_needs_workspace(B, Nq, Hq, Hk, d, page_size, max_pages, cache_type)
 
 
 def flash_attn_cached_fwd(Q, q_token_stride, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, O, LSE, B, Nq,
@@ -644,12 +651,15 @@ def attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_sc
         lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
     else:
         _plain(lse, "lse", (B, Hq, Nq), torch.float32, dev)
-    workspace, nbytes = _scratch(workspace, flash_attn_cached_workspace_size(B, Nq, Hq, Hk, d), dev)
+    lib, width = load(), block_table.shape[1]
+    ws, nbytes = None, 0
+    if workspace is not None or lib.flash_attn_cached_needs_workspace(B, Nq, Hq, Hk, d, page, width, kind):
+        workspace, nbytes = _scratch(workspace, lib.flash_attn_cached_workspace_size(B, Nq, Hq, Hk, d), dev)
+        ws = workspace.data_ptr()
     e4m3 = kind == FA_CACHE_E4M3
-    rc = load().flash_attn_cached_fwd(q.data_ptr(), tok, k_cache.data_ptr(), v_cache.data_ptr(),
-                                      k_scale.data_ptr() if e4m3 else None, v_scale.data_ptr() if e4m3 else None,
-                                      block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Nq,
-                                      Hq, Hk, d, pages, page, block_table.shape[1], scale, kind, opts,
-                                      workspace.data_ptr(), nbytes, _current_stream(dev))
+    rc = lib.flash_attn_cached_fwd(q.data_ptr(), tok, k_cache.data_ptr(), v_cache.data_ptr(),
+                                   k_scale.data_ptr() if e4m3 else None, v_scale.data_ptr() if e4m3 else None,
+                                   block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Nq, Hq,
+                                   Hk, d, pages, page, width, scale, kind, opts, ws, nbytes, _current_stream(dev))
     _check(rc, "flash_attn_cached_fwd")
     return out, lse

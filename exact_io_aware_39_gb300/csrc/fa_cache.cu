@@ -20,6 +20,8 @@
 //   * the products are mma.sync m16n8k16: the 16 rows fill it, where a
 //     tcgen05 product of 128 rows would be an eighth full or less, and the
 //     operands come from registers (Q, P, and with e4m3 the converted K and V);
+//   * calls of few, short sequences are served by a cluster per (sequence, head)
+//     instead, in one launch (WHOLE, below);
 //   * a warp that finishes a (sequence, head) whole writes O and the LSE; one
 //     that holds a part of it writes O unnormalised with the row's reference
 //     and sum, and a second kernel joins the parts (in a fixed order, so the
@@ -252,6 +254,7 @@ struct CachedParams {
   int num_pages, page_size, ps_log2, max_pages;
   float scale_log2;
   uint32_t wait_us, stall;
+  int cluster;         // WHOLE: CTAs to a unit
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -301,12 +304,32 @@ __device__ __forceinline__ void tma_load_2d_w(uint32_t dst, const CUtensorMap* m
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1) : "memory");
 }
 
+// barrier of a cluster's CTAs (all threads), and two floats of CTA `rank`'s
+// shared memory at this CTA's address
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float2 cluster_ld2(uint32_t addr, int rank) {
+  float2 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %2, %3;\n\t"
+      "ld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y) : "r"(addr), "r"(rank) : "memory");
+  return v;
+}
+
 // Walks the units of a range: tile j of n of (sequence b, sub = head * RT + row tile).
 struct Walk {
   int b, sub, j, n, len;
 };
 
-template <int D, bool E4M3, bool F16>
+// WHOLE: instead of cutting all units into ranges, a cluster of CTAs takes one
+// (sequence, key/value head, row tile) and cuts its tiles among its warps; the
+// parts meet in shared memory (a CTA's, then the cluster's), so there is neither
+// a workspace nor a second kernel. For calls of few, short sequences.
+template <int D, bool E4M3, bool F16, bool WHOLE>
 __global__ void __launch_bounds__(32 * kWarps, 1)
 fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const __grid_constant__ CUtensorMap tks, const __grid_constant__ CUtensorMap tvs,
@@ -348,66 +371,74 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     return n < 0 ? 0 : (n > cap ? cap : n);
   };
   auto tiles_of = [&](int len) -> int { return len > 0 ? (len + KT - 1) / KT : 1; };   // an empty sequence is one empty tile
-  long long* tot = reinterpret_cast<long long*>(smem + L::kScan);
-  long long* start_cum = tot + kWarps;
-  int* start_b = reinterpret_cast<int*>(start_cum + kWarps);
-  const int per = (p.B + 32 * kWarps - 1) / (32 * kWarps);
-  const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
-  long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(seq_len(b));
-  long long incl = mine;
+  int me = 0, todo = 0;
+  long long t0 = 0, total = 0;
+  int workers = 0;
+  Walk w0;
+  if constexpr (WHOLE) {
+    const int unit = (int)blockIdx.x / p.cluster, rank = (int)blockIdx.x % p.cluster;
+    w0.b = unit / SUB;
+    w0.sub = unit % SUB;
+    w0.len = same(seq_len(w0.b));
+    w0.n = tiles_of(w0.len);
+    const int all = kWarps * p.cluster, mine = kWarps * rank + warp;
+    w0.j = (int)((long long)w0.n * mine / all);
+    todo = (int)((long long)w0.n * (mine + 1) / all) - w0.j;
+    __syncthreads();   // (the barriers are initialised)
+  } else {
+    long long* tot = reinterpret_cast<long long*>(smem + L::kScan);
+    long long* start_t = tot + kWarps;      // first unit of each warp's range, then the tiles of the sequences before it
+    int* start_b = reinterpret_cast<int*>(start_t + kWarps);
+    const int per = (p.B + 32 * kWarps - 1) / (32 * kWarps);
+    const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
+    long long mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(seq_len(b));
+    long long incl = mine;
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
-    if (lane >= off) incl += o;
-  }
-  if (lane == 31) tot[warp] = incl;
-  __syncthreads();
-  long long before = 0, all = 0;
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    if (lane == 31) tot[warp] = incl;
+    __syncthreads();
+    long long before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += tot[w];
-    all += tot[w];
-  }
-  const long long total = all * SUB;
-  const int workers = (int)min((long long)(kWarps * gridDim.x), total);
-  // neighbouring ranges go to different SMs, so that a small call spreads out
-  auto worker_id = [&](int w) -> int { return w * (int)gridDim.x + (int)blockIdx.x; };
-  auto range_start = [&](int w) -> long long { return total * w / workers; };
-  {
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += tot[w];
+      all += tot[w];
+    }
+    total = all * SUB;
+    workers = (int)min((long long)(kWarps * gridDim.x), total);
+    // neighbouring ranges go to different SMs, so that a small call spreads out
+    me = warp * (int)gridDim.x + (int)blockIdx.x;
+    auto range_start = [&](int w) -> long long { return total * w / workers; };
+    t0 = me < workers ? range_start(me) : total;
+    if (lane == 0) start_t[warp] = t0;
+    __syncthreads();
     long long cum = before + incl - mine;   // tiles of the sequences before b_lo
     for (int b = b_lo; b < b_hi; ++b) {
-      const long long next = cum + tiles_of(seq_len(b));
+      const long long lo = cum * SUB, hi = (cum += tiles_of(seq_len(b))) * SUB;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (worker_id(w) >= workers) break;
-        const long long t0 = range_start(worker_id(w));
-        if (t0 >= cum * SUB && t0 < next * SUB) {
+      for (int w = 0; w < kWarps; ++w)
+        if (start_t[w] >= lo && start_t[w] < hi) {
           start_b[w] = b;
-          start_cum[w] = cum;
+          tot[w] = lo;
         }
-      }
-      cum = next;
     }
-  }
-  __syncthreads();
-  const int me = worker_id(warp);
-  if (me >= workers) {
-    grid_dep_launch();
-    return;
-  }
-  const long long t0 = range_start(me);
-  const int todo = same((int)(range_start(me + 1) - t0));
-  Walk w0;
-  w0.b = same(start_b[warp]);
-  w0.len = same(seq_len(w0.b));
-  w0.n = tiles_of(w0.len);
-  {
-    const long long rem = t0 - start_cum[warp] * SUB;
+    __syncthreads();
+    if (me >= workers) {
+      grid_dep_launch();
+      return;
+    }
+    todo = same((int)(range_start(me + 1) - t0));
+    w0.b = same(start_b[warp]);
+    w0.len = same(seq_len(w0.b));
+    w0.n = tiles_of(w0.len);
+    const long long rem = t0 - tot[warp];
     w0.sub = same((int)(rem / w0.n));
     w0.j = same((int)(rem % w0.n));
   }
-  grid_dep_launch();   // the joining kernel may be scheduled (it waits for this one's end)
+  grid_dep_launch();   // the next kernel may be scheduled (it waits for this one's end)
   auto advance = [&](Walk& w) {
     if (++w.j < w.n) return;
     w.j = 0;
@@ -477,7 +508,11 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
   constexpr int kSteps = D / 16;
   uint32_t qf[kSteps][4];
   float o[D / 8][4];
-  float m[2], l[2], qs[2];
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, qs[2];
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
   Walk w = w0;
   bool fresh = true;              // the next tile starts a (sequence, head, row tile) for this warp
   bool from_start = false;        // ... and is its first
@@ -487,7 +522,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     const int hk = w.sub / p.RT, rt = w.sub % p.RT;
     if (fresh) {
       fresh = false;
-      from_start = w.j == 0;
+      from_start = w.j == 0;   // (WHOLE: a warp has tiles of one sequence only, and this runs once)
 #pragma unroll
       for (int n = 0; n < D / 8; ++n)
 #pragma unroll
@@ -714,7 +749,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     __syncwarp();   // every lane has read the tile: its place may be loaded again
     if (issued < todo && p.stall == 0u) issue_next();
 
-    if (w.j == w.n - 1 || u == todo - 1) {
+    if (!WHOLE && (w.j == w.n - 1 || u == todo - 1)) {
       // the end of a (sequence, head, row tile), or of what this warp has of it
       fresh = true;
       const bool whole = from_start && w.j == w.n - 1;
@@ -781,6 +816,93 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
   if (!ok && lane == 0)
     for (int s = 0; s < L::kStages && s < issued; ++s)
       drain_wait(bar(s), (uint32_t)((issued - 1 - s) / L::kStages) & 1u);
+  if constexpr (WHOLE) {
+    // every warp's part in its own ring (whose tiles have all been read): rows of
+    // O at 0, references and sums behind them; the CTA's part in warp 0's ring
+    __syncwarp();
+    constexpr int kMl = kRows * D * 4, kCta = 12288, kCtaMl = kCta + kMl;
+    static_assert(kMl + kRows * 8 <= kCta && kCtaMl + kRows * 8 <= L::kWarpBytes, "a warp's ring holds its part");
+    uint8_t* my = smem + warp * L::kWarpBytes;
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      l[hh] += __shfl_xor_sync(0xFFFFFFFFu, l[hh], 1);
+      l[hh] += __shfl_xor_sync(0xFFFFFFFFu, l[hh], 2);
+      const int rr = g + 8 * hh;
+      float* po = reinterpret_cast<float*>(my) + rr * D;
+      if constexpr (!E4M3) {
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+          *reinterpret_cast<float2*>(po + 8 * n + 2 * t4) = make_float2(o[n][2 * hh], o[n][2 * hh + 1]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < kSteps; ++c)
+          *reinterpret_cast<float4*>(po + 16 * c + 4 * t4) =
+              make_float4(o[2 * c][2 * hh], o[2 * c + 1][2 * hh], o[2 * c][2 * hh + 1], o[2 * c + 1][2 * hh + 1]);
+      }
+      if (t4 == 0) reinterpret_cast<float2*>(my + kMl)[rr] = make_float2(m[hh], l[hh]);
+    }
+    __syncthreads();
+    const int hk = w0.sub / p.RT, rt = w0.sub % p.RT;
+    auto put = [&](int rr, int c, float a0, float a1, float M, float ls) {   // columns c, c + 1 of row rr
+      const int r = rt * kRows + rr;
+      if (r >= p.R) return;
+      const int i = r / p.G, h = hk * p.G + r % p.G;
+      const float inv = ls > 0.f ? 1.f / ls : (ls == 0.f ? 0.f : ls);
+      if (c < p.d)
+        *reinterpret_cast<uint32_t*>(p.o + (((int64_t)w0.b * p.Nq + i) * p.Hq + h) * p.d + c) = pack2<F16>(a0 * inv, a1 * inv);
+      if (c == 0)
+        p.lse[((int64_t)w0.b * p.Hq + h) * p.Nq + i] = ls == 0.f ? -INFINITY : (M + log2f(ls)) * 0.69314718055994531f;
+    };
+    // a thread joins two columns of a row at a time
+    for (int x = tid; x < kRows * D / 2; x += 32 * kWarps) {
+      const int rr = x / (D / 2), c = 2 * (x % (D / 2));
+      if (rt * kRows + rr >= p.R) break;   // (rows ascend with x)
+      float M = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k)
+        M = fmaxf(M, reinterpret_cast<const float2*>(smem + k * L::kWarpBytes + kMl)[rr].x);
+      const float ref = M == -INFINITY ? 0.f : M;
+      float ls = 0.f, a0 = 0.f, a1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float2 ml = reinterpret_cast<const float2*>(smem + k * L::kWarpBytes + kMl)[rr];
+        const float2 v = *reinterpret_cast<const float2*>(smem + k * L::kWarpBytes + (rr * D + c) * 4);
+        const float f = ex2(ml.x - ref);
+        ls = fmaf(f, ml.y, ls);
+        a0 = fmaf(f, v.x, a0);
+        a1 = fmaf(f, v.y, a1);
+      }
+      if (p.cluster == 1) {
+        put(rr, c, a0, a1, M, ls);
+      } else {
+        *reinterpret_cast<float2*>(smem + kCta + (rr * D + c) * 4) = make_float2(a0, a1);
+        if (c == 0) reinterpret_cast<float2*>(smem + kCtaMl)[rr] = make_float2(M, ls);
+      }
+    }
+    if (p.cluster > 1) {
+      cluster_sync();
+      // the CTAs share the rows out; each reads the others' parts of its rows
+      const int rank = (int)blockIdx.x % p.cluster;
+      for (int x = tid;; x += 32 * kWarps) {
+        const int rr = rank + p.cluster * (x / (D / 2)), c = 2 * (x % (D / 2));
+        if (rr >= kRows || rt * kRows + rr >= p.R) break;
+        float M = -INFINITY;
+        for (int k = 0; k < p.cluster; ++k) M = fmaxf(M, cluster_ld2(sbase + kCtaMl + 8 * rr, k).x);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float ls = 0.f, a0 = 0.f, a1 = 0.f;
+        for (int k = 0; k < p.cluster; ++k) {
+          const float2 ml = cluster_ld2(sbase + kCtaMl + 8 * rr, k);
+          const float2 v = cluster_ld2(sbase + kCta + (rr * D + c) * 4, k);
+          const float f = ex2(ml.x - ref);
+          ls = fmaf(f, ml.y, ls);
+          a0 = fmaf(f, v.x, a0);
+          a1 = fmaf(f, v.y, a1);
+        }
+        put(rr, c, a0, a1, M, ls);
+      }
+      cluster_sync();   // no CTA leaves while another reads its part
+    }
+  }
 }
 
 // Joins the parts of a query row. m is a part's reference, l its sum:
@@ -896,6 +1018,32 @@ CachedWorkspace cached_workspace_layout(int B, int Nq, int Hq, int Hk, int d) {
   return w;
 }
 
+// The number of CTAs (a cluster) that take a (sequence, head, row tile) together,
+// or 0 where the split over all warps of the GPU serves better. As many as the
+// card holds at once (15 clusters of 8, 36 of 4, 76 of 2: a cluster lives within
+// one group of SMs) and as have a tile for each warp. A tile costs a warp about
+// 0.9 us, so that is taken while a warp gets at most 16 tiles of the longest
+// sequence that the table has room for, 12 where less than half of the card works
+// (us, so and split; 8 key/value heads, d = 128: 1 x 1000 bf16 7.3 and 9.9,
+// 1 x 8000 13.3 and 16.0, 1 x 16000 20.9 and 21.7, 4 x 8000 26.0 and 30.4; e4m3
+// 1 x 16000 18.1 and 19.5, 1 x 32768 31.2 and 25.9).
+int whole_cluster(long long units, long long tiles) {
+  int c = 8;
+  const auto most = [](int cc) { return cc == 8 ? 15 : cc == 4 ? 36 : kMaxCtas / cc; };
+  while (c > 1 && (units > most(c) || tiles <= (long long)kWarps * (c / 2))) c /= 2;
+  if (units > most(c)) return 0;
+  const int per_warp = 2 * units * c > kMaxCtas ? 16 : 12;
+  return tiles <= (long long)per_warp * kWarps * c ? c : 0;
+}
+
+int tile_keys(int d, bool e4m3) { return !e4m3 && d > 64 ? 16 : 32; }   // CachedLayout::kKT
+
+int cached_whole(int B, int Nq, int Hq, int Hk, int d, int page_size, int max_pages, bool e4m3) {
+  const long long units = (long long)B * Hk * (((long long)Nq * (Hq / Hk) + kRows - 1) / kRows);
+  const int kt = tile_keys(d, e4m3);
+  return whole_cluster(units, ((long long)max_pages * page_size + kt - 1) / kt);
+}
+
 fa_status check_cached_shape(int B, int Nq, int Hq, int Hk, int d) {
   if (B < 1 || Nq < 1 || Hk < 1 || Hq < 1 || Hq % Hk != 0) return FA_ERR_INVALID_ARG;
   if (d < 8 || d > 128 || d % 8 != 0) return FA_ERR_UNSUPPORTED;
@@ -915,24 +1063,43 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 template <int D, bool E4M3, bool F16>
 cudaError_t launch_cached_d(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tks,
-                            const CUtensorMap& tvs, const CachedParams& p, cudaStream_t s) {
+                            const CUtensorMap& tvs, CachedParams p, cudaStream_t s) {
   using L = CachedLayout<D, E4M3>;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static PerDeviceOnce smem_set;
   e = once_per_device(smem_set, dev, [] {
-    return cudaFuncSetAttribute(fa_cached_kernel<D, E4M3, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                L::kSmemBytes);
+    const cudaError_t e1 = cudaFuncSetAttribute(fa_cached_kernel<D, E4M3, F16, false>,
+                                                cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+    return e1 != cudaSuccess ? e1
+                             : cudaFuncSetAttribute(fa_cached_kernel<D, E4M3, F16, true>,
+                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
   });
   if (e != cudaSuccess) return e;
+  if (p.cluster > 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.B * p.Hk * p.RT * p.cluster));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = L::kSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)p.cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, fa_cached_kernel<D, E4M3, F16, true>, tk, tv, tks, tvs, p);
+  }
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   // one CTA per SM, fewer when even full sequences have fewer units
   const double most = (double)p.B * p.Hk * p.RT * (((double)p.max_pages * p.page_size + L::kKT - 1) / L::kKT);
   int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   if (most < ctas) ctas = most < 1.0 ? 1 : (int)most;
-  e = launch_pdl(true, fa_cached_kernel<D, E4M3, F16>, dim3((unsigned)ctas), dim3(32 * kWarps), L::kSmemBytes, s, tk, tv,
+  e = launch_pdl(true, fa_cached_kernel<D, E4M3, F16, false>, dim3((unsigned)ctas), dim3(32 * kWarps), L::kSmemBytes, s, tk, tv,
                  tks, tvs, p);
   if (e != cudaSuccess) return e;
   const unsigned rows = (unsigned)(p.B * p.Hq * p.Nq);
@@ -1007,6 +1174,12 @@ size_t flash_attn_cached_workspace_size(int B, int Nq, int Hq, int Hk, int d) {
   return cached_workspace_layout(B, Nq, Hq, Hk, d).total;
 }
 
+int flash_attn_cached_needs_workspace(int B, int Nq, int Hq, int Hk, int d, int page_size, int max_pages,
+                                      int cache_type) {
+  if (check_cached_shape(B, Nq, Hq, Hk, d) != FA_OK || page_log2(page_size) < 0 || max_pages < 1) return 1;
+  return cached_whole(B, Nq, Hq, Hk, d, page_size, max_pages, cache_type == FA_CACHE_E4M3) > 0 ? 0 : 1;
+}
+
 fa_status flash_attn_cached_fwd(const void* Q, int64_t q_token_stride, const void* k_cache, const void* v_cache,
                                 const float* k_scale, const float* v_scale, const int32_t* block_table,
                                 const int32_t* seq_lens, void* O, float* LSE, int B, int Nq, int Hq, int Hk, int d,
@@ -1038,12 +1211,15 @@ fa_status flash_attn_cached_fwd(const void* Q, int64_t q_token_stride, const voi
            : (k_scale != nullptr || v_scale != nullptr))
     return FA_ERR_INVALID_ARG;
   const CachedWorkspace w = cached_workspace_layout(B, Nq, Hq, Hk, d);
-  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < w.total) return FA_ERR_WORKSPACE;
+  const int cluster = cached_whole(B, Nq, Hq, Hk, d, page_size, max_pages, e4m3);
+  if (!(cluster > 0 && workspace == nullptr) &&   // (such calls use none)
+      (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < w.total))
+    return FA_ERR_WORKSPACE;
   unsigned int* err = nullptr;
   if ((sr = internal_device_error_word(&err)) != FA_OK) return static_cast<fa_status>(sr);
 
   const int D = d <= 64 ? 64 : 128;
-  const int KT = (!e4m3 && D == 128) ? 16 : 32;
+  const int KT = tile_keys(d, e4m3);
   const uint32_t box_keys = (uint32_t)(page_size < KT ? page_size : KT);
   CUtensorMap tk, tv, tks, tvs;
   {
@@ -1097,6 +1273,7 @@ fa_status flash_attn_cached_fwd(const void* Q, int64_t q_token_stride, const voi
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_us = wait_us;
   p.stall = stall;
+  p.cluster = cluster;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorInvalidValue;
 #define FA_CACHED_CASE(DD, EE, FF) \

@@ -68,6 +68,11 @@ fa_status flash_attn_kv_cache_write(const void* K, const void* V, int64_t k_toke
  * split keys and where each one is); 0 for an invalid shape. */
 size_t flash_attn_cached_workspace_size(int B, int Nq, int Hq, int Hk, int d);
 
+/* 0 when a call of this shape uses no workspace (few sequences that a short
+ * table holds: parts are joined on chip), so that it may be NULL; else 1. */
+int flash_attn_cached_needs_workspace(int B, int Nq, int Hq, int Hk, int d, int page_size, int max_pages,
+                                      int cache_type);
+
 /*
  * Attention of the newest Nq tokens of each of B sequences (their keys and
  * values already in the cache): with n = seq_lens[b], token i of the Nq sees
@@ -88,7 +93,8 @@ size_t flash_attn_cached_workspace_size(int B, int Nq, int Hq, int Hk, int d);
  *   B, Nq, Hk, max_pages >= 1; Hq a multiple of Hk; scale finite, positive.
  *   workspace: at least flash_attn_cached_workspace_size(B, Nq, Hq, Hk, d)
  *         bytes, 256-byte aligned; contents on entry do not matter. Calls
- *         whose kernels may overlap need workspaces of their own.
+ *         whose kernels may overlap need workspaces of their own. May be NULL
+ *         where flash_attn_cached_needs_workspace says 0.
  * 16-bit caches form P V with P rounded to 16 bits; with e4m3 the products
  * run in fp16 on exact conversions of the payloads, the scales applied to S
  * and P in fp32. Sums and statistics are fp32; results do not change from

@@ -73,7 +73,11 @@ def test_cached_workspace(L):
         return (x + 255) // 256 * 256
     assert need == al(al(1216 * 2 * 16 * 128 * 4) + 1216 * 2 * 16 * 8) + al(2 * 8 * 8)
     assert _cached(L, nbytes=need - 1) == 3
-    assert _cached(L, ws=None) == 3
+    # a table of 4 pages of 16: joined on chip, no workspace needed; of 4096 pages: needed
+    assert L.flash_attn_cached_needs_workspace(2, 1, 32, 8, 128, 16, 4, 0) == 0
+    assert L.flash_attn_cached_needs_workspace(2, 1, 32, 8, 128, 16, 4096, 0) == 1
+    assert L.flash_attn_cached_needs_workspace(64, 1, 32, 8, 128, 16, 4, 0) == 1
+    assert _cached(L, ws=None, max_pages=4096) == 3
     assert _cached(L, ws=ctypes.c_void_p((1 << 20) + 16)) == 3
     for bad in ((0, 1, 32, 8, 128), (1, 0, 32, 8, 128), (1, 1, 30, 8, 128), (1, 1, 8, 8, 130), (1, 1, 8, 8, 256)):
         assert L.flash_attn_cached_workspace_size(*bad) == 0

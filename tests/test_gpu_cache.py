@@ -141,11 +141,13 @@ def test_write_edges_of_the_quantisation(fa):
 # attention against the cache
 # ---------------------------------------------------------------------------
 
-def _case(B, Nq, Hq, Hk, d, page, lens, dtype, e4m3, seed=0, spare=3, strided=False, qmul=1.0):
-    """A cache whose places behind the sequences' tokens all hold NaN."""
+def _case(B, Nq, Hq, Hk, d, page, lens, dtype, e4m3, seed=0, spare=3, strided=False, qmul=1.0, room=0):
+    """A cache whose places behind the sequences' tokens all hold NaN. room: the
+    tokens the table has columns for, where that is more than the lengths need
+    (a call of few sequences and little room is joined on chip)."""
     g = torch.Generator().manual_seed(seed)
     need = [-(-n // page) for n in lens]
-    pages, width = sum(need) + spare, max(1, max(need)) + 1
+    pages, width = sum(need) + spare, max(1, max(need), room // page) + 1
     perm = torch.randperm(pages, generator=g)
     table = torch.full((B, width), 1 << 30, dtype=torch.int32)      # behind the last page: not read
     owned = torch.zeros(pages, page, dtype=torch.bool)
@@ -220,10 +222,13 @@ CASES = [
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16", "bf16_e4m3", "fp16_e4m3"])
+@pytest.mark.parametrize("room", [0, 1 << 17], ids=["on_chip", "ranges"])
 @pytest.mark.parametrize("B,Nq,Hq,Hk,d,page,lens", CASES)
-def test_cached_attention(fa, B, Nq, Hq, Hk, d, page, lens, kind):
+def test_cached_attention(fa, B, Nq, Hq, Hk, d, page, lens, room, kind):
     dtype, e4m3 = (BF if kind.startswith("bf16") else FH), kind.endswith("e4m3")
-    c = _case(B, Nq, Hq, Hk, d, page, lens, dtype, e4m3, seed=len(lens) + d, strided=(Hq % 2 == 0))
+    c = _case(B, Nq, Hq, Hk, d, page, lens, dtype, e4m3, seed=len(lens) + d, strided=(Hq % 2 == 0), room=room)
+    needs = fa.flash_attn_cached_needs_workspace(B, Nq, Hq, Hk, d, page, c["table"].shape[1], int(e4m3))
+    assert needs == (1 if room else 0)
     scale = d ** -0.5
     o, lse = _run(fa, c, scale)
     _settled(fa)
@@ -251,14 +256,15 @@ def test_many_sequences_of_all_lengths(fa, e4m3):
     _check(c, 0.125, o, lse)
 
 
-def test_large_scores_and_scales_far_apart(fa):
+@pytest.mark.parametrize("room", [0, 1 << 17], ids=["on_chip", "ranges"])
+def test_large_scores_and_scales_far_apart(fa, room):
     """Scores in the hundreds move the running maximum often; value scales
     2^80 apart must not lose a token whose weight is large."""
-    c = _case(2, 1, 8, 2, 128, 16, [300, 90], BF, False, qmul=20.0)
+    c = _case(2, 1, 8, 2, 128, 16, [300, 90], BF, False, qmul=20.0, room=room)
     o, lse = _run(fa, c, 0.3)
     _settled(fa)
     _check(c, 0.3, o, lse)
-    c = _case(1, 1, 4, 1, 64, 16, [64], BF, True, qmul=0.01)
+    c = _case(1, 1, 4, 1, 64, 16, [64], BF, True, qmul=0.01, room=room)
     e = torch.linspace(-50, 30, 64).round()
     c["vs"][:] = float("nan")
     for j in range(64):
@@ -318,10 +324,11 @@ def test_shared_pages(fa):
     _check(c, 0.2, o, lse)
 
 
-def test_other_streams_and_replayed_graphs(fa):
+@pytest.mark.parametrize("room", [0, 1 << 17], ids=["on_chip", "ranges"])
+def test_other_streams_and_replayed_graphs(fa, room):
     """Two calls at once on two streams with workspaces of their own, and a
     captured call replayed after the lengths have changed."""
-    cs = [_case(4, 1, 8, 2, 128, 16, [n, 1, 300, 77], BF, e, seed=n) for n, e in ((500, False), (40, True))]
+    cs = [_case(4, 1, 8, 2, 128, 16, [n, 1, 300, 77], BF, e, seed=n, room=room) for n, e in ((500, False), (40, True))]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     torch.cuda.synchronize()
     res = []
@@ -366,9 +373,10 @@ def test_write_then_read_step_by_step(fa):
             _check(c, 0.1, o, lse)
 
 
+@pytest.mark.parametrize("room", [0, 1 << 17], ids=["on_chip", "ranges"])
 @pytest.mark.parametrize("e4m3", [False, True])
-def test_wait_runs_out_and_device_stays_usable(fa, e4m3):
-    c = _case(2, 1, 8, 2, 128, 16, [20000, 9000], BF, e4m3)
+def test_wait_runs_out_and_device_stays_usable(fa, e4m3, room):
+    c = _case(2, 1, 8, 2, 128, 16, [20000, 9000] if room else [7000, 5000], BF, e4m3, room=room)
     o, lse = _run(fa, c, 0.1)
     _settled(fa)
     _run(fa, c, 0.1, wait_limit_us=20000, test_stall=1)
