@@ -274,10 +274,9 @@ fa_status flash_attn_packed_bwd(const void* Q, const void* K, const void* V, con
   if (e != FA_OK) return static_cast<fa_status>(e);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* dq_acc = reinterpret_cast<float*>(ws + w.dq_off);
-  CUtensorMap tq, tk, tv, tdo, tdk, tdv, tdq;
+  CUtensorMap tq, tk, tv, tdo, tdq;
   if (packed_map(&tq, Q, o.f16, total, Hq, d, ss[0], kTile) || packed_map(&tk, K, o.f16, total, Hk, d, ss[1], kTile) ||
-      packed_map(&tv, V, o.f16, total, Hk, d, ss[2], kTile) || packed_map(&tdo, dO, o.f16, total, Hq, d, ss[4], kTile) ||
-      packed_map(&tdk, dK, o.f16, total, Hk, d, ss[6], kTile) || packed_map(&tdv, dV, o.f16, total, Hk, d, ss[7], kTile))
+      packed_map(&tv, V, o.f16, total, Hk, d, ss[2], kTile) || packed_map(&tdo, dO, o.f16, total, Hq, d, ss[4], kTile))
     return FA_ERR_CUDA;
   {
     // the dQ accumulator [Hq, padded rows, d], box 32 fp32 columns: whole
@@ -332,7 +331,7 @@ fa_status flash_attn_packed_bwd(const void* Q, const void* K, const void* V, con
                          reinterpret_cast<PackedItem*>(ws + w.item_off), w.cap_items,
                          reinterpret_cast<PackedItem*>(ws + w.tile_off), w.cap_tiles, err, s) != cudaSuccess)
     return FA_ERR_CUDA;
-  return launch_packed_bwd(o.f16, tq, tk, tv, tdo, tdk, tdv, tdq, p, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_packed_bwd(o.f16, tq, tk, tv, tdo, tdq, p, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"

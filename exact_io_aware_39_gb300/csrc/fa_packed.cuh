@@ -267,7 +267,7 @@ cudaError_t launch_packed_fwd(bool f16, const CUtensorMap& tq, const CUtensorMap
                               const PackedFwdParams& p, cudaStream_t s);
 
 cudaError_t launch_packed_bwd(bool f16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                              const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv,
-                              const CUtensorMap& tdq, const PackedBwdParams& p, cudaStream_t s);
+                              const CUtensorMap& tdo, const CUtensorMap& tdq, const PackedBwdParams& p,
+                              cudaStream_t s);
 
 }  // namespace fa

@@ -15,8 +15,10 @@
 //     before the products that read them, so what lies there (NaN included)
 //     reaches no sum;
 //   * the row statistics and the dQ accumulator are kept over sequences padded
-//     to whole tiles, where the 128-row copies need no bounds; rows of dK, dV
-//     past a sequence's end are not stored.
+//     to whole tiles, where the 128-row copies need no bounds;
+//   * dK and dV go from registers to global memory (as O does in the forward), so
+//     K and V of the next item load as soon as this one's last product has read
+//     theirs, while dK and dV are written.
 //
 // Launches (after the plan, for more than kDirect sequences): the pre-pass (D = rowsum(dO * O), LSE * log2 e,
 // zeroed accumulator), the main kernel, and dQ = 16-bit(scale * accumulator).
@@ -67,7 +69,7 @@ struct PackedBwdLayout {
   static constexpr int bdQFree = bdQFull + 1;
   static constexpr int bFinal = bdQFree + 1;
   static constexpr int bDrain = bFinal + 1;
-  static constexpr int bKVFree = bDrain + 1;   // [kKV]: the epilogue's staging has been read (2 arrivals)
+  static constexpr int bKVFree = bDrain + 1;   // [kKV]: the item's last product has read K and V
   // work items reach the other roles through a ring filled by the producer
   static constexpr int kItemRing = 4;
   static constexpr int bItemFull = bKVFree + kKV;            // [kItemRing]
@@ -89,9 +91,8 @@ struct PackedBwdLayout {
 template <int D, bool F16>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
-                   const __grid_constant__ CUtensorMap tdk, const __grid_constant__ CUtensorMap tdv,
-                   const __grid_constant__ CUtensorMap tdq, const PackedBwdParams p) {
+                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+                     const __grid_constant__ CUtensorMap tdq, const PackedBwdParams p) {
   using L = PackedBwdLayout<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -148,7 +149,6 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     for (int i = 0; i < L::kNumBars; ++i)
       mbar_init(bar(i), (i == L::bPFull || i == L::bdSFull || i == L::bdSHalf) ? (uint32_t)(4 * kGroups)
                         : i == L::bdQFree ? 4u                                       // the four drain warps
-                        : (i >= L::bKVFree && i < L::bKVFree + L::kKV) ? (uint32_t)kGroups   // one thread per compute group
                         : (!L::kGroupDrain && i >= L::bdOFree && i < L::bdOFree + L::kStages) ? 4u   // the drain warps
                         : (i >= L::bItemEmpty && i < L::bItemEmpty + L::kItemRing)
                             ? (uint32_t)(1 + 4 * kGroups + 4) : 1u);   // arrivals: MMA, compute and drain warps
@@ -284,6 +284,11 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         mbar_arrive(bar(L::bItemFull + rs));   // (release: the ring entry is visible to the waiters)
       }
       if (w.kj < 0) break;
+      if (k >= L::kKV)   // K and V wait for the item before: into L2 until then
+        for (int h = 0; h < L::kHalves; ++h) {
+          tma_prefetch_3d_w(&tk, 64 * h, w.hk, w.start + kTile * w.kj);
+          tma_prefetch_3d_w(&tv, 64 * h, w.hk, w.start + kTile * w.kj);
+        }
       const int steps = p.G * (w.nT - w.i0);
 #pragma unroll 1
       for (int it = 0, i = w.i0, hq = w.hk * p.G; it < steps; ++it, ++g) {
@@ -309,7 +314,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         ++nd;
         // K and V behind the first query tile of the item, whose loads only
         // wait for ring slots of the previous item: into buffer k % kKV, once the
-        // epilogue of the item that used it before has been read out of it
+        // last product of the item that used it before has read it
         if (it == 0) {
           const int kb = k % L::kKV;
           if (k >= L::kKV && !(ok = bar_wait_warp(bar(L::bKVFree + kb), (uint32_t)(k / L::kKV - 1) & 1u, ctl, 353))) break;
@@ -455,7 +460,10 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           if (!kEarlyS && more && !(ok = issue_s(sK, g + 1, tail_next))) break;
           i = inext;
         }
-        if (ok) mma_commit_w(bar(L::bFinal));   // dV and dK of the item are complete
+        if (ok) {
+          mma_commit_w(bar(L::bFinal));          // dV and dK of the item are complete
+          mma_commit_w(bar(L::bKVFree + kb));    // and K and V may be loaded over
+        }
       }
       mma_commit_w(bar(L::bDrain));
       drain_wait(bar(L::bDrain), 0);
@@ -472,27 +480,8 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     const float sl2 = p.scale_log2;
     bool ok = true;
     int g = 0, nf = 0;
-    int pending = -1;   // K/V buffer whose epilogue store has not been waited for yet (thread r == 0)
-    // the store out of buffer `pending` has read its staging: the buffer goes
-    // back to the producer
-    auto release_kv = [&]() {
-      if (pending >= 0) {
-        if (r == 0) {
-          bulk_wait_group_read_all();
-          mbar_arrive(bar(L::bKVFree + pending));
-        }
-        pending = -1;
-      }
-    };
-    // The four warps of a group meet at a named barrier in each item's
-    // epilogue; before it, and wherever one of them may have stopped (a wait
-    // that ran out or saw the abort flag), they agree with group_all, so that
-    // all of them take the same branch and none waits for one that has left.
-    const uint32_t gbar = 1u + (uint32_t)cw;
-    constexpr uint32_t kGThreads = 128u;
     for (int k = 0; ok; ++k) {
       const Item w = take_item(k, ok);
-      ok = group_all(gbar, kGThreads, ok);
       if (!ok || w.kj < 0) break;
       const int krow = kTile * w.kj + r;
       const int steps = p.G * (w.nT - w.i0);
@@ -546,7 +535,6 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive_warp(bar(L::bPFull));
-        if (it == 0) release_kv();   // the previous item's store has had this tile's time to read its staging
 
         // dS^T row: ds[c] = p[c] * (dP[c] - D[query c]) -> 16-bit -> swizzled smem
         if (!(ok = bar_wait_warp(bar(L::bdPFull), (uint32_t)g & 1u, ctl, 372))) break;
@@ -601,64 +589,42 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         mbar_arrive_warp(bar(L::bdSFull));
       }
 
-      // epilogue: the first warpgroup stores dV, the second scale * dK, staged
-      // in the item's V or K buffer once every MMA has read it: whole tiles by
-      // TMA, a sequence's last rows one by one
-      ok = group_all(gbar, kGThreads, ok);
-      if (!ok) break;
-      const int kb = k % L::kKV;
-      ok = bar_wait_warp(bar(L::bKV + kb), (uint32_t)(k / L::kKV) & 1u, ctl, 374);
-      if (ok) ok = bar_wait_warp(bar(L::bFinal), (uint32_t)nf & 1u, ctl, 375);
-      ok = group_all(gbar, kGThreads, ok);
-      if (!ok) break;
+      // epilogue: the first warpgroup writes dV, the second scale * dK, from
+      // registers: a lane holds 32 columns of its row at a time, as four 16-byte
+      // chunks; transposed across its quad it holds one chunk of four rows, and a
+      // quad writes 64 bytes of each, up to the sequence's end
+      if (!ok || !(ok = bar_wait_warp(bar(L::bFinal), (uint32_t)nf & 1u, ctl, 375))) break;
       ++nf;
       tc_fence_after();
       const bool is_v = cw == 0;
       const uint32_t tacc = (is_v ? tdV : tdK) + lane_off;
       const float mul = is_v ? 1.f : p.scale;
-      const int stage_off = (is_v ? L::kV : L::kK) + kb * L::kKVBytes;
-      uint8_t* stage = smem + stage_off;
-#pragma unroll
+      const int s4 = lane & 3;
+      const int row0 = kTile * w.kj + 32 * (warp & 3) + (lane & ~3);   // the quad's first row
+      const int64_t tok = is_v ? p.dv_tok : p.dk_tok;
+      uint16_t* op = (is_v ? p.dv : p.dk) + (int64_t)(w.start + row0) * tok + w.hk * (is_v ? p.dv_head : p.dk_head) + 8 * s4;
+#pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t u[32];
         tmem_ld32(tacc + 32u * cc, u);
         tmem_ld_wait(u);
-        uint32_t pk[16];
+        uint32_t y[4][4];   // [word of a chunk][chunk of this row, then row of the quad]
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-          pk[c] = pack2<F16>(__uint_as_float(u[2 * c]) * mul, __uint_as_float(u[2 * c + 1]) * mul);
+        for (int wd = 0; wd < 4; ++wd) {
 #pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4)
-          *reinterpret_cast<uint4*>(stage + tile_chunk(r, 4 * cc + k4)) =
-              make_uint4(pk[4 * k4], pk[4 * k4 + 1], pk[4 * k4 + 2], pk[4 * k4 + 3]);
-      }
-      tc_fence_before();
-      fence_proxy_async_smem();
-      named_bar_sync(gbar, kGThreads);
-      const int rows = w.len - kTile * w.kj;
-      if (rows >= kTile) {
-        if (r == 0) {
-          for (int h = 0; h < L::kHalves; ++h)
-            tma_store_3d(is_v ? &tdv : &tdk, sbase + stage_off + h * 16384, 64 * h, w.hk, w.start + kTile * w.kj);
-          bulk_commit_group();
+          for (int j = 0; j < 4; ++j)
+            y[wd][j] = pack2<F16>(__uint_as_float(u[8 * j + 2 * wd]) * mul, __uint_as_float(u[8 * j + 2 * wd + 1]) * mul);
+          quad_transpose(y[wd], (uint32_t)s4);
         }
-      } else {
-        const int64_t tok = is_v ? p.dv_tok : p.dk_tok;
-        uint16_t* op = (is_v ? p.dv : p.dk) + (int64_t)(w.start + kTile * w.kj) * tok +
-                       w.hk * (is_v ? p.dv_head : p.dk_head);
-        const int chunks = p.d >> 3;
-        for (int i = r; i < rows * chunks; i += 128) {
-          const int rr = i / chunks, ch = i % chunks;
-          *reinterpret_cast<uint4*>(op + rr * tok + 8 * ch) = *reinterpret_cast<const uint4*>(stage + tile_chunk(rr, ch));
+        if (32 * cc + 8 * s4 < p.d) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (row0 + j < w.len)
+              *reinterpret_cast<uint4*>(op + j * tok + 32 * cc) = make_uint4(y[0][j], y[1][j], y[2][j], y[3][j]);
         }
-        fence_proxy_async_smem();
-        named_bar_sync(gbar, kGThreads);   // every row is read before the buffer goes back to the producer
       }
-      pending = kb;
-      // with one K/V buffer the next item's K and V wait for this store
-      if (L::kKV == 1) release_kv();
+      tc_fence_before();   // (the next item's first dV waits for this warp's next P)
     }
-    if (r == 0) bulk_wait_group_read_all();   // the stores have read the staging; the grid's end makes them visible
   } else if (warp < kProducerWarp) {
     // ------------------------------------------------------------ dQ drain (thread = query row)
     // TMEM -> fp32 rows staged in this iteration's dO ring slot (dead once dQ
@@ -848,8 +814,8 @@ __global__ void __launch_bounds__(256) packed_bwd_dq_kernel(const PackedBwdParam
 
 template <int D, bool F16>
 cudaError_t launch_packed_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv,
-                                const CUtensorMap& tdq, const PackedBwdParams& p, cudaStream_t s) {
+                                const CUtensorMap& tdo, const CUtensorMap& tdq,
+                                const PackedBwdParams& p, cudaStream_t s) {
   using L = PackedBwdLayout<D>;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -873,7 +839,7 @@ cudaError_t launch_packed_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
   // a CTA per item where items are taken by cancelling CTAs, else one per SM
   const long long most = (long long)p.cap_tiles * p.Hk;
   e = launch_pdl(true, fa_packed_bwd_kernel<D, F16>, dim3((unsigned)(p.B <= kDirect || most < sms ? most : sms)),
-                 dim3(kBwdThreads), L::kSmemBytes, s, tq, tk, tv, tdo, tdk, tdv, tdq, q);
+                 dim3(kBwdThreads), L::kSmemBytes, s, tq, tk, tv, tdo, tdq, q);
   if (e != cudaSuccess) return e;
   return launch_pdl(true, packed_bwd_dq_kernel<F16>, tiles, dim3(256), 0, s, q);
 }
@@ -881,13 +847,13 @@ cudaError_t launch_packed_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
 }  // namespace
 
 cudaError_t launch_packed_bwd(bool f16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                              const CUtensorMap& tdo, const CUtensorMap& tdk, const CUtensorMap& tdv,
-                              const CUtensorMap& tdq, const PackedBwdParams& p, cudaStream_t s) {
+                              const CUtensorMap& tdo, const CUtensorMap& tdq,
+                              const PackedBwdParams& p, cudaStream_t s) {
   if (p.d <= 64)
-    return f16 ? launch_packed_bwd_d<64, true>(tq, tk, tv, tdo, tdk, tdv, tdq, p, s)
-               : launch_packed_bwd_d<64, false>(tq, tk, tv, tdo, tdk, tdv, tdq, p, s);
-  return f16 ? launch_packed_bwd_d<128, true>(tq, tk, tv, tdo, tdk, tdv, tdq, p, s)
-             : launch_packed_bwd_d<128, false>(tq, tk, tv, tdo, tdk, tdv, tdq, p, s);
+    return f16 ? launch_packed_bwd_d<64, true>(tq, tk, tv, tdo, tdq, p, s)
+               : launch_packed_bwd_d<64, false>(tq, tk, tv, tdo, tdq, p, s);
+  return f16 ? launch_packed_bwd_d<128, true>(tq, tk, tv, tdo, tdq, p, s)
+             : launch_packed_bwd_d<128, false>(tq, tk, tv, tdo, tdq, p, s);
 }
 
 }  // namespace fa
