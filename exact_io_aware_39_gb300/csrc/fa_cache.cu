@@ -208,19 +208,27 @@ cudaError_t launch_write(const WriteParams& p, cudaStream_t s) {
 // attention against the cache
 // --------------------------------------------------------------------------
 
-constexpr int kWarps = 8;
 constexpr int kMaxCtas = 152;
-constexpr int kMaxWorkers = kWarps * kMaxCtas;
+constexpr int kMaxWorkers = 12 * kMaxCtas;
 constexpr int kRows = 16;                 // query rows of a unit
 constexpr float kMoveThreshold = 8.0f;    // log2 units: the reference moves only past it
 
-// Shared-memory layout of one warp's ring. A tile is kKT keys: K, then V, each
+// Shared-memory layout, a ring of tiles for each warp. A tile is kKT keys: K, then V, each
 // as the TMA writes it (16-bit: 64-column atoms of 128-byte rows; e4m3: one
 // atom of D-byte rows), 128- or 64-byte swizzled, then with e4m3 the scales of
 // K and of V (each 16 keys at a pitch of 64 or, one page each, 128 bytes).
+//
+// Warps and tiles by type (D is 64 or 128): 16-bit rows are bound by the memory
+// system, and want large tiles (d = 128, 6 warps of 2 x 32 keys against 8 warps
+// of 3 x 16: 16 sequences of 8192-65536 tokens 245 and 255 us); e4m3 has twice
+// the keys, and so the work, to a byte, and wants warps.
+constexpr int kKeys = 32;   // of a tile
+constexpr int tile_warps(int D, bool e4m3) { return e4m3 ? 12 : (D == 128 ? 6 : 8); }
+
 template <int D, bool E4M3>
 struct CachedLayout {
-  static constexpr int kKT = (!E4M3 && D == 128) ? 16 : 32;
+  static constexpr int kKT = kKeys;
+  static constexpr int kWarps = tile_warps(D, E4M3);
   static constexpr int kRowBytes = E4M3 ? D : 128;              // of a swizzle atom
   static constexpr int kAtoms = E4M3 ? 1 : D / 64;
   static constexpr int kAtomBytes = kKT * kRowBytes;
@@ -228,13 +236,14 @@ struct CachedLayout {
   static constexpr int kScaleBytes = E4M3 ? 256 : 0;            // K or V
   // stages start at multiples of 1024 bytes; the scales of all stages follow
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = kStageBytes >= 8192 ? 3 : 6;
+  static constexpr int kStages = E4M3 ? (D == 128 ? 2 : 4) : (D == 128 ? 2 : 3);
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kScale = kWarps * kWarpBytes;
   static constexpr int kBar = kScale + kWarps * kStages * 2 * kScaleBytes;
   static constexpr int kMisc = kBar + 8 * kWarps * kStages;     // abort flag, -, wait limit, -
   static constexpr int kScan = kMisc + 16;                      // int64 [kWarps] totals, int64 [kWarps] starts, int [kWarps]
-  static constexpr int kSmemBytes = kScan + kWarps * 20;
+  static constexpr int kMl = (kScan + kWarps * 20 + 15) & ~15;  // (reference, sum) of kRows rows of each warp's part and of the CTA's
+  static constexpr int kSmemBytes = kMl + (kWarps + 1) * kRows * 8;
   static constexpr uint32_t kTxBytes = 2u * kTileBytes + (E4M3 ? 2u * kKT * 4u : 0u);
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
@@ -330,12 +339,12 @@ struct Walk {
 // parts meet in shared memory (a CTA's, then the cluster's), so there is neither
 // a workspace nor a second kernel. For calls of few, short sequences.
 template <int D, bool E4M3, bool F16, bool WHOLE>
-__global__ void __launch_bounds__(32 * kWarps, 1)
+__global__ void __launch_bounds__(32 * CachedLayout<D, E4M3>::kWarps, 1)
 fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const __grid_constant__ CUtensorMap tks, const __grid_constant__ CUtensorMap tvs,
                  const CachedParams p) {
   using L = CachedLayout<D, E4M3>;
-  constexpr int KT = L::kKT;
+  constexpr int KT = L::kKT, kWarps = L::kWarps;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   // (what is the same in all lanes of a warp comes from a shuffle, so that the
@@ -817,11 +826,12 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     for (int s = 0; s < L::kStages && s < issued; ++s)
       drain_wait(bar(s), (uint32_t)((issued - 1 - s) / L::kStages) & 1u);
   if constexpr (WHOLE) {
-    // every warp's part in its own ring (whose tiles have all been read): rows of
-    // O at 0, references and sums behind them; the CTA's part in warp 0's ring
+    // every warp's part in its own ring (whose tiles have all been read), the
+    // CTA's part behind warp 0's
     __syncwarp();
-    constexpr int kMl = kRows * D * 4, kCta = 12288, kCtaMl = kCta + kMl;
-    static_assert(kMl + kRows * 8 <= kCta && kCtaMl + kRows * 8 <= L::kWarpBytes, "a warp's ring holds its part");
+    constexpr int kCta = kRows * D * 4;
+    static_assert(2 * kCta <= L::kWarpBytes, "a ring holds two parts");
+    float2* mls = reinterpret_cast<float2*>(smem + L::kMl);   // [kWarps + 1][kRows]
     uint8_t* my = smem + warp * L::kWarpBytes;
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
@@ -839,7 +849,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
           *reinterpret_cast<float4*>(po + 16 * c + 4 * t4) =
               make_float4(o[2 * c][2 * hh], o[2 * c + 1][2 * hh], o[2 * c][2 * hh + 1], o[2 * c + 1][2 * hh + 1]);
       }
-      if (t4 == 0) reinterpret_cast<float2*>(my + kMl)[rr] = make_float2(m[hh], l[hh]);
+      if (t4 == 0) mls[warp * kRows + rr] = make_float2(m[hh], l[hh]);
     }
     __syncthreads();
     const int hk = w0.sub / p.RT, rt = w0.sub % p.RT;
@@ -860,12 +870,12 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
       float M = -INFINITY;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k)
-        M = fmaxf(M, reinterpret_cast<const float2*>(smem + k * L::kWarpBytes + kMl)[rr].x);
+        M = fmaxf(M, mls[k * kRows + rr].x);
       const float ref = M == -INFINITY ? 0.f : M;
       float ls = 0.f, a0 = 0.f, a1 = 0.f;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
-        const float2 ml = reinterpret_cast<const float2*>(smem + k * L::kWarpBytes + kMl)[rr];
+        const float2 ml = mls[k * kRows + rr];
         const float2 v = *reinterpret_cast<const float2*>(smem + k * L::kWarpBytes + (rr * D + c) * 4);
         const float f = ex2(ml.x - ref);
         ls = fmaf(f, ml.y, ls);
@@ -876,7 +886,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         put(rr, c, a0, a1, M, ls);
       } else {
         *reinterpret_cast<float2*>(smem + kCta + (rr * D + c) * 4) = make_float2(a0, a1);
-        if (c == 0) reinterpret_cast<float2*>(smem + kCtaMl)[rr] = make_float2(M, ls);
+        if (c == 0) mls[kWarps * kRows + rr] = make_float2(M, ls);
       }
     }
     if (p.cluster > 1) {
@@ -887,11 +897,11 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         const int rr = rank + p.cluster * (x / (D / 2)), c = 2 * (x % (D / 2));
         if (rr >= kRows || rt * kRows + rr >= p.R) break;
         float M = -INFINITY;
-        for (int k = 0; k < p.cluster; ++k) M = fmaxf(M, cluster_ld2(sbase + kCtaMl + 8 * rr, k).x);
+        for (int k = 0; k < p.cluster; ++k) M = fmaxf(M, cluster_ld2(sbase + L::kMl + 8 * (kWarps * kRows + rr), k).x);
         const float ref = M == -INFINITY ? 0.f : M;
         float ls = 0.f, a0 = 0.f, a1 = 0.f;
         for (int k = 0; k < p.cluster; ++k) {
-          const float2 ml = cluster_ld2(sbase + kCtaMl + 8 * rr, k);
+          const float2 ml = cluster_ld2(sbase + L::kMl + 8 * (kWarps * kRows + rr), k);
           const float2 v = cluster_ld2(sbase + kCta + (rr * D + c) * 4, k);
           const float f = ex2(ml.x - ref);
           ls = fmaf(f, ml.y, ls);
@@ -1027,21 +1037,18 @@ CachedWorkspace cached_workspace_layout(int B, int Nq, int Hq, int Hk, int d) {
 // (us, so and split; 8 key/value heads, d = 128: 1 x 1000 bf16 7.3 and 9.9,
 // 1 x 8000 13.3 and 16.0, 1 x 16000 20.9 and 21.7, 4 x 8000 26.0 and 30.4; e4m3
 // 1 x 16000 18.1 and 19.5, 1 x 32768 31.2 and 25.9).
-int whole_cluster(long long units, long long tiles) {
+int whole_cluster(long long units, long long tiles, int warps) {
   int c = 8;
   const auto most = [](int cc) { return cc == 8 ? 15 : cc == 4 ? 36 : kMaxCtas / cc; };
-  while (c > 1 && (units > most(c) || tiles <= (long long)kWarps * (c / 2))) c /= 2;
+  while (c > 1 && (units > most(c) || tiles <= (long long)warps * (c / 2))) c /= 2;
   if (units > most(c)) return 0;
   const int per_warp = 2 * units * c > kMaxCtas ? 16 : 12;
-  return tiles <= (long long)per_warp * kWarps * c ? c : 0;
+  return tiles <= (long long)per_warp * warps * c ? c : 0;
 }
-
-int tile_keys(int d, bool e4m3) { return !e4m3 && d > 64 ? 16 : 32; }   // CachedLayout::kKT
 
 int cached_whole(int B, int Nq, int Hq, int Hk, int d, int page_size, int max_pages, bool e4m3) {
   const long long units = (long long)B * Hk * (((long long)Nq * (Hq / Hk) + kRows - 1) / kRows);
-  const int kt = tile_keys(d, e4m3);
-  return whole_cluster(units, ((long long)max_pages * page_size + kt - 1) / kt);
+  return whole_cluster(units, ((long long)max_pages * page_size + kKeys - 1) / kKeys, tile_warps(d <= 64 ? 64 : 128, e4m3));
 }
 
 fa_status check_cached_shape(int B, int Nq, int Hq, int Hk, int d) {
@@ -1080,7 +1087,7 @@ cudaError_t launch_cached_d(const CUtensorMap& tk, const CUtensorMap& tv, const 
   if (p.cluster > 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.B * p.Hk * p.RT * p.cluster));
-    cfg.blockDim = dim3(32 * kWarps);
+    cfg.blockDim = dim3(32 * L::kWarps);
     cfg.dynamicSmemBytes = L::kSmemBytes;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
@@ -1099,11 +1106,11 @@ cudaError_t launch_cached_d(const CUtensorMap& tk, const CUtensorMap& tv, const 
   const double most = (double)p.B * p.Hk * p.RT * (((double)p.max_pages * p.page_size + L::kKT - 1) / L::kKT);
   int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   if (most < ctas) ctas = most < 1.0 ? 1 : (int)most;
-  e = launch_pdl(true, fa_cached_kernel<D, E4M3, F16, false>, dim3((unsigned)ctas), dim3(32 * kWarps), L::kSmemBytes, s, tk, tv,
+  e = launch_pdl(true, fa_cached_kernel<D, E4M3, F16, false>, dim3((unsigned)ctas), dim3(32 * L::kWarps), L::kSmemBytes, s, tk, tv,
                  tks, tvs, p);
   if (e != cudaSuccess) return e;
   const unsigned rows = (unsigned)(p.B * p.Hq * p.Nq);
-  if ((long long)p.B * p.Hk * p.RT * kManyParts <= (long long)kWarps * ctas)
+  if ((long long)p.B * p.Hk * p.RT * kManyParts <= (long long)L::kWarps * ctas)
     return launch_pdl(true, fa_cached_join_kernel<D, F16, 16>, dim3(rows), dim3(512), 0, s, p);
   return launch_pdl(true, fa_cached_join_kernel<D, F16, 1>, dim3((rows + 3) / 4), dim3(128), 0, s, p);
 }
@@ -1219,8 +1226,7 @@ fa_status flash_attn_cached_fwd(const void* Q, int64_t q_token_stride, const voi
   if ((sr = internal_device_error_word(&err)) != FA_OK) return static_cast<fa_status>(sr);
 
   const int D = d <= 64 ? 64 : 128;
-  const int KT = tile_keys(d, e4m3);
-  const uint32_t box_keys = (uint32_t)(page_size < KT ? page_size : KT);
+  const uint32_t box_keys = (uint32_t)(page_size < kKeys ? page_size : kKeys);
   CUtensorMap tk, tv, tks, tvs;
   {
     const uint64_t es = e4m3 ? 1 : 2;

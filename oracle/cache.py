@@ -27,12 +27,9 @@ def e4m3_rows(x):
     x = np.asarray(x, dtype=np.float64)
     fin = np.isfinite(x)
     top = np.where(fin, np.abs(x), 0.0).max(axis=-1)
-    scale = np.full(top.shape, 2.0 ** MIN_EXP)
-    for idx in np.ndindex(*top.shape):
-        e = MIN_EXP
-        while top[idx] > E4M3_MAX * 2.0 ** e:
-            e += 1
-        scale[idx] = 2.0 ** e
+    scale = np.full(top.shape, np.nan)
+    for e in range(130, MIN_EXP - 1, -1):                 # the last that holds is the smallest
+        scale[top <= E4M3_MAX * 2.0 ** e] = 2.0 ** e
     y = e4m3_round(np.where(fin, x, 0.0) / scale[..., None])
     return np.where(fin, y, np.nan), scale
 

@@ -71,7 +71,7 @@ def test_cached_workspace(L):
     need = L.flash_attn_cached_workspace_size(2, 1, 32, 8, 128)
     def al(x):
         return (x + 255) // 256 * 256
-    assert need == al(al(1216 * 2 * 16 * 128 * 4) + 1216 * 2 * 16 * 8) + al(2 * 8 * 8)
+    assert need == al(al(1824 * 2 * 16 * 128 * 4) + 1824 * 2 * 16 * 8) + al(2 * 8 * 8)
     assert _cached(L, nbytes=need - 1) == 3
     # a table of 4 pages of 16: joined on chip, no workspace needed; of 4096 pages: needed
     assert L.flash_attn_cached_needs_workspace(2, 1, 32, 8, 128, 16, 4, 0) == 0

@@ -376,7 +376,8 @@ def test_write_then_read_step_by_step(fa):
 @pytest.mark.parametrize("room", [0, 1 << 17], ids=["on_chip", "ranges"])
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_wait_runs_out_and_device_stays_usable(fa, e4m3, room):
-    c = _case(2, 1, 8, 2, 128, 16, [20000, 9000] if room else [7000, 5000], BF, e4m3, room=room)
+    # (more than one tile of 32 keys for most warps, so that a second one can fail to come)
+    c = _case(2, 1, 8, 2, 128, 16, [50000, 30000] if room else [9000, 7000], BF, e4m3, room=room)
     o, lse = _run(fa, c, 0.1)
     _settled(fa)
     _run(fa, c, 0.1, wait_limit_us=20000, test_stall=1)
