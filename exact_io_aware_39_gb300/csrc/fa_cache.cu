@@ -218,17 +218,27 @@ constexpr float kMoveThreshold = 8.0f;    // log2 units: the reference moves onl
 // atom of D-byte rows), 128- or 64-byte swizzled, then with e4m3 the scales of
 // K and of V (each 16 keys at a pitch of 64 or, one page each, 128 bytes).
 //
-// Warps and tiles by type (D is 64 or 128): 16-bit rows are bound by the memory
-// system, and want large tiles (d = 128, 6 warps of 2 x 32 keys against 8 warps
-// of 3 x 16: 16 sequences of 8192-65536 tokens 245 and 255 us); e4m3 has twice
-// the keys, and so the work, to a byte, and wants warps.
-constexpr int kKeys = 32;   // of a tile
-constexpr int tile_warps(int D, bool e4m3) { return e4m3 ? 12 : (D == 128 ? 6 : 8); }
+// Warps, keys of a tile and tiles of a ring, by the tile width D (64 or 128), the
+// type and the kernel. A tile costs a warp its latency, 1 us or so, so the split
+// over the GPU wants warps (16-bit, d = 128, 12 x 16 keys x 2 against 6 x 32 x 2:
+// 256 sequences of 20-200 tokens 28.7 and 37.4 us, 16 of 8192-65536 243 and 246;
+// e4m3, with twice the keys to a byte, 12 warps against 8: 131 and 140 us), while
+// the warps of a cluster join their parts, and four of them with larger tiles do
+// better (one sequence of 500 tokens 6.8 us with 4 x 32 x 3, 8.8 with 12 x 16 x 2).
+struct Shape {
+  int keys, warps, stages;
+};
+constexpr Shape cached_shape(int D, bool e4m3, bool whole) {
+  if (e4m3) return whole ? Shape{32, 8, D == 128 ? 3 : 4} : Shape{32, 12, D == 128 ? 2 : 4};
+  if (whole) return D == 128 ? Shape{32, 4, 3} : Shape{32, 8, 3};
+  return D == 128 ? Shape{16, 12, 2} : Shape{32, 12, 2};
+}
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool WHOLE>
 struct CachedLayout {
-  static constexpr int kKT = kKeys;
-  static constexpr int kWarps = tile_warps(D, E4M3);
+  static constexpr Shape kShape = cached_shape(D, E4M3, WHOLE);
+  static constexpr int kKT = kShape.keys;
+  static constexpr int kWarps = kShape.warps;
   static constexpr int kRowBytes = E4M3 ? D : 128;              // of a swizzle atom
   static constexpr int kAtoms = E4M3 ? 1 : D / 64;
   static constexpr int kAtomBytes = kKT * kRowBytes;
@@ -236,7 +246,7 @@ struct CachedLayout {
   static constexpr int kScaleBytes = E4M3 ? 256 : 0;            // K or V
   // stages start at multiples of 1024 bytes; the scales of all stages follow
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = E4M3 ? (D == 128 ? 2 : 4) : (D == 128 ? 2 : 3);
+  static constexpr int kStages = kShape.stages;
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kScale = kWarps * kWarpBytes;
   static constexpr int kBar = kScale + kWarps * kStages * 2 * kScaleBytes;
@@ -339,11 +349,11 @@ struct Walk {
 // parts meet in shared memory (a CTA's, then the cluster's), so there is neither
 // a workspace nor a second kernel. For calls of few, short sequences.
 template <int D, bool E4M3, bool F16, bool WHOLE>
-__global__ void __launch_bounds__(32 * CachedLayout<D, E4M3>::kWarps, 1)
+__global__ void __launch_bounds__(32 * CachedLayout<D, E4M3, WHOLE>::kWarps, 1)
 fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const __grid_constant__ CUtensorMap tks, const __grid_constant__ CUtensorMap tvs,
                  const CachedParams p) {
-  using L = CachedLayout<D, E4M3>;
+  using L = CachedLayout<D, E4M3, WHOLE>;
   constexpr int KT = L::kKT, kWarps = L::kWarps;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -1048,7 +1058,8 @@ int whole_cluster(long long units, long long tiles, int warps) {
 
 int cached_whole(int B, int Nq, int Hq, int Hk, int d, int page_size, int max_pages, bool e4m3) {
   const long long units = (long long)B * Hk * (((long long)Nq * (Hq / Hk) + kRows - 1) / kRows);
-  return whole_cluster(units, ((long long)max_pages * page_size + kKeys - 1) / kKeys, tile_warps(d <= 64 ? 64 : 128, e4m3));
+  const Shape sh = cached_shape(d <= 64 ? 64 : 128, e4m3, true);
+  return whole_cluster(units, ((long long)max_pages * page_size + sh.keys - 1) / sh.keys, sh.warps);
 }
 
 fa_status check_cached_shape(int B, int Nq, int Hq, int Hk, int d) {
@@ -1071,7 +1082,8 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 template <int D, bool E4M3, bool F16>
 cudaError_t launch_cached_d(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tks,
                             const CUtensorMap& tvs, CachedParams p, cudaStream_t s) {
-  using L = CachedLayout<D, E4M3>;
+  using L = CachedLayout<D, E4M3, false>;
+  using LW = CachedLayout<D, E4M3, true>;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1081,14 +1093,14 @@ cudaError_t launch_cached_d(const CUtensorMap& tk, const CUtensorMap& tv, const 
                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
     return e1 != cudaSuccess ? e1
                              : cudaFuncSetAttribute(fa_cached_kernel<D, E4M3, F16, true>,
-                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, LW::kSmemBytes);
   });
   if (e != cudaSuccess) return e;
   if (p.cluster > 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.B * p.Hk * p.RT * p.cluster));
-    cfg.blockDim = dim3(32 * L::kWarps);
-    cfg.dynamicSmemBytes = L::kSmemBytes;
+    cfg.blockDim = dim3(32 * LW::kWarps);
+    cfg.dynamicSmemBytes = LW::kSmemBytes;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1226,7 +1238,8 @@ fa_status flash_attn_cached_fwd(const void* Q, int64_t q_token_stride, const voi
   if ((sr = internal_device_error_word(&err)) != FA_OK) return static_cast<fa_status>(sr);
 
   const int D = d <= 64 ? 64 : 128;
-  const uint32_t box_keys = (uint32_t)(page_size < kKeys ? page_size : kKeys);
+  const int keys = cached_shape(D, e4m3, cluster > 0).keys;
+  const uint32_t box_keys = (uint32_t)(page_size < keys ? page_size : keys);
   CUtensorMap tk, tv, tks, tvs;
   {
     const uint64_t es = e4m3 ? 1 : 2;
