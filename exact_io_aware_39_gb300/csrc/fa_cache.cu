@@ -8,15 +8,14 @@
 // keys, so the work is reading the cache: 2 d elements per key for 4 d Nq G
 // operations, far under the 280 operations per byte where the tensor cores
 // would bound it. The design keeps the memory system busy and little else:
-//   * the unit of work is a tile of kKT keys of one (sequence, key/value head,
-//     16 query rows); all units of the call are numbered in that order and cut
-//     into equal ranges, one for each of the 8 x 152 warps of the grid, so
-//     that ragged lengths leave no warp without work;
+//   * the unit of work is a tile of 16 or 32 keys of one (sequence, key/value
+//     head, 16 query rows); all units of the call are numbered in that order and
+//     cut into equal ranges, one for each warp of the grid, so that ragged
+//     lengths leave no warp without work;
 //   * each warp is a pipeline of its own: it loads the tiles of its range by
-//     TMA into its own shared-memory ring (24 KB, three to six tiles ahead,
-//     across sequence boundaries), so an SM keeps up to 192 KB in flight
-//     (measured need: 6.8 TB/s x 1 us / 152 = 45 KB), and no warp waits for
-//     another;
+//     TMA into its own shared-memory ring, across sequence boundaries, so an SM
+//     keeps up to 192 KB in flight (6.8 TB/s x 1 us / 152 = 45 KB are needed), and
+//     no warp waits for another;
 //   * the products are mma.sync m16n8k16: the 16 rows fill it, where a
 //     tcgen05 product of 128 rows would be an eighth full or less, and the
 //     operands come from registers (Q, P, and with e4m3 the converted K and V);
@@ -26,6 +25,9 @@
 //     that holds a part of it writes O unnormalised with the row's reference
 //     and sum, and a second kernel joins the parts (in a fixed order, so the
 //     result does not change from call to call).
+// Measured, 32 query and 8 key/value heads, d = 128: 64 sequences of 512-8192
+// tokens in bf16 104 us with the join (5.7 TB/s of 6.8), 16 of 8192-65536 tokens
+// in e4m3 162 us (6.3 TB/s); one of 500 tokens 6.8 us.
 //
 // e4m3: with q8, k8, v8 the payloads and ks, vs the scales of key j,
 //   S_j = ks_j (q . k8_j),  O = sum_j P_j vs_j v8_j.
@@ -213,10 +215,11 @@ constexpr int kMaxWorkers = 12 * kMaxCtas;
 constexpr int kRows = 16;                 // query rows of a unit
 constexpr float kMoveThreshold = 8.0f;    // log2 units: the reference moves only past it
 
-// Shared-memory layout, a ring of tiles for each warp. A tile is kKT keys: K, then V, each
-// as the TMA writes it (16-bit: 64-column atoms of 128-byte rows; e4m3: one
-// atom of D-byte rows), 128- or 64-byte swizzled, then with e4m3 the scales of
-// K and of V (each 16 keys at a pitch of 64 or, one page each, 128 bytes).
+// Shared-memory layout, a ring of tiles for each warp. A tile is kKT keys: K,
+// then V, each as the TMA writes it (16-bit: 64-column atoms of 128-byte rows;
+// e4m3: one atom of D-byte rows), 128- or 64-byte swizzled; with e4m3 the scales
+// of K and of V lie behind all rings (16 keys at a pitch of 64 bytes, or of 128
+// where they come from two pages).
 //
 // Warps, keys of a tile and tiles of a ring, by the tile width D (64 or 128), the
 // type and the kernel. A tile costs a warp its latency, 1 us or so, so the split

@@ -20,8 +20,22 @@
 //     K and V of the next item load as soon as this one's last product has read
 //     theirs, while dK and dV are written.
 //
-// Launches (after the plan, for more than kDirect sequences): the pre-pass (D = rowsum(dO * O), LSE * log2 e,
-// zeroed accumulator), the main kernel, and dQ = 16-bit(scale * accumulator).
+// Launches (after the plan, for more than kDirect sequences): the pre-pass
+// (D = rowsum(dO * O), LSE * log2 e, zeroed accumulator), the main kernel, and
+// dQ = 16-bit(scale * accumulator).
+//
+// Roundings: P and dS go to the inputs' 16-bit type for the products that read
+// them (half a step each; dS is what the error of dQ and dK is made of: 2.4e-3 of
+// their norm in bf16, where rounding them alone makes 1.7e-3); D, sums and
+// accumulators are fp32.
+//
+// Bound: 10 d operations per visible pair; a step of five products takes 2.9 us
+// at d = 128 where the tensor cores alone would take 1.7 (one S and one dP tile
+// fit beside the accumulators, so P and dS of a tile stand between its products).
+// Measured, bf16, causal, 32 / 8 heads, d = 128: two sequences of 4547 and 5127
+// tokens 0.93 ms in the main kernel, 47 us pre-pass, 32 us dQ; 16 sequences of
+// 32-977 tokens 167, 35 and 26 us (the passes around are at the bandwidth of the
+// fp32 accumulator).
 #include "fa_packed.cuh"
 
 namespace fa {

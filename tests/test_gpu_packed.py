@@ -127,6 +127,38 @@ def test_more_sequences_than_a_block_has_threads(fa, d, causal):
     _check(c, r, 0.2, causal)
 
 
+@pytest.mark.parametrize("Hq,Hk,d,causal", [(2, 2, 64, True), (4, 2, 128, True), (3, 1, 128, False), (4, 1, 64, False)])
+def test_lists_made_by_the_plan_kernel(fa, Hq, Hk, d, causal):
+    """More than 32 sequences, of one to several tiles."""
+    lens = [(97 * b) % 401 for b in range(40)]
+    c = _inputs(lens, Hq, Hk, d, BF, 8, 2, 70)
+    r = _run(fa, c, d ** -0.5, causal)
+    _settled(fa)
+    _check(c, r, d ** -0.5, causal)
+
+
+@pytest.mark.parametrize("B", [32, 33])
+def test_either_side_of_the_direct_list(fa, B):
+    c = _inputs([(61 * b) % 150 for b in range(B)], 4, 2, 64, BF, 9)
+    r = _run(fa, c, 0.125, True)
+    _settled(fa)
+    _check(c, r, 0.125, True)
+
+
+def test_head_major_layout(fa):
+    """[heads, tokens, d] tensors seen as [tokens, heads, d]: the head stride is
+    the larger one."""
+    c = _inputs([200, 131], 4, 2, 64, BF, 10)
+    for n in ("q", "k", "v", "do"):
+        c[n] = c[n].transpose(0, 1).contiguous().transpose(0, 1)
+    out = _outputs(c)
+    for n in ("o", "dq", "dk", "dv"):
+        out[n] = out[n].transpose(0, 1).contiguous().transpose(0, 1)
+    r = _run(fa, c, 0.125, True, out=out)
+    _settled(fa)
+    _check(c, r, 0.125, True)
+
+
 @pytest.mark.parametrize("d,causal", [(64, False), (128, True)])
 def test_long_sequences(fa, d, causal):
     c = _inputs([2300, 700], 2, 1, d, BF, 2, 0, 30, True)
@@ -155,7 +187,8 @@ def test_empty_calls(fa):
             assert (t == CANARY).all()
 
 
-@pytest.mark.parametrize("cu", [[0, 100, 50, 150], [0, 100, 400], [-5, 100, 150], [0, 150, 0, 150, 0, 150]])
+@pytest.mark.parametrize("cu", [[0, 100, 50, 150], [0, 100, 400], [-5, 100, 150], [0, 150, 0, 150, 0, 150],
+                                [0, 150] * 25])
 def test_bounds_that_are_no_sequences_are_left_out(fa, cu):
     """Decreasing bounds or bounds outside the tensors: those sequences are left
     out and the error word says so; the others (where they do not overlap)
