@@ -415,41 +415,39 @@ def standard_attention_bwd(q, k, v, do, workspace, scale, stream=None, s16=False
 FA_CACHE_16BIT, FA_CACHE_E4M3 = 0, 1
 PACKED_DIRECT = 32           # a forward of so many sequences needs no workspace
 _I64x8, _I64x16 = ctypes.c_int64 * 8, ctypes.c_int64 * 16
-_opts = {}
+_default_options = {}        # dtype -> (reference to) its fa_options
+torch = None                 # bound with the library, by the first call
 
 
-def _options(t, wait_limit_us, test_stall):
-    """(reference to) the fa_options for t's dtype and the checking fields."""
-    import torch
-    if t.dtype not in (torch.bfloat16, torch.float16) or not t.is_cuda:
+def _begin(t, wait_limit_us=0, test_stall=0):
+    """The library, and (a reference to) the fa_options for t's dtype and the
+    checking fields."""
+    global torch
+    lib = _lib
+    if lib is None or torch is None:
+        import torch as module
+        torch, lib = module, load()
+        for dt, code in ((torch.bfloat16, FA_DTYPE_BF16), (torch.float16, FA_DTYPE_F16)):
+            _default_options[dt] = ctypes.byref(fa_options(code))
+    opts = _default_options.get(t.dtype)
+    if opts is None or not t.is_cuda:
         raise ValueError("q (or k) must be a bfloat16 or float16 CUDA tensor")
-    key = (t.dtype, wait_limit_us, test_stall)
-    o = _opts.get(key)
-    if o is None:
-        o = fa_options(FA_DTYPE_F16 if t.dtype == torch.float16 else FA_DTYPE_BF16, wait_limit_us=wait_limit_us,
-                       test_stall=test_stall)
-        o = ctypes.byref(o)
-        if not (wait_limit_us or test_stall):
-            _opts[key] = o
-    return o
+    if wait_limit_us or test_stall:
+        opts = ctypes.byref(fa_options(FA_DTYPE_F16 if t.dtype is torch.float16 else FA_DTYPE_BF16,
+                                       wait_limit_us=wait_limit_us, test_stall=test_stall))
+    return lib, opts
 
 
 def _elsewhere(stream, dev):
     """None when a call launches on the current stream of the current device
     (dev), else the context to allocate and launch in."""
-    import torch
     if stream is None:
-        if dev == torch.cuda.current_device():
+        if dev == torch._C._cuda_getDevice():
             return None
         return torch.cuda.stream(torch.cuda.current_stream(dev))
     if stream.device.index != dev:
         raise ValueError("the stream belongs to another device than the tensors")
     return torch.cuda.stream(stream)     # (also makes its device the current one)
-
-
-def _current_stream(dev):
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _rows16(t, name, shape, dtype, dev):
@@ -475,7 +473,6 @@ def _plain(t, name, shape, dtype, dev):
 
 def _scratch(workspace, need, dev):
     """The caller's workspace, or a new one: (tensor, bytes)."""
-    import torch
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=dev), need
     if workspace.get_device() != dev or not workspace.is_contiguous():
@@ -491,8 +488,7 @@ def attention_packed_fwd(q, k, v, cu_seqlens, scale, causal=True, out=None, lse=
     of a fused projection are. cu_seqlens: int32 [B + 1], sequence b is rows
     cu_seqlens[b] .. cu_seqlens[b + 1] - 1. Returns O like q and LSE float32
     [Hq, tokens]; rows of no sequence are left as they are in `out` and `lse`."""
-    import torch
-    opts = _options(q, wait_limit_us, test_stall)
+    lib, opts = _begin(q, wait_limit_us, test_stall)
     dev = q.get_device()
     ctx = _elsewhere(stream, dev)
     if ctx is not None:
@@ -515,11 +511,11 @@ def attention_packed_fwd(q, k, v, cu_seqlens, scale, causal=True, out=None, lse=
                 *_rows16(v, "v", (T, Hk, d), dt, dev), *_rows16(out, "out", (T, Hq, d), dt, dev))
     ws, nbytes = None, 0
     if B > PACKED_DIRECT or workspace is not None:
-        workspace, nbytes = _scratch(workspace, flash_attn_packed_workspace_size(B, T, Hq, Hk, d, 0), dev)
+        workspace, nbytes = _scratch(workspace, lib.flash_attn_packed_workspace_size(B, T, Hq, Hk, d, 0), dev)
         ws = workspace.data_ptr()
-    rc = load().flash_attn_packed_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                      cu_seqlens.data_ptr(), B, T, Hq, Hk, d, st, scale, 1 if causal else 0, opts, ws,
-                                      nbytes, _current_stream(dev))
+    rc = lib.flash_attn_packed_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                   cu_seqlens.data_ptr(), B, T, Hq, Hk, d, st, scale, 1 if causal else 0, opts, ws,
+                                   nbytes, torch._C._cuda_getCurrentRawStream(dev))
     _check(rc, "flash_attn_packed_fwd")
     return out, lse
 
@@ -530,8 +526,7 @@ def attention_packed_bwd(q, k, v, o, do, lse, cu_seqlens, scale, causal=True, wo
     output gradient do (like q); dK and dV are summed over the query heads that
     share a key/value head. Rows of no sequence are left as they are in dq, dk,
     dv (which may be strided like q, k, v)."""
-    import torch
-    opts = _options(q, wait_limit_us, test_stall)
+    lib, opts = _begin(q, wait_limit_us, test_stall)
     dev = q.get_device()
     ctx = _elsewhere(stream, dev)
     if ctx is not None:
@@ -555,18 +550,17 @@ def attention_packed_bwd(q, k, v, o, do, lse, cu_seqlens, scale, causal=True, wo
     st = _I64x16(*_rows16(q, "q", hq, dt, dev), *_rows16(k, "k", hk, dt, dev), *_rows16(v, "v", hk, dt, dev),
                  *_rows16(o, "o", hq, dt, dev), *_rows16(do, "do", hq, dt, dev), *_rows16(dq, "dq", hq, dt, dev),
                  *_rows16(dk, "dk", hk, dt, dev), *_rows16(dv, "dv", hk, dt, dev))
-    workspace, nbytes = _scratch(workspace, flash_attn_packed_workspace_size(B, T, Hq, Hk, d, 1), dev)
-    rc = load().flash_attn_packed_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
-                                      lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                                      cu_seqlens.data_ptr(), B, T, Hq, Hk, d, st, scale, 1 if causal else 0, opts,
-                                      workspace.data_ptr(), nbytes, _current_stream(dev))
+    workspace, nbytes = _scratch(workspace, lib.flash_attn_packed_workspace_size(B, T, Hq, Hk, d, 1), dev)
+    rc = lib.flash_attn_packed_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+                                   lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                   cu_seqlens.data_ptr(), B, T, Hq, Hk, d, st, scale, 1 if causal else 0, opts,
+                                   workspace.data_ptr(), nbytes, torch._C._cuda_getCurrentRawStream(dev))
     _check(rc, "flash_attn_packed_bwd")
     return dq, dk, dv
 
 
 def _cache_args(k_cache, v_cache, k_scale, v_scale, dtype, dev):
     """Checks the tensors of a paged cache; returns the cache type."""
-    import torch
     if k_cache.dim() != 4:
         raise ValueError("k_cache and v_cache must be [num_pages, Hk, page_size, d]")
     shape, kind = k_cache.shape, k_cache.dtype
@@ -592,8 +586,7 @@ def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, st
     cache of the tokens' dtype takes them as they are; a float8_e4m3fn cache
     takes them quantised, with one power-of-two scale per row in k_scale,
     v_scale (float32 [num_pages, Hk, page_size])."""
-    import torch
-    opts = _options(k, 0, 0)
+    lib, opts = _begin(k)
     dev = k.get_device()
     ctx = _elsewhere(stream, dev)
     if ctx is not None:
@@ -607,10 +600,10 @@ def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, st
     v_tok, v_head = _rows16(v, "v", (T, Hk, d), dt, dev)
     _plain(slots, "slots", (T,), torch.int64, dev)
     e4m3 = kind == FA_CACHE_E4M3
-    rc = load().flash_attn_kv_cache_write(k.data_ptr(), v.data_ptr(), k_tok, k_head, v_tok, v_head, slots.data_ptr(), T,
-                                          Hk, d, k_cache.data_ptr(), v_cache.data_ptr(),
-                                          k_scale.data_ptr() if e4m3 else None, v_scale.data_ptr() if e4m3 else None,
-                                          pages, page, kind, opts, _current_stream(dev))
+    rc = lib.flash_attn_kv_cache_write(k.data_ptr(), v.data_ptr(), k_tok, k_head, v_tok, v_head, slots.data_ptr(), T,
+                                       Hk, d, k_cache.data_ptr(), v_cache.data_ptr(),
+                                       k_scale.data_ptr() if e4m3 else None, v_scale.data_ptr() if e4m3 else None,
+                                       pages, page, kind, opts, torch._C._cuda_getCurrentRawStream(dev))
     _check(rc, "flash_attn_kv_cache_write")
 
 
@@ -623,8 +616,7 @@ def attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_sc
     int32 [B] counts each sequence's tokens, the newest Nq included. Token i of
     the Nq sees seq_lens - (Nq - 1 - i) keys; query head h reads key/value head
     h // (Hq // Hk). Returns O like q (contiguous) and LSE float32 [B, Hq, Nq]."""
-    import torch
-    opts = _options(q, wait_limit_us, test_stall)
+    lib, opts = _begin(q, wait_limit_us, test_stall)
     dev = q.get_device()
     ctx = _elsewhere(stream, dev)
     if ctx is not None:
@@ -651,7 +643,7 @@ def attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_sc
         lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
     else:
         _plain(lse, "lse", (B, Hq, Nq), torch.float32, dev)
-    lib, width = load(), block_table.shape[1]
+    width = block_table.shape[1]
     ws, nbytes = None, 0
     if workspace is not None or lib.flash_attn_cached_needs_workspace(B, Nq, Hq, Hk, d, page, width, kind):
         workspace, nbytes = _scratch(workspace, lib.flash_attn_cached_workspace_size(B, Nq, Hq, Hk, d), dev)
@@ -660,6 +652,6 @@ def attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_sc
     rc = lib.flash_attn_cached_fwd(q.data_ptr(), tok, k_cache.data_ptr(), v_cache.data_ptr(),
                                    k_scale.data_ptr() if e4m3 else None, v_scale.data_ptr() if e4m3 else None,
                                    block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Nq, Hq,
-                                   Hk, d, pages, page, width, scale, kind, opts, ws, nbytes, _current_stream(dev))
+                                   Hk, d, pages, page, width, scale, kind, opts, ws, nbytes, torch._C._cuda_getCurrentRawStream(dev))
     _check(rc, "flash_attn_cached_fwd")
     return out, lse
