@@ -225,14 +225,16 @@ constexpr float kMoveThreshold = 8.0f;    // log2 units: the reference moves onl
 // type and the kernel. A tile costs a warp its latency, 1 us or so, so the split
 // over the GPU wants warps (16-bit, d = 128, 12 x 16 keys x 2 against 6 x 32 x 2:
 // 256 sequences of 20-200 tokens 28.7 and 37.4 us, 16 of 8192-65536 243 and 246;
-// e4m3, with twice the keys to a byte, 12 warps against 8: 131 and 140 us), while
+// e4m3, with twice the keys to a byte, 12 warps against 8: 131 and 140 us; at
+// d = 64 with 64-key tiles, so that a step has as many bytes as at 128: 64
+// sequences of 512-8192 tokens 43 us, 48 with 12 x 32 x 4, 45 with 8 x 64 x 3), while
 // the warps of a cluster join their parts, and four of them with larger tiles do
 // better (one sequence of 500 tokens 6.8 us with 4 x 32 x 3, 8.8 with 12 x 16 x 2).
 struct Shape {
   int keys, warps, stages;
 };
 constexpr Shape cached_shape(int D, bool e4m3, bool whole) {
-  if (e4m3) return whole ? Shape{32, 8, D == 128 ? 3 : 4} : Shape{32, 12, D == 128 ? 2 : 4};
+  if (e4m3) return whole ? Shape{32, 8, D == 128 ? 3 : 4} : Shape{D == 128 ? 32 : 64, 12, 2};
   if (whole) return D == 128 ? Shape{32, 4, 3} : Shape{32, 8, 3};
   return D == 128 ? Shape{16, 12, 2} : Shape{32, 12, 2};
 }
@@ -246,17 +248,25 @@ struct CachedLayout {
   static constexpr int kAtoms = E4M3 ? 1 : D / 64;
   static constexpr int kAtomBytes = kKT * kRowBytes;
   static constexpr int kTileBytes = kAtoms * kAtomBytes;        // K or V
-  static constexpr int kScaleBytes = E4M3 ? 256 : 0;            // K or V
+  static constexpr int kScaleBytes = E4M3 ? 8 * kKT : 0;        // K or V
   // stages start at multiples of 1024 bytes; the scales of all stages follow
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kStages = kShape.stages;
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kScale = kWarps * kWarpBytes;
-  static constexpr int kBar = kScale + kWarps * kStages * 2 * kScaleBytes;
+  // What a tile's scales do to its scores: worked out by every lane for its own
+  // keys, or, with 64 keys, once per key and passed on through shared memory (per
+  // warp, by pairs of keys: the factors and the log2 added, then the reciprocals).
+  // The calls above at d = 64 40 us so and 43 without; at d = 128, with 32 keys,
+  // the step through memory costs more than it saves (136 and 131 us).
+  static constexpr bool kByKey = E4M3 && kKT == 64;
+  static constexpr int kFactorBytes = kByKey ? 12 * kKT : 0;
+  static constexpr int kFactors = kScale + kWarps * kStages * 2 * kScaleBytes;
+  static constexpr int kBar = kFactors + kWarps * kFactorBytes;
   static constexpr int kMisc = kBar + 8 * kWarps * kStages;     // abort flag, -, wait limit, -
   static constexpr int kScan = kMisc + 16;                      // int64 [kWarps] totals, int64 [kWarps] starts, int [kWarps]
   static constexpr int kMl = (kScan + kWarps * 20 + 15) & ~15;  // (reference, sum) of kRows rows of each warp's part and of the CTA's
-  static constexpr int kSmemBytes = kMl + (kWarps + 1) * kRows * 8;
+  static constexpr int kSmemBytes = kMl + (WHOLE ? (kWarps + 1) * kRows * 8 : 0);
   static constexpr uint32_t kTxBytes = 2u * kTileBytes + (E4M3 ? 2u * kKT * 4u : 0u);
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
@@ -477,12 +487,12 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
   const uint32_t ring = sbase + (uint32_t)(warp * L::kWarpBytes);
   const uint32_t sring = sbase + L::kScale + (uint32_t)(warp * L::kStages * 2 * L::kScaleBytes);
   const int box = p.page_size < KT ? p.page_size : KT;     // keys of a piece
-  const int pieces = KT / box;                             // 1 or 2
+  const int pieces = KT / box;                             // 1, 2 or 4
   const int nowhere = p.num_pages * p.Hk;                  // a coordinate past the cache: reads as zeros
   int issued = 0;
-  // page of lane i's piece of the tile (lanes 0 and 1), or -1
+  // page of lane i's piece of the tile, or -1
   auto page_of = [&](const Walk& w) -> int {
-    const int key = w.j * KT + (lane & 1) * box;
+    const int key = w.j * KT + (lane & (KT / 16 - 1)) * box;
     return w.b < p.B && key < w.len ? p.table[(int64_t)w.b * p.max_pages + (key >> p.ps_log2)] : -1;
   };
   auto issue = [&](const Walk& w, int pages) {
@@ -623,6 +633,23 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
       __syncwarp();
     }
 
+    [[maybe_unused]] float* f = reinterpret_cast<float*>(smem + L::kFactors + warp * L::kFactorBytes);   // (kByKey)
+    [[maybe_unused]] const uint8_t* ss = smem + (sring - sbase) + s * 2 * L::kScaleBytes;
+    // (16 keys of a page, or more of them in one piece)
+    [[maybe_unused]] auto place = [&](int key) -> int { return box == 16 ? (key >> 4) * 128 + (key & 15) * 4 : key * 4; };
+    if constexpr (L::kByKey) {
+#pragma unroll
+      for (int key = lane; key < KT; key += 32) {
+        const float ks = *reinterpret_cast<const float*>(ss + place(key));
+        const float vs = key < left ? *reinterpret_cast<const float*>(ss + L::kScaleBytes + place(key)) : 1.f;
+        const int at = 4 * (key >> 1) + (key & 1);
+        f[at] = ks * p.scale_log2;
+        f[at + 2] = __log2f(vs);
+        f[2 * KT + key] = __fdividef(1.f, vs);
+      }
+      __syncwarp();
+    }
+
     // S = Q K^T: sc[2 n + i] of key 8 n + 2 t4 + (i & 1), rows g (i < 2) and g + 8
     float sc[KT / 8][4];
 #pragma unroll
@@ -667,23 +694,28 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     // scores in log2 units; with e4m3 plus log2 of the value's scale
     float ivs[KT / 8][2];
     if constexpr (E4M3) {
-      const uint8_t* ss = smem + (sring - sbase) + s * 2 * L::kScaleBytes;
 #pragma unroll
       for (int n = 0; n < KT / 8; ++n) {
-        const int key = 8 * n + 2 * t4;
-        const int off = (box == 16 ? (key >> 4) * 128 + (key & 15) * 4 : key * 4);
-        const float2 ks2 = *reinterpret_cast<const float2*>(ss + off);
-        float2 vs2 = *reinterpret_cast<const float2*>(ss + L::kScaleBytes + off);
-        if (key >= left) vs2.x = 1.f;       // past the sequence: any scale, the weight is zero
-        if (key + 1 >= left) vs2.y = 1.f;
-        ivs[n][0] = __fdividef(1.f, vs2.x);
-        ivs[n][1] = __fdividef(1.f, vs2.y);
-        const float lv0 = __log2f(vs2.x), lv1 = __log2f(vs2.y);
-        const float a0 = ks2.x * p.scale_log2, a1 = ks2.y * p.scale_log2;
-        sc[n][0] = fmaf(sc[n][0] * qs[0], a0, lv0);
-        sc[n][1] = fmaf(sc[n][1] * qs[0], a1, lv1);
-        sc[n][2] = fmaf(sc[n][2] * qs[1], a0, lv0);
-        sc[n][3] = fmaf(sc[n][3] * qs[1], a1, lv1);
+        float4 fa;   // two keys' factors, then what is added
+        if constexpr (L::kByKey) {
+          fa = *reinterpret_cast<const float4*>(f + 4 * (4 * n + t4));
+          const float2 iv = *reinterpret_cast<const float2*>(f + 2 * KT + 2 * (4 * n + t4));
+          ivs[n][0] = iv.x;
+          ivs[n][1] = iv.y;
+        } else {
+          const int key = 8 * n + 2 * t4;
+          const float2 ks2 = *reinterpret_cast<const float2*>(ss + place(key));
+          float2 vs2 = *reinterpret_cast<const float2*>(ss + L::kScaleBytes + place(key));
+          if (key >= left) vs2.x = 1.f;       // past the sequence: any scale, the weight is zero
+          if (key + 1 >= left) vs2.y = 1.f;
+          ivs[n][0] = __fdividef(1.f, vs2.x);
+          ivs[n][1] = __fdividef(1.f, vs2.y);
+          fa = make_float4(ks2.x * p.scale_log2, ks2.y * p.scale_log2, __log2f(vs2.x), __log2f(vs2.y));
+        }
+        sc[n][0] = fmaf(sc[n][0] * qs[0], fa.x, fa.z);
+        sc[n][1] = fmaf(sc[n][1] * qs[0], fa.y, fa.w);
+        sc[n][2] = fmaf(sc[n][2] * qs[1], fa.x, fa.z);
+        sc[n][3] = fmaf(sc[n][3] * qs[1], fa.y, fa.w);
       }
     } else {
 #pragma unroll
