@@ -962,18 +962,20 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 
 // Joins the parts of a query row. m is a part's reference, l its sum:
 //   O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k,  M = max m_k.
-// WARPS warps share a row's parts out (a lane holds D / 32 columns); with
+// WARPS warps share a row's parts out (a lane holds D / 32 columns, and the
+// columns of kAhead parts are on their way before their weights are known); with
 // WARPS = 1 a block of four warps joins four rows. The rows of one launch have
-// about as many parts each as there are workers to a (sequence, head, row tile);
-// from kManyParts on 16 warps take a row, so that no warp walks a long list (one
-// sequence of 32768 tokens, 152 parts a row: the call takes 33.7 us so, 40.2 with
-// four warps), and below it one (256 sequences of 20-200 tokens: 33.0 us, against
-// 37.4 with a block of four warps for every row).
+// about as many parts each as there are workers to a (sequence, head, row tile):
+// from 8 kManyParts on 16 warps take a row, so that no warp walks a long list (one
+// sequence of 32768 tokens, 228 parts a row: the call takes 29.5 us so, 37.4 with
+// four warps), from kManyParts on four (16 sequences of 8192-65536 tokens in e4m3,
+// 14 parts: 129.7 us, 131.8 with one, 133.9 with 16), and below it one (256
+// sequences of 20-200 tokens: 33.0 us, against 37.4 with a block of four).
 constexpr int kManyParts = 8;
 
 template <int D, bool F16, int WARPS>
 __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) fa_cached_join_kernel(const CachedParams p) {
-  constexpr int C = D / 32;
+  constexpr int C = D / 32, kAhead = 8;
   __shared__ float sm_o[WARPS == 1 ? 1 : WARPS][D];
   __shared__ float2 sm_ml[WARPS];
   grid_dep_wait();   // the parts are complete
@@ -990,7 +992,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) fa_cached_join_
   const int rr = r % kRows, parts = f.y - f.x + 1;
   auto at = [&](int k) -> int64_t { return (int64_t)(2 * (f.x + k) + (k == 0 ? 1 : 0)) * kRows + rr; };
   // this warp's parts k0, k0 + step, ..., a lane looking after the weight of one
-  // of 32 of them, four parts' columns on their way at a time
+  // of 32 of them, kAhead parts' columns on their way at a time
   const int k0 = WARPS == 1 ? 0 : warp, step = WARPS;
   const int mine = k0 < parts ? (parts - k0 + step - 1) / step : 0;
   float M = -INFINITY, l = 0.f, acc[C];
@@ -999,6 +1001,27 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) fa_cached_join_
   for (int base = 0; base < mine; base += 32) {
     const int n = min(32, mine - base);
     const float2 ml = lane < n ? p.part_ml[at(k0 + step * (base + lane))] : make_float2(-INFINITY, 0.f);
+    // (the first columns are on their way while the weights are worked out)
+    float v[kAhead][C];
+    auto load = [&](int from) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (from + k < n) {
+          const float* po = p.part_o + at(k0 + step * (base + from + k)) * D + C * lane;
+          if constexpr (C == 4) {
+            const float4 x4 = *reinterpret_cast<const float4*>(po);
+            v[k][0] = x4.x;
+            v[k][1] = x4.y;
+            v[k][C - 2] = x4.z;
+            v[k][C - 1] = x4.w;
+          } else {
+            const float2 x2 = *reinterpret_cast<const float2*>(po);
+            v[k][0] = x2.x;
+            v[k][1] = x2.y;
+          }
+        }
+    };
+    load(0);
     float mx = ml.x;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
@@ -1011,15 +1034,15 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) fa_cached_join_
     l = fmaf(l, old, ls);
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] *= old;
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float* po = p.part_o + at(k0 + step * (base + k)) * D + C * lane;
-      const float w = __shfl_sync(0xFFFFFFFFu, wt, k);
+    for (int from = 0; from < n; from += kAhead) {
+      if (from > 0) load(from);
 #pragma unroll
-      for (int c = 0; c < C; c += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(po + c);
-        acc[c] = fmaf(w, v.x, acc[c]);
-        acc[c + 1] = fmaf(w, v.y, acc[c + 1]);
+      for (int k = 0; k < kAhead; ++k) {
+        const float w = __shfl_sync(0xFFFFFFFFu, wt, from + k);
+        if (from + k < n) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) acc[c] = fmaf(w, v[k][c], acc[c]);
+        }
       }
     }
   }
@@ -1157,8 +1180,11 @@ cudaError_t launch_cached_d(const CUtensorMap& tk, const CUtensorMap& tv, const 
                  tks, tvs, p);
   if (e != cudaSuccess) return e;
   const unsigned rows = (unsigned)(p.B * p.Hq * p.Nq);
-  if ((long long)p.B * p.Hk * p.RT * kManyParts <= (long long)L::kWarps * ctas)
+  const long long units = (long long)p.B * p.Hk * p.RT, workers = (long long)L::kWarps * ctas;
+  if (units * 8 * kManyParts <= workers)
     return launch_pdl(true, fa_cached_join_kernel<D, F16, 16>, dim3(rows), dim3(512), 0, s, p);
+  if (units * kManyParts <= workers)
+    return launch_pdl(true, fa_cached_join_kernel<D, F16, 4>, dim3(rows), dim3(128), 0, s, p);
   return launch_pdl(true, fa_cached_join_kernel<D, F16, 1>, dim3((rows + 3) / 4), dim3(128), 0, s, p);
 }
 
