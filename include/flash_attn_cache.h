@@ -16,7 +16,9 @@
  *                       infinities), with one fp32 scale per row
  *   k_scale, v_scale : fp32 [num_pages, Hk, page_size] (FA_CACHE_E4M3 only,
  *       else NULL). An element stands for payload * scale. The writer stores
- *       powers of two; the reader takes any positive finite scale >= 2^-64.
+ *       powers of two; the reader takes any scale from 2^-64 to 2^120 (value
+ *       scales of one sequence more than 2^100 apart may cost it weights
+ *       below 2^-26 of the largest).
  *   page_size is 16, 32, 64, 128 or 256. Token j of a sequence lives in place
  *   j mod page_size of page block_table[b][j / page_size].
  *

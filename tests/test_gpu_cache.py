@@ -324,6 +324,31 @@ def test_shared_pages(fa):
     _check(c, 0.2, o, lse)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_pages_past_32_bits(fa, e4m3):
+    """A cache of more than 2^31 elements whose last pages are written and read:
+    what a small cache gives, bit for bit."""
+    B, Hq, Hk, d, page, pages = 2, 8, 8, 128, 64, 36000
+    lens = [150, 70]
+    k, v = _rows(sum(lens), Hk, d, BF, 8, False)
+    ids = [[35999, 1, 33000], [35000, 34999, 0]]
+    q = torch.randn(B, 1, Hq, d, generator=torch.Generator().manual_seed(2)).to(BF).cuda()
+    res = []
+    for n, table in ((6, [[0, 1, 2], [3, 4, 5]]), (pages, ids)):
+        mk = lambda: torch.empty(n, Hk, page, d, dtype=torch.float8_e4m3fn if e4m3 else BF, device="cuda")
+        sc = lambda: torch.empty(n, Hk, page, device="cuda") if e4m3 else None
+        cache = (mk(), mk(), sc(), sc())
+        slots = [table[b][j // page] * page + j % page for b in range(B) for j in range(lens[b])]
+        fa.kv_cache_write(k, v, torch.tensor(slots, device="cuda"), *cache)
+        t = torch.tensor(table, dtype=torch.int32, device="cuda")
+        res.append(fa.attention_cached_fwd(q, cache[0], cache[1], t, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                           0.1, k_scale=cache[2], v_scale=cache[3]))
+        _settled(fa)
+        del cache
+    for a, b in zip(*res):
+        assert torch.equal(_bits(a), _bits(b)) and torch.isfinite(a.float()).all()
+
+
 @pytest.mark.parametrize("room", [0, 1 << 17], ids=["on_chip", "ranges"])
 def test_other_streams_and_replayed_graphs(fa, room):
     """Two calls at once on two streams with workspaces of their own, and a

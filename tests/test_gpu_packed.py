@@ -176,6 +176,31 @@ def test_large_scores(fa, d):
     _check(c, r, 0.25, True)
 
 
+def test_offsets_past_32_bits(fa):
+    """Every tensor a view of one buffer whose tokens are 2^26 elements apart:
+    the last tokens lie past 2^31 elements. The results are those of small
+    tensors, bit for bit (dQ's sums have one term here)."""
+    T, Hq, Hk, d = 40, 4, 2, 64
+    c = _inputs([33, 7], Hq, Hk, d, BF, 12)
+    want = _run(fa, c, 0.125, True)
+    _settled(fa)
+    big = torch.empty(T, 1 << 26, dtype=BF, device="cuda")
+    at = 1 << 25
+    def far(x):
+        nonlocal at
+        y = big[:, at:at + x.shape[1] * d].view(T, x.shape[1], d)
+        at += x.shape[1] * d
+        return y.copy_(x)
+    f = {n: far(c[n]) for n in ("q", "k", "v", "do")}
+    f["cu"] = c["cu"]
+    out = {n: far(torch.full_like(t, CANARY)) for n, t in want.items() if n != "lse"}
+    out["lse"] = torch.full_like(want["lse"], CANARY)
+    _run(fa, f, 0.125, True, out=out)
+    _settled(fa)
+    for n, t in want.items():
+        assert torch.equal(_bits(t), _bits(out[n].contiguous())), n
+
+
 def test_empty_calls(fa):
     for T, cu in ((0, [0, 0, 0]), (5, [0]), (5, [2, 2, 2])):
         q = torch.randn(T, 4, 64, device="cuda").to(BF)
