@@ -650,11 +650,15 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       const int s4 = lane & 3;
       const int row0 = kTile * qi + 32 * (warp & 3) + (lane & ~3);   // the quad's first row
       uint16_t* op = p.o + (int64_t)(w.start + row0) * p.o_tok + w.hq(t) * p.o_head + 8 * s4;
+      uint32_t next[32];   // (the next columns come while these are written)
+      tmem_ld32(tO, next);
 #pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t u[32];
-        tmem_ld32(tO + 32u * cc, u);
-        tmem_ld_wait(u);
+        tmem_ld_wait(next);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) u[i] = next[i];
+        if (cc + 1 < D / 32) tmem_ld32(tO + 32u * (cc + 1), next);
         uint32_t x[4][4];   // [word of a chunk][chunk of this row, then row of the quad]
 #pragma unroll
         for (int wd = 0; wd < 4; ++wd) {
