@@ -320,6 +320,8 @@ fa_status flash_attn_packed_bwd(const void* Q, const void* K, const void* V, con
   p.d = d;
   p.causal = causal;
   p.cap_tiles = w.cap_tiles;
+  p.parts = w.parts;
+  p.part = reinterpret_cast<float*>(ws + w.part_off);
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_us = o.wait_us;

@@ -26,8 +26,9 @@ struct PackedPlan {
 // Workspace sections (byte offsets, 256-aligned). The lists are sized for the
 // most tiles B sequences of `total` tokens can have.
 struct PackedWorkspace {
-  size_t plan_off, sorted_off, item_off, tile_off, dq_off, lse2_off, delta_off, total;
+  size_t plan_off, sorted_off, item_off, tile_off, dq_off, lse2_off, delta_off, part_off, total;
   int cap_items, cap_tiles;
+  int parts;   // backward: parts of a work item
   bool ok;   // the counts fit 32-bit work indices
 };
 
@@ -36,6 +37,22 @@ struct PackedWorkspace {
 // (24 sequences of 16-2048 tokens, 32 / 8 heads, d = 128: 124 us with pairs of
 // heads, 144 with pairs of tiles; one of 16384: 1217 and 1228).
 inline bool packed_pair_heads(int Hq, int Hk) { return (Hq / Hk) % 2 == 0; }
+
+// The backward's item is a key tile of a key/value head with all of its query
+// tiles, of all G query heads: G n steps for the first tile of a sequence of n
+// tiles. Where there are not two items for every SM, items are cut into parts
+// of about as many steps as an SM gets in all, whose dK and dV are summed by the
+// last pass.
+constexpr int kMaxParts = 16;
+inline int packed_bwd_parts(int B, int total, int Hk, int G, long long tiles) {
+  constexpr double kSms = 152.;
+  const double items = (double)tiles * Hk;
+  if (items >= 2. * kSms || B < 1) return 1;
+  const double n = (double)((total + (long long)kTile * B - 1) / ((long long)kTile * B));   // tiles of an average sequence
+  const double per_sm = items * G * (n + 1.) / 2. / kSms;
+  const double parts = G * n / (per_sm > 1. ? per_sm : 1.);
+  return parts >= kMaxParts ? kMaxParts : parts <= 1. ? 1 : (int)parts;
+}
 
 inline PackedWorkspace packed_workspace_layout(int B, int total, int Hq, int Hk, int d, bool backward) {
   auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
@@ -52,7 +69,10 @@ inline PackedWorkspace packed_workspace_layout(int B, int total, int Hq, int Hk,
   const size_t rows = backward ? (size_t)Hq * w.cap_tiles * kTile : 0;
   w.lse2_off = al(w.dq_off + rows * d * sizeof(float));
   w.delta_off = al(w.lse2_off + rows * sizeof(float));
-  w.total = al(w.delta_off + rows * sizeof(float));
+  w.part_off = al(w.delta_off + rows * sizeof(float));
+  w.parts = backward && w.ok ? packed_bwd_parts(B, total, Hk, Hq / Hk, tiles) : 1;
+  w.total = w.part_off;
+  if (w.parts > 1) w.total = al(w.part_off + (size_t)w.parts * 2 * Hk * w.cap_tiles * kTile * d * sizeof(float));
   return w;
 }
 
@@ -97,7 +117,9 @@ struct PackedBwdParams {
   int total, Hq, Hk, G, d, causal, cap_tiles;
   float scale, scale_log2;
   uint32_t wait_us, stall;
-  int group;                  // key/value heads per group of the work order
+  int parts;                  // of an item
+  float* part;                // parts > 1: fp32 [parts, 2 (dK, dV), Hk, cap_tiles * 128, d]
+  int group;                  // (key/value head, part) pairs per group of the work order
 };
 
 // Rows [start, start + len) of sequence b; an empty one (bad set) where its

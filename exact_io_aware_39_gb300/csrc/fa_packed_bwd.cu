@@ -85,15 +85,15 @@ struct PackedBwdLayout {
   static constexpr int bDrain = bFinal + 1;
   static constexpr int bKVFree = bDrain + 1;   // [kKV]: the item's last product has read K and V
   // work items reach the other roles through a ring filled by the producer
-  static constexpr int kItemRing = 4;
+  static constexpr int kItemRing = 4, kItemInts = 9;
   static constexpr int bItemFull = bKVFree + kKV;            // [kItemRing]
   static constexpr int bItemEmpty = bItemFull + kItemRing;   // [kItemRing]: MMA warp, compute and drain warps
   static constexpr int bdSHalf = bItemEmpty + kItemRing;     // the first 32 dS^T columns of each warpgroup
   static constexpr int bClc = bdSHalf + 1;                   // the next item's cancellation answer has arrived
   static constexpr int kNumBars = bClc + 1;
   static constexpr int kMisc = (kBar + 8 * kNumBars + 15) & ~15;   // tmem slot, abort flag, -, wait limit
-  static constexpr int kRing = kMisc + 16;                    // [kItemRing] x {key tile, head, first row, length, first padded tile, -, -, -}
-  static constexpr int kClc = kRing + 32 * kItemRing;   // 16-byte answer of a launch cancellation
+  static constexpr int kRing = kMisc + 16;                    // [kItemRing] x {key tile, head, first row, length, first padded tile, steps, first query head, first query tile, place of a part}
+  static constexpr int kClc = (kRing + 4 * kItemInts * kItemRing + 15) & ~15;   // 16-byte answer of a launch cancellation
   static constexpr int kSmemBytes = kClc + 16;
   // the dQ partial is drained per warp (each warp adds its own 32 rows) at
   // d = 128 and by the four warps together (whole 128-row boxes) at d = 64:
@@ -120,9 +120,11 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
 
   // An item: key tile kj of the sequence of rows start .. start + len - 1, for
   // key/value head hk; its query tiles i0 .. nT - 1 of each of the G query
-  // heads, a head after the other; slot0 is the sequence's first padded tile.
+  // heads, a head after the other, or `steps` of them from tile i of query head
+  // hq on, whose sums go to tile `place` of the parts (dK; dV's Hk cap_tiles
+  // behind); slot0 is the sequence's first padded tile.
   struct Item {
-    int kj, hk, start, len, slot0;
+    int kj, hk, start, len, slot0, steps, hq, i, place;
     int i0, nT;
     __device__ __forceinline__ int tail() const { return len & (kTile - 1); }
   };
@@ -130,20 +132,24 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile uint32_t* abort_flag = misc + 1;
   Ctl ctl{p.err, abort_flag};
-  volatile int* ring = reinterpret_cast<volatile int*>(smem + L::kRing);
+  int* ring = reinterpret_cast<int*>(smem + L::kRing);
   // item k of this CTA from the ring; kj < 0 when none is left or a wait
   // failed (then ok is false too)
   auto take_item = [&](int k, bool& ok) -> Item {
     const int rs = k % L::kItemRing;
     const uint32_t ph = (uint32_t)(k / L::kItemRing) & 1u;
     ok = bar_wait_warp(bar(L::bItemFull + rs), ph, ctl, 355);
-    Item w{-1, 0, 0, 0, 0, 0, 0};
+    Item w{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
     if (!ok) return w;
-    w.kj = __shfl_sync(0xFFFFFFFFu, ring[8 * rs], 0);   // (the same in all lanes, as the compiler then knows)
-    w.hk = __shfl_sync(0xFFFFFFFFu, ring[8 * rs + 1], 0);
-    w.start = __shfl_sync(0xFFFFFFFFu, ring[8 * rs + 2], 0);
-    w.len = __shfl_sync(0xFFFFFFFFu, ring[8 * rs + 3], 0);
-    w.slot0 = __shfl_sync(0xFFFFFFFFu, ring[8 * rs + 4], 0);
+    w.kj = __shfl_sync(0xFFFFFFFFu, ring[L::kItemInts * rs], 0);   // (the same in all lanes, as the compiler then knows)
+    w.hk = __shfl_sync(0xFFFFFFFFu, ring[L::kItemInts * rs + 1], 0);
+    w.start = __shfl_sync(0xFFFFFFFFu, ring[L::kItemInts * rs + 2], 0);
+    w.len = __shfl_sync(0xFFFFFFFFu, ring[L::kItemInts * rs + 3], 0);
+    w.slot0 = __shfl_sync(0xFFFFFFFFu, ring[L::kItemInts * rs + 4], 0);
+    w.steps = __shfl_sync(0xFFFFFFFFu, ring[L::kItemInts * rs + 5], 0);
+    w.hq = __shfl_sync(0xFFFFFFFFu, ring[L::kItemInts * rs + 6], 0);
+    w.i = __shfl_sync(0xFFFFFFFFu, ring[L::kItemInts * rs + 7], 0);
+    w.place = __shfl_sync(0xFFFFFFFFu, ring[L::kItemInts * rs + 8], 0);
     w.nT = (w.len + kTile - 1) / kTile;
     w.i0 = p.causal ? w.kj : 0;
     mbar_arrive_warp(bar(L::bItemEmpty + rs));
@@ -236,7 +242,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     } else {
       n_items = p.plan->items;
     }
-    const int total = n_items * p.Hk;
+    const int heads = p.Hk * p.parts, total = n_items * heads;
     int nq = 0, nd = 0, nkv = 0;
     bool clc_out = false;        // a cancellation answer is outstanding
     uint32_t clc = 0u;           // answers received
@@ -248,7 +254,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       if (k >= L::kItemRing &&
           !(ok = bar_wait_warp(bar(L::bItemEmpty + rs), (uint32_t)(k / L::kItemRing - 1) & 1u, ctl, 354)))
         break;
-      Item w{-1, 0, 0, 0, 0, 0, 0};
+      Item w{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
       for (bool first = k == 0;; first = false) {
         int item = (int)blockIdx.x;
         if (!first && !direct) {
@@ -269,7 +275,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         }
         if (item >= total) break;
         int hk = 0;
-        const int idx = split_grouped(item, p.group, n_items, p.Hk, &hk);
+        const int idx = split_grouped(item, p.group, n_items, heads, &hk);
         PackedItem pi;
         if (direct) {
           pi = dl.at(idx, p.causal != 0);
@@ -279,22 +285,41 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           pi = p.items[idx];
           if (pi.len <= 0) continue;     // left out by the plan
         }
-        w.kj = __shfl_sync(0xFFFFFFFFu, pi.c, 0);
-        w.hk = hk;
-        w.start = __shfl_sync(0xFFFFFFFFu, pi.start, 0);
         w.len = __shfl_sync(0xFFFFFFFFu, pi.len, 0);
-        w.slot0 = __shfl_sync(0xFFFFFFFFu, pi.slot0, 0);
         w.nT = (w.len + kTile - 1) / kTile;
-        w.i0 = p.causal ? w.kj : 0;
+        const int c = __shfl_sync(0xFFFFFFFFu, pi.c, 0);
+        w.i0 = p.causal ? c : 0;
+        w.start = __shfl_sync(0xFFFFFFFFu, pi.start, 0);
+        w.slot0 = __shfl_sync(0xFFFFFFFFu, pi.slot0, 0);
+        const int row = w.nT - w.i0, all = p.G * row;   // steps of the item, in query heads of `row`
+        w.hk = hk;
+        w.steps = all;
+        w.hq = hk * p.G;
+        w.i = w.i0;
+        if (p.parts > 1) {
+          const int part = hk % p.parts, parts = min(p.parts, all);
+          if (part >= parts) continue;
+          const int s0 = all * part / parts;
+          w.steps = all * (part + 1) / parts - s0;
+          w.hk = hk / p.parts;
+          w.hq = w.hk * p.G + s0 / row;
+          w.i += s0 % row;
+          w.place = (part * 2 * p.Hk + w.hk) * p.cap_tiles + w.slot0 + c;
+        }
+        w.kj = c;
         break;
       }
       if (!ok) break;
       if (lane == 0) {
-        ring[8 * rs] = w.kj;
-        ring[8 * rs + 1] = w.hk;
-        ring[8 * rs + 2] = w.start;
-        ring[8 * rs + 3] = w.len;
-        ring[8 * rs + 4] = w.slot0;
+        ring[L::kItemInts * rs] = w.kj;
+        ring[L::kItemInts * rs + 1] = w.hk;
+        ring[L::kItemInts * rs + 2] = w.start;
+        ring[L::kItemInts * rs + 3] = w.len;
+        ring[L::kItemInts * rs + 4] = w.slot0;
+        ring[L::kItemInts * rs + 5] = w.steps;
+        ring[L::kItemInts * rs + 6] = w.hq;
+        ring[L::kItemInts * rs + 7] = w.i;
+        ring[L::kItemInts * rs + 8] = w.place;
         mbar_arrive(bar(L::bItemFull + rs));   // (release: the ring entry is visible to the waiters)
       }
       if (w.kj < 0) break;
@@ -303,9 +328,8 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           tma_prefetch_3d_w(&tk, 64 * h, w.hk, w.start + kTile * w.kj);
           tma_prefetch_3d_w(&tv, 64 * h, w.hk, w.start + kTile * w.kj);
         }
-      const int steps = p.G * (w.nT - w.i0);
 #pragma unroll 1
-      for (int it = 0, i = w.i0, hq = w.hk * p.G; it < steps; ++it, ++g) {
+      for (int it = 0, i = w.i, hq = w.hq; it < w.steps; ++it, ++g) {
         if (p.stall != 0u && g >= 1) { ok = false; break; }   // test of the timeout path: Q of tile 1 never comes
         const int s = g % L::kStages;
         const uint32_t n = (uint32_t)(g / L::kStages);
@@ -391,8 +415,8 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       for (int k = 0; ok; ++k) {
         const Item w = take_item(k, ok);
         if (w.kj < 0) break;
-        int i = w.i0;
-        const int tail = w.tail(), steps = p.G * (w.nT - w.i0);
+        int i = w.i;
+        const int tail = w.tail(), steps = w.steps;
         const int kb = k % L::kKV;
         const uint32_t sK = sbase + L::kK + kb * L::kKVBytes, sV = sbase + L::kV + kb * L::kKVBytes;
         const uint32_t mK = desc_lo(desc_mnmajor(sK, 0));
@@ -498,8 +522,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       const Item w = take_item(k, ok);
       if (!ok || w.kj < 0) break;
       const int krow = kTile * w.kj + r;
-      const int steps = p.G * (w.nT - w.i0);
-      for (int it = 0, i = w.i0; it < steps; ++it, ++g, i = i + 1 < w.nT ? i + 1 : w.i0) {
+      for (int it = 0, i = w.i; it < w.steps; ++it, ++g, i = i + 1 < w.nT ? i + 1 : w.i0) {
         const bool partial = (p.causal && i == w.kj) || (w.kj + 1) * kTile > w.len;
         const int s = g % L::kStages;
         if (!(ok = bar_wait_warp(bar(L::bQFull + s), (uint32_t)(g / L::kStages) & 1u, ctl, 370))) break;
@@ -612,6 +635,24 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       tc_fence_after();
       const bool is_v = cw == 0;
       const uint32_t tacc = (is_v ? tdV : tdK) + lane_off;
+      if (p.parts > 1) {
+        // a part: fp32 sums into its own place, each thread its row (past the
+        // sequence's end too: the tile is the item's own, and those are not read)
+        float* part = p.part + ((size_t)kTile * (w.place + (is_v ? p.Hk * p.cap_tiles : 0)) + r) * p.d;
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t u[32];
+          tmem_ld32(tacc + 32u * cc, u);
+          tmem_ld_wait(u);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (32 * cc + 4 * j < p.d)
+              *reinterpret_cast<uint4*>(part + 32 * cc + 4 * j) =
+                  make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+        }
+        tc_fence_before();
+        continue;
+      }
       const float mul = is_v ? 1.f : p.scale;
       const int s4 = lane & 3;
       const int row0 = kTile * w.kj + 32 * (warp & 3) + (lane & ~3);   // the quad's first row
@@ -666,8 +707,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       const Item w = take_item(k, ok);
       if constexpr (L::kGroupDrain) ok = group_all(kDrainBar, 128, ok);
       if (!ok || w.kj < 0) break;
-      const int steps = p.G * (w.nT - w.i0);
-      for (int it = 0, i = w.i0, hq = w.hk * p.G; it < steps; ++it, ++g) {
+      for (int it = 0, i = w.i, hq = w.hq; it < w.steps; ++it, ++g) {
         const int s = g % L::kStages;
         const uint32_t stage = (uint32_t)(L::kdO + s * L::kTileBytes);
         ok = bar_wait_warp(bar(L::bdQFull), (uint32_t)g & 1u, ctl, 380);
@@ -800,27 +840,61 @@ __global__ void __launch_bounds__(256) packed_bwd_pre_kernel(const PackedBwdPara
   }
 }
 
-// dQ = 16-bit(scale * accumulator), one thread per 8 columns of a row.
-template <bool F16>
+// dQ = 16-bit(scale * accumulator), one thread per 8 columns of a row. With
+// items in parts (PARTS), blocks behind those sum the parts of dK and dV, kSumRows rows
+// of a tile each, in the order of the parts.
+constexpr int kSumRows = 32;
+
+template <bool F16, bool PARTS>
 __global__ void __launch_bounds__(256) packed_bwd_dq_kernel(const PackedBwdParams p) {
   grid_dep_launch();
-  const int tile = (int)(blockIdx.x / (unsigned)p.Hq), h = (int)(blockIdx.x % (unsigned)p.Hq);
-  const PackedItem it = padded_tile(p, tile);
-  if (it.len == 0) return;
-  const size_t row_off = ((size_t)h * p.cap_tiles + tile) * kTile;
   const int parts = p.d / 8;
-  const int rows = min(kTile, it.len - kTile * it.c);
+  auto put = [](uint16_t* dst, const float4& a, const float4& c, float mul) {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack2<F16>(a.x * mul, a.y * mul), pack2<F16>(a.z * mul, a.w * mul),
+                                                pack2<F16>(c.x * mul, c.y * mul), pack2<F16>(c.z * mul, c.w * mul));
+  };
+  const unsigned n_dq = (unsigned)p.cap_tiles * (unsigned)p.Hq;
+  if (!PARTS || blockIdx.x < n_dq) {
+    const int tile = (int)(blockIdx.x / (unsigned)p.Hq), h = (int)(blockIdx.x % (unsigned)p.Hq);
+    const PackedItem it = padded_tile(p, tile);
+    if (it.len == 0) return;
+    const size_t row_off = ((size_t)h * p.cap_tiles + tile) * kTile;
+    const int rows = min(kTile, it.len - kTile * it.c);
+    for (int i = (int)threadIdx.x; i < rows * parts; i += 256) {
+      const int r = i / parts, part = i % parts;
+      const float4* src = reinterpret_cast<const float4*>(p.dq_acc + (row_off + r) * p.d + 8 * part);
+      const int64_t t = (int64_t)it.start + kTile * it.c + r;
+      put(p.dq + t * p.dq_tok + h * p.dq_head + 8 * part, src[0], src[1], p.scale);
+    }
+    return;
+  }
+  if constexpr (!PARTS) return;
+  unsigned x = blockIdx.x - n_dq;
+  const int first = kSumRows * (int)(x % (kTile / kSumRows));
+  x /= kTile / kSumRows;
+  const bool is_v = x % 2 != 0;
+  x /= 2;
+  const int hk = (int)(x % (unsigned)p.Hk), tile = (int)(x / (unsigned)p.Hk);
+  const PackedItem it = padded_tile(p, tile);
+  const int rows = min(kSumRows, it.len - kTile * it.c - first);
+  if (it.len == 0 || rows <= 0) return;
+  const int nT = (it.len + kTile - 1) / kTile;
+  const int n = min(p.parts, p.G * (nT - (p.causal ? it.c : 0)));   // parts with steps
+  const size_t head = (size_t)p.cap_tiles * kTile * p.d, step = 2 * p.Hk * head;
+  const float* base = p.part + ((is_v ? p.Hk : 0) + hk) * head + ((size_t)tile * kTile + first) * p.d;
+  uint16_t* out = is_v ? p.dv + hk * p.dv_head : p.dk + hk * p.dk_head;
+  const int64_t tok = is_v ? p.dv_tok : p.dk_tok;
   for (int i = (int)threadIdx.x; i < rows * parts; i += 256) {
-    const int r = i / parts, part = i % parts;
-    const float4* src = reinterpret_cast<const float4*>(p.dq_acc + (row_off + r) * p.d + 8 * part);
-    const float4 a = src[0], c = src[1];
-    uint4 out;
-    out.x = pack2<F16>(a.x * p.scale, a.y * p.scale);
-    out.y = pack2<F16>(a.z * p.scale, a.w * p.scale);
-    out.z = pack2<F16>(c.x * p.scale, c.y * p.scale);
-    out.w = pack2<F16>(c.z * p.scale, c.w * p.scale);
-    const int64_t t = (int64_t)it.start + kTile * it.c + r;
-    *reinterpret_cast<uint4*>(p.dq + t * p.dq_tok + h * p.dq_head + 8 * part) = out;
+    const float4* src = reinterpret_cast<const float4*>(base + 8 * (size_t)i);   // (rows are p.d = 8 parts floats apart)
+    float4 a = src[0], c = src[1];
+#pragma unroll 4
+    for (int k = 1; k < n; ++k) {
+      const float4* y = reinterpret_cast<const float4*>(base + k * step + 8 * (size_t)i);
+      const float4 ya = y[0], yc = y[1];
+      a = make_float4(a.x + ya.x, a.y + ya.y, a.z + ya.z, a.w + ya.w);
+      c = make_float4(c.x + yc.x, c.y + yc.y, c.z + yc.z, c.w + yc.w);
+    }
+    put(out + ((int64_t)it.start + kTile * it.c + first + i / parts) * tok + 8 * (i % parts), a, c, is_v ? 1.f : p.scale);
   }
 }
 
@@ -843,7 +917,7 @@ cudaError_t launch_packed_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
   PackedBwdParams q = p;
   // Q and dO (16-bit) and the fp32 dQ accumulator of a key/value head's G query
   // heads are re-read by all of its key tiles
-  q.group = l2_head_group(8.0 * p.total * p.d * p.G, p.Hk);
+  q.group = l2_head_group(8.0 * p.total * p.d * p.G, p.Hk) * p.parts;
   const dim3 tiles((unsigned)p.cap_tiles * (unsigned)p.Hq);
   // Only the main kernel is launched ahead of its predecessor's end. With the two
   // passes launched ahead as well, their blocks are scheduled between those of a
@@ -853,11 +927,13 @@ cudaError_t launch_packed_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
   e = launch_pdl(false, packed_bwd_pre_kernel<D / 8, F16>, tiles, dim3(256), 0, s, q);
   if (e != cudaSuccess) return e;
   // a CTA per item where items are taken by cancelling CTAs, else one per SM
-  const long long most = (long long)p.cap_tiles * p.Hk;
+  const long long most = (long long)p.cap_tiles * p.Hk * p.parts;
   e = launch_pdl(true, fa_packed_bwd_kernel<D, F16>, dim3((unsigned)(p.B <= kDirect || most < sms ? most : sms)),
                  dim3(kBwdThreads), L::kSmemBytes, s, tq, tk, tv, tdo, tdq, q);
   if (e != cudaSuccess) return e;
-  return launch_pdl(false, packed_bwd_dq_kernel<F16>, tiles, dim3(256), 0, s, q);
+  if (p.parts == 1) return launch_pdl(false, packed_bwd_dq_kernel<F16, false>, tiles, dim3(256), 0, s, q);
+  const unsigned sums = (unsigned)p.cap_tiles * (unsigned)p.Hk * 2u * (kTile / kSumRows);
+  return launch_pdl(false, packed_bwd_dq_kernel<F16, true>, dim3(tiles.x + sums), dim3(256), 0, s, q);
 }
 
 }  // namespace

@@ -99,7 +99,15 @@ def test_workspace_size(L):
     rows = Hq * tiles * 128
     want = al(want + rows * d * 4)
     want = al(al(want + rows * 4) + rows * 4)
-    assert L.flash_attn_packed_workspace_size(B, total, Hq, 2, d, 1) == want
+    # 24 items of 3 + 5 steps for 152 SMs: in as many parts as an item has steps
+    # (4 heads, 2 tiles of an average sequence), each with its dK and dV
+    part = 8 * 2 * 2 * tiles * 128 * d * 4
+    assert L.flash_attn_packed_workspace_size(B, total, Hq, 2, d, 1) == al(want + part)
+    # two items for every SM: no parts
+    B, total, tiles, Hk = 5, 20000, 20000 // 128 + 5, 2
+    rows = Hq * tiles * 128
+    want = al(al(al(al(al(256) + 4 * B) + 16 * tiles) + 16 * tiles) + rows * d * 4)
+    assert L.flash_attn_packed_workspace_size(B, total, Hq, Hk, d, 1) == al(al(want + rows * 4) + rows * 4)
     for bad in ((-1, 1, 1, 1, 64), (1, 1, 3, 2, 64), (1, 1, 1, 1, 256), (1, 1, 1, 1, 4)):
         assert L.flash_attn_packed_workspace_size(*bad, 0) == 0
 
