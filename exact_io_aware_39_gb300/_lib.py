@@ -414,7 +414,7 @@ def standard_attention_bwd(q, k, v, do, workspace, scale, stream=None, s16=False
 # helpers look at each tensor once and build nothing twice.
 
 FA_CACHE_16BIT, FA_CACHE_E4M3 = 0, 1
-PACKED_DIRECT = 32           # a forward of so many sequences needs no workspace
+PACKED_DIRECT = 128          # a forward of so many sequences needs no workspace
 # (int64 strides as bytes: packing them takes a tenth of a ctypes array's time)
 _pack8, _pack16 = struct.Struct("=8q").pack, struct.Struct("=16q").pack
 _default_options = {}        # dtype -> (reference to) its fa_options

@@ -77,8 +77,11 @@ inline PackedWorkspace packed_workspace_layout(int B, int total, int Hq, int Hk,
 }
 
 // Up to kDirect sequences: no plan kernel runs, every warp that needs the work
-// list makes it from the bounds, a lane per sequence (DirectList).
-constexpr int kDirect = 32;
+// list makes it from the bounds (DirectList): 10 us less for a forward call, 19
+// for forward and backward (33 sequences of 40 tokens: 17.5 -> 8.2 and 47.7 ->
+// 29.0 us).
+constexpr int kDirect = 128, kManySlots = kDirect / 32;
+inline bool packed_many(int B) { return B > 32 && B <= kDirect; }
 
 struct PackedFwdParams {
   const int32_t* cu;          // [B + 1]
@@ -139,95 +142,156 @@ __device__ __forceinline__ void report_bounds(unsigned int* err, int b) {
   }
 }
 
-// The work list of up to 32 sequences, held by a warp: lane b has sequence b
-// and its n units of `rows` rows, slot0 the units of the sequences before it. A
-// sequence that would end past `cap` units in all (only bounds that overlap can
-// name so many) is left out. Units are listed as the plan kernel lists
-// them: causal, by the number c of units before them, descending, and for each
-// c the sequences that have one; not causal, sequence by sequence, the longest
-// first. All lanes call the members together.
+// The work list of up to kDirect sequences, held by a warp: lane l has the
+// sequences l, l + 32, ... (its slots) and their n units of `rows` rows, slot0
+// the units before each of them, lane by lane. A sequence that would end past
+// `cap` units in all (only bounds that overlap can name so many) is left out.
+// Units are listed as the plan kernel lists them: causal, by the number c of
+// units before them, descending, and for each c the sequences that have one; not
+// causal, sequence by sequence, the longest first. All lanes call the members
+// together. kSlots = kManySlots holds them all, 1 up to 32
+// (kernels are built for either: the claim of an item stands before its loads, and
+// with four slots for every call 24 prompts took 107 us, not 105).
+template <int kSlots>
 struct DirectList {
-  int start, len, n, slot0, items;
-  int c, off;        // causal: items with more than c units before them, and how many
-  int rank, first;   // not causal: place of this lane's sequence by length, and of its first unit
+  int start[kSlots], len[kSlots], n[kSlots], slot0[kSlots], items;
+  int c, off;          // causal: items with more than c units before them, and how many
+  int first[kSlots];   // not causal: list place of a sequence's first unit
   // the sequences alone (err may be null)
   __device__ __forceinline__ void read(const int32_t* cu, int B, int total, int rows, int cap, unsigned int* err) {
     const int lane = threadIdx.x & 31;
-    start = len = 0;
-    bool bad = false;
-    if (lane < B) len = seq_bounds(cu, lane, total, start, bad);
-    n = (len + rows - 1) / rows;
-    int upto = n;
+    bool bad[kSlots];
+    int mine = 0;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      const int b = 32 * s + lane;
+      start[s] = len[s] = 0;
+      bad[s] = false;
+      if (b < B) len[s] = seq_bounds(cu, b, total, start[s], bad[s]);
+      n[s] = (len[s] + rows - 1) / rows;
+      mine += n[s];
+    }
+    int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
       if (lane >= o) upto += y;
     }
-    slot0 = upto - n;
-    if (upto > cap) {
-      bad = true;
-      len = n = 0;
+    upto -= mine;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      slot0[s] = upto;
+      upto += n[s];
+      if (upto > cap) {
+        bad[s] = bad[s] || n[s] > 0;
+        len[s] = n[s] = 0;
+      }
+      if (bad[s] && err != nullptr) report_bounds(err, 32 * s + lane);
     }
-    if (bad && err != nullptr) report_bounds(err, lane);
+  }
+  __device__ __forceinline__ int most() const {
+    int m = 0;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) m = max(m, n[s]);
+    return __reduce_max_sync(0xFFFFFFFFu, m);
+  }
+  // sequences with more than c units
+  __device__ __forceinline__ int count(int c) const {
+    int x = 0;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) x += __popc(__ballot_sync(0xFFFFFFFFu, n[s] > c));
+    return x;
   }
   __device__ __forceinline__ void init(const int32_t* cu, int B, int total, int rows, int cap, bool causal,
                                        unsigned int* err) {
     const int lane = threadIdx.x & 31;
     read(cu, B, total, rows, cap, err);
-    items = __reduce_add_sync(0xFFFFFFFFu, n);
-    c = __reduce_max_sync(0xFFFFFFFFu, n) - 1;
+    items = 0;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      items += n[s];
+      first[s] = 0;
+    }
+    items = __reduce_add_sync(0xFFFFFFFFu, items);
+    c = most() - 1;
     off = 0;
-    rank = first = 0;
     if (!causal)
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s)
 #pragma unroll 1
-      for (int l = 0; l < 32; ++l) {
-        const int o = __shfl_sync(0xFFFFFFFFu, n, l);
-        if (o > n || (o == n && l < lane)) {
-          ++rank;
-          first += o;
+        for (int l = 0; l < 32; ++l) {
+          const int o = __shfl_sync(0xFFFFFFFFu, n[s], l);
+#pragma unroll
+          for (int t = 0; t < kSlots; ++t)
+            if (o > n[t] || (o == n[t] && (s < t || (s == t && l < lane)))) first[t] += o;
         }
-      }
   }
   __device__ __forceinline__ PackedItem at(int idx, bool causal) {
-    int b;
-    PackedItem it;
+    uint32_t mine = 0u;
+    int t = 0;           // the slot; the lane is mine's lowest
     if (causal) {
       if (idx < off) {     // the order starts again for another group of heads
-        c = __reduce_max_sync(0xFFFFFFFFu, n) - 1;
+        c = most() - 1;
         off = 0;
       }
-      uint32_t has = __ballot_sync(0xFFFFFFFFu, n > c);
+      int x = count(c);
 #pragma unroll 1
-      while (c > 0 && idx >= off + __popc(has)) {
-        off += __popc(has);
+      while (c > 0 && idx >= off + x) {
+        off += x;
         --c;
-        has = __ballot_sync(0xFFFFFFFFu, n > c);
+        x = count(c);
       }
+      int r = idx - off;
+      mine = __ballot_sync(0xFFFFFFFFu, n[0] > c);
+#pragma unroll
+      for (int s = 1; s < kSlots; ++s)
+        if (t == s - 1 && r >= __popc(mine)) {
+          r -= __popc(mine);
+          t = s;
+          mine = __ballot_sync(0xFFFFFFFFu, n[s] > c);
+        }
 #pragma unroll 1
-      for (int r = idx - off; r > 0; --r) has &= has - 1;
-      b = __ffs(has) - 1;
-      it.c = c;
+      for (; r > 0; --r) mine &= mine - 1;
     } else {
-      const uint32_t mine = __ballot_sync(0xFFFFFFFFu, n > 0 && idx >= first && idx < first + n);
-      b = __ffs(mine) - 1;
-      it.c = idx - __shfl_sync(0xFFFFFFFFu, first, b);
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s)
+        if (mine == 0u) {
+          mine = __ballot_sync(0xFFFFFFFFu, n[s] > 0 && idx >= first[s] && idx < first[s] + n[s]);
+          t = s;
+        }
     }
-    it.start = __shfl_sync(0xFFFFFFFFu, start, b);
-    it.len = __shfl_sync(0xFFFFFFFFu, len, b);
-    it.slot0 = __shfl_sync(0xFFFFFFFFu, slot0, b);
+    PackedItem it = get(t, __ffs(mine) - 1);
+    it.c = causal ? c : idx - it.c;
     return it;
   }
   // the unit at place `slot` of the sequences' order; len 0 where there is none
   __device__ __forceinline__ PackedItem unit(int slot) const {
-    const uint32_t mine = __ballot_sync(0xFFFFFFFFu, slot >= slot0 && slot < slot0 + n);
-    PackedItem it{0, 0, 0, 0};
-    if (mine == 0u) return it;
-    const int b = __ffs(mine) - 1;
-    it.start = __shfl_sync(0xFFFFFFFFu, start, b);
-    it.len = __shfl_sync(0xFFFFFFFFu, len, b);
-    it.slot0 = __shfl_sync(0xFFFFFFFFu, slot0, b);
+    uint32_t mine = 0u;
+    int t = 0;
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s)
+      if (mine == 0u) {
+        mine = __ballot_sync(0xFFFFFFFFu, slot >= slot0[s] && slot < slot0[s] + n[s]);
+        t = s;
+      }
+    if (mine == 0u) return PackedItem{0, 0, 0, 0};
+    PackedItem it = get(t, __ffs(mine) - 1);
     it.c = slot - it.slot0;
     return it;
+  }
+  // the sequence in slot t of lane l (c: its `first`)
+  __device__ __forceinline__ PackedItem get(int t, int l) const {
+    int st = start[0], le = len[0], sl = slot0[0], fi = first[0];
+#pragma unroll
+    for (int s = 1; s < kSlots; ++s)
+      if (t == s) {
+        st = start[s];
+        le = len[s];
+        sl = slot0[s];
+        fi = first[s];
+      }
+    return PackedItem{__shfl_sync(0xFFFFFFFFu, st, l), __shfl_sync(0xFFFFFFFFu, le, l), __shfl_sync(0xFFFFFFFFu, fi, l),
+                      __shfl_sync(0xFFFFFFFFu, sl, l)};
   }
 };
 

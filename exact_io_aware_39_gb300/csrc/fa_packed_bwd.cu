@@ -7,6 +7,11 @@
 //     over the G query heads of that head and their live query tiles, so dK and
 //     dV of a shared head are summed in TMEM, in a fixed order, and written
 //     once; nothing of them is added through memory;
+//   * where there are few items (few key/value heads, few tiles) they are cut into
+//     parts, ranges of those (query head, query tile) steps, whose fp32 sums the
+//     last pass adds up in order (packed_bwd_parts: forward and backward of 17
+//     documents of 10-676 tokens, 7 / 1 heads, d = 80: 107 us whole, 49 in parts;
+//     of three of 5-200, 8 / 2 heads, d = 64: 25.7 and 22.4);
 //   * items come from a list made on the device, heaviest first, as in the
 //     forward (fa_packed_fwd.cu);
 //   * tiles are boxes of the strided [token, head, d] tensors and may run into
@@ -37,6 +42,8 @@
 // 32-977 tokens 167, 35 and 26 us (the passes around are at the bandwidth of the
 // fp32 accumulator).
 #include "fa_packed.cuh"
+
+#include <type_traits>
 
 namespace fa {
 
@@ -102,7 +109,7 @@ struct PackedBwdLayout {
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
-template <int D, bool F16>
+template <int D, bool F16, int SLOTS>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -234,7 +241,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     // up to kDirect sequences: the list is made here and items are taken by
     // cancelling CTAs of the grid that have not started; else both are the plan's
     const bool direct = p.B <= kDirect;
-    DirectList dl;
+    DirectList<SLOTS> dl;
     int n_items = 0;
     if (direct) {
       dl.init(p.cu, p.B, p.total, kTile, p.cap_tiles, p.causal != 0, p.err);
@@ -786,10 +793,11 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   }
 }
 
-// Padded tile `tile`; len 0 where there is none (whole warps call it together).
+// Padded tile `tile`, from a list of SLOTS sequences a lane or (0) the plan's; len 0 where there is none (whole warps call it together).
+template <int SLOTS>
 __device__ __forceinline__ PackedItem padded_tile(const PackedBwdParams& p, int tile) {
-  if (p.B <= kDirect) {
-    DirectList dl;
+  if constexpr (SLOTS > 0) {
+    DirectList<SLOTS> dl;
     dl.read(p.cu, p.B, p.total, kTile, p.cap_tiles, nullptr);
     return dl.unit(tile);
   }
@@ -799,11 +807,11 @@ __device__ __forceinline__ PackedItem padded_tile(const PackedBwdParams& p, int 
 // Per padded tile and query head: D = rowsum(dO * O) and LSE * log2(e) of its
 // rows (0 and +inf past the sequence), and the dQ accumulator's tile zeroed.
 // LANES neighbouring threads take a row, 8 columns each.
-template <int LANES, bool F16>
+template <int LANES, bool F16, int SLOTS>
 __global__ void __launch_bounds__(256) packed_bwd_pre_kernel(const PackedBwdParams p) {
   grid_dep_launch();
   const int tile = (int)(blockIdx.x / (unsigned)p.Hq), h = (int)(blockIdx.x % (unsigned)p.Hq);
-  const PackedItem it = padded_tile(p, tile);
+  const PackedItem it = padded_tile<SLOTS>(p, tile);
   if (it.len == 0) return;
   const size_t row_off = ((size_t)h * p.cap_tiles + tile) * kTile;
   const int part = (int)threadIdx.x % LANES;
@@ -845,7 +853,7 @@ __global__ void __launch_bounds__(256) packed_bwd_pre_kernel(const PackedBwdPara
 // of a tile each, in the order of the parts.
 constexpr int kSumRows = 32;
 
-template <bool F16, bool PARTS>
+template <bool F16, bool PARTS, int SLOTS>
 __global__ void __launch_bounds__(256) packed_bwd_dq_kernel(const PackedBwdParams p) {
   grid_dep_launch();
   const int parts = p.d / 8;
@@ -856,7 +864,7 @@ __global__ void __launch_bounds__(256) packed_bwd_dq_kernel(const PackedBwdParam
   const unsigned n_dq = (unsigned)p.cap_tiles * (unsigned)p.Hq;
   if (!PARTS || blockIdx.x < n_dq) {
     const int tile = (int)(blockIdx.x / (unsigned)p.Hq), h = (int)(blockIdx.x % (unsigned)p.Hq);
-    const PackedItem it = padded_tile(p, tile);
+    const PackedItem it = padded_tile<SLOTS>(p, tile);
     if (it.len == 0) return;
     const size_t row_off = ((size_t)h * p.cap_tiles + tile) * kTile;
     const int rows = min(kTile, it.len - kTile * it.c);
@@ -875,7 +883,7 @@ __global__ void __launch_bounds__(256) packed_bwd_dq_kernel(const PackedBwdParam
   const bool is_v = x % 2 != 0;
   x /= 2;
   const int hk = (int)(x % (unsigned)p.Hk), tile = (int)(x / (unsigned)p.Hk);
-  const PackedItem it = padded_tile(p, tile);
+  const PackedItem it = padded_tile<SLOTS>(p, tile);
   const int rows = min(kSumRows, it.len - kTile * it.c - first);
   if (it.len == 0 || rows <= 0) return;
   const int nT = (it.len + kTile - 1) / kTile;
@@ -898,7 +906,7 @@ __global__ void __launch_bounds__(256) packed_bwd_dq_kernel(const PackedBwdParam
   }
 }
 
-template <int D, bool F16>
+template <int D, bool F16, int SLOTS>
 cudaError_t launch_packed_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const CUtensorMap& tdo, const CUtensorMap& tdq,
                                 const PackedBwdParams& p, cudaStream_t s) {
@@ -908,7 +916,7 @@ cudaError_t launch_packed_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
   if (e != cudaSuccess) return e;
   static PerDeviceOnce smem_set;
   e = once_per_device(smem_set, dev, [] {
-    return cudaFuncSetAttribute(fa_packed_bwd_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(fa_packed_bwd_kernel<D, F16, SLOTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 L::kSmemBytes);
   });
   if (e != cudaSuccess) return e;
@@ -924,16 +932,22 @@ cudaError_t launch_packed_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
   // kernel still running: forward and backward of 16 documents 308 us against
   // 286, of two long sequences 1273 against 1250 (one short one 25.5 against 25.8).
   // 16 lanes cover d <= 128, 8 cover d <= 64
-  e = launch_pdl(false, packed_bwd_pre_kernel<D / 8, F16>, tiles, dim3(256), 0, s, q);
+  // (up to kDirect sequences the passes' blocks read the bounds themselves)
+  const bool direct = p.B <= kDirect;
+  e = launch_pdl(false, direct ? packed_bwd_pre_kernel<D / 8, F16, SLOTS> : packed_bwd_pre_kernel<D / 8, F16, 0>, tiles,
+                 dim3(256), 0, s, q);
   if (e != cudaSuccess) return e;
   // a CTA per item where items are taken by cancelling CTAs, else one per SM
   const long long most = (long long)p.cap_tiles * p.Hk * p.parts;
-  e = launch_pdl(true, fa_packed_bwd_kernel<D, F16>, dim3((unsigned)(p.B <= kDirect || most < sms ? most : sms)),
+  e = launch_pdl(true, fa_packed_bwd_kernel<D, F16, SLOTS>, dim3((unsigned)(direct || most < sms ? most : sms)),
                  dim3(kBwdThreads), L::kSmemBytes, s, tq, tk, tv, tdo, tdq, q);
   if (e != cudaSuccess) return e;
-  if (p.parts == 1) return launch_pdl(false, packed_bwd_dq_kernel<F16, false>, tiles, dim3(256), 0, s, q);
+  if (p.parts == 1)
+    return launch_pdl(false, direct ? packed_bwd_dq_kernel<F16, false, SLOTS> : packed_bwd_dq_kernel<F16, false, 0>,
+                      tiles, dim3(256), 0, s, q);
   const unsigned sums = (unsigned)p.cap_tiles * (unsigned)p.Hk * 2u * (kTile / kSumRows);
-  return launch_pdl(false, packed_bwd_dq_kernel<F16, true>, dim3(tiles.x + sums), dim3(256), 0, s, q);
+  return launch_pdl(false, direct ? packed_bwd_dq_kernel<F16, true, SLOTS> : packed_bwd_dq_kernel<F16, true, 0>,
+                    dim3(tiles.x + sums), dim3(256), 0, s, q);
 }
 
 }  // namespace
@@ -941,11 +955,15 @@ cudaError_t launch_packed_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
 cudaError_t launch_packed_bwd(bool f16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const CUtensorMap& tdo, const CUtensorMap& tdq,
                               const PackedBwdParams& p, cudaStream_t s) {
-  if (p.d <= 64)
-    return f16 ? launch_packed_bwd_d<64, true>(tq, tk, tv, tdo, tdq, p, s)
-               : launch_packed_bwd_d<64, false>(tq, tk, tv, tdo, tdq, p, s);
-  return f16 ? launch_packed_bwd_d<128, true>(tq, tk, tv, tdo, tdq, p, s)
-             : launch_packed_bwd_d<128, false>(tq, tk, tv, tdo, tdq, p, s);
+  auto run = [&](auto many) -> cudaError_t {
+    constexpr int SLOTS = many ? kManySlots : 1;
+    if (p.d <= 64)
+      return f16 ? launch_packed_bwd_d<64, true, SLOTS>(tq, tk, tv, tdo, tdq, p, s)
+                 : launch_packed_bwd_d<64, false, SLOTS>(tq, tk, tv, tdo, tdq, p, s);
+    return f16 ? launch_packed_bwd_d<128, true, SLOTS>(tq, tk, tv, tdo, tdq, p, s)
+               : launch_packed_bwd_d<128, false, SLOTS>(tq, tk, tv, tdo, tdq, p, s);
+  };
+  return packed_many(p.B) ? run(std::true_type{}) : run(std::false_type{});
 }
 
 }  // namespace fa

@@ -11,7 +11,7 @@
 //     tile still fills both softmax groups), else two neighbouring tiles of a
 //     head;
 //   * the items of a call are listed on the device (the lengths are there),
-//     heaviest first: for up to 32 sequences by every producer warp for itself
+//     heaviest first: for up to 128 sequences by every producer warp for itself
 //     (DirectList), for more by a plan kernel. A CTA takes its own item, then,
 //     as it gets ready for one, the next of a counter that the plan kernel zeroed
 //     or, without one, a CTA of the grid that has not started, cancelled through
@@ -40,6 +40,8 @@
 // passes through all of the kernel's code, which at 96 KB missed the instruction
 // cache all the way and now has 55.
 #include "fa_packed.cuh"
+
+#include <type_traits>
 
 namespace fa {
 
@@ -118,7 +120,7 @@ struct Pair {
   __device__ __forceinline__ int tail() const { return len & (kTile - 1); }
 };
 
-template <int D, bool F16>
+template <int D, bool F16, int SLOTS>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv, const PackedFwdParams p) {
@@ -204,7 +206,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     // together, within a group the list heaviest first, and for each unit the
     // heads of the group.
     const bool direct = p.B <= kDirect;
-    DirectList dl;
+    DirectList<SLOTS> dl;
     int n_items = 0;
     if (direct) {
       dl.init(p.cu, p.B, p.total, p.pair_heads ? kTile : 2 * kTile, p.cap_items, p.causal != 0, p.err);
@@ -690,7 +692,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   }
 }
 
-template <int D, bool F16>
+template <int D, bool F16, int SLOTS>
 cudaError_t launch_packed_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const PackedFwdParams& p, cudaStream_t s) {
   using L = PackedFwdLayout<D>;
@@ -699,7 +701,7 @@ cudaError_t launch_packed_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
   if (e != cudaSuccess) return e;
   static PerDeviceOnce smem_set;
   e = once_per_device(smem_set, dev, [] {
-    return cudaFuncSetAttribute(fa_packed_fwd_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(fa_packed_fwd_kernel<D, F16, SLOTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 L::kSmemBytes);
   });
   if (e != cudaSuccess) return e;
@@ -711,7 +713,7 @@ cudaError_t launch_packed_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
   q.group = p.G / (p.Hq / p.heads) * l2_head_group(4.0 * p.total * p.d, p.Hq / p.G);
   // a CTA per item where items are taken by cancelling CTAs, else one per SM
   const long long most = (long long)p.cap_items * p.heads;
-  return launch_pdl(true, fa_packed_fwd_kernel<D, F16>, dim3((unsigned)(p.B <= kDirect || most < sms ? most : sms)),
+  return launch_pdl(true, fa_packed_fwd_kernel<D, F16, SLOTS>, dim3((unsigned)(p.B <= kDirect || most < sms ? most : sms)),
                     dim3(kFwdThreads), L::kSmemBytes, s, tq, tk, tv, q);
 }
 
@@ -719,9 +721,15 @@ cudaError_t launch_packed_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
 
 cudaError_t launch_packed_fwd(bool f16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const PackedFwdParams& p, cudaStream_t s) {
-  if (p.d <= 64)
-    return f16 ? launch_packed_fwd_d<64, true>(tq, tk, tv, p, s) : launch_packed_fwd_d<64, false>(tq, tk, tv, p, s);
-  return f16 ? launch_packed_fwd_d<128, true>(tq, tk, tv, p, s) : launch_packed_fwd_d<128, false>(tq, tk, tv, p, s);
+  auto run = [&](auto many) -> cudaError_t {
+    constexpr int SLOTS = many ? kManySlots : 1;
+    if (p.d <= 64)
+      return f16 ? launch_packed_fwd_d<64, true, SLOTS>(tq, tk, tv, p, s)
+                 : launch_packed_fwd_d<64, false, SLOTS>(tq, tk, tv, p, s);
+    return f16 ? launch_packed_fwd_d<128, true, SLOTS>(tq, tk, tv, p, s)
+               : launch_packed_fwd_d<128, false, SLOTS>(tq, tk, tv, p, s);
+  };
+  return packed_many(p.B) ? run(std::true_type{}) : run(std::false_type{});
 }
 
 }  // namespace fa

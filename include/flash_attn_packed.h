@@ -35,7 +35,7 @@
  *    be 0 and tile_record NULL (FA_ERR_UNSUPPORTED otherwise).
  *  - workspace: at least flash_attn_packed_workspace_size(...) bytes, 256-byte
  *    aligned; contents on entry do not matter. Calls whose kernels may overlap
- *    need workspaces of their own. A forward call of at most 32 sequences uses
+ *    need workspaces of their own. A forward call of at most 128 sequences uses
  *    none (workspace may be NULL).
  */
 #ifndef FLASH_ATTN_PACKED_H
@@ -50,7 +50,8 @@ extern "C" {
 /* Bytes of device workspace of a forward (backward = 0) or backward (1) call:
  * the list of work items and, for the backward, the fp32 dQ accumulator and
  * two row vectors, over sequences padded to multiples of 128 tokens (at most
- * total + 128 B of them). 0 for an invalid shape. */
+ * total + 128 B of them), and, where the call's key tiles alone would not fill
+ * the GPU, up to 16 fp32 parts of dK and dV. 0 for an invalid shape. */
 size_t flash_attn_packed_workspace_size(int B, int total, int Hq, int Hk, int d, int backward);
 
 /*

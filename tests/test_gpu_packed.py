@@ -127,17 +127,19 @@ def test_more_sequences_than_a_block_has_threads(fa, d, causal):
     _check(c, r, 0.2, causal)
 
 
+@pytest.mark.parametrize("B", [40, 130])
 @pytest.mark.parametrize("Hq,Hk,d,causal", [(2, 2, 64, True), (4, 2, 128, True), (3, 1, 128, False), (4, 1, 64, False)])
-def test_lists_made_by_the_plan_kernel(fa, Hq, Hk, d, causal):
-    """More than 32 sequences, of one to several tiles."""
-    lens = [(97 * b) % 401 for b in range(40)]
+def test_many_sequences_of_several_tiles(fa, Hq, Hk, d, causal, B):
+    """Lists of more than 32 sequences (several to a lane) and of more than 128
+    (made by the plan kernel)."""
+    lens = [(97 * b) % 401 for b in range(B)]
     c = _inputs(lens, Hq, Hk, d, BF, 8, 2, 70)
     r = _run(fa, c, d ** -0.5, causal)
     _settled(fa)
     _check(c, r, d ** -0.5, causal)
 
 
-@pytest.mark.parametrize("B", [32, 33])
+@pytest.mark.parametrize("B", [31, 32, 33, 127, 128, 129])
 def test_either_side_of_the_direct_list(fa, B):
     c = _inputs([(61 * b) % 150 for b in range(B)], 4, 2, 64, BF, 9)
     r = _run(fa, c, 0.125, True)
@@ -213,7 +215,7 @@ def test_empty_calls(fa):
 
 
 @pytest.mark.parametrize("cu", [[0, 100, 50, 150], [0, 100, 400], [-5, 100, 150], [0, 150, 0, 150, 0, 150],
-                                [0, 150] * 25])
+                                [0, 150] * 25, [0, 150] * 70])
 def test_bounds_that_are_no_sequences_are_left_out(fa, cu):
     """Decreasing bounds or bounds outside the tensors: those sequences are left
     out and the error word says so; the others (where they do not overlap)

@@ -45,7 +45,7 @@ SHAPES = [
     (dict(d=12), 2), (dict(d=136), 2), (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1),
     (dict(scale=float("inf")), 1), (dict(causal=2), 1), (dict(total=1 << 30, Hq=64), 2), (dict(B=1 << 30), 2),
     (dict(LSE=None), 1), (dict(cu=None), 1), (dict(cu=ctypes.c_void_p((1 << 20) + 2)), 1),
-    (dict(ws=None, B=40), 3), (dict(ws=ctypes.c_void_p((1 << 20) + 16)), 3), (dict(nbytes=100), 3),
+    (dict(ws=None, B=140), 3), (dict(ws=ctypes.c_void_p((1 << 20) + 16)), 3), (dict(nbytes=100), 3),
 ]
 
 
