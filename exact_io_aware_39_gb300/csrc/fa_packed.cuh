@@ -38,6 +38,13 @@ struct PackedWorkspace {
 // heads, 144 with pairs of tiles; one of 16384: 1217 and 1228).
 inline bool packed_pair_heads(int Hq, int Hk) { return (Hq / Hk) % 2 == 0; }
 
+// Up to kDirect sequences: no plan kernel runs, every warp that needs the work
+// list makes it from the bounds (DirectList): 10 us less for a forward call, 19
+// for forward and backward (33 sequences of 40 tokens: 17.5 -> 8.2 and 47.7 ->
+// 29.0 us).
+constexpr int kDirect = 128, kManySlots = kDirect / 32;
+inline bool packed_many(int B) { return B > 32 && B <= kDirect; }
+
 // The backward's item is a key tile of a key/value head with all of its query
 // tiles, of all G query heads: G n steps for the first tile of a sequence of n
 // tiles. Where there are not two items for every SM, items are cut into parts
@@ -47,7 +54,7 @@ constexpr int kMaxParts = 16;
 inline int packed_bwd_parts(int B, int total, int Hk, int G, long long tiles) {
   constexpr double kSms = 152.;
   const double items = (double)tiles * Hk;
-  if (items >= 2. * kSms || B < 1) return 1;
+  if (items >= 2. * kSms || B < 1 || B > kDirect) return 1;   // (with more than kDirect sequences it would be 1)
   const double n = (double)((total + (long long)kTile * B - 1) / ((long long)kTile * B));   // tiles of an average sequence
   const double per_sm = items * G * (n + 1.) / 2. / kSms;
   const double parts = G * n / (per_sm > 1. ? per_sm : 1.);
@@ -75,13 +82,6 @@ inline PackedWorkspace packed_workspace_layout(int B, int total, int Hq, int Hk,
   if (w.parts > 1) w.total = al(w.part_off + (size_t)w.parts * 2 * Hk * w.cap_tiles * kTile * d * sizeof(float));
   return w;
 }
-
-// Up to kDirect sequences: no plan kernel runs, every warp that needs the work
-// list makes it from the bounds (DirectList): 10 us less for a forward call, 19
-// for forward and backward (33 sequences of 40 tokens: 17.5 -> 8.2 and 47.7 ->
-// 29.0 us).
-constexpr int kDirect = 128, kManySlots = kDirect / 32;
-inline bool packed_many(int B) { return B > 32 && B <= kDirect; }
 
 struct PackedFwdParams {
   const int32_t* cu;          // [B + 1]

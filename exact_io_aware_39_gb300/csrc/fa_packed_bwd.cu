@@ -946,8 +946,7 @@ cudaError_t launch_packed_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
     return launch_pdl(false, direct ? packed_bwd_dq_kernel<F16, false, SLOTS> : packed_bwd_dq_kernel<F16, false, 0>,
                       tiles, dim3(256), 0, s, q);
   const unsigned sums = (unsigned)p.cap_tiles * (unsigned)p.Hk * 2u * (kTile / kSumRows);
-  return launch_pdl(false, direct ? packed_bwd_dq_kernel<F16, true, SLOTS> : packed_bwd_dq_kernel<F16, true, 0>,
-                    dim3(tiles.x + sums), dim3(256), 0, s, q);
+  return launch_pdl(false, packed_bwd_dq_kernel<F16, true, SLOTS>, dim3(tiles.x + sums), dim3(256), 0, s, q);
 }
 
 }  // namespace

@@ -147,6 +147,34 @@ def test_either_side_of_the_direct_list(fa, B):
     _check(c, r, 0.125, True)
 
 
+@pytest.mark.parametrize("Hq,Hk,d,causal,dtype", [(32, 16, 64, True, BF), (16, 16, 128, True, FH),
+                                                  (48, 16, 128, False, BF), (16, 16, 40, False, BF)])
+def test_items_enough_to_stay_whole(fa, Hq, Hk, d, causal, dtype):
+    """More than two items of the backward for every SM: dK and dV are written
+    by the items themselves. (The other tests have fewer, whose parts are
+    summed.)"""
+    lens = [400, 300, 129, 77, 128, 1, 0, 250, 513]
+    c = _inputs(lens, Hq, Hk, d, dtype, 13, 3, 5, True)
+    assert (c["q"].shape[0] // 128 + len(lens)) * Hk >= 304
+    r = _run(fa, c, d ** -0.5, causal)
+    _settled(fa)
+    _check(c, r, d ** -0.5, causal)
+    r2 = _run(fa, c, d ** -0.5, causal)
+    _settled(fa)
+    for key in ("o", "lse", "dk", "dv"):
+        assert torch.equal(_bits(r[key].contiguous()), _bits(r2[key].contiguous())), key
+
+
+@pytest.mark.parametrize("G,n,causal", [(1, 900, True), (1, 900, False), (7, 260, True), (16, 128, False), (5, 1, True)])
+def test_items_in_parts(fa, G, n, causal):
+    """One key/value head: an item's steps (query head, query tile) in up to 16
+    ranges that begin and end inside a head."""
+    c = _inputs([n], G, 1, 64, BF, 14)
+    r = _run(fa, c, 0.125, causal)
+    _settled(fa)
+    _check(c, r, 0.125, causal)
+
+
 def test_head_major_layout(fa):
     """[heads, tokens, d] tensors seen as [tokens, heads, d]: the head stride is
     the larger one."""
