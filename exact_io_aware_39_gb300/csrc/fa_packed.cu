@@ -238,8 +238,9 @@ fa_status flash_attn_packed_fwd(const void* Q, const void* K, const void* V, voi
   p.stall = o.stall;
   p.cu = cu_seqlens;
   p.B = B;
-  p.cap_items = w.cap_items;
-  p.pair_heads = packed_pair_heads(Hq, Hk);
+  p.split = packed_split(B, total, Hq, w.cap_tiles, causal != 0);
+  p.cap_items = p.split ? w.cap_tiles : w.cap_items;
+  p.pair_heads = !p.split && packed_pair_heads(Hq, Hk);
   p.heads = p.pair_heads ? Hq / 2 : Hq;
   if (B > kDirect &&
       launch_packed_plan(cu_seqlens, B, total, p.pair_heads ? kTile : 2 * kTile, causal, false, p.plan,

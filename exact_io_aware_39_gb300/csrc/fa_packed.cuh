@@ -38,6 +38,17 @@ struct PackedWorkspace {
 // heads, 144 with pairs of tiles; one of 16384: 1217 and 1228).
 inline bool packed_pair_heads(int Hq, int Hk) { return (Hq / Hk) % 2 == 0; }
 
+// Where there are not more query tiles than SMs, the forward's item is one query
+// tile whose key tiles the two softmax groups take in turn (SPLIT), so that the
+// longest item is half as long: one sequence of 2176 tokens, 5 heads, causal, 17.9
+// us against 27.2 in pairs at d = 128, 14.9 against 21.5 at 64. Causal, whose items
+// differ in length, up to 256 tiles (two sequences of 3149 tokens, 4 heads: 24.2 and
+// 39.3; 288 tiles of 1100 tokens 19.1 and 18.9); not causal, 192 tiles of 700 tokens
+// would take 19.6 us and take 16.6. Sequences of one tile have nothing to share out.
+inline bool packed_split(int B, int total, int Hq, int cap_tiles, bool causal) {
+  return B <= 32 && total > kTile * B && (long long)cap_tiles * Hq <= (causal ? 256 : 152);
+}
+
 // Up to kDirect sequences: no plan kernel runs, every warp that needs the work
 // list makes it from the bounds (DirectList): 10 us less for a forward call, 19
 // for forward and backward (33 sequences of 40 tokens: 17.5 -> 8.2 and 47.7 ->
@@ -97,6 +108,7 @@ struct PackedFwdParams {
   uint32_t wait_us, stall;
   int cap_items;
   int pair_heads;             // an item's two query tiles: one tile of two heads, or two tiles of one head
+  int split;                  // an item is one query tile, its keys shared out between the softmax groups
   int heads;                  // Hq, or with pair_heads Hq / 2
   int group;                  // of those, per group of the work order
 };

@@ -9,7 +9,8 @@
 //     tile of two neighbouring query heads of one key/value head where the group
 //     size is even (both then end at the same key tile, and a sequence of one
 //     tile still fills both softmax groups), else two neighbouring tiles of a
-//     head;
+//     head. Calls of few query tiles take one to an item instead and share its key
+//     tiles out between the groups, whose sums are joined from TMEM (SPLIT);
 //   * the items of a call are listed on the device (the lengths are there),
 //     heaviest first: for up to 128 sequences by every producer warp for itself
 //     (DirectList), for more by a plan kernel. A CTA takes its own item, then,
@@ -53,7 +54,7 @@ constexpr int kOtherRegs = 72;
 constexpr float kRescaleThreshold = 8.0f; // log2 units
 constexpr float kSpecSumLimit = 256.0f;    // 2^kRescaleThreshold
 
-template <int D>
+template <int D, bool SPLIT>
 struct PackedFwdLayout {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kHalves = D / 64;
@@ -90,17 +91,23 @@ struct PackedFwdLayout {
   static constexpr int bItemFull = bPHalf + 2;        // [kItemRing]
   static constexpr int bItemEmpty = bItemFull + kItemRing;   // [kItemRing], 10: V producer, MMA and softmax warps
   static constexpr int bClc = bItemEmpty + kItemRing;        // the next item's cancellation answer has arrived
-  static constexpr int bDrain = bClc + 1;
+  // split keys: O_1 and the second group's statistics are complete; they have been read
+  static constexpr int bStats = bClc + 1;             // 4 arrivals
+  static constexpr int bJoined = bStats + 1;          // 4
+  static constexpr int bDrain = SPLIT ? bJoined + 1 : bStats;
   static constexpr int kNumBars = bDrain + 1;
   static constexpr int kMisc = (kBar + 8 * kNumBars + 15) & ~15;   // tmem slot, abort flag, -, wait limit
   static constexpr int kRing = kMisc + 16;            // [kItemRing] x {first row, length, unit or -1, head}
   static constexpr int kClc = kRing + 16 * kItemRing;   // 16-byte answer of a launch cancellation
-  static constexpr int kSmemBytes = kClc + 16;
+  static constexpr int kStats = kClc + 16;              // [128] (reference, sum) of the second group's rows
+  static constexpr int kSmemBytes = kStats + (SPLIT ? 8 * kTile : 0);
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
 // An item as the roles see it: its two query tiles, and the key tiles 0 .. n - 1
-// live for either.
+// live for either. SPLIT: one query tile, whose even key tiles are the first
+// softmax group's and whose odd ones the second's.
+template <bool SPLIT>
 struct Pair {
   int start, len, c, head;      // c < 0: no item
   int nT, n;
@@ -109,22 +116,31 @@ struct Pair {
     pair_heads = p.pair_heads != 0;
     causal = p.causal != 0;
     nT = (len + kTile - 1) / kTile;
-    n = causal ? last(has(1) ? 1 : 0) + 1 : nT;
+    if constexpr (SPLIT) n = causal ? c + 1 : nT;
+    else n = causal ? last(has(1) ? 1 : 0) + 1 : nT;
   }
-  __device__ __forceinline__ bool has(int t) const { return t == 0 || pair_heads || 2 * c + 1 < nT; }
-  __device__ __forceinline__ int qi(int t) const { return pair_heads ? c : 2 * c + t; }
-  __device__ __forceinline__ int hq(int t) const { return pair_heads ? 2 * head + t : head; }
-  __device__ __forceinline__ int last(int t) const { return causal ? qi(t) : nT - 1; }   // last key tile live for t
+  __device__ __forceinline__ bool has(int t) const {
+    if constexpr (SPLIT) return t < n;
+    return t == 0 || pair_heads || 2 * c + 1 < nT;
+  }
+  __device__ __forceinline__ int qi(int t) const { return SPLIT || pair_heads ? c : 2 * c + t; }
+  __device__ __forceinline__ int hq(int t) const { return SPLIT ? head : pair_heads ? 2 * head + t : head; }
+  // first and last key tile of t, which has every one (SPLIT: every second) between them
+  __device__ __forceinline__ int first(int t) const { return SPLIT ? t : 0; }
+  __device__ __forceinline__ int last(int t) const {
+    if constexpr (SPLIT) return n - 1 - ((n - 1 - t) & 1);
+    return causal ? qi(t) : nT - 1;
+  }
   __device__ __forceinline__ bool partial(int e, int q) const { return (causal && e == q) || (e + 1) * kTile > len; }
   // valid rows of the last key tile when it is not full, else 0
   __device__ __forceinline__ int tail() const { return len & (kTile - 1); }
 };
 
-template <int D, bool F16, int SLOTS>
+template <int D, bool F16, int SLOTS, bool SPLIT>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv, const PackedFwdParams p) {
-  using L = PackedFwdLayout<D>;
+  using L = PackedFwdLayout<D, SPLIT>;
   // With P over S (d = 128), P of a tile's first 64 keys goes to the tensor
   // core before the rest is formed, and its half of P V runs meanwhile; the
   // softmax then always takes the row max first, since P may not be formed
@@ -158,7 +174,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   if (tid == 0) {
     auto arrivals = [](int i) -> uint32_t {
       if ((i >= L::bPFull && i < L::bPFull + 2) || (i >= L::bSFree && i < L::bSFree + 2) ||
-          (i >= L::bPHalf && i < L::bPHalf + 2))
+          (i >= L::bPHalf && i < L::bPHalf + 2) || (SPLIT && (i == L::bStats || i == L::bJoined)))
         return 4u;
       return i >= L::bItemEmpty && i < L::bItemEmpty + L::kItemRing ? 10u : 1u;
     };
@@ -182,7 +198,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
 
   // Item k of this CTA from the ring; w.c < 0 when none is left or a wait
   // failed (then ok is false too). Executed by whole warps.
-  auto take_item = [&](int k, Pair& w) -> bool {
+  auto take_item = [&](int k, Pair<SPLIT>& w) -> bool {
     const int rs = k % L::kItemRing;
     w.c = -1;
     if (!bar_wait_warp(bar(L::bItemFull + rs), (uint32_t)(k / L::kItemRing) & 1u, ctl, 319)) return false;
@@ -209,7 +225,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     DirectList<SLOTS> dl;
     int n_items = 0;
     if (direct) {
-      dl.init(p.cu, p.B, p.total, p.pair_heads ? kTile : 2 * kTile, p.cap_items, p.causal != 0, p.err);
+      dl.init(p.cu, p.B, p.total, SPLIT || p.pair_heads ? kTile : 2 * kTile, p.cap_items, p.causal != 0, p.err);
       n_items = dl.items;
     } else {
       n_items = p.plan->items;
@@ -246,7 +262,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         if (!ok) break;
         if (item < 0) item = total;
       }
-      Pair w;
+      Pair<SPLIT> w;
       w.c = -1;
       if (item < total) {
         int head = 0;
@@ -325,7 +341,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     regs_dec<kOtherRegs>();
     if (lane == 0) tma_prefetch_map(&tv);
     int nv = 0;
-    Pair w;
+    Pair<SPLIT> w;
     bool ok = true;
     for (int k = 0; ok && take_item(k, w) && w.c >= 0; ++k) {
       const int hk = w.hq(0) / p.G;
@@ -381,7 +397,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     int zeroed = -1;                 // last V ring entry whose rows past the sequence were zeroed
     bool open = false;               // V ring entry nv - 1 has not gone back to the producer
     bool ok = true, more = true;
-    Pair w;
+    Pair<SPLIT> w;
     for (int k = 0; ok && more; ++k) {
       if (!(ok = take_item(k, w))) break;
       more = w.c >= 0;
@@ -397,20 +413,22 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       // every line of the kernel, and a larger one misses the instruction cache;
       // with copies of its own for the end of an item, items of one key tile
       // took 4.9 us instead of 4.2.)
-      bool first = !more;
-      if (more) {
+      bool first = !more || SPLIT;   // (SPLIT: a pending product may belong to a group that this item does not have)
+      if (!SPLIT && more) {
         const bool there = mbar_test(bar(L::bQFull + q_slot(0)), q_phase(0)) &&
                            mbar_test(bar(L::bKFull + nk % L::kStagesK), (uint32_t)(nk / L::kStagesK) & 1u);
         first = !__all_sync(0xFFFFFFFFu, there);
       }
-#pragma unroll 1
-      for (int e = first ? -1 : 0; e < n && ok; ++e) {
+      // entry e, for both query tiles (which = 2) or, SPLIT, for one group; a
+      // constant, so that the products' operands stay uniform registers
+      auto entry = [&](const int e, auto which) {
+        constexpr int kWhich = which;
         const int sk = nk % L::kStagesK;
         bool k_ready = false;
         // S_t = Q_t K_e^T
         auto issue_s = [&](int t) -> bool {
           if (L::kOwnP && ns[t] > 0 && !bar_wait_warp(bar(L::bSFree + t), (ns[t] - 1u) & 1u, ctl, 318)) return false;
-          if (e == 0 && !bar_wait_warp(bar(L::bQFull + q_slot(t)), q_phase(t), ctl, 314)) return false;
+          if (e == w.first(t) && !bar_wait_warp(bar(L::bQFull + q_slot(t)), q_phase(t), ctl, 314)) return false;
           if (!k_ready && !bar_wait_warp(bar(L::bKFull + sk), (uint32_t)(nk / L::kStagesK) & 1u, ctl, 317)) return false;
           k_ready = true;
           tc_fence_after();
@@ -446,42 +464,56 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           }
           if constexpr (L::kOwnP) mma_commit_w(bar(L::bPVDone + t));   // P_t may be rewritten, O_t rescaled
           if (plast[t]) mma_commit_w(bar(L::bOFinal + t));             // O_t is complete
+          if constexpr (SPLIT) mma_commit_w(bar(L::bVEmpty + sv));     // V of the entry is this group's alone
           ++npv[t];
           return true;
         };
         // the entry's PV becomes the pending one once the one before it is on its way
         auto set_pending = [&](int t) {
           pend[t] = nv;
-          pfirst[t] = e == 0;
+          pfirst[t] = e == w.first(t);
           plast[t] = e == last[t];
           ptail[t] = e == w.nT - 1 ? tail : 0;
         };
+        auto on = [](int t) -> bool { return kWhich == 2 || t == kWhich; };
         if constexpr (L::kOwnP) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
-            if (ok && e >= 0 && e <= last[t]) ok = issue_s(t);
-          if (!ok) break;
+            if (ok && e >= 0 && e <= last[t] && on(t)) ok = issue_s(t);
+          if (!ok) return;
           if (e >= 0) mma_commit_w(bar(L::bKEmpty + sk));   // K_e is no longer needed
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (ok && pend[t] >= 0) ok = issue_pv(t);
-            if (e >= 0 && e <= last[t]) set_pending(t);
+            if (ok && pend[t] >= 0 && on(t)) ok = issue_pv(t);
+            if (e >= 0 && e <= last[t] && on(t)) set_pending(t);
           }
         } else {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (ok && pend[t] >= 0) ok = issue_pv(t);
-            if (ok && e >= 0 && e <= last[t] && (ok = issue_s(t))) set_pending(t);
+            if (ok && pend[t] >= 0 && on(t)) ok = issue_pv(t);
+            if (ok && e >= 0 && e <= last[t] && on(t) && (ok = issue_s(t))) set_pending(t);
           }
           if (ok && e >= 0) mma_commit_w(bar(L::bKEmpty + sk));   // K_e is no longer needed
         }
-        if (!ok) break;
-        if (open) mma_commit_w(bar(L::bVEmpty + (nv - 1) % L::kStagesV));   // both PVs of the entry before are issued
+        if (!ok) return;
+        if (!SPLIT && open) mma_commit_w(bar(L::bVEmpty + (nv - 1) % L::kStagesV));   // both PVs of the entry before are issued
         open = e >= 0;
         if (e >= 0) {
           ++nk;
           ++nv;
         }
+      };
+      using Both = std::integral_constant<int, 2>;
+      if constexpr (SPLIT) {
+        entry(-1, Both{});
+#pragma unroll 1
+        for (int e = 0; e < n && ok; e += 2) {
+          entry(e, std::integral_constant<int, 0>{});
+          if (e + 1 < n && ok) entry(e + 1, std::integral_constant<int, 1>{});
+        }
+      } else {
+#pragma unroll 1
+        for (int e = first ? -1 : 0; e < n && ok; ++e) entry(e, Both{});
       }
       if (more) {
         ++nq[0];
@@ -502,16 +534,17 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     const uint32_t tP = L::kOwnP ? tmem + 256u + 2u * D + 64u * (uint32_t)t + lane_off : tS;
     const float sl2 = p.scale_log2;
     uint32_t nS = 0u, nO = 0u;               // S tiles and final O read by this group
+    uint32_t nJ = 0u;                        // SPLIT: items of two groups so far
     bool ok = true;
-    Pair w;
+    Pair<SPLIT> w;
     for (int k = 0; ok && take_item(k, w) && w.c >= 0; ++k) {
       if (!w.has(t)) continue;
       const int qi = w.qi(t), last = w.last(t);
       const int row = kTile * qi + r;        // query index within the sequence
       float m_ref = -INFINITY;
       float l = 0.f;
-      for (int e = 0; e <= last; ++e) {
-        const uint32_t n = (uint32_t)e;      // S tiles of this item before this one
+      for (int e = w.first(t); e <= last; e += SPLIT ? 2 : 1) {
+        const uint32_t n = (uint32_t)(e - w.first(t));   // 0: the first S tile of this item
         if (!(ok = bar_wait_warp(bar(L::bSFull + t), nS & 1u, ctl, 320 + t))) break;
         tc_fence_after();
         float x[128];
@@ -536,6 +569,11 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         if constexpr (L::kOwnP) {   // S_t is in registers: the next S_t may be computed
           tc_fence_before();
           mbar_arrive_warp(bar(L::bSFree + t));
+        }
+        if (SPLIT && t == 1 && n == 0u && nJ > 0u) {
+          // the first group has read O_1 of the item before: its product may be overwritten
+          if (!(ok = bar_wait_warp(bar(L::bJoined), (nJ - 1u) & 1u, ctl, 328))) break;
+          tc_fence_after();
         }
         if (w.partial(e, qi)) {
           // a key is masked when it lies past the row (causal) or past the
@@ -648,6 +686,33 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       if (!ok) break;
       ++nO;
       tc_fence_after();
+      // SPLIT: the first group joins what the second has, whose O it reads from TMEM:
+      //   O = (2^(m0 - M) O_0 + 2^(m1 - M) O_1) / (2^(m0 - M) l_0 + 2^(m1 - M) l_1)
+      float w0 = 1.f, w1 = 0.f;
+      const bool join = SPLIT && w.has(1);
+      if constexpr (SPLIT) {
+        float2* stats = reinterpret_cast<float2*>(smem + L::kStats);
+        if (join && t == 1) {
+          stats[r] = make_float2(m_ref, l);
+          tc_fence_before();
+          mbar_arrive_warp(bar(L::bStats));
+          ++nJ;
+          continue;
+        }
+        if (join) {
+          if (!(ok = bar_wait_warp(bar(L::bOFinal + 1), nJ & 1u, ctl, 325) &&
+                     bar_wait_warp(bar(L::bStats), nJ & 1u, ctl, 329)))
+            break;
+          ++nJ;
+          tc_fence_after();
+          const float2 o1 = stats[r];
+          const float M = fmaxf(m_ref, o1.x), ref = M == -INFINITY ? 0.f : M;
+          w0 = ex2(m_ref - ref);
+          w1 = ex2(o1.x - ref);
+          l = fmaf(w0, l, w1 * o1.y);
+          m_ref = M;
+        }
+      }
       const float inv_l = 1.f / l;
       const int s4 = lane & 3;
       const int row0 = kTile * qi + 32 * (warp & 3) + (lane & ~3);   // the quad's first row
@@ -661,6 +726,16 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
 #pragma unroll
         for (int i = 0; i < 32; ++i) u[i] = next[i];
         if (cc + 1 < D / 32) tmem_ld32(tO + 32u * (cc + 1), next);
+        if constexpr (SPLIT) {
+          if (join) {
+            uint32_t u1[32];
+            tmem_ld32(tO + (uint32_t)D + 32u * cc, u1);
+            tmem_ld_wait(u1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              u[i] = __float_as_uint(fmaf(w1, __uint_as_float(u1[i]), w0 * __uint_as_float(u[i])));
+          }
+        }
         uint32_t x[4][4];   // [word of a chunk][chunk of this row, then row of the quad]
 #pragma unroll
         for (int wd = 0; wd < 4; ++wd) {
@@ -679,6 +754,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       if (row < w.len)
         p.lse[(size_t)w.hq(t) * p.total + w.start + row] = (m_ref + log2f(l)) * 0.69314718055994531f;
       tc_fence_before();   // (the next PV of this tile waits for this group's next P)
+      if (join) mbar_arrive_warp(bar(L::bJoined));
     }
   } else {
     regs_dec<kOtherRegs>();   // warp 11: no role
@@ -692,16 +768,16 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   }
 }
 
-template <int D, bool F16, int SLOTS>
+template <int D, bool F16, int SLOTS, bool SPLIT>
 cudaError_t launch_packed_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const PackedFwdParams& p, cudaStream_t s) {
-  using L = PackedFwdLayout<D>;
+  using L = PackedFwdLayout<D, SPLIT>;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static PerDeviceOnce smem_set;
   e = once_per_device(smem_set, dev, [] {
-    return cudaFuncSetAttribute(fa_packed_fwd_kernel<D, F16, SLOTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(fa_packed_fwd_kernel<D, F16, SLOTS, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 L::kSmemBytes);
   });
   if (e != cudaSuccess) return e;
@@ -713,7 +789,7 @@ cudaError_t launch_packed_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
   q.group = p.G / (p.Hq / p.heads) * l2_head_group(4.0 * p.total * p.d, p.Hq / p.G);
   // a CTA per item where items are taken by cancelling CTAs, else one per SM
   const long long most = (long long)p.cap_items * p.heads;
-  return launch_pdl(true, fa_packed_fwd_kernel<D, F16, SLOTS>, dim3((unsigned)(p.B <= kDirect || most < sms ? most : sms)),
+  return launch_pdl(true, fa_packed_fwd_kernel<D, F16, SLOTS, SPLIT>, dim3((unsigned)(p.B <= kDirect || most < sms ? most : sms)),
                     dim3(kFwdThreads), L::kSmemBytes, s, tq, tk, tv, q);
 }
 
@@ -721,15 +797,18 @@ cudaError_t launch_packed_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
 
 cudaError_t launch_packed_fwd(bool f16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const PackedFwdParams& p, cudaStream_t s) {
-  auto run = [&](auto many) -> cudaError_t {
+  auto run = [&](auto many, auto split) -> cudaError_t {
     constexpr int SLOTS = many ? kManySlots : 1;
+    constexpr bool SPLIT = split;
     if (p.d <= 64)
-      return f16 ? launch_packed_fwd_d<64, true, SLOTS>(tq, tk, tv, p, s)
-                 : launch_packed_fwd_d<64, false, SLOTS>(tq, tk, tv, p, s);
-    return f16 ? launch_packed_fwd_d<128, true, SLOTS>(tq, tk, tv, p, s)
-               : launch_packed_fwd_d<128, false, SLOTS>(tq, tk, tv, p, s);
+      return f16 ? launch_packed_fwd_d<64, true, SLOTS, SPLIT>(tq, tk, tv, p, s)
+                 : launch_packed_fwd_d<64, false, SLOTS, SPLIT>(tq, tk, tv, p, s);
+    return f16 ? launch_packed_fwd_d<128, true, SLOTS, SPLIT>(tq, tk, tv, p, s)
+               : launch_packed_fwd_d<128, false, SLOTS, SPLIT>(tq, tk, tv, p, s);
   };
-  return packed_many(p.B) ? run(std::true_type{}) : run(std::false_type{});
+  using Yes = std::true_type;
+  using No = std::false_type;
+  return p.split ? run(No{}, Yes{}) : packed_many(p.B) ? run(Yes{}, No{}) : run(No{}, No{});
 }
 
 }  // namespace fa

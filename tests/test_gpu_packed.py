@@ -147,6 +147,26 @@ def test_either_side_of_the_direct_list(fa, B):
     _check(c, r, 0.125, True)
 
 
+@pytest.mark.parametrize("lens,Hq,Hk,causal", [([300, 140, 1000, 128, 1], 12, 3, True), ([1300], 14, 7, True),
+                                               ([700, 90, 0, 129], 8, 8, False), ([257, 256, 255], 5, 1, True)])
+@pytest.mark.parametrize("d,dtype", [(64, BF), (128, FH), (96, BF)])
+def test_query_tiles_on_their_own(fa, lens, Hq, Hk, causal, d, dtype):
+    """Few query tiles: the forward takes one to an item, its key tiles in turn
+    by two groups, up to two items to a block and items of one key tile between."""
+    c = _inputs(lens, Hq, Hk, d, dtype, 15, 2, 9, True)
+    T = c["q"].shape[0]
+    assert T > 128 * len(lens) and (T // 128 + len(lens)) * Hq <= (256 if causal else 152)
+    for qmul in (1.0, 20.0):          # (20: the groups' references differ)
+        c["q"].mul_(qmul)
+        r = _run(fa, c, d ** -0.5, causal)
+        _settled(fa)
+        _check(c, r, d ** -0.5, causal)
+        r2 = _run(fa, c, d ** -0.5, causal)
+        _settled(fa)
+        for key in ("o", "lse", "dk", "dv"):
+            assert torch.equal(_bits(r[key].contiguous()), _bits(r2[key].contiguous())), key
+
+
 @pytest.mark.parametrize("Hq,Hk,d,causal,dtype", [(32, 16, 64, True, BF), (16, 16, 128, True, FH),
                                                   (48, 16, 128, False, BF), (16, 16, 40, False, BF)])
 def test_items_enough_to_stay_whole(fa, Hq, Hk, d, causal, dtype):
@@ -293,9 +313,10 @@ def test_streams_and_replayed_graphs(fa):
         _check(c, out, 0.1, True, cu)
 
 
+@pytest.mark.parametrize("Hq,Hk", [(4, 2), (64, 64)], ids=["few_tiles", "many_tiles"])
 @pytest.mark.parametrize("d", [64, 128])
-def test_wait_runs_out_and_device_stays_usable(fa, d):
-    c = _inputs([700, 300], 4, 2, d, BF, 5)
+def test_wait_runs_out_and_device_stays_usable(fa, d, Hq, Hk):
+    c = _inputs([700, 300], Hq, Hk, d, BF, 5)
     r = _run(fa, c, 0.1, True)
     _settled(fa)
     fa.attention_packed_fwd(c["q"], c["k"], c["v"], c["cu"], 0.1, wait_limit_us=20000, test_stall=1)
