@@ -8,7 +8,7 @@
 // keys, so the work is reading the cache: 2 d elements per key for 4 d Nq G
 // operations, far under the 280 operations per byte where the tensor cores
 // would bound it. The design keeps the memory system busy and little else:
-//   * the unit of work is a tile of 16 or 32 keys of one (sequence, key/value
+//   * the unit of work is a tile of 16 to 64 keys of one (sequence, key/value
 //     head, 16 query rows); all units of the call are numbered in that order and
 //     cut into equal ranges, one for each warp of the grid, so that ragged
 //     lengths leave no warp without work;
@@ -27,7 +27,7 @@
 //     result does not change from call to call).
 // Measured, 32 query and 8 key/value heads, d = 128: 64 sequences of 512-8192
 // tokens in bf16 104 us with the join (5.7 TB/s of 6.8), 16 of 8192-65536 tokens
-// in e4m3 162 us (6.3 TB/s); one of 500 tokens 6.8 us.
+// in e4m3 160 us (6.4 TB/s); one of 500 tokens 6.8 us.
 //
 // e4m3: with q8, k8, v8 the payloads and ks, vs the scales of key j,
 //   S_j = ks_j (q . k8_j),  O = sum_j P_j vs_j v8_j.
@@ -227,7 +227,8 @@ constexpr float kMoveThreshold = 8.0f;    // log2 units: the reference moves onl
 // 256 sequences of 20-200 tokens 28.7 and 37.4 us, 16 of 8192-65536 243 and 246;
 // e4m3, with twice the keys to a byte, 12 warps against 8: 131 and 140 us; at
 // d = 64 with 64-key tiles, so that a step has as many bytes as at 128: 64
-// sequences of 512-8192 tokens 43 us, 48 with 12 x 32 x 4, 45 with 8 x 64 x 3), while
+// sequences of 512-8192 tokens 43 us, 48 with 12 x 32 x 4, 45 with 8 x 64 x 3,
+// before the join's and the scales' later steps), while
 // the warps of a cluster join their parts, and four of them with larger tiles do
 // better (one sequence of 500 tokens 6.8 us with 4 x 32 x 3, 8.8 with 12 x 16 x 2).
 struct Shape {
@@ -257,7 +258,7 @@ struct CachedLayout {
   // What a tile's scales do to its scores: worked out by every lane for its own
   // keys, or, with 64 keys, once per key and passed on through shared memory (per
   // warp, by pairs of keys: the factors and the log2 added, then the reciprocals).
-  // The calls above at d = 64 40 us so and 43 without; at d = 128, with 32 keys,
+  // The calls above at d = 64 41 us so and 43 without; at d = 128, with 32 keys,
   // the step through memory costs more than it saves (136 and 131 us).
   static constexpr bool kByKey = E4M3 && kKT == 64;
   static constexpr int kFactorBytes = kByKey ? 12 * kKT : 0;
