@@ -36,6 +36,12 @@
 // the second product are formed as 2^(s_j + log2 vs_j - m) with m the running
 // maximum of s_j + log2 vs_j, so they are at most 2^8 and lose nothing to
 // fp16's range however the scales differ; the row sum adds w_j / vs_j in fp32.
+// A value scale of 0 (a page outside the cache reads so, and a scale tensor may
+// start so) has no logarithm: it becomes the writer's smallest scale, so that its
+// w_j outweighs no other, and its row of V zeros in shared memory. (Looking for
+// them among the scales in registers takes 0.7 % of a call on 16 sequences of
+// 381292 tokens in all, d = 128, and 3 % of one on 16000; replacing each as it is
+// used took 6 % of the former, looking in shared memory ahead of the products 2.5.)
 #include "flash_attn_cache.h"
 #include "fa_common.cuh"
 #include "fa_ptx.cuh"
@@ -638,11 +644,23 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     [[maybe_unused]] const uint8_t* ss = smem + (sring - sbase) + s * 2 * L::kScaleBytes;
     // (16 keys of a page, or more of them in one piece)
     [[maybe_unused]] auto place = [&](int key) -> int { return box == 16 ? (key >> 4) * 128 + (key & 15) * 4 : key * 4; };
+    // a value's scale of 0 becomes 2^-64 and its row of V zeros (a lane writes the
+    // chunks first .. last - 1 of it); in a branch of the whole warp that seldom runs
+    [[maybe_unused]] auto no_scale = [&](float& vs, int key, int first, int last) {
+      if (vs == 0.f) {
+        vs = 0x1p-64f;
+        for (int c = first; c < last; ++c)
+          *reinterpret_cast<uint4*>(smem + (sv - sbase) + key * L::kRowBytes + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();   // (as above)
+      __syncwarp();
+    };
     if constexpr (L::kByKey) {
 #pragma unroll
       for (int key = lane; key < KT; key += 32) {
         const float ks = *reinterpret_cast<const float*>(ss + place(key));
-        const float vs = key < left ? *reinterpret_cast<const float*>(ss + L::kScaleBytes + place(key)) : 1.f;
+        float vs = key < left ? *reinterpret_cast<const float*>(ss + L::kScaleBytes + place(key)) : 1.f;
+        if (__any_sync(0xFFFFFFFFu, vs == 0.f)) no_scale(vs, key, 0, L::kRowBytes / 16);
         const int at = 4 * (key >> 1) + (key & 1);
         f[at] = ks * p.scale_log2;
         f[at + 2] = __log2f(vs);
@@ -695,6 +713,26 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     // scores in log2 units; with e4m3 plus log2 of the value's scale
     float ivs[KT / 8][2];
     if constexpr (E4M3) {
+      [[maybe_unused]] float2 vs2[KT / 8];
+      if constexpr (!L::kByKey) {
+        float least = 1.f;
+#pragma unroll
+        for (int n = 0; n < KT / 8; ++n) {
+          const int key = 8 * n + 2 * t4;
+          vs2[n] = *reinterpret_cast<const float2*>(ss + L::kScaleBytes + place(key));
+          if (key >= left) vs2[n].x = 1.f;       // past the sequence: any scale, the weight is zero
+          if (key + 1 >= left) vs2[n].y = 1.f;
+          least = fmin3(least, vs2[n].x, vs2[n].y);
+        }
+        // (eight lanes hold a key's scale and share its row's chunks out)
+        if (__any_sync(0xFFFFFFFFu, least == 0.f))
+#pragma unroll
+          for (int n = 0; n < KT / 8; ++n) {
+            const int key = 8 * n + 2 * t4, end = g < L::kRowBytes / 16 ? g + 1 : g;
+            no_scale(vs2[n].x, key, g, end);
+            no_scale(vs2[n].y, key + 1, g, end);
+          }
+      }
 #pragma unroll
       for (int n = 0; n < KT / 8; ++n) {
         float4 fa;   // two keys' factors, then what is added
@@ -706,12 +744,9 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         } else {
           const int key = 8 * n + 2 * t4;
           const float2 ks2 = *reinterpret_cast<const float2*>(ss + place(key));
-          float2 vs2 = *reinterpret_cast<const float2*>(ss + L::kScaleBytes + place(key));
-          if (key >= left) vs2.x = 1.f;       // past the sequence: any scale, the weight is zero
-          if (key + 1 >= left) vs2.y = 1.f;
-          ivs[n][0] = __fdividef(1.f, vs2.x);
-          ivs[n][1] = __fdividef(1.f, vs2.y);
-          fa = make_float4(ks2.x * p.scale_log2, ks2.y * p.scale_log2, __log2f(vs2.x), __log2f(vs2.y));
+          ivs[n][0] = __fdividef(1.f, vs2[n].x);
+          ivs[n][1] = __fdividef(1.f, vs2[n].y);
+          fa = make_float4(ks2.x * p.scale_log2, ks2.y * p.scale_log2, __log2f(vs2[n].x), __log2f(vs2[n].y));
         }
         sc[n][0] = fmaf(sc[n][0] * qs[0], fa.x, fa.z);
         sc[n][1] = fmaf(sc[n][1] * qs[0], fa.y, fa.w);

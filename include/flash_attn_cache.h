@@ -16,9 +16,9 @@
  *                       infinities), with one fp32 scale per row
  *   k_scale, v_scale : fp32 [num_pages, Hk, page_size] (FA_CACHE_E4M3 only,
  *       else NULL). An element stands for payload * scale. The writer stores
- *       powers of two; the reader takes any scale from 2^-64 to 2^120 (value
- *       scales of one sequence more than 2^100 apart may cost it weights
- *       below 2^-26 of the largest).
+ *       powers of two; the reader takes 0 and any scale from 2^-64 to 2^120
+ *       (value scales of one sequence more than 2^100 apart may cost it weights
+ *       below 2^-26 of the largest; one of 0 counts as 2^-64 here).
  *   page_size is 16, 32, 64, 128 or 256. Token j of a sequence lives in place
  *   j mod page_size of page block_table[b][j / page_size].
  *
@@ -86,7 +86,9 @@ int flash_attn_cached_needs_workspace(int B, int Nq, int Hq, int Hk, int d, int 
  *         elements apart (a multiple of 8, at least Hq d), heads d apart
  *   O   : out, 16-bit [B, Nq, Hq, d];  LSE : out, fp32 [B, Hq, Nq]
  *   block_table : in, int32 [B, max_pages]; entries past a sequence's last
- *         page are not read. A page outside the cache reads as zeros.
+ *         page are not read. A page outside the cache reads as zeros (with
+ *         FA_CACHE_E4M3 its scales too): its keys have a score of 0 and take
+ *         their weight of a value of zeros.
  *   seq_lens : in, int32 [B], clamped to [0, max_pages * page_size]
  *   A token that sees no key gets O = 0, LSE = -inf. What the cache holds
  *   behind a sequence's last token does not matter (NaN neither); the keys,

@@ -455,3 +455,72 @@ def test_helpers_refuse_what_does_not_fit(fa):
     badw(k_scale=None, v_scale=None)
     badw(k_cache=torch.zeros(3, 2, 16, 64, device="cuda"), v_cache=torch.zeros(3, 2, 16, 64, device="cuda"))
     _settled(fa)
+
+
+def _check_zero_scales(c, scale, o, lse):
+    """As _check, for sequences in which values have a scale of 0. Such a key is
+    weighed in units of 2^-64, the writer's smallest scale: s - 64, under 128 for
+    the scores here, is rounded to within 2^-18 of log2 units, so the weight (of
+    a value of zeros, which counts in the sum alone) to within 2^-18 of itself.
+    LSE takes that error, and half a step and the error of log2 of a sum of up to
+    2^128 in the same units (2^-18 + 2^-17): 2^-16 in all, times ln 2. A weight in
+    fp16 is off by up to 2^-25 of the largest, whose key adds 1 / its scale to the
+    sum: 2^-25 448 scale a key, and 448 scale is at most twice the row's maximum."""
+    q = c["q"]
+    ro, rl, absv, mag = C.cached_attention(_f64(q), c["k_f64"], c["v_f64"], c["table"].cpu().numpy(),
+                                           c["lens"].cpu().numpy(), scale)
+    assert 1.45 * mag.max() < 60                            # |s| in log2 units
+    u = 2.0 ** -8 if q.dtype == BF else 2.0 ** -11
+    ds = ((q.shape[3] + 4) * 2.0 ** -24 * mag + 2.0 ** -20).transpose(0, 2, 1)[..., None]
+    tol = (2.0 ** -11 + 2 * ds + 2.0 ** -17) * absv + u * np.abs(ro)
+    tol = tol + 2 * int(c["lens"].max()) * 2.0 ** -25 * np.abs(c["v_f64"]).max()
+    got, gl = _f64(o), lse.cpu().double().numpy()
+    assert np.isfinite(got).all() and np.isfinite(gl).all()
+    assert (np.abs(got - ro) <= tol).all(), np.abs(got - ro).max()
+    lt = ds[..., 0].transpose(0, 2, 1) + 2.0 ** -23 * np.abs(rl) + 2.0 ** -16
+    assert (np.abs(gl - rl) <= lt).all(), np.abs(gl - rl).max()
+    return ro
+
+
+@pytest.mark.parametrize("dtype", [BF, FH], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("room", [0, 1 << 17], ids=["on_chip", "ranges"])
+@pytest.mark.parametrize("d,page", [(64, 16), (64, 64), (128, 16), (128, 64), (80, 32), (48, 256)])
+def test_e4m3_pages_outside_the_cache_and_scales_of_zero(fa, d, page, room, dtype):
+    """In an e4m3 cache a page outside it reads as zeros too (scales among them),
+    and so does a row whose stored scale is 0, whatever its payload."""
+    lens = [150, 70, 33, 64]
+    c = _case(4, 2, 8, 2, d, page, lens, dtype, True, seed=4, qmul=0.02, room=room)
+    needs = fa.flash_attn_cached_needs_workspace(4, 2, 8, 2, d, page, c["table"].shape[1], 1)
+    assert needs == (1 if room else 0)
+    t = c["table"].cpu()
+    if page < 150:
+        c["table"][0, 1] = -1                               # amid a sequence
+    c["table"][1, 0] = 1 << 30                              # its first page
+    c["table"][2, :-(-33 // page)] = c["k"].shape[0]        # all of it
+    gone = [(0, 0), (0, 7), (0, 149), (3, 31), (3, 32), (3, 63)]
+    for b, j in gone:                                       # stored zeros under payloads that are none
+        at = (int(t[b, j // page]), slice(None), j % page)
+        c["vs"][at] = 0.0
+        c["v_f64"][at] = 0.0
+    at = (int(t[3, 5 // page]), slice(None), 5 % page)
+    c["ks"][at] = 0.0
+    c["k_f64"][at] = 0.0
+    o, lse = _run(fa, c, 0.2)
+    _settled(fa)
+    ro = _check_zero_scales(c, 0.2, o, lse)
+    assert (ro[2] == 0).all() and (o[2] == 0).all()
+    # value scales small enough that a unit scale would outweigh them all
+    live = c["vs"] == c["vs"]
+    c["vs"][live] *= 2.0 ** -40
+    c["v_f64"] *= 2.0 ** -40
+    o, lse = _run(fa, c, 0.2, lse=lse)
+    _settled(fa)
+    if dtype == BF:                                         # (fp16 cannot hold such outputs)
+        _check_zero_scales(c, 0.2, o, lse)
+    # nothing but scales of zero
+    c["vs"][live] = 0.0
+    c["v_f64"][:] = 0.0
+    o, lse = _run(fa, c, 0.2)
+    _settled(fa)
+    _check_zero_scales(c, 0.2, o, lse)
+    assert (o == 0).all()
