@@ -524,3 +524,31 @@ def test_e4m3_pages_outside_the_cache_and_scales_of_zero(fa, d, page, room, dtyp
     _settled(fa)
     _check_zero_scales(c, 0.2, o, lse)
     assert (o == 0).all()
+
+
+def test_write_edges_of_the_values(fa):
+    """The rows of test_write_edges_of_the_quantisation's kinds as values under
+    other keys: each tensor's payloads and scales are its own."""
+    d = 32
+    for dtype in (BF, FH):
+        big, tiny = torch.finfo(dtype).max, torch.finfo(dtype).smallest_normal
+        r = torch.zeros(10, d)
+        r[1, 30], r[2, 14:18] = -tiny, torch.tensor([big, -tiny, -big, 1.0])
+        r[3, 15:19] = torch.tensor([448.0, 17.0, -0.017, 19.0])
+        r[4, :3] = torch.tensor([450.0, -449.9, 1.0])
+        r[5] = torch.arange(d) * -1.0625
+        r[6, 15:18] = torch.tensor([float("-inf"), -3.0, 2.0])
+        r[7, 15:18] = torch.tensor([-300.0, float("nan"), 0.001])
+        r[8] = float("inf")
+        r[9] = torch.linspace(-448, 448, d)
+        k, v = r.to(dtype), r.roll(3, 0).flip(1).to(dtype)
+        kc, vc, ks, vs = _empty_cache(1, 1, 16, d, dtype, True)
+        fa.kv_cache_write(k[:, None].cuda(), v[:, None].cuda(), torch.arange(10, device="cuda"), kc, vc, ks, vs)
+        _settled(fa)
+        for x, cache, scale in ((k, kc, ks), (v, vc, vs)):
+            y, sc = C.e4m3_rows(_f64(x))
+            got = cache[0, 0, :10].float().cpu().numpy()
+            assert np.array_equal(np.isnan(got), np.isnan(y))
+            assert np.array_equal(np.nan_to_num(got), np.nan_to_num(y))
+            assert np.array_equal(scale[0, 0, :10].cpu().numpy(), sc)
+            assert (scale[0, 0, 10:] == 7.0).all()
