@@ -428,9 +428,10 @@ def _begin(t, wait_limit_us=0, test_stall=0):
     lib = _lib
     if lib is None or torch is None:
         import torch as module
-        torch, lib = module, load()
-        for dt, code in ((torch.bfloat16, FA_DTYPE_BF16), (torch.float16, FA_DTYPE_F16)):
+        lib = load()
+        for dt, code in ((module.bfloat16, FA_DTYPE_BF16), (module.float16, FA_DTYPE_F16)):
             _default_options[dt] = ctypes.byref(fa_options(code))
+        torch = module     # last: another thread's call that finds it finds the options too
     opts = _default_options.get(t.dtype)
     if opts is None or not t.is_cuda:
         raise ValueError("q (or k) must be a bfloat16 or float16 CUDA tensor")

@@ -119,3 +119,33 @@ def test_helpers_refuse_cpu_tensors(L):
         L.attention_packed_fwd(q, q, q, cu, 0.1)
     with pytest.raises(ValueError):
         L.attention_packed_bwd(q, q, q, q, q, torch.zeros(2, 4), cu, 0.1)
+
+
+def test_first_calls_of_two_threads(L, monkeypatch):
+    """A thread whose first call comes while another's prepares the helpers gets
+    its options too."""
+    import threading
+    from types import SimpleNamespace
+    monkeypatch.setattr(L, "torch", None)
+    monkeypatch.setattr(L, "_default_options", {})
+    make, got = L.fa_options, []
+    tensors = [SimpleNamespace(dtype=dt, is_cuda=True) for dt in (torch.bfloat16, torch.float16)]
+
+    def second():
+        for t in tensors:
+            try:
+                got.append(L._begin(t))
+            except ValueError as e:
+                got.append(e)
+
+    class Slowly(make):
+        def __init__(self, *a, **kw):
+            if threading.current_thread() is threading.main_thread():
+                other = threading.Thread(target=second)
+                other.start()
+                other.join()
+            super().__init__(*a, **kw)
+
+    monkeypatch.setattr(L, "fa_options", Slowly)
+    got.append(L._begin(tensors[0]))
+    assert len(got) >= 3 and all(isinstance(x, tuple) and x[1] is not None for x in got), got
