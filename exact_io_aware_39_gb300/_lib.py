@@ -474,6 +474,11 @@ def _plain(t, name, shape, dtype, dev):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{dev}")
 
 
+def _past_32_bits():
+    # (the C calls count in 32 bits, and ctypes would pass on what is left of a larger size)
+    raise ValueError("a size does not fit 32 bits")
+
+
 def _scratch(workspace, need, dev):
     """The caller's workspace, or a new one: (tensor, bytes)."""
     if workspace is None:
@@ -503,6 +508,8 @@ def attention_packed_fwd(q, k, v, cu_seqlens, scale, causal=True, out=None, lse=
         raise ValueError("q must be [tokens, Hq, d], k and v [tokens, Hk, d], cu_seqlens [B + 1]")
     T, Hq, d = q.shape
     Hk, B = k.shape[1], cu_seqlens.numel() - 1
+    if (T | Hq | Hk | d | B) >> 31:
+        _past_32_bits()
     _plain(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
     if out is None:
         out = torch.empty((T, Hq, d), dtype=dt, device=dev)
@@ -541,6 +548,8 @@ def attention_packed_bwd(q, k, v, o, do, lse, cu_seqlens, scale, causal=True, wo
         raise ValueError("q must be [tokens, Hq, d], k and v [tokens, Hk, d], cu_seqlens [B + 1]")
     T, Hq, d = q.shape
     Hk, B = k.shape[1], cu_seqlens.numel() - 1
+    if (T | Hq | Hk | d | B) >> 31:
+        _past_32_bits()
     hq, hk = (T, Hq, d), (T, Hk, d)
     _plain(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32, dev)
     _plain(lse, "lse", (Hq, T), torch.float32, dev)
@@ -598,7 +607,11 @@ def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, st
     dt = k.dtype
     kind = _cache_args(k_cache, v_cache, k_scale, v_scale, dt, dev)
     pages, Hk, page, d = k_cache.shape
-    T = k.shape[0] if k.dim() == 3 else -1
+    if k.dim() != 3:
+        raise ValueError("k and v must be [T, Hk, d]")
+    T = k.shape[0]
+    if (T | pages | Hk | page | d) >> 31:
+        _past_32_bits()
     k_tok, k_head = _rows16(k, "k", (T, Hk, d), dt, dev)
     v_tok, v_head = _rows16(v, "v", (T, Hk, d), dt, dev)
     _plain(slots, "slots", (T,), torch.int64, dev)
@@ -632,11 +645,14 @@ def attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_sc
     if q.dim() != 4 or q.shape[3] != d or block_table.dim() != 2:
         raise ValueError("q must be [B, Nq, Hq, d] with the cache's d, block_table [B, max_pages]")
     B, Nq, Hq, _ = q.shape
+    width = block_table.shape[1]
+    if (B | Nq | Hq | width | pages | Hk | page | d) >> 31:
+        _past_32_bits()
     s0, s1, s2, s3 = q.stride()
     if s3 != 1 or (Hq > 1 and s2 != d) or (B > 1 and Nq > 1 and s0 != Nq * s1):
         raise ValueError("q: a token's heads must be contiguous and the tokens evenly spaced")
     tok = s1 if Nq > 1 else (s0 if B > 1 else Hq * d)
-    _plain(block_table, "block_table", (B, block_table.shape[1]), torch.int32, dev)
+    _plain(block_table, "block_table", (B, width), torch.int32, dev)
     _plain(seq_lens, "seq_lens", (B,), torch.int32, dev)
     if out is None:
         out = torch.empty((B, Nq, Hq, d), dtype=dt, device=dev)
@@ -646,7 +662,6 @@ def attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_sc
         lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
     else:
         _plain(lse, "lse", (B, Hq, Nq), torch.float32, dev)
-    width = block_table.shape[1]
     ws, nbytes = None, 0
     if workspace is not None or lib.flash_attn_cached_needs_workspace(B, Nq, Hq, Hk, d, page, width, kind):
         workspace, nbytes = _scratch(workspace, lib.flash_attn_cached_workspace_size(B, Nq, Hq, Hk, d), dev)

@@ -149,3 +149,37 @@ def test_first_calls_of_two_threads(L, monkeypatch):
     monkeypatch.setattr(L, "fa_options", Slowly)
     got.append(L._begin(tensors[0]))
     assert len(got) >= 3 and all(isinstance(x, tuple) and x[1] is not None for x in got), got
+
+
+def test_sizes_past_32_bits_are_refused(L, monkeypatch):
+    """The C calls count in 32 bits; a size of 2^32 and a bit must not arrive as
+    the bit."""
+    class Library:
+        def __getattr__(self, name):
+            raise AssertionError(f"{name} was called")
+
+    monkeypatch.setattr(L, "torch", torch)
+    monkeypatch.setattr(L, "_begin", lambda *a: (Library(), None))
+    monkeypatch.setattr(L, "_elsewhere", lambda *a: None)
+    far = (1 << 32) + 8
+    mk = lambda *s, dtype=torch.bfloat16: torch.empty(*s, dtype=dtype, device="meta")
+    i32, f32 = torch.int32, torch.float32
+    for T, H, d in ((far, 1, 8), (8, far, 8), (8, 1, far)):
+        x, lse = mk(T, H, d), mk(H, T, dtype=f32)
+        cu = mk(3, dtype=i32)
+        with pytest.raises(ValueError, match="32 bits"):
+            L.attention_packed_fwd(x, x, x, cu, 0.1, out=x, lse=lse)
+        with pytest.raises(ValueError, match="32 bits"):
+            L.attention_packed_bwd(x, x, x, x, x, lse, cu, 0.1, dq=x, dk=x, dv=x)
+    x, lse = mk(8, 1, 8), mk(1, 8, dtype=f32)
+    with pytest.raises(ValueError, match="32 bits"):
+        L.attention_packed_fwd(x, x, x, mk(far, dtype=i32), 0.1, out=x, lse=lse)
+    for pages, T, d in ((4, far, 8), (far, 8, 8), (4, 8, far)):
+        c, x = mk(pages, 1, 16, d), mk(T, 1, d)
+        with pytest.raises(ValueError, match="32 bits"):
+            L.kv_cache_write(x, x, mk(T, dtype=torch.int64), c, c)
+    for B, Nq, Hq, width in ((far, 1, 1, 4), (2, far, 1, 4), (2, 1, far, 4), (2, 1, 1, far)):
+        c, q = mk(4, 1, 16, 8), mk(B, Nq, Hq, 8)
+        with pytest.raises(ValueError, match="32 bits"):
+            L.attention_cached_fwd(q, c, c, mk(B, width, dtype=i32), mk(B, dtype=i32), 0.1, out=q,
+                                   lse=mk(B, Hq, Nq, dtype=f32))
