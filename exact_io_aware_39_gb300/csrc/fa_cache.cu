@@ -25,9 +25,11 @@
 //     that holds a part of it writes O unnormalised with the row's reference
 //     and sum, and a second kernel joins the parts (in a fixed order, so the
 //     result does not change from call to call).
-// Measured, 32 query and 8 key/value heads, d = 128: 64 sequences of 512-8192
-// tokens in bf16 104 us with the join (5.7 TB/s of 6.8), 16 of 8192-65536 tokens
-// in e4m3 160 us (6.4 TB/s); one of 500 tokens 6.8 us.
+// Measured (the kernels, replayed from a graph), 32 query and 8 key/value heads,
+// d = 128: 64 sequences of 144891 tokens in all (512-8192 each) in bf16 101 us with
+// the join (5.9 TB/s of 6.8), 16 of 485214 in all (8192-65536 each) in e4m3 161 us
+// (6.4 TB/s); one of 500 tokens 6.8 us. The sizes below are those of these calls
+// where no other number of tokens is given.
 //
 // e4m3: with q8, k8, v8 the payloads and ks, vs the scales of key j,
 //   S_j = ks_j (q . k8_j),  O = sum_j P_j vs_j v8_j.
@@ -229,14 +231,15 @@ constexpr float kMoveThreshold = 8.0f;    // log2 units: the reference moves onl
 //
 // Warps, keys of a tile and tiles of a ring, by the tile width D (64 or 128), the
 // type and the kernel. A tile costs a warp its latency, 1 us or so, so the split
-// over the GPU wants warps (16-bit, d = 128, 12 x 16 keys x 2 against 6 x 32 x 2:
-// 256 sequences of 20-200 tokens 28.7 and 37.4 us, 16 of 8192-65536 243 and 246;
-// e4m3, with twice the keys to a byte, 12 warps against 8: 131 and 140 us; at
-// d = 64 with 64-key tiles, so that a step has as many bytes as at 128: 64
-// sequences of 512-8192 tokens 43 us, 48 with 12 x 32 x 4, 45 with 8 x 64 x 3,
-// before the join's and the scales' later steps), while
-// the warps of a cluster join their parts, and four of them with larger tiles do
-// better (one sequence of 500 tokens 6.8 us with 4 x 32 x 3, 8.8 with 12 x 16 x 2).
+// over the GPU wants warps. 16-bit, d = 128, 12 x 16 keys x 2 against 6 x 32 x 2:
+// the 64 sequences 101 and 113 us, 256 of 19381 tokens in all (20-200 each) 28.9 and
+// 37.6, 16 of 381292 in all 240 and 240. e4m3, with twice the keys to a byte, 12
+// warps of 32 keys x 2 against 8 x 32 x 3: the 16 sequences 161 and 174 us; at d =
+// 64 with 64-key tiles, so that a step has as many bytes as at 128: 64 sequences of
+// 151070 tokens in all 39 us, 46 with 12 x 32 x 4, 43 with 8 x 64 x 3. The warps of
+// a cluster join their parts, and four of them with larger tiles do better: one
+// sequence of 500 tokens 6.8 us with 4 x 32 x 3, 7.5 with 12 x 16 x 2, four of 4000
+// 15.9 and 16.9.
 struct Shape {
   int keys, warps, stages;
 };
@@ -264,8 +267,9 @@ struct CachedLayout {
   // What a tile's scales do to its scores: worked out by every lane for its own
   // keys, or, with 64 keys, once per key and passed on through shared memory (per
   // warp, by pairs of keys: the factors and the log2 added, then the reciprocals).
-  // The calls above at d = 64 41 us so and 43 without; at d = 128, with 32 keys,
-  // the step through memory costs more than it saves (136 and 131 us).
+  // 64 sequences of 151070 tokens in all at d = 64 39 us so and 42 without; at d =
+  // 128, with 32 keys, the step through memory costs more than it saves (the 16
+  // sequences 164 and 161 us).
   static constexpr bool kByKey = E4M3 && kKT == 64;
   static constexpr int kFactorBytes = kByKey ? 12 * kKT : 0;
   static constexpr int kFactors = kScale + kWarps * kStages * 2 * kScaleBytes;
@@ -803,7 +807,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         l[i >> 1] += E4M3 ? sc[n][i] * ivs[n][i & 1] : sc[n][i];
       }
     // O += P V, 16 keys at a time; P goes to 16 bits (of the inputs' type, or
-    // fp16 with e4m3: weights of at most 2^8 lose 2^-12 of themselves at most,
+    // fp16 with e4m3: weights of at most 2^8 lose 2^-11 of themselves at most,
     // or 2^-25 next to a largest one of about 1)
 #pragma unroll
     for (int kk = 0; kk < KT / 16; ++kk) {
@@ -1004,9 +1008,9 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 // about as many parts each as there are workers to a (sequence, head, row tile):
 // from 8 kManyParts on 16 warps take a row, so that no warp walks a long list (one
 // sequence of 32768 tokens, 228 parts a row: the call takes 29.5 us so, 37.4 with
-// four warps), from kManyParts on four (16 sequences of 8192-65536 tokens in e4m3,
-// 14 parts: 129.7 us, 131.8 with one, 133.9 with 16), and below it one (256
-// sequences of 20-200 tokens: 33.0 us, against 37.4 with a block of four).
+// four warps), from kManyParts on four (the 16 sequences in e4m3, 14 parts: 161 us,
+// 164 with one, 166 with 16), and below it one (256 sequences of 19381 tokens in all:
+// 28.9 us, against 35.6 with a block of four).
 constexpr int kManyParts = 8;
 
 template <int D, bool F16, int WARPS>
@@ -1138,9 +1142,13 @@ CachedWorkspace cached_workspace_layout(int B, int Nq, int Hq, int Hk, int d) {
 // one group of SMs) and as have a tile for each warp. A tile costs a warp about
 // 0.9 us, so that is taken while a warp gets at most 16 tiles of the longest
 // sequence that the table has room for, 12 where less than half of the card works
-// (us, so and split; 8 key/value heads, d = 128: 1 x 1000 bf16 7.3 and 9.9,
-// 1 x 8000 13.3 and 16.0, 1 x 16000 20.9 and 21.7, 4 x 8000 26.0 and 30.4; e4m3
-// 1 x 16000 18.1 and 19.5, 1 x 32768 31.2 and 25.9).
+// (us, so and, with a table of 262144 keys, split; inputs not in L2, 8 key/value
+// heads, d = 128: 1 x 500 bf16 7.1 and 8.8, 1 x 4000 10.0 and 11.9, 1 x 8000 14.1 and
+// 14.7, 16 x 500 11.8 and 16.3, 4 x 8000 26.7 and 31.4; e4m3 1 x 4000 9.2 and 10.9,
+// 1 x 8000 12.7 and 14.5, 4 x 8000 21.1 and 24.5). Towards the end of a single
+// sequence's range the split has become the faster one, since its join loads parts
+// early: 1 x 12000 bf16 18.1 and 16.8; e4m3 1 x 16000 19.1 and 18.3, 1 x 24000 25.4
+// and 21.3.
 int whole_cluster(long long units, long long tiles, int warps) {
   int c = 8;
   const auto most = [](int cc) { return cc == 8 ? 15 : cc == 4 ? 36 : kMaxCtas / cc; };

@@ -34,8 +34,8 @@ struct PackedWorkspace {
 
 // The forward's work item is one query tile of two neighbouring query heads of
 // a key/value head where there are such pairs, else two query tiles of a head
-// (24 sequences of 16-2048 tokens, 32 / 8 heads, d = 128: 124 us with pairs of
-// heads, 144 with pairs of tiles; one of 16384: 1217 and 1228).
+// (24 sequences of 16-2048 tokens, 32 / 8 heads, d = 128: 105 us with pairs of
+// heads, 118 with pairs of tiles; one of 16384: 1211 and 1232).
 inline bool packed_pair_heads(int Hq, int Hk) { return (Hq / Hk) % 2 == 0; }
 
 // Where there are not more query tiles than SMs, the forward's item is one query

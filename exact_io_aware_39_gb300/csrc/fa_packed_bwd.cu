@@ -188,7 +188,7 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     tmem_relinquish();
   }
   // global memory is read and written only from here on: what the pre-pass
-  // wrote (row statistics, zeroed accumulator and work counter) is visible
+  // wrote (row statistics, zeroed accumulator) is visible, and the plan
   grid_dep_wait();
   grid_dep_launch();
   tc_fence_before();
@@ -402,9 +402,8 @@ fa_packed_bwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       const uint32_t dS0 = desc_lo(desc_mnmajor(sbase + L::kdS, 0));
       bool ok = true;
       int g = 0;
-      // Shared-memory descriptors are built as a base plus a constant step per
-      // K step wherever that keeps within the MMA thread's registers, so that
-      // issuing an MMA costs the thread one 64-bit add.
+      // Shared-memory descriptors are a base's low word plus a constant step per
+      // K step (mma_ss_lo).
       // S^T = K Q^T of running query tile g1 (tail: its first row past the
       // sequence, or 0)
       auto issue_s = [&](uint32_t sK, int g1, int tail) -> bool {

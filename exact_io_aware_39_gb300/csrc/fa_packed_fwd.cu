@@ -32,10 +32,11 @@
 //
 // Bound: 4 d operations per visible pair on the tensor cores, and one
 // exponential per pair, which at d = 64 takes as long (16 per clock and SM); for
-// short sequences an item's way from its loads to its O. Measured, bf16, causal,
-// 32 query and 8 key/value heads, d = 128: one sequence of 16384 tokens 1.22 ms
-// (1.81 PFLOP/s, 95 % of the measured dense peak); 24 sequences of 16-2048 tokens
-// 106 us (1.07 PFLOP/s). The second was 150 + 10 us with a barrier of all roles
+// short sequences an item's way from its loads to its O. Measured (the kernel,
+// replayed a few times from a graph), bf16, causal, 32 query and 8 key/value heads,
+// d = 128: one sequence of 16384 tokens 1.22 ms (1.81 PFLOP/s, 95 % of the measured
+// dense peak; call after call for seconds, under the power cap, 1.34 ms); 24 sequences
+// of 16-2048 tokens 106 us (1.07 PFLOP/s). The second was 150 + 10 us with a barrier of all roles
 // around each item and the plan kernel for every call, 124 with the ring and the
 // pairs of heads (144 with pairs of tiles), and the rest is code size: an item
 // passes through all of the kernel's code, which at 96 KB missed the instruction

@@ -27,7 +27,8 @@
  * argument errors returned before any launch; no device memory allocated),
  * except that d is a multiple of 8 from 8 to 128 (of 16 with FA_CACHE_E4M3).
  * Of the options only dtype, wait_limit_us and test_stall are used; p_drop
- * must be 0 and tile_record NULL (FA_ERR_UNSUPPORTED otherwise).
+ * must be 0 and tile_record NULL (FA_ERR_UNSUPPORTED otherwise). The writer
+ * waits for nothing and refuses test_stall (FA_ERR_UNSUPPORTED).
  */
 #ifndef FLASH_ATTN_CACHE_H
 #define FLASH_ATTN_CACHE_H
@@ -71,7 +72,9 @@ fa_status flash_attn_kv_cache_write(const void* K, const void* V, int64_t k_toke
 size_t flash_attn_cached_workspace_size(int B, int Nq, int Hq, int Hk, int d);
 
 /* 0 when a call of this shape uses no workspace (few sequences that a short
- * table holds: parts are joined on chip), so that it may be NULL; else 1. */
+ * table holds: parts are joined on chip, which is the faster way for short
+ * sequences), so that it may be NULL; else 1. What counts is max_pages, since
+ * the lengths are on the device. */
 int flash_attn_cached_needs_workspace(int B, int Nq, int Hq, int Hk, int d, int page_size, int max_pages,
                                       int cache_type);
 

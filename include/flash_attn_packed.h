@@ -37,6 +37,9 @@
  *    aligned; contents on entry do not matter. Calls whose kernels may overlap
  *    need workspaces of their own. A forward call of at most 128 sequences uses
  *    none (workspace may be NULL).
+ *  - Launches are sized by B and total, since the bounds are on the device:
+ *    tensors much longer than their sequences cost time for rows that no
+ *    sequence has.
  */
 #ifndef FLASH_ATTN_PACKED_H
 #define FLASH_ATTN_PACKED_H

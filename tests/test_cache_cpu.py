@@ -97,3 +97,9 @@ def test_helpers_refuse_cpu_tensors(L):
     with pytest.raises(ValueError):
         L.attention_cached_fwd(k[:, None], c, c, torch.zeros(4, 1, dtype=torch.int32),
                                torch.ones(4, dtype=torch.int32), 0.1)
+
+
+def test_write_refuses_a_stall(L):
+    """(it has no wait that could run out)"""
+    assert _write(L, opts=L.fa_options(test_stall=1)) == 2
+    assert _write(L, opts=L.fa_options(test_stall=2)) == 1
