@@ -30,7 +30,7 @@
 // dQ = 16-bit(scale * accumulator).
 //
 // Roundings: P and dS go to the inputs' 16-bit type for the products that read
-// them (half a step each; dS is what the error of dQ and dK is made of: 2.4e-3 of
+// them (half a step each; dS is what the error of dQ and dK is made of: 2.5e-3 of
 // their norm in bf16, where rounding them alone makes 1.7e-3); D, sums and
 // accumulators are fp32.
 //
