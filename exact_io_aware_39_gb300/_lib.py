@@ -1,6 +1,6 @@
 """ctypes binding of libflashattn.so: the C ABI of include/flash_attn.h,
-flash_attn_packed.h, flash_attn_cache.h and standard_attn.h under the same names, plus thin helpers
-that take torch tensors.
+flash_attn_packed.h, flash_attn_cache.h, flash_attn_scored.h and standard_attn.h under the same names,
+plus thin helpers that take torch tensors.
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels behind the C ABI. There is no CPU or PyTorch fallback; if the shared
@@ -34,6 +34,7 @@ EXPORTS = [
     "flash_attn_packed_workspace_size", "flash_attn_packed_fwd", "flash_attn_packed_bwd",
     "flash_attn_kv_cache_write", "flash_attn_cached_workspace_size", "flash_attn_cached_needs_workspace",
     "flash_attn_cached_fwd",
+    "flash_attn_packed_scored_fwd", "flash_attn_packed_scored_bwd",
     "standard_attn_workspace_size", "standard_attn_fwd", "standard_attn_bwd",
 ]
 
@@ -52,6 +53,15 @@ class fa_options(ctypes.Structure):
                  test_stall=0):
         super().__init__(ctypes.sizeof(fa_options), dtype, float(p_drop), 0, int(seed), tile_record,
                          int(wait_limit_us), int(test_stall))
+
+
+class fa_scores(ctypes.Structure):
+    """Mirror of the C struct fa_scores (size is set by the constructor)."""
+    _fields_ = [("size", ctypes.c_uint32), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
+
+    def __init__(self, softcap=0.0, slopes=None, prefix_lens=None):
+        super().__init__(ctypes.sizeof(fa_scores), float(softcap), slopes, prefix_lens)
 
 
 class FlashAttnError(RuntimeError):
@@ -102,6 +112,11 @@ def load(path=LIB_PATH):
     lib.flash_attn_packed_fwd.restype = i32
     lib.flash_attn_packed_bwd.argtypes = [vp] * 10 + [i32] * 5 + [vp, f32, i32, opt_p, vp, sz, vp]
     lib.flash_attn_packed_bwd.restype = i32
+    # (scores: an fa_scores by reference, or its bytes)
+    lib.flash_attn_packed_scored_fwd.argtypes = [vp] * 6 + [i32] * 5 + [vp, f32, i32, vp, opt_p, vp, sz, vp]
+    lib.flash_attn_packed_scored_fwd.restype = i32
+    lib.flash_attn_packed_scored_bwd.argtypes = [vp] * 10 + [i32] * 5 + [vp, f32, i32, vp, opt_p, vp, sz, vp]
+    lib.flash_attn_packed_scored_bwd.restype = i32
     lib.flash_attn_kv_cache_write.argtypes = [vp, vp, i64, i64, i64, i64, vp, i32, i32, i32, vp, vp, vp, vp, i32, i32,
                                               i32, opt_p, vp]
     lib.flash_attn_kv_cache_write.restype = i32
@@ -197,6 +212,23 @@ def flash_attn_packed_bwd(Q, K, V, O, dO, LSE, dQ, dK, dV, cu_seqlens, B, total,
     return load().flash_attn_packed_bwd(Q, K, V, O, dO, LSE, dQ, dK, dV, cu_seqlens, B, total, Hq, Hk, d, strides, scale,
                                         causal, None if options is None else ctypes.byref(options), workspace,
                                         workspace_bytes, stream)
+
+
+def flash_attn_packed_scored_fwd(Q, K, V, O, LSE, cu_seqlens, B, total, Hq, Hk, d, strides, scale, causal, scores, options,
+                                 workspace, workspace_bytes, stream):
+    return load().flash_attn_packed_scored_fwd(Q, K, V, O, LSE, cu_seqlens, B, total, Hq, Hk, d, strides, scale, causal,
+                                               None if scores is None else ctypes.byref(scores),
+                                               None if options is None else ctypes.byref(options), workspace,
+                                               workspace_bytes, stream)
+
+
+def flash_attn_packed_scored_bwd(Q, K, V, O, dO, LSE, dQ, dK, dV, cu_seqlens, B, total, Hq, Hk, d, strides, scale,
+                                 causal, scores, options, workspace, workspace_bytes, stream):
+    return load().flash_attn_packed_scored_bwd(Q, K, V, O, dO, LSE, dQ, dK, dV, cu_seqlens, B, total, Hq, Hk, d,
+                                               strides, scale, causal,
+                                               None if scores is None else ctypes.byref(scores),
+                                               None if options is None else ctypes.byref(options), workspace,
+                                               workspace_bytes, stream)
 
 
 def flash_attn_kv_cache_write(K, V, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots, T, Hk, d,
@@ -417,6 +449,7 @@ FA_CACHE_16BIT, FA_CACHE_E4M3 = 0, 1
 PACKED_DIRECT = 128          # a forward of so many sequences needs no workspace
 # (int64 strides as bytes: packing them takes a tenth of a ctypes array's time)
 _pack8, _pack16 = struct.Struct("=8q").pack, struct.Struct("=16q").pack
+_pack_scores = struct.Struct("=IfQQ").pack     # fa_scores
 _default_options = {}        # dtype -> (reference to) its fa_options
 torch = None                 # bound with the library, by the first call
 
@@ -488,21 +521,35 @@ def _scratch(workspace, need, dev):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _scores(softcap, slopes, prefix_lens, Hq, B, dev):
+    """The fa_scores of a call as bytes."""
+    if slopes is not None:
+        _plain(slopes, "slopes", (Hq,), torch.float32, dev)
+    if prefix_lens is not None:
+        _plain(prefix_lens, "prefix_lens", (B,), torch.int32, dev)
+    return _pack_scores(24, softcap, 0 if slopes is None else slopes.data_ptr(),
+                        0 if prefix_lens is None else prefix_lens.data_ptr())
+
+
 def attention_packed_fwd(q, k, v, cu_seqlens, scale, causal=True, out=None, lse=None, workspace=None, stream=None,
-                         wait_limit_us=0, test_stall=0):
+                         wait_limit_us=0, test_stall=0, softcap=0.0, slopes=None, prefix_lens=None):
     """O, LSE of attention within each sequence of a packed batch. q: bf16 or
     fp16 [tokens, Hq, d]; k, v: [tokens, Hk, d], Hq a multiple of Hk (query
     head h reads key/value head h // (Hq // Hk)); rows may be strided, as views
     of a fused projection are. cu_seqlens: int32 [B + 1], sequence b is rows
     cu_seqlens[b] .. cu_seqlens[b + 1] - 1. Returns O like q and LSE float32
-    [Hq, tokens]; rows of no sequence are left as they are in `out` and `lse`."""
+    [Hq, tokens]; rows of no sequence are left as they are in `out` and `lse`.
+    softcap > 0 caps the scores: softcap * tanh(score / softcap). slopes, float32
+    [Hq], lowers those of head h by slopes[h] times the distance of query and key.
+    prefix_lens, int32 [B], lets all tokens of a sequence see its first
+    prefix_lens[b] (causal calls only)."""
     lib, opts = _begin(q, wait_limit_us, test_stall)
     dev = q.get_device()
     ctx = _elsewhere(stream, dev)
     if ctx is not None:
         with ctx:
             return attention_packed_fwd(q, k, v, cu_seqlens, scale, causal, out, lse, workspace, None, wait_limit_us,
-                                        test_stall)
+                                        test_stall, softcap, slopes, prefix_lens)
     dt = q.dtype
     if q.dim() != 3 or k.dim() != 3 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("q must be [tokens, Hq, d], k and v [tokens, Hk, d], cu_seqlens [B + 1]")
@@ -523,6 +570,13 @@ def attention_packed_fwd(q, k, v, cu_seqlens, scale, causal=True, out=None, lse=
     if B > PACKED_DIRECT or workspace is not None:
         workspace, nbytes = _scratch(workspace, lib.flash_attn_packed_workspace_size(B, T, Hq, Hk, d, 0), dev)
         ws = workspace.data_ptr()
+    if softcap or slopes is not None or prefix_lens is not None:
+        rc = lib.flash_attn_packed_scored_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                              cu_seqlens.data_ptr(), B, T, Hq, Hk, d, st, scale, 1 if causal else 0,
+                                              _scores(softcap, slopes, prefix_lens, Hq, B, dev), opts, ws, nbytes,
+                                              torch._C._cuda_getCurrentRawStream(dev))
+        _check(rc, "flash_attn_packed_scored_fwd")
+        return out, lse
     rc = lib.flash_attn_packed_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                                    cu_seqlens.data_ptr(), B, T, Hq, Hk, d, st, scale, 1 if causal else 0, opts, ws,
                                    nbytes, torch._C._cuda_getCurrentRawStream(dev))
@@ -531,18 +585,19 @@ def attention_packed_fwd(q, k, v, cu_seqlens, scale, causal=True, out=None, lse=
 
 
 def attention_packed_bwd(q, k, v, o, do, lse, cu_seqlens, scale, causal=True, workspace=None, dq=None, dk=None, dv=None,
-                         stream=None, wait_limit_us=0, test_stall=0):
+                         stream=None, wait_limit_us=0, test_stall=0, softcap=0.0, slopes=None, prefix_lens=None):
     """dQ, dK, dV of attention_packed_fwd from its inputs, its O and LSE and the
     output gradient do (like q); dK and dV are summed over the query heads that
     share a key/value head. Rows of no sequence are left as they are in dq, dk,
-    dv (which may be strided like q, k, v)."""
+    dv (which may be strided like q, k, v). softcap, slopes (which get no gradient)
+    and prefix_lens as in the forward call."""
     lib, opts = _begin(q, wait_limit_us, test_stall)
     dev = q.get_device()
     ctx = _elsewhere(stream, dev)
     if ctx is not None:
         with ctx:
             return attention_packed_bwd(q, k, v, o, do, lse, cu_seqlens, scale, causal, workspace, dq, dk, dv, None,
-                                        wait_limit_us, test_stall)
+                                        wait_limit_us, test_stall, softcap, slopes, prefix_lens)
     dt = q.dtype
     if q.dim() != 3 or k.dim() != 3 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("q must be [tokens, Hq, d], k and v [tokens, Hk, d], cu_seqlens [B + 1]")
@@ -563,6 +618,14 @@ def attention_packed_bwd(q, k, v, o, do, lse, cu_seqlens, scale, causal=True, wo
                  *_rows16(o, "o", hq, dt, dev), *_rows16(do, "do", hq, dt, dev), *_rows16(dq, "dq", hq, dt, dev),
                  *_rows16(dk, "dk", hk, dt, dev), *_rows16(dv, "dv", hk, dt, dev))
     workspace, nbytes = _scratch(workspace, lib.flash_attn_packed_workspace_size(B, T, Hq, Hk, d, 1), dev)
+    if softcap or slopes is not None or prefix_lens is not None:
+        rc = lib.flash_attn_packed_scored_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+                                              lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                              cu_seqlens.data_ptr(), B, T, Hq, Hk, d, st, scale, 1 if causal else 0,
+                                              _scores(softcap, slopes, prefix_lens, Hq, B, dev), opts,
+                                              workspace.data_ptr(), nbytes, torch._C._cuda_getCurrentRawStream(dev))
+        _check(rc, "flash_attn_packed_scored_bwd")
+        return dq, dk, dv
     rc = lib.flash_attn_packed_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
                                    lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                                    cu_seqlens.data_ptr(), B, T, Hq, Hk, d, st, scale, 1 if causal else 0, opts,

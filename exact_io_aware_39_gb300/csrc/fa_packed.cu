@@ -1,7 +1,7 @@
 // Attention over packed sequences: argument checks, tensor maps, the plan
 // kernel and the launch sequences. The kernels are in fa_packed_fwd.cu and
 // fa_packed_bwd.cu.
-#include "flash_attn_packed.h"
+#include "flash_attn_scored.h"
 #include "fa_packed.cuh"
 
 #include <cmath>
@@ -23,7 +23,7 @@ constexpr int kMaxUnits = kMaxN / kTile;   // most tiles of a sequence: 1024
 // sorted order, which gives every unit its place without a search. Not causal:
 // a unit costs its sequence's length, so the units follow the sorted order.
 __global__ void __launch_bounds__(kPlanThreads)
-packed_plan_kernel(const int32_t* __restrict__ cu, int B, int total, int rows, int causal, int backward,
+packed_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ prefix, int B, int total, int rows, int causal, int backward,
                    PackedPlan* plan, int* sorted, PackedItem* items, int cap_items, PackedItem* tiles, int cap_tiles,
                    unsigned int* err) {
   __shared__ int hist[kMaxUnits + 1];      // sequences with that many units; then the next free rank
@@ -89,7 +89,11 @@ packed_plan_kernel(const int32_t* __restrict__ cu, int B, int total, int rows, i
     const int rank = base + tid;
     int start = 0, len = 0;
     bool bad;
-    if (rank < live) len = seq(sorted[rank], start, bad);
+    int pre = 0;
+    if (rank < live) {
+      len = seq(sorted[rank], start, bad);
+      pre = seq_prefix(prefix, sorted[rank], len);
+    }
     const int n = units(len);
     int sum = 0;
     const int first = carry[0] + block_scan(n, (base / kPlanThreads) & 1, sum) - n;
@@ -101,10 +105,11 @@ packed_plan_kernel(const int32_t* __restrict__ cu, int B, int total, int rows, i
       if (nn == 0) continue;
       const int s = __shfl_sync(0xFFFFFFFFu, start, l), ln = __shfl_sync(0xFFFFFFFFu, len, l);
       const int f = __shfl_sync(0xFFFFFFFFu, first, l), rk = __shfl_sync(0xFFFFFFFFu, rank, l);
+      const int pr = __shfl_sync(0xFFFFFFFFu, pre, l);
       for (int c = lane; c < nn; c += 32) {
         // backward, causal: key tile kj has nn - 1 - kj query tiles behind it
         // (a sequence past the padded rows -- bounds that overlap -- is left out)
-        const PackedItem it{s, backward && f + nn > cap_tiles ? 0 : ln, backward && causal ? nn - 1 - c : c, f};
+        const PackedItem it{s, backward && f + nn > cap_tiles ? 0 : ln, with_prefix(backward && causal ? nn - 1 - c : c, pr), f};
         const int at = causal ? off[c] + rk : f + c;
         if (at < cap_items) items[at] = it;
         if (backward && f + c < cap_tiles) tiles[f + c] = PackedItem{s, ln, c, f};
@@ -168,34 +173,27 @@ fa_status packed_options(const fa_options* options, PackedOptions* o) {
 
 }  // namespace
 
-cudaError_t launch_packed_plan(const int32_t* cu, int B, int total, int rows, int causal, bool backward,
-                               PackedPlan* plan, int* sorted, PackedItem* items, int cap_items, PackedItem* tiles,
+cudaError_t launch_packed_plan(const int32_t* cu, const int32_t* prefix, int B, int total, int rows, int causal,
+                               bool backward, PackedPlan* plan, int* sorted, PackedItem* items, int cap_items, PackedItem* tiles,
                                int cap_tiles, unsigned int* err, cudaStream_t s) {
-  packed_plan_kernel<<<1, kPlanThreads, 0, s>>>(cu, B, total, rows, causal, backward ? 1 : 0, plan, sorted, items,
+  packed_plan_kernel<<<1, kPlanThreads, 0, s>>>(cu, prefix, B, total, rows, causal, backward ? 1 : 0, plan, sorted, items,
                                                 cap_items, tiles, cap_tiles, err);
   return cudaGetLastError();
 }
 
-}  // namespace fa
+namespace {
 
-using namespace fa;
-
-extern "C" {
-
-size_t flash_attn_packed_workspace_size(int B, int total, int Hq, int Hk, int d, int backward) {
-  if (check_packed_shape(B, total, Hq, Hk, d) != FA_OK) return 0;
-  return packed_workspace_layout(B, total, Hq, Hk, d, backward != 0).total;
-}
-
-fa_status flash_attn_packed_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE,
+fa_status packed_fwd_call(const void* Q, const void* K, const void* V, void* O, float* LSE,
                                 const int32_t* cu_seqlens, int B, int total, int Hq, int Hk, int d,
-                                const int64_t* strides, float scale, int causal, const fa_options* options,
+                                const int64_t* strides, float scale, int causal, const fa_scores* scores, const fa_options* options,
                                 void* workspace, size_t workspace_bytes, void* stream) {
   fa_status st = check_packed_shape(B, total, Hq, Hk, d);
   if (st != FA_OK) return st;
   if (!std::isfinite(scale) || scale <= 0.f || (causal != 0 && causal != 1)) return FA_ERR_INVALID_ARG;
   PackedOptions o;
   if ((st = packed_options(options, &o)) != FA_OK) return st;
+  ScoreParams score;
+  if ((st = read_scores(scores, scale, causal, false, &score)) != FA_OK) return st;
   Strides sq, sk, sv, so;
   if (!read_strides(strides, 0, Hq, d, &sq) || !read_strides(strides, 1, Hk, d, &sk) ||
       !read_strides(strides, 2, Hk, d, &sv) || !read_strides(strides, 3, Hq, d, &so))
@@ -238,27 +236,31 @@ fa_status flash_attn_packed_fwd(const void* Q, const void* K, const void* V, voi
   p.stall = o.stall;
   p.cu = cu_seqlens;
   p.B = B;
+  p.score = score;
   p.split = packed_split(B, total, Hq, w.cap_tiles, causal != 0);
   p.cap_items = p.split ? w.cap_tiles : w.cap_items;
   p.pair_heads = !p.split && packed_pair_heads(Hq, Hk);
   p.heads = p.pair_heads ? Hq / 2 : Hq;
   if (B > kDirect &&
-      launch_packed_plan(cu_seqlens, B, total, p.pair_heads ? kTile : 2 * kTile, causal, false, p.plan,
+      launch_packed_plan(cu_seqlens, p.score.prefix, B, total, p.pair_heads ? kTile : 2 * kTile, causal, false, p.plan,
                          reinterpret_cast<int*>(ws + w.sorted_off), reinterpret_cast<PackedItem*>(ws + w.item_off),
                          w.cap_items, nullptr, 0, err, s) != cudaSuccess)
     return FA_ERR_CUDA;
-  return launch_packed_fwd(o.f16, tq, tk, tv, p, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const auto launch = score.cap ? launch_packed_fwd_cap : score.slopes || score.prefix ? launch_packed_fwd_bias : launch_packed_fwd;
+  return launch(o.f16, tq, tk, tv, p, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-fa_status flash_attn_packed_bwd(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+fa_status packed_bwd_call(const void* Q, const void* K, const void* V, const void* O, const void* dO,
                                 const float* LSE, void* dQ, void* dK, void* dV, const int32_t* cu_seqlens, int B,
                                 int total, int Hq, int Hk, int d, const int64_t* strides, float scale, int causal,
-                                const fa_options* options, void* workspace, size_t workspace_bytes, void* stream) {
+                                const fa_scores* scores, const fa_options* options, void* workspace, size_t workspace_bytes, void* stream) {
   fa_status st = check_packed_shape(B, total, Hq, Hk, d);
   if (st != FA_OK) return st;
   if (!std::isfinite(scale) || scale <= 0.f || (causal != 0 && causal != 1)) return FA_ERR_INVALID_ARG;
   PackedOptions o;
   if ((st = packed_options(options, &o)) != FA_OK) return st;
+  ScoreParams score;
+  if ((st = read_scores(scores, scale, causal, false, &score)) != FA_OK) return st;
   Strides ss[8];   // Q, K, V, O, dO, dQ, dK, dV
   const int heads[8] = {Hq, Hk, Hk, Hq, Hq, Hq, Hk, Hk};
   for (int i = 0; i < 8; ++i)
@@ -329,12 +331,61 @@ fa_status flash_attn_packed_bwd(const void* Q, const void* K, const void* V, con
   p.stall = o.stall;
   p.cu = cu_seqlens;
   p.B = B;
+  p.score = score;
   if (B > kDirect &&
-      launch_packed_plan(cu_seqlens, B, total, kTile, causal, true, p.plan, reinterpret_cast<int*>(ws + w.sorted_off),
+      launch_packed_plan(cu_seqlens, p.score.prefix, B, total, kTile, causal, true, p.plan, reinterpret_cast<int*>(ws + w.sorted_off),
                          reinterpret_cast<PackedItem*>(ws + w.item_off), w.cap_items,
                          reinterpret_cast<PackedItem*>(ws + w.tile_off), w.cap_tiles, err, s) != cudaSuccess)
     return FA_ERR_CUDA;
-  return launch_packed_bwd(o.f16, tq, tk, tv, tdo, tdq, p, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const auto launch = score.cap ? launch_packed_bwd_cap : score.slopes || score.prefix ? launch_packed_bwd_bias : launch_packed_bwd;
+  return launch(o.f16, tq, tk, tv, tdo, tdq, p, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t flash_attn_packed_workspace_size(int B, int total, int Hq, int Hk, int d, int backward) {
+  if (check_packed_shape(B, total, Hq, Hk, d) != FA_OK) return 0;
+  return packed_workspace_layout(B, total, Hq, Hk, d, backward != 0).total;
+}
+
+fa_status flash_attn_packed_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                                const int32_t* cu_seqlens, int B, int total, int Hq, int Hk, int d,
+                                const int64_t* strides, float scale, int causal, const fa_options* options,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  return packed_fwd_call(Q, K, V, O, LSE, cu_seqlens, B, total, Hq, Hk, d, strides, scale, causal, nullptr, options,
+                         workspace, workspace_bytes, stream);
+}
+
+fa_status flash_attn_packed_scored_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                                       const int32_t* cu_seqlens, int B, int total, int Hq, int Hk, int d,
+                                       const int64_t* strides, float scale, int causal, const fa_scores* scores,
+                                       const fa_options* options, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+  return packed_fwd_call(Q, K, V, O, LSE, cu_seqlens, B, total, Hq, Hk, d, strides, scale, causal, scores, options,
+                         workspace, workspace_bytes, stream);
+}
+
+fa_status flash_attn_packed_bwd(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                                const float* LSE, void* dQ, void* dK, void* dV, const int32_t* cu_seqlens, int B,
+                                int total, int Hq, int Hk, int d, const int64_t* strides, float scale, int causal,
+                                const fa_options* options, void* workspace, size_t workspace_bytes, void* stream) {
+  return packed_bwd_call(Q, K, V, O, dO, LSE, dQ, dK, dV, cu_seqlens, B, total, Hq, Hk, d, strides, scale, causal,
+                         nullptr, options, workspace, workspace_bytes, stream);
+}
+
+fa_status flash_attn_packed_scored_bwd(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                                       const float* LSE, void* dQ, void* dK, void* dV, const int32_t* cu_seqlens,
+                                       int B, int total, int Hq, int Hk, int d, const int64_t* strides, float scale,
+                                       int causal, const fa_scores* scores, const fa_options* options,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  return packed_bwd_call(Q, K, V, O, dO, LSE, dQ, dK, dV, cu_seqlens, B, total, Hq, Hk, d, strides, scale, causal,
+                         scores, options, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -4,6 +4,7 @@
 
 #include "fa_common.cuh"
 #include "fa_ptx.cuh"
+#include "fa_scores.cuh"
 #include "fa_warp.cuh"
 
 namespace fa {
@@ -14,6 +15,13 @@ namespace fa {
 struct PackedItem {
   int start, len, c, slot0;
 };
+// With a prefix mask, an item that is handed on (in a list or a ring) has its
+// sequence's prefix length above the tile number in c.
+constexpr int kPrefixShift = 11;
+static_assert(kMaxN / kTile < (1 << kPrefixShift) && kMaxN <= (0x7FFFFFFF >> kPrefixShift), "prefix and tile number share c");
+__host__ __device__ __forceinline__ int with_prefix(int c, int prefix) { return c | (prefix << kPrefixShift); }
+__host__ __device__ __forceinline__ int tile_of(int c) { return c & ((1 << kPrefixShift) - 1); }
+__host__ __device__ __forceinline__ int prefix_of(int c) { return c >> kPrefixShift; }
 
 // Written by the plan kernel at the head of the workspace.
 struct PackedPlan {
@@ -111,6 +119,7 @@ struct PackedFwdParams {
   int split;                  // an item is one query tile, its keys shared out between the softmax groups
   int heads;                  // Hq, or with pair_heads Hq / 2
   int group;                  // of those, per group of the work order
+  ScoreParams score;
 };
 
 struct PackedBwdParams {
@@ -135,6 +144,7 @@ struct PackedBwdParams {
   int parts;                  // of an item
   float* part;                // parts > 1: fp32 [parts, 2 (dK, dV), Hk, cap_tiles * 128, d]
   int group;                  // (key/value head, part) pairs per group of the work order
+  ScoreParams score;
 };
 
 // Rows [start, start + len) of sequence b; an empty one (bad set) where its
@@ -144,6 +154,11 @@ __device__ __forceinline__ int seq_bounds(const int32_t* cu, int b, int total, i
   bad = s < 0 || e < s || e > total || e - s > kMaxN;
   start = s;
   return bad ? 0 : e - s;
+}
+
+// The prefix of sequence b (len tokens); 0 without a prefix mask.
+__device__ __forceinline__ int seq_prefix(const int32_t* prefix, int b, int len) {
+  return prefix == nullptr ? 0 : max(0, min(prefix[b], len));
 }
 
 __device__ __forceinline__ void report_bounds(unsigned int* err, int b) {
@@ -164,22 +179,27 @@ __device__ __forceinline__ void report_bounds(unsigned int* err, int b) {
 // together. kSlots = kManySlots holds them all, 1 up to 32
 // (kernels are built for either: the claim of an item stands before its loads, and
 // with four slots for every call 24 prompts took 107 us, not 105).
-template <int kSlots>
+// kPre: the sequences' prefixes too (that of the last one named is in `prefix`).
+template <int kSlots, bool kPre = false>
 struct DirectList {
   int start[kSlots], len[kSlots], n[kSlots], slot0[kSlots], items;
+  int pre[kPre ? kSlots : 1], prefix;
   int c, off;          // causal: items with more than c units before them, and how many
   int first[kSlots];   // not causal: list place of a sequence's first unit
   // the sequences alone (err may be null)
-  __device__ __forceinline__ void read(const int32_t* cu, int B, int total, int rows, int cap, unsigned int* err) {
+  __device__ __forceinline__ void read(const int32_t* cu, const int32_t* prefixes, int B, int total, int rows, int cap,
+                                       unsigned int* err) {
     const int lane = threadIdx.x & 31;
     bool bad[kSlots];
     int mine = 0;
+    prefix = 0;
 #pragma unroll
     for (int s = 0; s < kSlots; ++s) {
       const int b = 32 * s + lane;
       start[s] = len[s] = 0;
       bad[s] = false;
       if (b < B) len[s] = seq_bounds(cu, b, total, start[s], bad[s]);
+      if constexpr (kPre) pre[s] = b < B ? seq_prefix(prefixes, b, len[s]) : 0;
       n[s] = (len[s] + rows - 1) / rows;
       mine += n[s];
     }
@@ -214,10 +234,10 @@ struct DirectList {
     for (int s = 0; s < kSlots; ++s) x += __popc(__ballot_sync(0xFFFFFFFFu, n[s] > c));
     return x;
   }
-  __device__ __forceinline__ void init(const int32_t* cu, int B, int total, int rows, int cap, bool causal,
-                                       unsigned int* err) {
+  __device__ __forceinline__ void init(const int32_t* cu, const int32_t* prefixes, int B, int total, int rows, int cap,
+                                       bool causal, unsigned int* err) {
     const int lane = threadIdx.x & 31;
-    read(cu, B, total, rows, cap, err);
+    read(cu, prefixes, B, total, rows, cap, err);
     items = 0;
 #pragma unroll
     for (int s = 0; s < kSlots; ++s) {
@@ -277,7 +297,7 @@ struct DirectList {
     return it;
   }
   // the unit at place `slot` of the sequences' order; len 0 where there is none
-  __device__ __forceinline__ PackedItem unit(int slot) const {
+  __device__ __forceinline__ PackedItem unit(int slot) {
     uint32_t mine = 0u;
     int t = 0;
 #pragma unroll
@@ -292,8 +312,15 @@ struct DirectList {
     return it;
   }
   // the sequence in slot t of lane l (c: its `first`)
-  __device__ __forceinline__ PackedItem get(int t, int l) const {
+  __device__ __forceinline__ PackedItem get(int t, int l) {
     int st = start[0], le = len[0], sl = slot0[0], fi = first[0];
+    if constexpr (kPre) {
+      int pr = pre[0];
+#pragma unroll
+      for (int s = 1; s < kSlots; ++s)
+        if (t == s) pr = pre[s];
+      prefix = __shfl_sync(0xFFFFFFFFu, pr, l);
+    }
 #pragma unroll
     for (int s = 1; s < kSlots; ++s)
       if (t == s) {
@@ -358,16 +385,19 @@ __device__ __forceinline__ uint32_t tile_chunk(int r, int c) {
   return (uint32_t)((c >> 3) * 16384 + (r >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// rows: rows of a unit (a work item's share of a sequence).
-cudaError_t launch_packed_plan(const int32_t* cu, int B, int total, int rows, int causal, bool backward,
-                               PackedPlan* plan, int* sorted, PackedItem* items, int cap_items, PackedItem* tiles, int cap_tiles,
+// rows: rows of a unit (a work item's share of a sequence). prefix: [B] or null.
+cudaError_t launch_packed_plan(const int32_t* cu, const int32_t* prefix, int B, int total, int rows, int causal,
+                               bool backward, PackedPlan* plan, int* sorted, PackedItem* items, int cap_items, PackedItem* tiles, int cap_tiles,
                                unsigned int* err, cudaStream_t s);
 
-cudaError_t launch_packed_fwd(bool f16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                              const PackedFwdParams& p, cudaStream_t s);
-
-cudaError_t launch_packed_bwd(bool f16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                              const CUtensorMap& tdo, const CUtensorMap& tdq, const PackedBwdParams& p,
-                              cudaStream_t s);
+// One for each kind of score (kScorePlain, kScoreCap, kScoreBias), from a
+// translation unit of its own.
+using PackedFwdLaunch = cudaError_t(bool f16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                    const PackedFwdParams& p, cudaStream_t s);
+using PackedBwdLaunch = cudaError_t(bool f16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                    const CUtensorMap& tdo, const CUtensorMap& tdq, const PackedBwdParams& p,
+                                    cudaStream_t s);
+PackedFwdLaunch launch_packed_fwd, launch_packed_fwd_cap, launch_packed_fwd_bias;
+PackedBwdLaunch launch_packed_bwd, launch_packed_bwd_cap, launch_packed_bwd_bias;
 
 }  // namespace fa

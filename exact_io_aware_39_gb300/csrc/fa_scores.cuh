@@ -1,0 +1,111 @@
+// Scores that are capped by a tanh or lowered with distance
+// (flash_attn_scored.h): the host's reading of fa_scores and the arithmetic
+// that the kernels share. In log2 units, with k = scale / softcap, c2 = softcap
+// log2(e) and s the raw product Q . K,
+//   t2 = c2 tanh(k s),  u2 = t2 - slope log2(e) |i - j|.
+#pragma once
+
+#include "flash_attn_scored.h"
+#include "fa_ptx.cuh"
+
+#include <cmath>
+#include <cstddef>
+
+namespace fa {
+
+// What a packed kernel does to its scores: nothing; cap (and perhaps bias and
+// prefix); bias or prefix without a cap.
+constexpr int kScorePlain = 0, kScoreCap = 1, kScoreBias = 2;
+
+struct ScoreParams {
+  const float* slopes;       // [Hq] or null
+  const int32_t* prefix;     // [B] or null
+  float limit;               // |s| up to which the polynomial holds (kCapSmall / k), or -1: nowhere
+  float a0, a1, a2, a3;      // there t2 = s (a0 + s^2 (a1 + s^2 (a2 + s^2 a3)))
+  float k, e2, c2;           // k; 2 k log2(e): exp(2 k s) = 2^(e2 s); c2
+  int cap;
+};
+
+// tanh(y) = y (C0 + C1 y^2 + C2 y^4 + C3 y^6) for |y| <= 0.4, to 9.8e-8 of the
+// value: the polynomial of least relative error (Remez exchange, in 64 bits).
+constexpr float kCapSmall = 0.4f;
+constexpr float kTanh0 = 0.999999902f, kTanh1 = -0.333313625f, kTanh2 = 0.132709768f, kTanh3 = -0.0475536036f;
+
+// Reads a caller's fa_scores (may be null). Returns FA_OK or the refusal.
+inline fa_status read_scores(const fa_scores* scores, float scale, int causal, bool cached, ScoreParams* out) {
+  *out = ScoreParams{};
+  out->limit = -1.f;
+  if (scores == nullptr) return FA_OK;
+  fa_scores s{};
+  if (scores->size < offsetof(fa_scores, softcap) + sizeof(float)) return FA_ERR_INVALID_ARG;
+  s.softcap = scores->softcap;
+  if (scores->size >= offsetof(fa_scores, slopes) + sizeof(void*)) s.slopes = scores->slopes;
+  if (scores->size >= offsetof(fa_scores, prefix_lens) + sizeof(void*)) s.prefix_lens = scores->prefix_lens;
+  if (!std::isfinite(s.softcap) || s.softcap < 0.f) return FA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(s.slopes) | reinterpret_cast<uintptr_t>(s.prefix_lens)) & 3) return FA_ERR_INVALID_ARG;
+  if (s.prefix_lens != nullptr && cached) return FA_ERR_UNSUPPORTED;
+  if (s.prefix_lens != nullptr && !causal) return FA_ERR_INVALID_ARG;
+  out->slopes = s.slopes;
+  out->prefix = s.prefix_lens;
+  if (s.softcap == 0.f) return FA_OK;
+  if (s.softcap < 0x1p-10f || s.softcap > 0x1p10f) return FA_ERR_UNSUPPORTED;
+  const double k = (double)scale / s.softcap, c2 = s.softcap * 1.4426950408889634;
+  if (k > 0x1p60 || k < 0x1p-60) return FA_ERR_UNSUPPORTED;   // (its square stays an fp32 number)
+  out->cap = 1;
+  out->k = (float)k;
+  out->e2 = (float)(2. * 1.4426950408889634 * k);
+  out->c2 = (float)c2;
+  // (past these k, k^7 leaves the fp32 range)
+  if (k < 0x1p15 && k > 0x1p-15) {
+    out->limit = (float)(kCapSmall / k);
+    out->a0 = (float)(c2 * k * kTanh0);
+    out->a1 = (float)(c2 * k * k * k * kTanh1);
+    out->a2 = (float)(c2 * k * k * k * k * k * kTanh2);
+    out->a3 = (float)(c2 * k * k * k * k * k * k * k * kTanh3);
+  }
+  return FA_OK;
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tanh(k s) = 1 - 2 / (1 + exp(2 k s)), to about 2^-22 absolutely (one
+// exponential and a reciprocal of 2^-22 each); exp = inf and 0 give 1 and -1.
+__device__ __forceinline__ float tanh_exp(float s, const ScoreParams& p) {
+  return fmaf(-2.f, rcp_approx(1.f + ex2(s * p.e2)), 1.f);
+}
+// the same for a pair, whose denominators share a reciprocal: 1 / a = b / (a b).
+// The exponents are held to 60, where tanh is 1 in fp32, so that a b is finite
+// (a NaN stays one, and makes its neighbour one).
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float2 tanh_exp2(float2 s, const ScoreParams& p) {
+  const float2 a = make_float2(ex2(min_nan(s.x * p.e2, 60.f)), ex2(min_nan(s.y * p.e2, 60.f)));
+  const float2 b = __fadd2_rn(a, make_float2(1.f, 1.f));
+  const float r = -2.f * rcp_approx(b.x * b.y);
+  return make_float2(fmaf(r, b.y, 1.f), fmaf(r, b.x, 1.f));
+}
+// t2 of a pair of small scores (|s| <= limit)
+__device__ __forceinline__ float2 cap_small2(float2 s, const ScoreParams& p) {
+  const float2 z = __fmul2_rn(s, s);
+  float2 r = __ffma2_rn(z, make_float2(p.a3, p.a3), make_float2(p.a2, p.a2));
+  r = __ffma2_rn(z, r, make_float2(p.a1, p.a1));
+  r = __ffma2_rn(z, r, make_float2(p.a0, p.a0));
+  return __fmul2_rn(s, r);
+}
+// t2 of one score of any size: the polynomial where it holds
+__device__ __forceinline__ float cap_any(float s, const ScoreParams& p) {
+  const float z = s * s;
+  const float small = s * fmaf(z, fmaf(z, fmaf(z, p.a3, p.a2), p.a1), p.a0);
+  return fabsf(s) <= p.limit ? small : p.c2 * tanh_exp(s, p);
+}
+#endif
+
+}  // namespace fa
