@@ -34,7 +34,8 @@ EXPORTS = [
     "flash_attn_packed_workspace_size", "flash_attn_packed_fwd", "flash_attn_packed_bwd",
     "flash_attn_kv_cache_write", "flash_attn_cached_workspace_size", "flash_attn_cached_needs_workspace",
     "flash_attn_cached_fwd",
-    "flash_attn_packed_scored_fwd", "flash_attn_packed_scored_bwd",
+    "flash_attn_packed_scored_fwd", "flash_attn_packed_scored_bwd", "flash_attn_cached_scored_fwd",
+    "flash_attn_cached_weights", "flash_attn_kv_cache_evict",
     "standard_attn_workspace_size", "standard_attn_fwd", "standard_attn_bwd",
 ]
 
@@ -126,6 +127,12 @@ def load(path=LIB_PATH):
     lib.flash_attn_cached_needs_workspace.restype = i32
     lib.flash_attn_cached_fwd.argtypes = [vp, i64] + [vp] * 8 + [i32] * 8 + [f32, i32, opt_p, vp, sz, vp]
     lib.flash_attn_cached_fwd.restype = i32
+    lib.flash_attn_cached_scored_fwd.argtypes = [vp, i64] + [vp] * 8 + [i32] * 8 + [f32, i32, vp, opt_p, vp, sz, vp]
+    lib.flash_attn_cached_scored_fwd.restype = i32
+    lib.flash_attn_cached_weights.argtypes = [vp, i64] + [vp] * 7 + [i32] * 8 + [f32, i32, vp, opt_p, vp]
+    lib.flash_attn_cached_weights.restype = i32
+    lib.flash_attn_kv_cache_evict.argtypes = [vp] * 10 + [i32] * 10 + [opt_p, vp]
+    lib.flash_attn_kv_cache_evict.restype = i32
     lib.standard_attn_workspace_size.argtypes = [i32, i32, i32]
     lib.standard_attn_workspace_size.restype = sz
     lib.standard_attn_fwd.argtypes = [vp] * 5 + [i32, i32, i32, i32, f32, i32, vp, vp, opt_p, i32, vp, sz, vp]
@@ -253,6 +260,33 @@ def flash_attn_cached_fwd(Q, q_token_stride, k_cache, v_cache, k_scale, v_scale,
                                         LSE, B, Nq, Hq, Hk, d, num_pages, page_size, max_pages, scale, cache_type,
                                         None if options is None else ctypes.byref(options), workspace,
                                         workspace_bytes, stream)
+
+
+def flash_attn_cached_scored_fwd(Q, q_token_stride, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, O, LSE, B,
+                                 Nq, Hq, Hk, d, num_pages, page_size, max_pages, scale, cache_type, scores, options,
+                                 workspace, workspace_bytes, stream):
+    return load().flash_attn_cached_scored_fwd(Q, q_token_stride, k_cache, v_cache, k_scale, v_scale, block_table,
+                                               seq_lens, O, LSE, B, Nq, Hq, Hk, d, num_pages, page_size, max_pages,
+                                               scale, cache_type, None if scores is None else ctypes.byref(scores),
+                                               None if options is None else ctypes.byref(options), workspace,
+                                               workspace_bytes, stream)
+
+
+def flash_attn_cached_weights(Q, q_token_stride, k_cache, k_scale, block_table, seq_lens, LSE, past, weights, B, Nq, Hq,
+                              Hk, d, num_pages, page_size, max_pages, scale, cache_type, scores, options, stream):
+    return load().flash_attn_cached_weights(Q, q_token_stride, k_cache, k_scale, block_table, seq_lens, LSE, past,
+                                            weights, B, Nq, Hq, Hk, d, num_pages, page_size, max_pages, scale,
+                                            cache_type, None if scores is None else ctypes.byref(scores),
+                                            None if options is None else ctypes.byref(options), stream)
+
+
+def flash_attn_kv_cache_evict(k_cache, v_cache, k_scale, v_scale, weights, block_table, seq_lens, new_table, new_lens,
+                              kept, B, Hk, d, num_pages, page_size, max_pages, new_pages, budget, recent, cache_type,
+                              options, stream):
+    return load().flash_attn_kv_cache_evict(k_cache, v_cache, k_scale, v_scale, weights, block_table, seq_lens,
+                                            new_table, new_lens, kept, B, Hk, d, num_pages, page_size, max_pages,
+                                            new_pages, budget, recent, cache_type,
+                                            None if options is None else ctypes.byref(options), stream)
 
 
 def standard_attn_workspace_size(B, H, N):
@@ -454,17 +488,23 @@ _default_options = {}        # dtype -> (reference to) its fa_options
 torch = None                 # bound with the library, by the first call
 
 
+def _bind():
+    """Loads the library and binds torch and the options, once."""
+    global torch
+    import torch as module
+    lib = load()
+    for dt, code in ((module.bfloat16, FA_DTYPE_BF16), (module.float16, FA_DTYPE_F16)):
+        _default_options[dt] = ctypes.byref(fa_options(code))
+    torch = module     # last: another thread's call that finds it finds the options too
+    return lib
+
+
 def _begin(t, wait_limit_us=0, test_stall=0):
     """The library, and (a reference to) the fa_options for t's dtype and the
     checking fields."""
-    global torch
     lib = _lib
     if lib is None or torch is None:
-        import torch as module
-        lib = load()
-        for dt, code in ((module.bfloat16, FA_DTYPE_BF16), (module.float16, FA_DTYPE_F16)):
-            _default_options[dt] = ctypes.byref(fa_options(code))
-        torch = module     # last: another thread's call that finds it finds the options too
+        lib = _bind()
     opts = _default_options.get(t.dtype)
     if opts is None or not t.is_cuda:
         raise ValueError("q (or k) must be a bfloat16 or float16 CUDA tensor")
@@ -686,25 +726,10 @@ def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, st
     _check(rc, "flash_attn_kv_cache_write")
 
 
-def attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_scale=None, v_scale=None, out=None,
-                         lse=None, workspace=None, stream=None, wait_limit_us=0, test_stall=0):
-    """O, LSE of the newest Nq tokens of B sequences against their keys and
-    values in a paged cache. q: bf16 or fp16 [B, Nq, Hq, d] (a token's heads
-    contiguous, tokens may be strided); the cache, its scales and the slots'
-    meaning as in kv_cache_write; block_table int32 [B, max_pages]; seq_lens
-    int32 [B] counts each sequence's tokens, the newest Nq included. Token i of
-    the Nq sees seq_lens - (Nq - 1 - i) keys; query head h reads key/value head
-    h // (Hq // Hk). Returns O like q (contiguous) and LSE float32 [B, Hq, Nq]."""
-    lib, opts = _begin(q, wait_limit_us, test_stall)
-    dev = q.get_device()
-    ctx = _elsewhere(stream, dev)
-    if ctx is not None:
-        with ctx:
-            return attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale, out, lse,
-                                        workspace, None, wait_limit_us, test_stall)
-    dt = q.dtype
-    kind = _cache_args(k_cache, v_cache, k_scale, v_scale, dt, dev)
-    pages, Hk, page, d = k_cache.shape
+def _newest(q, block_table, seq_lens, cache_shape, dev):
+    """Checks the queries of the newest tokens and their sequences against a
+    cache of this shape; returns B, Nq, Hq, the table's width, the token stride."""
+    pages, Hk, page, d = cache_shape
     if q.dim() != 4 or q.shape[3] != d or block_table.dim() != 2:
         raise ValueError("q must be [B, Nq, Hq, d] with the cache's d, block_table [B, max_pages]")
     B, Nq, Hq, _ = q.shape
@@ -714,9 +739,34 @@ def attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_sc
     s0, s1, s2, s3 = q.stride()
     if s3 != 1 or (Hq > 1 and s2 != d) or (B > 1 and Nq > 1 and s0 != Nq * s1):
         raise ValueError("q: a token's heads must be contiguous and the tokens evenly spaced")
-    tok = s1 if Nq > 1 else (s0 if B > 1 else Hq * d)
     _plain(block_table, "block_table", (B, width), torch.int32, dev)
     _plain(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    return B, Nq, Hq, width, s1 if Nq > 1 else (s0 if B > 1 else Hq * d)
+
+
+def attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_scale=None, v_scale=None, out=None,
+                         lse=None, workspace=None, stream=None, wait_limit_us=0, test_stall=0, softcap=0.0,
+                         slopes=None):
+    """O, LSE of the newest Nq tokens of B sequences against their keys and
+    values in a paged cache. q: bf16 or fp16 [B, Nq, Hq, d] (a token's heads
+    contiguous, tokens may be strided); the cache, its scales and the slots'
+    meaning as in kv_cache_write; block_table int32 [B, max_pages]; seq_lens
+    int32 [B] counts each sequence's tokens, the newest Nq included. Token i of
+    the Nq sees seq_lens - (Nq - 1 - i) keys; query head h reads key/value head
+    h // (Hq // Hk). Returns O like q (contiguous) and LSE float32 [B, Hq, Nq].
+    softcap > 0 caps the scores: softcap * tanh(score / softcap). slopes, float32
+    [Hq], lowers those of head h by slopes[h] times the distance of query and key."""
+    lib, opts = _begin(q, wait_limit_us, test_stall)
+    dev = q.get_device()
+    ctx = _elsewhere(stream, dev)
+    if ctx is not None:
+        with ctx:
+            return attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_scale, v_scale, out, lse,
+                                        workspace, None, wait_limit_us, test_stall, softcap, slopes)
+    dt = q.dtype
+    kind = _cache_args(k_cache, v_cache, k_scale, v_scale, dt, dev)
+    pages, Hk, page, d = k_cache.shape
+    B, Nq, Hq, width, tok = _newest(q, block_table, seq_lens, k_cache.shape, dev)
     if out is None:
         out = torch.empty((B, Nq, Hq, d), dtype=dt, device=dev)
     else:
@@ -730,9 +780,105 @@ def attention_cached_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, k_sc
         workspace, nbytes = _scratch(workspace, lib.flash_attn_cached_workspace_size(B, Nq, Hq, Hk, d), dev)
         ws = workspace.data_ptr()
     e4m3 = kind == FA_CACHE_E4M3
+    if softcap or slopes is not None:
+        rc = lib.flash_attn_cached_scored_fwd(q.data_ptr(), tok, k_cache.data_ptr(), v_cache.data_ptr(),
+                                              k_scale.data_ptr() if e4m3 else None, v_scale.data_ptr() if e4m3 else None,
+                                              block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+                                              lse.data_ptr(), B, Nq, Hq, Hk, d, pages, page, width, scale, kind,
+                                              _scores(softcap, slopes, None, Hq, B, dev), opts, ws, nbytes,
+                                              torch._C._cuda_getCurrentRawStream(dev))
+        _check(rc, "flash_attn_cached_scored_fwd")
+        return out, lse
     rc = lib.flash_attn_cached_fwd(q.data_ptr(), tok, k_cache.data_ptr(), v_cache.data_ptr(),
                                    k_scale.data_ptr() if e4m3 else None, v_scale.data_ptr() if e4m3 else None,
                                    block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Nq, Hq,
                                    Hk, d, pages, page, width, scale, kind, opts, ws, nbytes, torch._C._cuda_getCurrentRawStream(dev))
     _check(rc, "flash_attn_cached_fwd")
     return out, lse
+
+
+def attention_cached_weights(q, k_cache, block_table, seq_lens, lse, scale, weights, k_scale=None, past=None,
+                             stream=None, wait_limit_us=0, test_stall=0, softcap=0.0, slopes=None):
+    """What each cached token received from the newest Nq tokens of its sequence,
+    per key/value head, added to what it had before: into weights, float32
+    [num_pages, Hk, page_size] like the scales of a cache, goes past (the same
+    shape, weights itself perhaps; None: nothing) plus the sum over the queries
+    and the heads of a group of exp(score - lse). The newest Nq tokens have no
+    past. q, the keys' cache, block_table, seq_lens, scale, softcap and slopes as
+    in attention_cached_fwd, lse float32 [B, Hq, Nq] from it. Places of no token
+    are left as they are. Returns weights."""
+    lib, opts = _begin(q, wait_limit_us, test_stall)
+    dev = q.get_device()
+    ctx = _elsewhere(stream, dev)
+    if ctx is not None:
+        with ctx:
+            return attention_cached_weights(q, k_cache, block_table, seq_lens, lse, scale, weights, k_scale, past, None,
+                                            wait_limit_us, test_stall, softcap, slopes)
+    kind = _cache_args(k_cache, k_cache, k_scale, k_scale, q.dtype, dev)
+    pages, Hk, page, d = k_cache.shape
+    B, Nq, Hq, width, tok = _newest(q, block_table, seq_lens, k_cache.shape, dev)
+    _plain(lse, "lse", (B, Hq, Nq), torch.float32, dev)
+    _plain(weights, "weights", (pages, Hk, page), torch.float32, dev)
+    if past is not None:
+        _plain(past, "past", (pages, Hk, page), torch.float32, dev)
+    rc = lib.flash_attn_cached_weights(q.data_ptr(), tok, k_cache.data_ptr(),
+                                       k_scale.data_ptr() if kind == FA_CACHE_E4M3 else None, block_table.data_ptr(),
+                                       seq_lens.data_ptr(), lse.data_ptr(), None if past is None else past.data_ptr(),
+                                       weights.data_ptr(), B, Nq, Hq, Hk, d, pages, page, width, scale, kind,
+                                       _scores(softcap, slopes, None, Hq, B, dev), opts,
+                                       torch._C._cuda_getCurrentRawStream(dev))
+    _check(rc, "flash_attn_cached_weights")
+    return weights
+
+
+def kv_cache_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, budget, recent, k_scale=None,
+                   v_scale=None, new_lens=None, kept=None, stream=None):
+    """Shortens B cached sequences to at most budget tokens for each key/value
+    head: their `recent` newest and the others with the largest weights (float32
+    [num_pages, Hk, page_size], see attention_cached_weights; of equal ones the
+    earlier). Those that stay keep their order and are copied, with their scales
+    and weights, to the pages of new_table (int32 [B, new_pages]), which must be in
+    no block_table; the old pages are only read. Returns the new lengths, int32
+    [B], and the kept tokens' former places, int32 [B, Hk, budget], -1 past them."""
+    lib = _lib
+    if lib is None or torch is None:
+        lib = _bind()
+    if not weights.is_cuda or (k_cache.dtype not in _default_options and k_cache.dtype is not torch.float8_e4m3fn):
+        raise ValueError("the cache must be bfloat16, float16 or float8_e4m3fn, and weights a CUDA tensor")
+    dev = weights.get_device()
+    ctx = _elsewhere(stream, dev)
+    if ctx is not None:
+        with ctx:
+            return kv_cache_evict(k_cache, v_cache, weights, block_table, seq_lens, new_table, budget, recent, k_scale,
+                                  v_scale, new_lens, kept)
+    kind = _cache_args(k_cache, v_cache, k_scale, v_scale, k_cache.dtype, dev)
+    pages, Hk, page, d = k_cache.shape
+    if block_table.dim() != 2 or new_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages], new_table [B, new_pages]")
+    B, width = block_table.shape
+    new_width = new_table.shape[1]
+    budget, recent = int(budget), int(recent)
+    if (B | width | new_width | pages | Hk | page | d | max(budget, 0) | max(recent, 0)) >> 31:
+        _past_32_bits()
+    if budget < 1 or not 0 <= recent <= budget:
+        raise ValueError("budget must be at least 1 and recent between 0 and it")
+    _plain(weights, "weights", (pages, Hk, page), torch.float32, dev)
+    _plain(block_table, "block_table", (B, width), torch.int32, dev)
+    _plain(new_table, "new_table", (B, new_width), torch.int32, dev)
+    _plain(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    if new_lens is None:
+        new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+    else:
+        _plain(new_lens, "new_lens", (B,), torch.int32, dev)
+    if kept is None:
+        kept = torch.empty((B, Hk, budget), dtype=torch.int32, device=dev)
+    else:
+        _plain(kept, "kept", (B, Hk, budget), torch.int32, dev)
+    e4m3 = kind == FA_CACHE_E4M3
+    rc = lib.flash_attn_kv_cache_evict(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if e4m3 else None,
+                                       v_scale.data_ptr() if e4m3 else None, weights.data_ptr(), block_table.data_ptr(),
+                                       seq_lens.data_ptr(), new_table.data_ptr(), new_lens.data_ptr(), kept.data_ptr(),
+                                       B, Hk, d, pages, page, width, new_width, budget, recent, kind, None,
+                                       torch._C._cuda_getCurrentRawStream(dev))
+    _check(rc, "flash_attn_kv_cache_evict")
+    return new_lens, kept

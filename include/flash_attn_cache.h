@@ -1,7 +1,8 @@
 /*
  * flash_attn_cache.h -- C ABI of serving from a paged key/value cache: the
  * writer that puts new keys and values into the cache (as 16-bit values or
- * quantised to e4m3), and the attention of the newest tokens against it.
+ * quantised to e4m3), the attention of the newest tokens against it, and its
+ * shortening to the tokens that received the most attention.
  *
  * The method is the one of flash_attn.h: tiles of keys are streamed past
  * resident queries with an online softmax. A query of one token has no second
@@ -112,6 +113,38 @@ fa_status flash_attn_cached_fwd(const void* Q, int64_t q_token_stride, const voi
                                 const int32_t* seq_lens, void* O, float* LSE, int B, int Nq, int Hq, int Hk,
                                 int d, int num_pages, int page_size, int max_pages, float scale, int cache_type,
                                 const fa_options* options, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Shortens cached sequences to the tokens that received the most attention, per
+ * key/value head. A sequence of n tokens keeps, for each head, min(n, budget):
+ * all of them when n <= budget, else its `recent` newest and, of the others, the
+ * budget - recent with the largest weights (of equal ones the earlier). They
+ * keep their order, and are copied to the places 0, 1, ... of the pages of
+ * new_table: rows of K and V, with FA_CACHE_E4M3 their scales, and their weights.
+ * The old pages are only read, and are the caller's to use again.
+ *   k_cache, v_cache, k_scale, v_scale : in and out, the cache
+ *   weights   : in and out, fp32 [num_pages, Hk, page_size] (see
+ *               flash_attn_cached_weights); one that is negative or NaN counts as 0
+ *   block_table : in, int32 [B, max_pages];  seq_lens : in, int32 [B], clamped to
+ *               [0, max_pages * page_size]
+ *   new_table : in, int32 [B, new_pages], new_pages * page_size >= budget. Its
+ *               pages must be distinct and in no sequence's block_table, else what
+ *               they hold afterwards is unspecified. Entries past the kept tokens
+ *               are not read. A row whose new page lies outside the cache is not
+ *               copied; one whose old page does is written as zeros.
+ *   new_lens  : out, int32 [B]: min(n, budget); may be seq_lens itself
+ *   kept      : out, int32 [B, Hk, budget]: the former places of the kept tokens,
+ *               ascending, then -1
+ *   1 <= budget, 0 <= recent <= budget; Hk >= 1; all but the caches 4-byte aligned.
+ * What lies behind in a shortened sequence is closer afterwards: distances
+ * (fa_scores' slopes) count cached tokens.
+ * Of the options none is used (test_stall is refused); no workspace.
+ */
+fa_status flash_attn_kv_cache_evict(void* k_cache, void* v_cache, float* k_scale, float* v_scale, float* weights,
+                                    const int32_t* block_table, const int32_t* seq_lens, const int32_t* new_table,
+                                    int32_t* new_lens, int32_t* kept, int B, int Hk, int d, int num_pages,
+                                    int page_size, int max_pages, int new_pages, int budget, int recent,
+                                    int cache_type, const fa_options* options, void* stream);
 
 #ifdef __cplusplus
 }

@@ -66,6 +66,43 @@ fa_status flash_attn_packed_scored_bwd(const void* Q, const void* K, const void*
                                        int causal, const fa_scores* scores, const fa_options* options,
                                        void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * flash_attn_cached_fwd with such scores (softcap and slopes; query i of the
+ * newest Nq is at place n - Nq + i of its sequence of n cached tokens, key j at
+ * place j): arguments, workspace (flash_attn_cached_workspace_size,
+ * flash_attn_cached_needs_workspace), options and errors as there.
+ */
+fa_status flash_attn_cached_scored_fwd(const void* Q, int64_t q_token_stride, const void* k_cache, const void* v_cache,
+                                       const float* k_scale, const float* v_scale, const int32_t* block_table,
+                                       const int32_t* seq_lens, void* O, float* LSE, int B, int Nq, int Hq, int Hk,
+                                       int d, int num_pages, int page_size, int max_pages, float scale,
+                                       int cache_type, const fa_scores* scores, const fa_options* options,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Adds up what each cached token received from the newest Nq tokens, per
+ * key/value head: for every sequence of n tokens and token j < n,
+ *   weights_j = past_j + sum over i and the G query heads of exp(u_ij - LSE_i)
+ * over the queries i that see key j. For the Nq newest tokens (j >= n - Nq), and
+ * with past = NULL for all, past_j counts as 0: a place's former token leaves
+ * nothing behind.
+ *   Q, LSE  : in, as given to and by flash_attn_cached_fwd (or _scored_fwd with
+ *             the same scores). Nq may be any number of newest tokens: the last
+ *             32 of a prompt, for instance. A query whose LSE is -inf gives nothing.
+ *   past    : in, fp32 [num_pages, Hk, page_size], or NULL
+ *   weights : out, the same; may be past itself. Places of no token are left as
+ *             they were, as are those of pages outside the cache.
+ *   Both 8-byte aligned. A page belongs to one sequence of the call: of two that
+ *   share it, either's sums remain.
+ *   No workspace. Results do not change from call to call. Of the options dtype,
+ *   wait_limit_us and test_stall are used, as in flash_attn_cached_fwd.
+ */
+fa_status flash_attn_cached_weights(const void* Q, int64_t q_token_stride, const void* k_cache, const float* k_scale,
+                                    const int32_t* block_table, const int32_t* seq_lens, const float* LSE,
+                                    const float* past, float* weights, int B, int Nq, int Hq, int Hk, int d,
+                                    int num_pages, int page_size, int max_pages, float scale, int cache_type,
+                                    const fa_scores* scores, const fa_options* options, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

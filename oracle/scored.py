@@ -103,3 +103,77 @@ def packed_attention(q, k, v, do, cu, scale, causal, u16, softcap=0.0, slopes=No
         for name in ("dK", "dV"):
             tol[name][r] += u16 * np.abs(val[name][r]) + a
     return val, tol
+
+
+def _tokens(cache, table_row, n, hk):
+    """Rows (or weights) of a sequence's n tokens for head hk; zeros where a page
+    lies outside the cache."""
+    page = cache.shape[2]
+    out = np.zeros((n,) + cache.shape[3:])
+    for j in range(n):
+        p = int(table_row[j // page])
+        if 0 <= p < cache.shape[0]:
+            out[j] = cache[p, hk, j % page]
+    return out
+
+
+def cached_attention(q, k_cache, v_cache, block_table, seq_lens, scale, softcap=0.0, slopes=None, lse=None):
+    """The newest tokens against caches of dequantised values. Returns values O
+    [B, Nq, Hq, d] and LSE [B, Hq, Nq], the bounds of the weights' relative errors
+    averaged over each row (like LSE) and sum_j P_j |V_j| and sum_j P_j e_j |V_j|
+    (like O), e_j the bound of a weight's relative error. With lse [B, Hq, Nq] also W,
+    a list of [Hk, n] arrays for the sequences: what each token received by that
+    LSE, and its bounds."""
+    q = np.asarray(q, dtype=np.float64)
+    B, Nq, Hq, d = q.shape
+    pages, Hk, page, _ = k_cache.shape
+    G = Hq // Hk
+    r = dict(O=np.zeros(q.shape), LSE=np.full((B, Hq, Nq), -np.inf), avg=np.zeros((B, Hq, Nq)), absv=np.zeros(q.shape),
+             errv=np.zeros(q.shape), W=[], tolW=[])
+    for b in range(B):
+        n = min(max(int(seq_lens[b]), 0), block_table.shape[1] * page)
+        at = np.arange(n)
+        rows = np.arange(n - Nq, n)
+        seen = at[None, :] <= rows[:, None]
+        W, tolW = np.zeros((Hk, n)), np.zeros((Hk, n))
+        for h in range(Hq if n else 0):
+            hk = h // G
+            ks, vs = _tokens(k_cache, block_table[b], n, hk), _tokens(v_cache, block_table[b], n, hk)
+            slope = 0.0 if slopes is None else float(slopes[h])
+            u, t, _ = scores(q[b, :, h], ks, scale, softcap, slope, rows, at)
+            P, L = softmax(u, seen)
+            r["LSE"][b, h], r["O"][b, :, h] = L, P @ vs
+            e = np.where(seen, score_error(q[b, :, h], ks, scale, softcap, slope, rows, at, u, t, L), 0.0)
+            r["avg"][b, h] = (P * e).sum(axis=1)
+            rel = np.expm1(e + r["avg"][b, h][:, None]) + 2.0 ** -19
+            r["absv"][b, :, h], r["errv"][b, :, h] = P @ np.abs(vs), (P * rel) @ np.abs(vs)
+            if lse is not None:
+                given = lse[b, h].astype(np.float64)
+                live = seen & np.isfinite(given)[:, None]
+                g = np.where(np.isfinite(given), given, 0.0)[:, None]
+                w = np.where(live, np.exp(np.where(live, u - g, 0.0)), 0.0)
+                ew = score_error(q[b, :, h], ks, scale, softcap, slope, rows, at, u, t, given)
+                W[hk] += w.sum(axis=0)
+                tolW[hk] += (w * np.where(live, np.expm1(ew) + 2.0 ** -20, 0.0)).sum(axis=0)
+        r["W"].append(W)
+        r["tolW"].append(tolW + (Nq * G + 2) * 2.0 ** -24 * W)
+    return r
+
+
+def evict(weights, block_table, seq_lens, budget, recent, page):
+    """Former places [B][Hk] of the tokens that stay, ascending. weights: [pages,
+    Hk, page]; those of pages outside the cache, negative ones and NaN count as 0."""
+    out = []
+    for b in range(len(seq_lens)):
+        n = min(max(int(seq_lens[b]), 0), block_table.shape[1] * page)
+        heads = []
+        for hk in range(weights.shape[1]):
+            tokens = list(range(n))
+            if n > budget:
+                w = _tokens(weights, block_table[b], n, hk)
+                w = np.where(w > 0, w, 0.0)
+                older = sorted(range(n - recent), key=lambda j: (-w[j], j))[:budget - recent]
+                tokens = sorted(older) + list(range(n - recent, n))
+            heads.append(tokens)
+        out.append(heads)
+    return out

@@ -65,3 +65,67 @@ def test_helpers_refuse_cpu_tensors(L):
     cu = torch.tensor([0, 4], dtype=torch.int32)
     with pytest.raises(ValueError):
         L.attention_packed_fwd(q, q, q, cu, 0.1, softcap=30.0)
+
+
+ODD = ctypes.c_void_p((1 << 20) + 4)
+
+
+def _cached(L, scores=None, Q=P, kc=P, vc=P, table=P, lens=P, LSE=P, **kw):
+    a = dict(tok=4096, B=2, Nq=1, Hq=32, Hk=8, d=128, pages=10, page=16, width=4, scale=0.1, kind=0, ks=None, opts=None)
+    a.update(kw)
+    vs = a["ks"]
+    yield L.flash_attn_cached_scored_fwd(Q, a["tok"], kc, vc, a["ks"], vs, table, lens, P, LSE, a["B"], a["Nq"], a["Hq"],
+                                         a["Hk"], a["d"], a["pages"], a["page"], a["width"], a["scale"], a["kind"],
+                                         scores, a["opts"], P, 1 << 40, None)
+    yield L.flash_attn_cached_weights(Q, a["tok"], kc, a["ks"], table, lens, LSE, None, vc, a["B"], a["Nq"], a["Hq"],
+                                      a["Hk"], a["d"], a["pages"], a["page"], a["width"], a["scale"], a["kind"], scores,
+                                      a["opts"], None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(Q=None), 1), (dict(kc=ctypes.c_void_p((1 << 20) + 8)), 1), (dict(vc=ODD), 1), (dict(vc=None), 1),
+    (dict(table=None), 1), (dict(lens=ctypes.c_void_p((1 << 20) + 2)), 1), (dict(LSE=None), 1), (dict(B=0), 1),
+    (dict(Nq=0), 1), (dict(Hq=31), 1), (dict(scale=0.0), 1), (dict(kind=2), 2), (dict(kind=1), 1), (dict(ks=P), 1),
+    (dict(kind=1, ks=P, d=72), 2), (dict(d=12), 2), (dict(page=24), 2), (dict(width=0), 1), (dict(tok=4095), 1),
+    (dict(tok=2048), 1), (dict(pages=1 << 30), 2), (dict(width=1 << 27), 2),
+])
+def test_cached_refusals(L, kw, want):
+    for st in _cached(L, **kw):
+        assert st == want
+
+
+def test_cached_scores_and_options(L):
+    for kw, want in ((dict(softcap=-1.0), 1), (dict(softcap=1e9), 2), (dict(slopes=(1 << 20) + 1), 1),
+                     (dict(prefix_lens=1 << 20), 2)):
+        for st in _cached(L, scores=L.fa_scores(**kw)):
+            assert st == want
+    for opts, want in ((L.fa_options(7), 2), (L.fa_options(p_drop=0.1), 2), (L.fa_options(tile_record=1 << 20), 2),
+                       (L.fa_options(test_stall=2), 1)):
+        for st in _cached(L, opts=opts):
+            assert st == want
+    assert L.flash_attn_cached_weights(P, 4096, P, None, P, P, P, ODD, P, 2, 1, 32, 8, 128, 10, 16, 4, 0.1, 0, None, None,
+                                       None) == 1       # past
+
+
+def _evict(L, kc=P, vc=P, ks=None, vs=None, w=P, table=P, lens=P, new=P, nl=P, kept=P, B=2, Hk=8, d=128, pages=10, page=16,
+           width=4, new_width=2, budget=32, recent=8, kind=0, opts=None):
+    return L.flash_attn_kv_cache_evict(kc, vc, ks, vs, w, table, lens, new, nl, kept, B, Hk, d, pages, page, width,
+                                       new_width, budget, recent, kind, opts, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(kc=None), 1), (dict(vc=ctypes.c_void_p((1 << 20) + 8)), 1), (dict(w=None), 1), (dict(table=None), 1),
+    (dict(lens=None), 1), (dict(new=None), 1), (dict(nl=None), 1), (dict(kept=None), 1),
+    (dict(kept=ctypes.c_void_p((1 << 20) + 2)), 1), (dict(B=0), 1), (dict(Hk=0), 1), (dict(pages=0), 1),
+    (dict(width=0), 1), (dict(new_width=0), 1), (dict(budget=0), 1), (dict(budget=33), 1), (dict(recent=-1), 1),
+    (dict(recent=33), 1), (dict(kind=2), 2), (dict(d=12), 2), (dict(d=136), 2), (dict(page=24), 2), (dict(ks=P, vs=P), 1),
+    (dict(kind=1), 1), (dict(kind=1, ks=P), 1), (dict(kind=1, ks=P, vs=P, d=72), 2), (dict(width=1 << 27), 2),
+    (dict(new_width=1 << 27, budget=1 << 20), 2), (dict(B=1 << 20, Hk=1 << 12), 2),
+])
+def test_evict_refusals(L, kw, want):
+    assert _evict(L, **kw) == want
+
+
+def test_evict_options(L):
+    for opts, want in ((L.fa_options(7), 2), (L.fa_options(p_drop=0.1), 2), (L.fa_options(test_stall=1), 2)):
+        assert _evict(L, opts=opts) == want
