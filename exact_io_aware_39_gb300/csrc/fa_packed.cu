@@ -112,7 +112,7 @@ packed_plan_kernel(const int32_t* __restrict__ cu, const int32_t* __restrict__ p
         const PackedItem it{s, backward && f + nn > cap_tiles ? 0 : ln, with_prefix(backward && causal ? nn - 1 - c : c, pr), f};
         const int at = causal ? off[c] + rk : f + c;
         if (at < cap_items) items[at] = it;
-        if (backward && f + c < cap_tiles) tiles[f + c] = PackedItem{s, ln, c, f};
+        if (backward && f + c < cap_tiles) tiles[f + c] = PackedItem{s, ln, with_prefix(c, pr), f};
       }
     }
     __syncthreads();

@@ -234,10 +234,14 @@ struct DirectList {
     for (int s = 0; s < kSlots; ++s) x += __popc(__ballot_sync(0xFFFFFFFFu, n[s] > c));
     return x;
   }
+  // (per: the units are so many of those of `rows` rows, which slot0 goes on counting)
   __device__ __forceinline__ void init(const int32_t* cu, const int32_t* prefixes, int B, int total, int rows, int cap,
-                                       bool causal, unsigned int* err) {
+                                       bool causal, unsigned int* err, int per = 1) {
     const int lane = threadIdx.x & 31;
     read(cu, prefixes, B, total, rows, cap, err);
+    if (per > 1)
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s) n[s] = (n[s] + per - 1) / per;
     items = 0;
 #pragma unroll
     for (int s = 0; s < kSlots; ++s) {

@@ -26,8 +26,14 @@
 //     theirs, while dK and dV are written.
 //
 // Launches (after the plan, for more than kDirect sequences): the pre-pass
-// (D = rowsum(dO * O), LSE * log2 e, zeroed accumulator), the main kernel, and
-// dQ = 16-bit(scale * accumulator).
+// (D = rowsum(dO * O), LSE * log2 e, zeroed accumulator; for scores of their own
+// D = rowsum(P * dP), fa_packed_dots.cuh), the main kernel, and dQ = 16-bit(scale
+// * accumulator).
+//
+// Scores of their own (SCORE): P = exp(u - LSE) of the capped and lowered scores
+// u, and dS = P (dP - D) (1 - tanh^2), whose factor joins P in registers once P has
+// been packed for dV. With a prefix, a key tile that begins in it has all query
+// tiles of its sequence.
 //
 // Roundings: P and dS go to the inputs' 16-bit type for the products that read
 // them (half a step each; dS is what the error of dQ and dK is made of: 2.5e-3 of
@@ -44,6 +50,7 @@
 #pragma once
 
 #include "fa_packed.cuh"
+#include "fa_packed_dots.cuh"
 
 #include <type_traits>
 
@@ -885,7 +892,11 @@ __device__ __forceinline__ PackedItem padded_tile(const PackedBwdParams& p, int 
     if constexpr (PRE) *prefix = dl.prefix;
     return it;
   }
-  return tile < p.plan->tiles ? p.tiles[tile] : PackedItem{0, 0, 0, 0};
+  if (tile >= p.plan->tiles) return PackedItem{0, 0, 0, 0};
+  PackedItem it = p.tiles[tile];
+  it.c = tile_of(it.c);   // (its prefix lies above)
+  // (a sequence past the padded rows, of bounds that overlap, is left out)
+  return it.slot0 + (it.len + kTile - 1) / kTile > p.cap_tiles ? PackedItem{0, 0, 0, 0} : it;
 }
 
 // Per padded tile and query head: D = rowsum(dO * O) and LSE * log2(e) of its
@@ -1019,7 +1030,8 @@ cudaError_t launch_packed_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
   // 16 lanes cover d <= 128, 8 cover d <= 64
   // (up to kDirect sequences the passes' blocks read the bounds themselves)
   const bool direct = p.B <= kDirect;
-  e = launch_pdl(false, direct ? packed_bwd_pre_kernel<D / 8, F16, SLOTS> : packed_bwd_pre_kernel<D / 8, F16, 0>, tiles,
+  if constexpr (SCORE != kScorePlain) e = launch_packed_dots<D, F16, SCORE>(tq, tk, tv, tdo, q, sms, s);
+  else e = launch_pdl(false, direct ? packed_bwd_pre_kernel<D / 8, F16, SLOTS> : packed_bwd_pre_kernel<D / 8, F16, 0>, tiles,
                  dim3(256), 0, s, q);
   if (e != cudaSuccess) return e;
   // a CTA per item where items are taken by cancelling CTAs, else one per SM

@@ -44,6 +44,7 @@
 #pragma once
 
 #include "fa_packed.cuh"
+#include "fa_packed_rows.cuh"
 
 #include <type_traits>
 
@@ -51,9 +52,6 @@ namespace fa {
 
 namespace {
 
-constexpr int kFwdThreads = 384;
-constexpr int kSoftmaxRegs = 216;   // 2 x 128 x 216 + 128 x 72 = 384 x 168 registers
-constexpr int kOtherRegs = 72;
 constexpr float kRescaleThreshold = 8.0f; // log2 units
 constexpr float kSpecSumLimit = 256.0f;    // 2^kRescaleThreshold
 
@@ -106,114 +104,6 @@ struct PackedFwdLayout {
   static constexpr int kSmemBytes = kStats + (SPLIT ? 8 * kTile : 0);
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
-
-// An item as the roles see it: its two query tiles, and the key tiles 0 .. n - 1
-// live for either. SPLIT: one query tile, whose even key tiles are the first
-// softmax group's and whose odd ones the second's.
-// With scores of their own (PRE), every query sees the first `pre` keys.
-template <bool SPLIT, bool PRE>
-struct Pair {
-  int start, len, c, head;      // c < 0: no item
-  int nT, n;
-  int pre, pre_last;            // PRE: the prefix, and its last key tile (-1: none)
-  bool pair_heads, causal;
-  // c: as the ring has it
-  __device__ __forceinline__ void finish(const PackedFwdParams& p) {
-    pair_heads = p.pair_heads != 0;
-    causal = p.causal != 0;
-    nT = (len + kTile - 1) / kTile;
-    pre = 0;
-    pre_last = -1;
-    if constexpr (PRE)
-      if (c >= 0) {
-        pre = prefix_of(c);
-        pre_last = (pre + kTile - 1) / kTile - 1;
-        c = tile_of(c);
-      }
-    if constexpr (SPLIT) n = causal ? max(c, pre_last) + 1 : nT;
-    else n = causal ? last(has(1) ? 1 : 0) + 1 : nT;
-  }
-  __device__ __forceinline__ bool has(int t) const {
-    if constexpr (SPLIT) return t < n;
-    return t == 0 || pair_heads || 2 * c + 1 < nT;
-  }
-  __device__ __forceinline__ int qi(int t) const { return SPLIT || pair_heads ? c : 2 * c + t; }
-  __device__ __forceinline__ int hq(int t) const { return SPLIT ? head : pair_heads ? 2 * head + t : head; }
-  // first and last key tile of t, which has every one (SPLIT: every second) between them
-  __device__ __forceinline__ int first(int t) const { return SPLIT ? t : 0; }
-  __device__ __forceinline__ int last(int t) const {
-    if constexpr (SPLIT) return n - 1 - ((n - 1 - t) & 1);
-    if constexpr (PRE) return causal ? max(qi(t), pre_last) : nT - 1;
-    return causal ? qi(t) : nT - 1;
-  }
-  __device__ __forceinline__ bool partial(int e, int q) const {
-    if constexpr (PRE) return (causal && e >= q && (e + 1) * kTile > pre) || (e + 1) * kTile > len;
-    return (causal && e == q) || (e + 1) * kTile > len;
-  }
-  // valid rows of the last key tile when it is not full, else 0
-  __device__ __forceinline__ int tail() const { return len & (kTile - 1); }
-};
-
-// Brings a row of scores (raw products of query `row` with the keys from `key0`
-// on) to log2 units, capped and lowered with the distance; key0 - row = far.
-// side: -1 where all of these keys lie before the query's tile, 1 behind it, 0 in
-// it. masked: columns from `lim` on are no keys of the row (what lies there may
-// be NaN, which must not meet its neighbour).
-template <int SCORE>
-__device__ __forceinline__ void score_row(float (&x)[128], const ScoreParams& sp, float sl2, float slope2, float far,
-                                          int side, bool masked, int lim) {
-  if constexpr (SCORE == kScoreCap) {
-    if (masked)
-#pragma unroll
-      for (int i = 0; i < 128; ++i)
-        if (i >= lim) x[i] = 0.f;
-    float top[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) top[k] = fmaxf(fabsf(x[k]), fabsf(x[4 + k]));
-#pragma unroll
-    for (int i = 8; i < 128; i += 8)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) top[k] = fmax3(top[k], fabsf(x[i + k]), fabsf(x[i + 4 + k]));
-    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-    if (__all_sync(0xFFFFFFFFu, most <= sp.limit)) {
-#pragma unroll
-      for (int i = 0; i < 128; i += 2) {
-        const float2 t = cap_small2(make_float2(x[i], x[i + 1]), sp);
-        x[i] = t.x;
-        x[i + 1] = t.y;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 128; i += 2) {
-        const float2 t = tanh_exp2(make_float2(x[i], x[i + 1]), sp);
-        x[i] = t.x * sp.c2;
-        x[i + 1] = t.y * sp.c2;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 128; i += 2) {
-      const float2 t = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(sl2, sl2));
-      x[i] = t.x;
-      x[i + 1] = t.y;
-    }
-  }
-  if (sp.slopes != nullptr) {
-    if (side == 0) {
-#pragma unroll
-      for (int i = 0; i < 128; ++i) x[i] = fmaf(-slope2, fabsf(far + (float)i), x[i]);
-    } else {
-      const float sl = side < 0 ? slope2 : -slope2;
-#pragma unroll
-      for (int i = 0; i < 128; i += 2) {
-        const float2 d = __fadd2_rn(make_float2(far, far), make_float2((float)i, (float)(i + 1)));
-        const float2 t = __ffma2_rn(make_float2(sl, sl), d, make_float2(x[i], x[i + 1]));
-        x[i] = t.x;
-        x[i + 1] = t.y;
-      }
-    }
-  }
-}
 
 template <int D, bool F16, int SLOTS, bool SPLIT, int SCORE>
 __global__ void __launch_bounds__(kFwdThreads, 1)
@@ -286,14 +176,14 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     w.len = __shfl_sync(0xFFFFFFFFu, ring[4 * rs + 1], 0);
     w.c = __shfl_sync(0xFFFFFFFFu, ring[4 * rs + 2], 0);
     w.head = __shfl_sync(0xFFFFFFFFu, ring[4 * rs + 3], 0);
-    w.finish(p);
+    w.finish(p.pair_heads != 0, p.causal != 0);
     mbar_arrive_warp(bar(L::bItemEmpty + rs));
     return true;
   };
 
   if (warp == 8) {
     // ------------------------------------------------------------ items, Q and K producer
-    regs_dec<kOtherRegs>();
+    regs_dec<kRowOtherRegs>();
     if (lane == 0) {
       tma_prefetch_map(&tq);
       tma_prefetch_map(&tk);
@@ -355,7 +245,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         if (PRE && direct) w.c = with_prefix(pi.c, dl.prefix);
         ring_c = w.c;
         w.head = head;
-        w.finish(p);
+        w.finish(p.pair_heads != 0, p.causal != 0);
       }
       if (lane == 0) {
         ring[4 * rs] = w.start;
@@ -421,7 +311,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   } else if (warp == 10) {
     // ------------------------------------------------------------ V producer
     // (its own warp, so that the K ring can run ahead of the V ring)
-    regs_dec<kOtherRegs>();
+    regs_dec<kRowOtherRegs>();
     if (lane == 0) tma_prefetch_map(&tv);
     int nv = 0;
     Pair<SPLIT, PRE> w;
@@ -457,7 +347,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     // before both PV, so S_t(e+1) is computed while group t still works on
     // S_t(e). The last PVs of an item stay pending into the next one, unless
     // its first loads are not there yet.
-    regs_dec<kOtherRegs>();
+    regs_dec<kRowOtherRegs>();
     constexpr uint32_t idS = idesc_16<F16>(128, 128, false, false);
     constexpr uint32_t idO = idesc_16<F16>(128, D, false, true);
     const uint32_t tS[2] = {tmem + 0u, tmem + 128u};
@@ -847,7 +737,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       if (join) mbar_arrive_warp(bar(L::bJoined));
     }
   } else {
-    regs_dec<kOtherRegs>();   // warp 11: no role
+    regs_dec<kRowOtherRegs>();   // warp 11: no role
   }
   tc_fence_before();
   __syncthreads();

@@ -86,8 +86,8 @@ def packed_attention(q, k, v, do, cu, scale, causal, u16, softcap=0.0, slopes=No
             avg = (P * eU).sum(axis=1, keepdims=True)
             eP = np.expm1(eU + avg) + 2 * f32
             tO = P * (u16 + eP) @ np.abs(V) + a * n * np.abs(V).max() + u16 * np.abs(O) + a
-            tD = (np.abs(dO) * tO).sum(axis=1, keepdims=True)
             dPm = 2.0 ** -24 * d * (np.abs(dO) @ np.abs(V).T)
+            tD = (P * (eP * np.abs(dP) + dPm)).sum(axis=1, keepdims=True)   # D = rowsum(P dP) in fp32
             raw = (d + 4) * 2.0 ** -24 * scale * (np.abs(Q) @ np.abs(K).T)
             eF = 0.77 * raw / softcap + 2.0 ** -18 if softcap else 0.0
             tS = np.where(seen, (u16 + eP) * np.abs(dS) + P * f * (tD + dPm) + P * np.abs(dP - D) * eF + a

@@ -8,6 +8,7 @@ import torch
 
 from oracle import scored as S
 from test_gpu_packed import BF, CANARY, FH, _bits, _f64, _inputs, _outputs, _settled, fa  # noqa: F401 (fa: the fixture)
+from test_gpu_packed import _check as packed_check
 
 pytestmark = pytest.mark.gpu
 
@@ -149,14 +150,15 @@ def test_prefixes_around_tiles(fa, pre):  # noqa: F811
 
 
 def test_plain_scores_by_way_of_the_scored_calls(fa):  # noqa: F811
-    """No cap, slopes of zero: the plain calls' results within the same bounds;
-    a scored call without any of them is the plain call, bit for bit."""
+    """No cap, slopes of zero: the plain calls' results within their bounds, and
+    within the narrower ones of D = rowsum(P dP); a scored call without any of them is the plain call, bit for bit."""
     c = _inputs([333, 90], 4, 2, 128, BF, 11)
     plain = _run(fa, c, 0.1, True, {})
     kw = dict(slopes=torch.zeros(4, device="cuda"))
     r = _run(fa, c, 0.1, True, kw)
     _settled(fa)
-    _check(c, plain, 0.1, True, {})
+    for res in (plain, r):
+        packed_check(c, res, 0.1, True)
     _check(c, r, 0.1, True, kw)
     o, lse = torch.full_like(plain["o"], CANARY), torch.full_like(plain["lse"], CANARY)
     p = lambda t: t.data_ptr()
