@@ -10,10 +10,10 @@
 // are off by what rounding dS and the results makes.
 //
 // The roles are those of the forward (fa_packed_fwd.cuh): a work item is two
-// query tiles that share the loads of K and V, one warpgroup for each (thread =
-// row), which reads S_t = Q_t K^T and dP_t = dO_t V^T from TMEM (four regions of
-// 128 columns, all there are) and frees each as soon as it is in registers, so that
-// the tensor core works on one group's products while the other group sums.
+// query tiles that share the loads of K and V, two warpgroups for each (thread =
+// row and half of its columns), which read S_t = Q_t K^T and dP_t = dO_t V^T from
+// TMEM (four regions of 128 columns, all there are) and free each as soon as it is
+// in registers, so that the tensor core works on the next one meanwhile.
 // Bound: 4 d operations per visible pair on the tensor cores, and the scores'
 // arithmetic.
 #pragma once
@@ -39,10 +39,10 @@ struct PackedDotsLayout {
   static constexpr int bEmpty = bFull + kStages;                // [kStages]
   static constexpr int bSFull = bEmpty + kStages;               // [2]
   static constexpr int bPFull = bSFull + 2;                     // [2]
-  static constexpr int bSFree = bPFull + 2;                     // [2], 4 arrivals: S_t is in registers
-  static constexpr int bPFree = bSFree + 2;                     // [2], 4: dP_t
+  static constexpr int bSFree = bPFull + 2;                     // [2], 8 arrivals: S_t is in registers
+  static constexpr int bPFree = bSFree + 2;                     // [2], 8: dP_t
   static constexpr int bItemFull = bPFree + 2;                  // [kItemRing]
-  static constexpr int bItemEmpty = bItemFull + kItemRing;      // [kItemRing], 9: MMA and softmax warps
+  static constexpr int bItemEmpty = bItemFull + kItemRing;      // [kItemRing], 17: MMA and row warps
   static constexpr int bClc = bItemEmpty + kItemRing;
   static constexpr int bDrain = bClc + 1;
   static constexpr int kNumBars = bDrain + 1;
@@ -50,12 +50,13 @@ struct PackedDotsLayout {
   static constexpr int kRing = kMisc + 16;                      // [kItemRing] x {first row, length, unit or -1, head, first padded tile, -}
   static constexpr int kRingInts = 5;
   static constexpr int kClc = (kRing + 4 * kRingInts * kItemRing + 15) & ~15;
-  static constexpr int kSmemBytes = kClc + 16;
+  static constexpr int kEx = kClc + 16;                         // [2] x [2] x [128] sums of a query tile's halves
+  static constexpr int kSmemBytes = kEx + 4 * kTile * 4;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
 template <int D, bool F16, int SCORE>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+__global__ void __launch_bounds__(kHalfThreads, 1)
 fa_packed_dots_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                       const PackedBwdParams p, const int pair_heads, const int heads, const int group) {
@@ -82,13 +83,13 @@ fa_packed_dots_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
   }
   if (tid == 0) {
     for (int i = 0; i < L::kNumBars; ++i)
-      mbar_init(bar(i), i >= L::bSFree && i < L::bPFree + 2 ? 4u
-                        : i >= L::bItemEmpty && i < L::bItemEmpty + L::kItemRing ? 9u : 1u);
+      mbar_init(bar(i), i >= L::bSFree && i < L::bPFree + 2 ? 8u
+                        : i >= L::bItemEmpty && i < L::bItemEmpty + L::kItemRing ? 17u : 1u);
     abort_flag[0] = 0u;
     abort_flag[2] = p.wait_us;   // the wait limit, read by the slow path of every wait
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(smem_u32(misc), 512);
     tmem_relinquish();
   }
@@ -115,9 +116,9 @@ fa_packed_dots_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
     return true;
   };
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ------------------------------------------------------------ items and loads
-    regs_dec<kRowOtherRegs>();
+    regs_dec<kHalfOtherRegs>();
     if (lane == 0) {
       tma_prefetch_map(&tq);
       tma_prefetch_map(&tk);
@@ -249,12 +250,12 @@ fa_packed_dots_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
       for (int s = 0; s < L::kStages && s < nl; ++s)
         drain_wait(bar(L::bFull + s), (uint32_t)((nl - 1 - s) / L::kStages) & 1u);
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ------------------------------------------------------------ MMA issuer
     // (the whole warp runs the schedule, one elected lane issues): per entry e,
     // S_t = Q_t K_e^T for both query tiles, then dP_t = dO_t V_e^T, each once its
     // group has read the region's last contents
-    regs_dec<kRowOtherRegs>();
+    regs_dec<kHalfOtherRegs>();
     constexpr uint32_t id = idesc_16<F16>(128, 128, false, false);
     const uint32_t dQ0 = desc_lo(desc_kmajor(sbase + L::kQ, 0));
     const uint32_t dKV0 = desc_lo(desc_kmajor(sbase + L::kKV, 0));
@@ -297,102 +298,96 @@ fa_packed_dots_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
     // every MMA issued has completed before TMEM is freed
     mma_commit_w(bar(L::bDrain));
     drain_wait(bar(L::bDrain), 0);
-  } else if (warp < 8) {
-    // ------------------------------------------------------------ rows
-    regs_inc<kSoftmaxRegs>();
-    const int t = warp >> 2, r = tid & 127;
+  } else if (warp < 16) {
+    // ------------------------------------------------------------ rows (thread = row and half of its columns)
+    // The two groups of a query tile meet at the start and the end of an item, and
+    // agree there whether all their waits held.
+    regs_inc<kHalfRegs>();
+    const int t = warp >> 3, h = (warp >> 2) & 1, r = tid & 127;
+    const uint32_t pair_bar = 1u + (uint32_t)t;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + 128u * (uint32_t)t + lane_off, tP = tS + 256u;
-    float slope2 = 0.f;
+    const uint32_t tS = tmem + 128u * (uint32_t)t + 64u * (uint32_t)h + lane_off, tP = tS + 256u;
+    volatile float* ex = reinterpret_cast<volatile float*>(smem + L::kEx) + 2 * kTile * t + r;
     uint32_t n = 0u;               // entries of this group so far
     int slot0 = 0;
-    bool ok = true;
     Item w;
-    for (int k = 0; ok && take_item(k, w, slot0) && w.c >= 0; ++k) {
+    for (int k = 0;; ++k) {
+      bool ok = take_item(k, w, slot0);
+      ok = group_all(pair_bar, 256u, ok);
+      if (!ok || w.c < 0) break;
       if (!w.has(t)) continue;
       const int qi = w.qi(t), last = w.last(t), hq = w.hq(t);
       const int row = kTile * qi + r;        // query index within the sequence
       const bool live = row < w.len;
       const size_t at = ((size_t)hq * p.cap_tiles + slot0 + qi) * kTile;   // the tile's first padded row
       const float lse2 = live ? p.lse[(size_t)hq * p.total + w.start + row] * 1.4426950408889634f : INFINITY;
-      if (p.score.slopes != nullptr) slope2 = p.score.slopes[hq] * 1.4426950408889634f;
+      const float slope2 = p.score.slopes != nullptr ? p.score.slopes[hq] * 1.4426950408889634f : 0.f;
       {
-        // the warp's rows of the dQ accumulator (rows past the sequence are added
-        // to as well, and never read)
+        // the warp's rows of the dQ accumulator, every second piece (rows past the
+        // sequence are added to as well, and never read)
         const int rows = min(32, w.len - (row - lane));
         float4* z = reinterpret_cast<float4*>(p.dq_acc + (at + r - lane) * p.d);
-        for (int i = lane; i < rows * p.d / 4; i += 32) z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = lane + 32 * h; i < rows * p.d / 4; i += 64) z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
       float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       for (int e = 0; e <= last; ++e, ++n) {
         if (!(ok = bar_wait_warp(bar(L::bSFull + t), n & 1u, ctl, 394))) break;
         tc_fence_after();
-        float x[128];
-        {
-          uint32_t u0[32], u1[32], u2[32], u3[32];
-          tmem_ld32(tS + 0u, u0);
-          tmem_ld32(tS + 32u, u1);
-          tmem_ld32(tS + 64u, u2);
-          tmem_ld32(tS + 96u, u3);
-          tmem_ld_wait(u0);
-          tmem_ld_wait(u1);
-          tmem_ld_wait(u2);
-          tmem_ld_wait(u3);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            x[i] = __uint_as_float(u0[i]);
-            x[32 + i] = __uint_as_float(u1[i]);
-            x[64 + i] = __uint_as_float(u2[i]);
-            x[96 + i] = __uint_as_float(u3[i]);
-          }
-        }
+        uint32_t u[2][32];
+        tmem_ld32(tS, u[0]);
+        tmem_ld32(tS + 32u, u[1]);
+        tmem_ld_wait(u[0]);
+        tmem_ld_wait(u[1]);
         tc_fence_before();
         mbar_arrive_warp(bar(L::bSFree + t));
         // (as in the forward: keys from column `lim` on are masked)
         const bool partial = w.partial(e, qi);
-        const int lim = (w.causal ? min(max(row + 1, w.pre), w.len) : w.len) - kTile * e;
-        score_row<SCORE>(x, p.score, p.scale_log2, slope2, (float)(kTile * e - row), e < qi ? -1 : e > qi ? 1 : 0, partial,
-                         lim);
+        const int lim = (w.causal ? min(max(row + 1, w.pre), w.len) : w.len) - kTile * e - 64 * h;
+        const ScoreTile st = score_tile<SCORE>(p.score, slope2, kTile * e + 64 * h, row, e < qi ? -1 : e > qi ? 1 : 0,
+                                               e == qi && (!w.causal || w.pre > kTile * e), partial, lim);
+        score_args<SCORE, false>(u, p.score, p.scale_log2, st, -lse2);
         if (!(ok = bar_wait_warp(bar(L::bPFull + t), n & 1u, ctl, 395))) break;
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t u[32];
-          tmem_ld32(tP + 32u * c, u);
-          tmem_ld_wait(u);
-          if (c == 3) {
-            tc_fence_before();
-            mbar_arrive_warp(bar(L::bPFree + t));
-          }
-          if (partial) {   // (what lies past the sequence may be NaN: neither its score nor its dP counts)
+        for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= lim) {
-                x[32 * c + i] = -INFINITY;
-                u[i] = 0u;
-              }
-          }
+          for (int c = 0; c < 2; ++c) {
+            uint32_t v[16];
+            tmem_ld16(tP + 32u * hh + 16u * c, v);
+            if (hh + c == 2) {
+              tc_fence_before();
+              mbar_arrive_warp(bar(L::bPFree + t));
+            }
+            if (partial) {   // (what lies past the sequence may be NaN)
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 a = __fadd2_rn(make_float2(x[32 * c + i], x[32 * c + i + 1]), make_float2(-lse2, -lse2));
-            sum[(i >> 1) & 3] = __ffma2_rn(make_float2(ex2(a.x), ex2(a.y)),
-                                           make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), sum[(i >> 1) & 3]);
+              for (int i = 0; i < 16; ++i)
+                if (32 * hh + 16 * c + i >= lim) v[i] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float2 a = pair_of(u[hh], 16 * c + i);
+              sum[(i >> 1) & 3] = __ffma2_rn(make_float2(ex2(a.x), ex2(a.y)),
+                                             make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sum[(i >> 1) & 3]);
+            }
           }
         }
       }
+      const float2 s = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+      ex[kTile * h] = s.x + s.y;
+      ok = group_all(pair_bar, 256u, ok);
       if (!ok) break;
-      const float2 s01 = __fadd2_rn(sum[0], sum[1]), s23 = __fadd2_rn(sum[2], sum[3]);
-      const float2 s = __fadd2_rn(s01, s23);
-      p.delta[at + r] = live ? s.x + s.y : 0.f;
-      p.lse2[at + r] = lse2;
+      if (h == 0) {
+        p.delta[at + r] = live ? ex[0] + ex[kTile] : 0.f;
+        p.lse2[at + r] = lse2;
+      }
     }
   } else {
-    regs_dec<kRowOtherRegs>();   // warps 10 and 11: no role
+    regs_dec<kHalfOtherRegs>();   // warps 18 and 19: no role
   }
   tc_fence_before();
   __syncthreads();
   if (tid == 0) report_aborted(ctl);
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -419,7 +414,7 @@ cudaError_t launch_packed_dots(const CUtensorMap& tq, const CUtensorMap& tk, con
   const long long most = units * heads;
   return launch_pdl(false, fa_packed_dots_kernel<D, F16, SCORE>,
                     dim3((unsigned)(p.B <= kDirect ? most : (long long)p.cap_tiles * heads < sms ? (long long)p.cap_tiles * heads : sms)),
-                    dim3(kFwdThreads), L::kSmemBytes, s, tq, tk, tv, tdo, p, (int)pair_heads, heads, group);
+                    dim3(kHalfThreads), L::kSmemBytes, s, tq, tk, tv, tdo, p, (int)pair_heads, heads, group);
 }
 
 }  // namespace

@@ -55,8 +55,13 @@ namespace {
 constexpr float kRescaleThreshold = 8.0f; // log2 units
 constexpr float kSpecSumLimit = 256.0f;    // 2^kRescaleThreshold
 
-template <int D, bool SPLIT>
+template <int D, bool SPLIT, bool PRE>
 struct PackedFwdLayout {
+  // Softmax warpgroups of a query tile: one, or for scores of their own two with
+  // half of a row's columns each
+  static constexpr int kParts = PRE ? 2 : 1;
+  static constexpr int kOther = 8 * kParts;                     // the first of the four warps behind them
+  static constexpr int kThreads = 32 * (kOther + 4);
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kHalves = D / 64;
   // separate K and V rings; the K ring is the deeper one, since the S MMAs
@@ -69,7 +74,12 @@ struct PackedFwdLayout {
   // S_t is then free as soon as its softmax group has read it into registers,
   // and the next S_t is computed while that group works on this one. At d = 128
   // the four regions fill TMEM and P is packed over S in place.
-  static constexpr bool kOwnP = (D == 64);
+  // For scores of their own, whose softmax takes longer than the products, P has its
+  // columns at d = 128 too: the two query tiles share one S region there, which is
+  // free as soon as one tile's groups have read it into registers, so that the next
+  // S is computed while they work.
+  static constexpr bool kOwnP = (D == 64) || PRE;
+  static constexpr bool kSharedS = PRE && D == 128;
   static constexpr int kQBuf = (D == 64) ? 2 : 1;
   static constexpr int kItemRing = 4;
   static constexpr int kQ = 0;                              // [2][kQBuf] tiles
@@ -101,21 +111,26 @@ struct PackedFwdLayout {
   static constexpr int kRing = kMisc + 16;            // [kItemRing] x {first row, length, unit or -1, head}
   static constexpr int kClc = kRing + 16 * kItemRing;   // 16-byte answer of a launch cancellation
   static constexpr int kStats = kClc + 16;              // [128] (reference, sum) of the second group's rows
-  static constexpr int kSmemBytes = kStats + (SPLIT ? 8 * kTile : 0);
+  // PRE: what a tile's two groups tell each other, [query tile] [half] [128], and,
+  // split, the second tile's references [128]
+  static constexpr int kEx = kClc + 16, kExRef = kEx + 4 * kTile * 4;
+  static constexpr int kSmemBytes = PRE ? kExRef + (SPLIT ? 4 * kTile : 0) : kStats + (SPLIT ? 8 * kTile : 0);
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
 template <int D, bool F16, int SLOTS, bool SPLIT, int SCORE>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+__global__ void __launch_bounds__(PackedFwdLayout<D, SPLIT, SCORE != kScorePlain>::kThreads, 1)
 fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv, const PackedFwdParams p) {
-  using L = PackedFwdLayout<D, SPLIT>;
+  using L = PackedFwdLayout<D, SPLIT, SCORE != kScorePlain>;
   // With P over S (d = 128), P of a tile's first 64 keys goes to the tensor
   // core before the rest is formed, and its half of P V runs meanwhile; the
   // softmax then always takes the row max first, since P may not be formed
   // again once half of it has been used
-  constexpr bool kHalfP = !L::kOwnP;
+  // (scores of their own have a warpgroup for either half, which hand P over together)
   constexpr bool PRE = SCORE != kScorePlain;
+  constexpr bool kHalfP = !L::kOwnP && !PRE;
+  constexpr int kOtherRegs = PRE ? kHalfOtherRegs : kRowOtherRegs;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
 
@@ -145,15 +160,15 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     auto arrivals = [](int i) -> uint32_t {
       if ((i >= L::bPFull && i < L::bPFull + 2) || (i >= L::bSFree && i < L::bSFree + 2) ||
           (i >= L::bPHalf && i < L::bPHalf + 2) || (SPLIT && (i == L::bStats || i == L::bJoined)))
-        return 4u;
-      return i >= L::bItemEmpty && i < L::bItemEmpty + L::kItemRing ? 10u : 1u;
+        return 4u * L::kParts;
+      return i >= L::bItemEmpty && i < L::bItemEmpty + L::kItemRing ? 2u + 8u * L::kParts : 1u;
     };
     for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), arrivals(i));
     abort_flag[0] = 0u;
     abort_flag[2] = p.wait_us;   // the wait limit, read by the slow path of every wait
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == L::kOther + 1) {
     tmem_alloc(smem_u32(misc), 512);
     tmem_relinquish();
   }
@@ -181,9 +196,9 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     return true;
   };
 
-  if (warp == 8) {
+  if (warp == L::kOther) {
     // ------------------------------------------------------------ items, Q and K producer
-    regs_dec<kRowOtherRegs>();
+    regs_dec<kOtherRegs>();
     if (lane == 0) {
       tma_prefetch_map(&tq);
       tma_prefetch_map(&tk);
@@ -308,10 +323,10 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       for (int s = 0; s < L::kStagesK && s < nk; ++s)
         drain_wait(bar(L::bKFull + s), (uint32_t)((nk - 1 - s) / L::kStagesK) & 1u);
     }
-  } else if (warp == 10) {
+  } else if (warp == L::kOther + 2) {
     // ------------------------------------------------------------ V producer
     // (its own warp, so that the K ring can run ahead of the V ring)
-    regs_dec<kRowOtherRegs>();
+    regs_dec<kOtherRegs>();
     if (lane == 0) tma_prefetch_map(&tv);
     int nv = 0;
     Pair<SPLIT, PRE> w;
@@ -335,7 +350,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
 #pragma unroll 1
       for (int s = 0; s < L::kStagesV && s < nv; ++s)
         drain_wait(bar(L::bVFull + s), (uint32_t)((nv - 1 - s) / L::kStagesV) & 1u);
-  } else if (warp == 9) {
+  } else if (warp == L::kOther + 1) {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp runs the schedule; one elected lane issues each MMA and
     // commit. At entry e, for each Q tile t, first the pending O_t += P_t V of
@@ -347,19 +362,21 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     // before both PV, so S_t(e+1) is computed while group t still works on
     // S_t(e). The last PVs of an item stay pending into the next one, unless
     // its first loads are not there yet.
-    regs_dec<kRowOtherRegs>();
+    regs_dec<kOtherRegs>();
     constexpr uint32_t idS = idesc_16<F16>(128, 128, false, false);
     constexpr uint32_t idO = idesc_16<F16>(128, D, false, true);
-    const uint32_t tS[2] = {tmem + 0u, tmem + 128u};
+    const uint32_t tS[2] = {tmem + 0u, tmem + (L::kSharedS ? 0u : 128u)};
     const uint32_t tO[2] = {tmem + 256u, tmem + 256u + (uint32_t)D};
-    // P_t: over S_t, or in columns of its own (after O_1)
-    const uint32_t tP[2] = {L::kOwnP ? tmem + 256u + 2u * D : tS[0], L::kOwnP ? tmem + 320u + 2u * D : tS[1]};
+    // P_t: over S_t, or in columns of its own (after O_1; where S is shared, behind it)
+    constexpr uint32_t kP0 = L::kSharedS ? 128u : 256u + 2u * D;
+    const uint32_t tP[2] = {L::kOwnP ? tmem + kP0 : tS[0], L::kOwnP ? tmem + kP0 + 64u : tS[1]};
     const uint32_t dQ0 = desc_lo(desc_kmajor(sbase + L::kQ, 0));
     const uint32_t dK0 = desc_lo(desc_kmajor(sbase + L::kK, 0));
     const uint32_t dV0 = desc_lo(desc_mnmajor(sbase + L::kV, 0));
     constexpr uint32_t kSlotStep = (uint32_t)(L::kTileBytes >> 4);
     int nk = 0, nv = 0;              // K and V ring entries of the entries before this one
     int nq[2] = {0, 0};              // items with query tile t so far
+    [[maybe_unused]] int last_s = -1;   // shared S: the tile of the last one
     uint32_t ns[2] = {0u, 0u}, npv[2] = {0u, 0u};   // S and PV groups issued per Q tile
     // the pending PV of each Q tile: its V ring entry or -1, whether it is the
     // item's first (overwrites O_t) and last, and the valid rows of a V tile
@@ -400,7 +417,12 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         bool k_ready = false;
         // S_t = Q_t K_e^T
         auto issue_s = [&](int t) -> bool {
-          if (L::kOwnP && ns[t] > 0 && !bar_wait_warp(bar(L::bSFree + t), (ns[t] - 1u) & 1u, ctl, 318)) return false;
+          if constexpr (L::kSharedS) {
+            if (last_s >= 0 && !bar_wait_warp(bar(L::bSFree + last_s), ((last_s ? ns[1] : ns[0]) - 1u) & 1u, ctl, 318)) return false;
+            last_s = t;
+          } else if (L::kOwnP && ns[t] > 0 && !bar_wait_warp(bar(L::bSFree + t), (ns[t] - 1u) & 1u, ctl, 318)) {
+            return false;
+          }
           if (e == w.first(t) && !bar_wait_warp(bar(L::bQFull + q_slot(t)), q_phase(t), ctl, 314)) return false;
           if (!k_ready && !bar_wait_warp(bar(L::bKFull + sk), (uint32_t)(nk / L::kStagesK) & 1u, ctl, 317)) return false;
           k_ready = true;
@@ -449,7 +471,20 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           ptail[t] = e == w.nT - 1 ? tail : 0;
         };
         auto on = [](int t) -> bool { return kWhich == 2 || t == kWhich; };
-        if constexpr (L::kOwnP) {
+        if constexpr (L::kSharedS) {
+          // S_0(e), PV_0(e - 1), S_1(e), PV_1(e - 1): S_1 waits until S_0 has been read,
+          // which is after P_0(e - 1) was written. (A group reads its first S of an item
+          // once its last O of the item before is written: there PV goes first.)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!on(t)) continue;
+            if (ok && e <= 0 && pend[t] >= 0) ok = issue_pv(t);
+            if (ok && e >= 0 && e <= last[t]) ok = issue_s(t);
+            if (ok && e >= 0 && (t == 1 || kWhich == 0)) mma_commit_w(bar(L::bKEmpty + sk));   // K_e is no longer needed
+            if (ok && pend[t] >= 0) ok = issue_pv(t);
+            if (e >= 0 && e <= last[t]) set_pending(t);
+          }
+        } else if constexpr (L::kOwnP) {
 #pragma unroll
           for (int t = 0; t < 2; ++t)
             if (ok && e >= 0 && e <= last[t] && on(t)) ok = issue_s(t);
@@ -496,7 +531,231 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     // every MMA issued has completed before TMEM is freed
     mma_commit_w(bar(L::bDrain));
     drain_wait(bar(L::bDrain), 0);
-  } else if (warp < 8) {
+  } else if (PRE && warp < L::kOther) {
+    // ------------------------------------------------------------ softmax groups, scores of their own
+    // Thread = row and half of its columns; the two groups of a query tile share a
+    // row's reference (exchanged for every tile) and add their sums at the end. After
+    // each wait that one of them may fail they agree with group_all, so that they
+    // always take the same branch and none waits where the other has left.
+    if constexpr (PRE) {
+    regs_inc<kHalfRegs>();
+    const int t = warp >> 3, h = (warp >> 2) & 1;
+    const int r = tid & 127;
+    const uint32_t pair_bar = 1u + (uint32_t)t;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + (uint32_t)((L::kSharedS ? 0 : t * 128) + 64 * h) + lane_off;
+    const uint32_t tO = tmem + 256u + (uint32_t)(t * D) + lane_off;
+    const uint32_t tP = tmem + (L::kSharedS ? 128u : 256u + 2u * D) + 64u * (uint32_t)t + lane_off + 32u * (uint32_t)h;
+    constexpr int kCols0 = D / 64;           // 32-column steps of O that a half rescales and writes
+    const float sl2 = p.scale_log2;
+    const bool bounded = SCORE == kScoreCap && !F16 && p.score.bounded;
+    // (P in fp16 ends at 2^16; moves stop all rows of a tile, so they are rare here)
+    constexpr float kMove = F16 ? 14.f : 30.f;
+    volatile float* ex = reinterpret_cast<volatile float*>(smem + L::kEx) + r;   // [query tile][half][128]
+    uint32_t nS = 0u, nO = 0u;               // S tiles and final O read by this group
+    uint32_t nJ = 0u;                        // SPLIT: items of two groups so far
+    Pair<SPLIT, PRE> w;
+    for (int k = 0;; ++k) {
+      bool ok = take_item(k, w);
+      ok = group_all(pair_bar, 256u, ok);
+      if (!ok || w.c < 0) break;
+      if (!w.has(t)) continue;
+      const int qi = w.qi(t), last = w.last(t);
+      const int row = kTile * qi + r;        // query index within the sequence
+      const float slope2 = p.score.slopes != nullptr ? p.score.slopes[w.hq(t)] * 1.4426950408889634f : 0.f;
+      float m_ref = 0.f;
+      float l = 0.f;
+      for (int e = w.first(t); e <= last; e += SPLIT ? 2 : 1) {
+        const bool begin = e == w.first(t);
+        ok = ok && bar_wait_warp(bar(L::bSFull + t), nS & 1u, ctl, 320 + t);
+        tc_fence_after();
+        uint32_t u[2][32];
+        tmem_ld32(tS, u[0]);
+        tmem_ld32(tS + 32u, u[1]);
+        tmem_ld_wait(u[0]);
+        tmem_ld_wait(u[1]);
+        tc_fence_before();
+        mbar_arrive_warp(bar(L::bSFree + t));   // this half of S_t is in registers
+        // keys from column `lim` on are masked: they lie past the row and the
+        // prefix (causal), or past the sequence (never all of a row's columns in a
+        // tile; rows past the sequence are not stored)
+        const bool partial = w.partial(e, qi);
+        const int lim = (w.causal ? min(max(row + 1, w.pre), w.len) : w.len) - kTile * e - 64 * h;
+        float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t pk[2][16];
+        // 2^x of 32 arguments; P goes to 16 bits (half a step per weight), the row sum
+        // takes the unrounded values
+        auto weights = [&](int hh) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float p0 = ex2(__uint_as_float(u[hh][2 * i]));
+            const float p1 = ex2(__uint_as_float(u[hh][2 * i + 1]));
+            sum4[i & 3] = __fadd2_rn(sum4[i & 3], make_float2(p0, p1));
+            pk[hh][i] = pack2<F16>(p0, p1);
+          }
+        };
+        if (bounded) {
+          // (against a reference of 0: no maximum, and the two halves need not agree)
+          const bool small = cap_vote(u, p.score, partial, lim);
+          if (small && !partial) {
+            // (in one piece, so that the polynomial of some scores runs beside the
+            // exponentials of others)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 a = cap_small2(pair_of(u[hh], 2 * i), p.score);
+                const float p0 = ex2(a.x);
+                const float p1 = ex2(a.y);
+                sum4[i & 3] = __fadd2_rn(sum4[i & 3], make_float2(p0, p1));
+                pk[hh][i] = pack2<F16>(p0, p1);
+              }
+          } else {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              cap_args(u[hh], p.score, partial, lim - 32 * hh, small, 0.f);
+              weights(hh);
+            }
+          }
+          if (SPLIT && t == 1 && begin && nJ > 0u) ok = ok && bar_wait_warp(bar(L::bJoined), (nJ - 1u) & 1u, ctl, 328);
+        } else {
+          const ScoreTile st = score_tile<SCORE>(p.score, slope2, kTile * e + 64 * h, row, e < qi ? -1 : e > qi ? 1 : 0,
+                                                 e == qi && (!w.causal || w.pre > kTile * e), partial, lim);
+          // The exponents against the row's reference as it is, which moves only where
+          // one passes it by more than the threshold, and in an item's first tile. (Where
+          // the tile's largest bias lies above it, against that: from a reference that
+          // is far below, they would be rounded in its units.)
+          const float above = score_base(p.score, slope2, kTile * e, row, e < qi ? -1 : e > qi ? 1 : 0);
+          const float base = begin ? (above > -INFINITY ? above : 0.f) : fmaxf(m_ref, above);
+          const float mx = score_args<SCORE, true>(u, p.score, sl2, st, -base);
+          if (!group_all(pair_bar, 256u, ok && !begin && base <= m_ref && mx <= kMove)) {
+            // (the first group has read O_1 and what goes with it of the item before)
+            if (SPLIT && t == 1 && begin && nJ > 0u) ok = ok && bar_wait_warp(bar(L::bJoined), (nJ - 1u) & 1u, ctl, 328);
+            // the previous O_t += P_t V has completed: O_t may be rescaled
+            if (!begin) ok = ok && bar_wait_warp(bar(L::bPVDone + t), (nS - 1u) & 1u, ctl, 326 + t);
+            ex[kTile * (2 * t + h)] = mx;
+            if (!(ok = group_all(pair_bar, 256u, ok))) break;
+            tc_fence_after();
+            const float top = fmaxf(mx, ex[kTile * (2 * t + (h ^ 1))]);
+            const float up = begin ? 0.f : base - m_ref;
+            const bool move = begin || top + up > kMove;
+            float alpha = 1.f, shift = up;
+            if (move) {
+              const float by = top > -INFINITY ? top : 0.f;   // (0: nothing to move to)
+              alpha = begin ? 0.f : ex2(m_ref - (base + by));
+              shift = -by;
+              m_ref = base + by;
+              l *= alpha;
+            }
+            // (warp-collective: a warp rescales when any of its rows needs it, 16 columns
+            // at a time beside the scores)
+            if (!begin && __any_sync(0xFFFFFFFFu, move)) {
+#pragma unroll 1
+              for (uint32_t cc = 0; cc < 2 * kCols0; ++cc) {
+                uint32_t o[16];
+                tmem_ld16(tO + 32u * kCols0 * h + 16u * cc, o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st16(tO + 32u * kCols0 * h + 16u * cc, o);
+              }
+            }
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) put_pair(u[hh], i, __fadd2_rn(pair_of(u[hh], i), make_float2(shift, shift)));
+          }
+          weights(0);
+          weights(1);
+        }
+        const float2 s4 = __fadd2_rn(__fadd2_rn(sum4[0], sum4[1]), __fadd2_rn(sum4[2], sum4[3]));
+        l += s4.x + s4.y;
+        // P's columns are free once the product before has read them
+        if (nS > 0u) ok = ok && bar_wait_warp(bar(L::bPVDone + t), (nS - 1u) & 1u, ctl, 326 + t);
+        tc_fence_after();
+        tmem_st16(tP, pk[0]);
+        tmem_st16(tP + 16u, pk[1]);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive_warp(bar(L::bPFull + t));
+        ++nS;
+      }
+      // O / l and the LSE, once the last PV has completed; a half writes half of the
+      // columns
+      if (ok) ok = bar_wait_warp(bar(L::bOFinal + t), nO & 1u, ctl, 324 + t);
+      // (the other half has read what it needed: the last PV waited for its P)
+      if (ok) ex[kTile * (2 * t + h)] = l;
+      const bool join = SPLIT && w.has(1);
+      float* ref1 = reinterpret_cast<float*>(smem + L::kExRef);
+      if (SPLIT && join && t == 1 && h == 0 && ok) ref1[r] = m_ref;
+      ok = group_all(pair_bar, 256u, ok);
+      if (!ok) break;
+      ++nO;
+      tc_fence_after();
+      float w0 = 1.f, w1 = 0.f;
+      if (SPLIT && join && t == 1) {
+        // (the sums stay where the first group finds them until it has joined them)
+        tc_fence_before();
+        mbar_arrive_warp(bar(L::bStats));
+        ++nJ;
+        continue;
+      }
+      l += ex[kTile * (2 * t + (h ^ 1))];
+      if constexpr (SPLIT) {
+        if (join) {
+          ok = bar_wait_warp(bar(L::bOFinal + 1), nJ & 1u, ctl, 325) && bar_wait_warp(bar(L::bStats), nJ & 1u, ctl, 329);
+          ok = group_all(pair_bar, 256u, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const float m1 = ref1[r], l1 = ex[kTile * 2] + ex[kTile * 3];
+          ++nJ;
+          const float M = fmaxf(m_ref, m1), ref = M == -INFINITY ? 0.f : M;
+          w0 = ex2(m_ref - ref);
+          w1 = ex2(m1 - ref);
+          l = fmaf(w0, l, w1 * l1);
+          m_ref = M;
+        }
+      }
+      const float inv_l = 1.f / l;
+      const int s4 = lane & 3;
+      const int row0 = kTile * qi + 32 * (warp & 3) + (lane & ~3);   // the quad's first row
+      uint16_t* op = p.o + (int64_t)(w.start + row0) * p.o_tok + w.hq(t) * p.o_head + 8 * s4;
+#pragma unroll 1
+      for (int cc = kCols0 * h; cc < kCols0 * (h + 1); ++cc) {
+        uint32_t o[32];
+        tmem_ld32(tO + 32u * cc, o);
+        tmem_ld_wait(o);
+        if constexpr (SPLIT) {
+          if (join) {
+            uint32_t o1[32];
+            tmem_ld32(tO + (uint32_t)D + 32u * cc, o1);
+            tmem_ld_wait(o1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(fmaf(w1, __uint_as_float(o1[i]), w0 * __uint_as_float(o[i])));
+          }
+        }
+        uint32_t x[4][4];   // [word of a chunk][chunk of this row, then row of the quad]
+#pragma unroll
+        for (int wd = 0; wd < 4; ++wd) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            x[wd][j] = pack2<F16>(__uint_as_float(o[8 * j + 2 * wd]) * inv_l, __uint_as_float(o[8 * j + 2 * wd + 1]) * inv_l);
+          quad_transpose(x[wd], (uint32_t)s4);
+        }
+        if (32 * cc + 8 * s4 < p.d) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (row0 + j < w.len)
+              *reinterpret_cast<uint4*>(op + j * p.o_tok + 32 * cc) = make_uint4(x[0][j], x[1][j], x[2][j], x[3][j]);
+        }
+      }
+      if (h == 0 && row < w.len)
+        p.lse[(size_t)w.hq(t) * p.total + w.start + row] = (m_ref + log2f(l)) * 0.69314718055994531f;
+      tc_fence_before();   // (the next PV of this tile waits for these groups' next P)
+      if (join) mbar_arrive_warp(bar(L::bJoined));
+    }
+    }
+  } else if (!PRE && warp < 8) {
     // ------------------------------------------------------------ softmax groups
     regs_inc<kSoftmaxRegs>();
     const int t = warp >> 2;                 // Q tile of this warpgroup
@@ -506,7 +765,6 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     const uint32_t tO = tmem + 256u + (uint32_t)(t * D) + lane_off;
     const uint32_t tP = L::kOwnP ? tmem + 256u + 2u * D + 64u * (uint32_t)t + lane_off : tS;
     const float sl2 = p.scale_log2;
-    [[maybe_unused]] float slope2 = 0.f;     // SCORE: of the item's head
     uint32_t nS = 0u, nO = 0u;               // S tiles and final O read by this group
     uint32_t nJ = 0u;                        // SPLIT: items of two groups so far
     bool ok = true;
@@ -515,7 +773,6 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       if (!w.has(t)) continue;
       const int qi = w.qi(t), last = w.last(t);
       const int row = kTile * qi + r;        // query index within the sequence
-      if (PRE && p.score.slopes != nullptr) slope2 = p.score.slopes[w.hq(t)] * 1.4426950408889634f;
       float m_ref = -INFINITY;
       float l = 0.f;
       for (int e = w.first(t); e <= last; e += SPLIT ? 2 : 1) {
@@ -550,15 +807,11 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           if (!(ok = bar_wait_warp(bar(L::bJoined), (nJ - 1u) & 1u, ctl, 328))) break;
           tc_fence_after();
         }
-        const bool partial = w.partial(e, qi);
-        // a key is masked when it lies past the row (causal) or past the
-        // sequence: key >= min(row + 1, length), i.e. column i >= lim (never
-        // all of a row's columns; rows past the sequence are not stored);
-        // with a prefix, past both it and the row
-        const int lim = (w.causal ? min(PRE ? max(row + 1, w.pre) : row + 1, w.len) : w.len) - kTile * e;
-        if constexpr (SCORE != kScorePlain)
-          score_row<SCORE>(x, p.score, sl2, slope2, (float)(kTile * e - row), e < qi ? -1 : e > qi ? 1 : 0, partial, lim);
-        if (partial) {
+        if (w.partial(e, qi)) {
+          // a key is masked when it lies past the row (causal) or past the
+          // sequence: key >= min(row + 1, length), i.e. column i >= lim (never
+          // all of a row's columns; rows past the sequence are not stored)
+          const int lim = (w.causal ? min(row + 1, w.len) : w.len) - kTile * e;
 #pragma unroll
           for (int i = 0; i < 128; ++i)
             if (i >= lim) x[i] = -INFINITY;
@@ -594,7 +847,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
 #pragma unroll
             for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(mx8[k], x[120 + k]);
             const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-            const float m_new = PRE ? mx : mx * sl2;   // (PRE: x is in log2 units)
+            const float m_new = mx * sl2;
             // move the reference max only when the row max grew by more than the
             // threshold; the O rescale is warp-collective (tcgen05.ld/st), so a
             // warp rescales when any of its rows needs it (alpha = 1 for the rest)
@@ -629,8 +882,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
             uint32_t pk[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float2 x2 = make_float2(x[64 * hh + 2 * i], x[64 * hh + 2 * i + 1]);
-              const float2 a = PRE ? __fadd2_rn(x2, nref2) : __ffma2_rn(x2, sl2x2, nref2);
+              const float2 a = __ffma2_rn(make_float2(x[64 * hh + 2 * i], x[64 * hh + 2 * i + 1]), sl2x2, nref2);
               const float p0 = ex2(a.x);
               const float p1 = ex2(a.y);
               sum4[i & 3] = __fadd2_rn(sum4[i & 3], make_float2(p0, p1));
@@ -737,12 +989,12 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       if (join) mbar_arrive_warp(bar(L::bJoined));
     }
   } else {
-    regs_dec<kRowOtherRegs>();   // warp 11: no role
+    regs_dec<kOtherRegs>();   // the last warp: no role
   }
   tc_fence_before();
   __syncthreads();
   if (tid == 0) report_aborted(ctl);
-  if (warp == 9) {
+  if (warp == L::kOther + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -751,7 +1003,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
 template <int D, bool F16, int SLOTS, bool SPLIT, int SCORE>
 cudaError_t launch_packed_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const PackedFwdParams& p, cudaStream_t s) {
-  using L = PackedFwdLayout<D, SPLIT>;
+  using L = PackedFwdLayout<D, SPLIT, SCORE != kScorePlain>;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -770,7 +1022,7 @@ cudaError_t launch_packed_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, co
   // a CTA per item where items are taken by cancelling CTAs, else one per SM
   const long long most = (long long)p.cap_items * p.heads;
   return launch_pdl(true, fa_packed_fwd_kernel<D, F16, SLOTS, SPLIT, SCORE>, dim3((unsigned)(p.B <= kDirect || most < sms ? most : sms)),
-                    dim3(kFwdThreads), L::kSmemBytes, s, tq, tk, tv, q);
+                    dim3(L::kThreads), L::kSmemBytes, s, tq, tk, tv, q);
 }
 
 template <int SCORE>

@@ -11,6 +11,8 @@ namespace {
 constexpr int kFwdThreads = 384;
 constexpr int kSoftmaxRegs = 216;   // 2 x 128 x 216 + 128 x 72 = 384 x 168 registers
 constexpr int kRowOtherRegs = 72;
+// with two warpgroups to a row: 4 x 128 x 104 + 128 x 64 = 640 x 96 registers
+constexpr int kHalfThreads = 640, kHalfRegs = 104, kHalfOtherRegs = 64;
 
 // An item as the roles see it: its two query tiles, and the key tiles 0 .. n - 1
 // live for either. SPLIT: one query tile, whose even key tiles are the first
@@ -59,79 +61,153 @@ struct Pair {
   __device__ __forceinline__ int tail() const { return len & (kTile - 1); }
 };
 
-// Brings a row of scores (raw products of query `row` with the keys from `key0`
-// on) to log2 units, capped and lowered with the distance; key0 - row = far.
-// side: -1 where all of these keys lie before the query's tile, 1 behind it, 0 in
-// it. masked: columns from `lim` on are no keys of the row (what lies there may
-// be NaN, which must not meet its neighbour).
+// Scores of their own, of one row against half of a tile's keys: 64 columns in
+// registers of one thread.
+//
+// (A thread for a whole row, as for plain scores, took 440 us for two sequences of
+// 4547 and 5127 tokens, 32 / 8 heads, d = 128, with a cap: seven more operations a
+// score in two warps of an SM's quarter. Two threads to a row 411, 64 KB of code
+// less than 93; P in columns of its own, so that the next S is computed meanwhile,
+// and weights that need no maximum 325; plain scores take 242.)
+//
+// What is uniform for a row and a tile: the bias of key j is +-slope (j - i) where
+// all keys lie on one side (linear), counted up beside the scores; else, in the
+// query's own tile, -slope |j - i|. far = first key - query.
+struct ScoreTile {
+  float slope, far;          // slope: signed, in log2 units
+  bool bias, linear, partial;
+  int lim;                   // columns from here on are no keys of the row (partial)
+};
+
 template <int SCORE>
-__device__ __forceinline__ void score_row(float (&x)[128], const ScoreParams& sp, float sl2, float slope2, float far,
-                                          int side, bool masked, int lim) {
-  if constexpr (SCORE == kScoreCap) {
-    if (masked)
+__device__ __forceinline__ ScoreTile score_tile(const ScoreParams& sp, float slope2, int key0, int row, int side,
+                                                bool both_sides, bool partial, int lim) {
+  ScoreTile s;
+  s.bias = sp.slopes != nullptr;
+  s.linear = !both_sides;
+  s.slope = side > 0 ? -slope2 : slope2;
+  s.far = (float)(key0 - row);
+  s.partial = partial;
+  s.lim = lim;
+  return s;
+}
+
+// The largest bias of a row's keys in the tile from key0 on (about: masked keys
+// count); -inf without a bias.
+__device__ __forceinline__ float score_base(const ScoreParams& sp, float slope2, int key0, int row, int side) {
+  if (sp.slopes == nullptr) return -INFINITY;
+  const int first = key0 - row, last = first + kTile - 1;
+  const int nearest = side < 0 ? -last : side > 0 ? first : 0, farthest = side < 0 ? -first : side > 0 ? last : kTile - 1;
+  return -slope2 * (float)(slope2 >= 0.f ? nearest : farthest);
+}
+
+// The bias of columns c, c + 1, ... + 31 (and nref) by step: four chains of four
+// steps, each rounded once.
+struct BiasSteps {
+  float2 d[4], step;
+  __device__ __forceinline__ BiasSteps(const ScoreTile& s, int c, float nref) {
 #pragma unroll
-      for (int i = 0; i < 128; ++i)
-        if (i >= lim) x[i] = 0.f;
-    float top[4];
+    for (int k = 0; k < 4; ++k) {
+      const float j = s.far + (float)(c + 2 * k);
+      d[k] = make_float2(fmaf(s.slope, j, nref), fmaf(s.slope, j + 1.f, nref));
+    }
+    step = make_float2(8.f * s.slope, 8.f * s.slope);
+  }
+  __device__ __forceinline__ float2 next(int k) {
+    const float2 b = d[k];
+    d[k] = __fadd2_rn(d[k], step);
+    return b;
+  }
+};
+
+__device__ __forceinline__ float2 pair_of(const uint32_t (&u)[32], int i) {
+  return make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1]));
+}
+__device__ __forceinline__ void put_pair(uint32_t (&u)[32], int i, float2 x) {
+  u[i] = __float_as_uint(x.x);
+  u[i + 1] = __float_as_uint(x.y);
+}
+__device__ __forceinline__ void mask_columns(uint32_t (&u)[32], int lim, float with) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) top[k] = fmaxf(fabsf(x[k]), fabsf(x[4 + k]));
+  for (int i = 0; i < 32; ++i)
+    if (i >= lim) u[i] = __float_as_uint(with);
+}
+
+// A cap's first step on a row's 64 raw scores: whether all of them, of all rows of
+// the warp, are within the polynomial's limit. What lies in masked columns may be
+// NaN, which must not meet its neighbour in tanh_exp2: it becomes zeros.
+__device__ __forceinline__ bool cap_vote(uint32_t (&u)[2][32], const ScoreParams& sp, bool partial, int lim) {
+  if (partial) {
+    mask_columns(u[0], lim, 0.f);
+    mask_columns(u[1], lim - 32, 0.f);
+  }
+  float top[4];
 #pragma unroll
-    for (int i = 8; i < 128; i += 8)
+  for (int k = 0; k < 4; ++k) top[k] = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) top[k] = fmax3(top[k], fabsf(x[i + k]), fabsf(x[i + 4 + k]));
-    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-    if (__all_sync(0xFFFFFFFFu, most <= sp.limit)) {
+  for (int i = 0; i < 64; i += 2)
+    top[(i >> 1) & 3] = fmax3(top[(i >> 1) & 3], fabsf(__uint_as_float(u[i >> 5][i & 31])),
+                              fabsf(__uint_as_float(u[i >> 5][(i & 31) + 1])));
+  return __all_sync(0xFFFFFFFFu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) <= sp.limit);
+}
+
+// The cap of 32 scores, and nref; -inf where masked (partial: from column lim on).
+__device__ __forceinline__ void cap_args(uint32_t (&u)[32], const ScoreParams& sp, bool partial, int lim, bool small,
+                                         float nref) {
+  const float2 n2 = make_float2(nref, nref);
+  if (small) {
 #pragma unroll
-      for (int i = 0; i < 128; i += 2) {
-        const float2 t = cap_small2(make_float2(x[i], x[i + 1]), sp);
-        x[i] = t.x;
-        x[i + 1] = t.y;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 128; i += 2) {
-        const float2 t = tanh_exp2(make_float2(x[i], x[i + 1]), sp);
-        x[i] = t.x * sp.c2;
-        x[i + 1] = t.y * sp.c2;
-      }
+    for (int i = 0; i < 32; i += 2) {
+      const float2 x = pair_of(u, i);
+      put_pair(u, i, __ffma2_rn(x, cap_small_factor2(x, sp), n2));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 128; i += 2) {
-      const float2 t = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(sl2, sl2));
-      x[i] = t.x;
-      x[i + 1] = t.y;
+    for (int i = 0; i < 32; i += 2) put_pair(u, i, __ffma2_rn(tanh_exp2(pair_of(u, i), sp), make_float2(sp.c2, sp.c2), n2));
+  }
+  if (partial) mask_columns(u, lim, -INFINITY);
+}
+
+// The arguments of the exponential, u2 + nref in log2 units, from a row's 64 raw
+// scores; -inf where masked. Returns their maximum (MAX).
+template <int SCORE, bool MAX>
+__device__ __forceinline__ float score_args(uint32_t (&u)[2][32], const ScoreParams& sp, float sl2, const ScoreTile& s,
+                                            float nref) {
+  if constexpr (SCORE == kScoreCap) {
+    const bool small = cap_vote(u, sp, s.partial, s.lim);
+    cap_args(u[0], sp, s.partial, s.lim, small, nref);
+    cap_args(u[1], sp, s.partial, s.lim - 32, small, nref);
+  } else if (s.partial) {
+    mask_columns(u[0], s.lim, -INFINITY);
+    mask_columns(u[1], s.lim - 32, -INFINITY);
+  }
+  if (SCORE == kScoreBias || s.bias) {
+    const float mul = SCORE == kScoreCap ? 1.f : sl2, start = SCORE == kScoreCap ? 0.f : nref;
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      if (s.linear) {
+        BiasSteps b(s, 32 * hh, start);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2)
+          put_pair(u[hh], i, __ffma2_rn(pair_of(u[hh], i), make_float2(mul, mul), b.next((i >> 1) & 3)));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float d = s.far + (float)(32 * hh + i);
+          const float2 x = __ffma2_rn(pair_of(u[hh], i), make_float2(mul, mul), make_float2(start, start));
+          put_pair(u[hh], i, make_float2(fmaf(-s.slope, fabsf(d), x.x), fmaf(-s.slope, fabsf(d + 1.f), x.y)));
+        }
+      }
     }
   }
-  if (sp.slopes != nullptr) {
-    // the distances count up beside the scores (as constants they would take a
-    // register each)
-    float2 d[4];
+  if (!MAX) return 0.f;
+  float hi[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) d[k] = make_float2(far + (float)(2 * k), far + (float)(2 * k + 1));
-    const float2 step = make_float2(8.f, 8.f);
-    if (side == 0) {
+  for (int k = 0; k < 4; ++k) hi[k] = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 128; i += 8)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          x[i + 2 * k] = fmaf(-slope2, fabsf(d[k].x), x[i + 2 * k]);
-          x[i + 2 * k + 1] = fmaf(-slope2, fabsf(d[k].y), x[i + 2 * k + 1]);
-          d[k] = __fadd2_rn(d[k], step);
-        }
-    } else {
-      const float sl = side < 0 ? slope2 : -slope2;
-#pragma unroll
-      for (int i = 0; i < 128; i += 8)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 t = __ffma2_rn(make_float2(sl, sl), d[k], make_float2(x[i + 2 * k], x[i + 2 * k + 1]));
-          x[i + 2 * k] = t.x;
-          x[i + 2 * k + 1] = t.y;
-          d[k] = __fadd2_rn(d[k], step);
-        }
-    }
-  }
+  for (int i = 0; i < 64; i += 2)
+    hi[(i >> 1) & 3] = fmax3(hi[(i >> 1) & 3], __uint_as_float(u[i >> 5][i & 31]), __uint_as_float(u[i >> 5][(i & 31) + 1]));
+  return fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
 }
 
 }  // namespace

@@ -24,7 +24,13 @@ struct ScoreParams {
   float a0, a1, a2, a3;      // there t2 = s (a0 + s^2 (a1 + s^2 (a2 + s^2 a3)))
   float k, e2, c2;           // k; 2 k log2(e): exp(2 k s) = 2^(e2 s); c2
   int cap;
+  int bounded;               // capped without a bias, at most kFreeRange
 };
+
+// P in bf16 and its fp32 sums reach 2^127 and down to 2^-126. Where a cap bounds the
+// scores by at most this in log2 units (a softcap of 55), weights are 2^u2 as it is and
+// no row needs a reference: at most 2^80 each, they leave room for values of 2^30.
+constexpr float kFreeRange = 80.f;
 
 // tanh(y) = y (C0 + C1 y^2 + C2 y^4 + C3 y^6) for |y| <= 0.4, to 9.8e-8 of the
 // value: the polynomial of least relative error (Remez exchange, in 64 bits).
@@ -55,6 +61,7 @@ inline fa_status read_scores(const fa_scores* scores, float scale, int causal, b
   out->k = (float)k;
   out->e2 = (float)(2. * 1.4426950408889634 * k);
   out->c2 = (float)c2;
+  out->bounded = s.slopes == nullptr && c2 <= kFreeRange;
   // (past these k, k^7 leaves the fp32 range)
   if (k < 0x1p15 && k > 0x1p-15) {
     out->limit = (float)(kCapSmall / k);
@@ -92,13 +99,15 @@ __device__ __forceinline__ float2 tanh_exp2(float2 s, const ScoreParams& p) {
   const float r = -2.f * rcp_approx(b.x * b.y);
   return make_float2(fmaf(r, b.y, 1.f), fmaf(r, b.x, 1.f));
 }
-// t2 of a pair of small scores (|s| <= limit)
-__device__ __forceinline__ float2 cap_small2(float2 s, const ScoreParams& p) {
+// t2 = s times this, of a pair of small scores (|s| <= limit)
+__device__ __forceinline__ float2 cap_small_factor2(float2 s, const ScoreParams& p) {
   const float2 z = __fmul2_rn(s, s);
   float2 r = __ffma2_rn(z, make_float2(p.a3, p.a3), make_float2(p.a2, p.a2));
   r = __ffma2_rn(z, r, make_float2(p.a1, p.a1));
-  r = __ffma2_rn(z, r, make_float2(p.a0, p.a0));
-  return __fmul2_rn(s, r);
+  return __ffma2_rn(z, r, make_float2(p.a0, p.a0));
+}
+__device__ __forceinline__ float2 cap_small2(float2 s, const ScoreParams& p) {
+  return __fmul2_rn(s, cap_small_factor2(s, p));
 }
 // t2 of one score of any size: the polynomial where it holds
 __device__ __forceinline__ float cap_any(float s, const ScoreParams& p) {
