@@ -202,9 +202,10 @@ fa_status cached_fwd_call(const void* Q, int64_t q_token_stride, const void* k_c
   p.part_ml = reinterpret_cast<float2*>(ws + w.ml_off);
   p.info = reinterpret_cast<int2*>(ws + w.info_off);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = p.score.cap || p.score.slopes != nullptr
-                            ? launch_cached_scored(e4m3, f16, tk, tv, tks, tvs, p, s)
-                            : launch_cached_score<false>(e4m3, f16, tk, tv, tks, tvs, p, s);
+  const auto launch = p.score.cap      ? launch_cached_cap
+                      : p.score.slopes ? launch_cached_bias
+                                       : launch_cached_score<kScorePlain>;
+  const cudaError_t e = launch(e4m3, f16, tk, tv, tks, tvs, p, s);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

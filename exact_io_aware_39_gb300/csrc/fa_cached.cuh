@@ -88,7 +88,7 @@ constexpr Shape cached_shape(int D, bool e4m3, bool whole) {
   return D == 128 ? Shape{16, 12, 2} : Shape{32, 12, 2};
 }
 
-template <int D, bool E4M3, bool WHOLE>
+template <int D, bool E4M3, bool WHOLE, bool SCORED>
 struct CachedLayout {
   static constexpr Shape kShape = cached_shape(D, E4M3, WHOLE);
   static constexpr int kKT = kShape.keys;
@@ -108,8 +108,9 @@ struct CachedLayout {
   // warp, by pairs of keys: the factors and the log2 added, then the reciprocals).
   // 64 sequences of 151070 tokens in all at d = 64 39 us so and 42 without; at d =
   // 128, with 32 keys, the step through memory costs more than it saves (the 16
-  // sequences 164 and 161 us).
-  static constexpr bool kByKey = E4M3 && kKT == 64;
+  // sequences 164 and 161 us), but for scores of their own, which have more to do
+  // beside the loads (lowered with distance 176 us so and 187).
+  static constexpr bool kByKey = E4M3 && (kKT == 64 || SCORED);
   static constexpr int kFactorBytes = kByKey ? 12 * kKT : 0;
   static constexpr int kFactors = kScale + kWarps * kStages * 2 * kScaleBytes;
   static constexpr int kBar = kFactors + kWarps * kFactorBytes;
@@ -139,13 +140,14 @@ struct CachedParams {
   float scale_log2;
   uint32_t wait_us, stall;
   int cluster;         // WHOLE: CTAs to a unit
-  ScoreParams score;   // SCORED
+  ScoreParams score;
 };
 
-// Launchers of the attention with capped or biased scores and of the sums of its
-// weights, each in a translation unit of its own.
-cudaError_t launch_cached_scored(bool e4m3, bool f16, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tks,
+// Launchers of the attention for scores of their own (kScoreCap, kScoreBias), each
+// from a translation unit of its own.
+using CachedLaunch = cudaError_t(bool e4m3, bool f16, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tks,
                                  const CUtensorMap& tvs, const CachedParams& p, cudaStream_t s);
+CachedLaunch launch_cached_cap, launch_cached_bias;
 
 namespace {
 
@@ -223,15 +225,16 @@ struct Walk {
 // parts meet in shared memory (a CTA's, then the cluster's), so there is neither
 // a workspace nor a second kernel. For calls of few, short sequences.
 //
-// SCORED: scores are capped, or lowered with the distance from the query's place
+// SCORE: scores are capped, or lowered with the distance from the query's place
 // (fa_scores.cuh), between the first product and the softmax.
-template <int D, bool E4M3, bool F16, bool WHOLE, bool SCORED>
-__global__ void __launch_bounds__(32 * CachedLayout<D, E4M3, WHOLE>::kWarps, 1)
+template <int D, bool E4M3, bool F16, bool WHOLE, int SCORE>
+__global__ void __launch_bounds__(32 * CachedLayout<D, E4M3, WHOLE, SCORE != kScorePlain>::kWarps, 1)
 fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const __grid_constant__ CUtensorMap tks, const __grid_constant__ CUtensorMap tvs,
                  const CachedParams p) {
-  using L = CachedLayout<D, E4M3, WHOLE>;
+  using L = CachedLayout<D, E4M3, WHOLE, SCORE != kScorePlain>;
   constexpr int KT = L::kKT, kWarps = L::kWarps;
+  constexpr bool SCORED = SCORE != kScorePlain;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   // (what is the same in all lanes of a warp comes from a shuffle, so that the
@@ -405,7 +408,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
   uint32_t qf[kSteps][4];
   float o[D / 8][4];
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, qs[2];
-  [[maybe_unused]] float slope2[2] = {0.f, 0.f};   // SCORED: of the two rows' heads
+  [[maybe_unused]] float slope2[2] = {0.f, 0.f};   // of the two rows' heads
 #pragma unroll
   for (int n = 0; n < D / 8; ++n)
 #pragma unroll
@@ -522,7 +525,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         float vs = key < left ? *reinterpret_cast<const float*>(ss + L::kScaleBytes + place(key)) : 1.f;
         if (__any_sync(0xFFFFFFFFu, vs == 0.f)) no_scale(vs, key, 0, L::kRowBytes / 16);
         const int at = 4 * (key >> 1) + (key & 1);
-        f[at] = SCORED ? ks : ks * p.scale_log2;
+        f[at] = SCORE == kScoreCap ? ks : ks * p.scale_log2;
         f[at + 2] = __log2f(vs);
         f[2 * KT + key] = __fdividef(1.f, vs);
       }
@@ -570,15 +573,20 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
             mma_f16(sc[n], qf[4 * c4 + i], e4m3_to_f16(b[i] & 0xFFFFu), e4m3_to_f16(b[i] >> 16));
         }
     }
-    // SCORED: a raw product of row hh and key `key` + 2 t4 of the tile to log2
-    // units, capped and lowered with the distance; query i is at place len - Nq + i
-    [[maybe_unused]] float far[2];
+    // Scores of their own: query i is at place len - Nq + i, `far` keys behind the
+    // lane's first. (Keys past a row's place, whose bias would have the other sign,
+    // are masked below.) Their arithmetic shows beside the loads, so it is left out
+    // for rows 8-15 of a unit that has none.
+    const bool upper = !SCORED || p.R - rt * kRows > 8;
+    [[maybe_unused]] float bias0[2] = {0.f, 0.f};
     if constexpr (SCORED)
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) far[hh] = (float)(left - p.Nq + (rt * kRows + g + 8 * hh) / p.G - 2 * t4);
+      for (int hh = 0; hh < 2; ++hh)
+        bias0[hh] = -slope2[hh] * (float)(left - p.Nq + (rt * kRows + g + 8 * hh) / p.G - 2 * t4);
+    // a capped product in log2 units, or one that is already, less its bias
     [[maybe_unused]] auto score2 = [&](float s, int hh, int key) -> float {
-      const float t = p.score.cap ? cap_any(s, p.score) : s * p.scale_log2;
-      return p.score.slopes != nullptr ? fmaf(-slope2[hh], fabsf(far[hh] - (float)key), t) : t;
+      const float u = SCORE == kScoreCap ? cap_any(s, p.score) : s;
+      return u + fmaf(slope2[hh], (float)key, bias0[hh]);
     };
     // scores in log2 units; with e4m3 plus log2 of the value's scale
     float ivs[KT / 8][2];
@@ -616,14 +624,16 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
           const float2 ks2 = *reinterpret_cast<const float2*>(ss + place(key));
           ivs[n][0] = __fdividef(1.f, vs2[n].x);
           ivs[n][1] = __fdividef(1.f, vs2[n].y);
-          const float mul = SCORED ? 1.f : p.scale_log2;
+          const float mul = SCORE == kScoreCap ? 1.f : p.scale_log2;
           fa = make_float4(ks2.x * mul, ks2.y * mul, __log2f(vs2[n].x), __log2f(vs2[n].y));
         }
         if constexpr (SCORED) {
           sc[n][0] = score2(sc[n][0] * qs[0] * fa.x, 0, 8 * n) + fa.z;
           sc[n][1] = score2(sc[n][1] * qs[0] * fa.y, 0, 8 * n + 1) + fa.w;
-          sc[n][2] = score2(sc[n][2] * qs[1] * fa.x, 1, 8 * n) + fa.z;
-          sc[n][3] = score2(sc[n][3] * qs[1] * fa.y, 1, 8 * n + 1) + fa.w;
+          if (upper) {
+            sc[n][2] = score2(sc[n][2] * qs[1] * fa.x, 1, 8 * n) + fa.z;
+            sc[n][3] = score2(sc[n][3] * qs[1] * fa.y, 1, 8 * n + 1) + fa.w;
+          }
           continue;
         }
         sc[n][0] = fmaf(sc[n][0] * qs[0], fa.x, fa.z);
@@ -635,7 +645,11 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
 #pragma unroll
       for (int n = 0; n < KT / 8; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[n][i] = SCORED ? score2(sc[n][i], i >> 1, 8 * n + (i & 1)) : sc[n][i] * p.scale_log2;
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (!SCORED) sc[n][i] *= p.scale_log2;
+          else if (i < 2 || upper)
+            sc[n][i] = score2(SCORE == kScoreCap ? sc[n][i] : sc[n][i] * p.scale_log2, i >> 1, 8 * n + (i & 1));
+        }
     }
     if (left - (p.Nq - 1) < KT) {
       // token i sees the first left - (Nq - 1 - i) keys from here
@@ -654,6 +668,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     bool move = false;
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
+      if (SCORED && hh == 1 && !upper) continue;
       float mx = -INFINITY;
 #pragma unroll
       for (int n = 0; n < KT / 8; ++n) mx = fmaxf(mx, fmaxf(sc[n][2 * hh], sc[n][2 * hh + 1]));
@@ -677,6 +692,10 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     for (int n = 0; n < KT / 8; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        if (SCORED && i >= 2 && !upper) {   // (rows that are none: products of zeros)
+          sc[n][i] = 0.f;
+          continue;
+        }
         sc[n][i] = ex2(sc[n][i] - ref[i >> 1]);
         l[i >> 1] += E4M3 ? sc[n][i] * ivs[n][i & 1] : sc[n][i];
       }
@@ -1124,20 +1143,20 @@ bool cached_maps(CUtensorMap* m, CUtensorMap* ms, const void* cache, const float
   return !internal_tensor_map(ms, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, scale, sdims, sstr, sbox, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-template <int D, bool E4M3, bool F16, bool SCORED>
+template <int D, bool E4M3, bool F16, int SCORE>
 cudaError_t launch_cached_d(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tks,
                             const CUtensorMap& tvs, CachedParams p, cudaStream_t s) {
-  using L = CachedLayout<D, E4M3, false>;
-  using LW = CachedLayout<D, E4M3, true>;
+  using L = CachedLayout<D, E4M3, false, SCORE != kScorePlain>;
+  using LW = CachedLayout<D, E4M3, true, SCORE != kScorePlain>;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static PerDeviceOnce smem_set;
   e = once_per_device(smem_set, dev, [] {
-    const cudaError_t e1 = cudaFuncSetAttribute(fa_cached_kernel<D, E4M3, F16, false, SCORED>,
+    const cudaError_t e1 = cudaFuncSetAttribute(fa_cached_kernel<D, E4M3, F16, false, SCORE>,
                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
     return e1 != cudaSuccess ? e1
-                             : cudaFuncSetAttribute(fa_cached_kernel<D, E4M3, F16, true, SCORED>,
+                             : cudaFuncSetAttribute(fa_cached_kernel<D, E4M3, F16, true, SCORE>,
                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, LW::kSmemBytes);
   });
   if (e != cudaSuccess) return e;
@@ -1155,7 +1174,7 @@ cudaError_t launch_cached_d(const CUtensorMap& tk, const CUtensorMap& tv, const 
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fa_cached_kernel<D, E4M3, F16, true, SCORED>, tk, tv, tks, tvs, p);
+    return cudaLaunchKernelEx(&cfg, fa_cached_kernel<D, E4M3, F16, true, SCORE>, tk, tv, tks, tvs, p);
   }
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
@@ -1163,7 +1182,7 @@ cudaError_t launch_cached_d(const CUtensorMap& tk, const CUtensorMap& tv, const 
   const double most = (double)p.B * p.Hk * p.RT * (((double)p.max_pages * p.page_size + L::kKT - 1) / L::kKT);
   int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   if (most < ctas) ctas = most < 1.0 ? 1 : (int)most;
-  e = launch_pdl(true, fa_cached_kernel<D, E4M3, F16, false, SCORED>, dim3((unsigned)ctas), dim3(32 * L::kWarps), L::kSmemBytes, s, tk, tv,
+  e = launch_pdl(true, fa_cached_kernel<D, E4M3, F16, false, SCORE>, dim3((unsigned)ctas), dim3(32 * L::kWarps), L::kSmemBytes, s, tk, tv,
                  tks, tvs, p);
   if (e != cudaSuccess) return e;
   const unsigned rows = (unsigned)(p.B * p.Hq * p.Nq);
@@ -1175,12 +1194,12 @@ cudaError_t launch_cached_d(const CUtensorMap& tk, const CUtensorMap& tv, const 
   return launch_pdl(true, fa_cached_join_kernel<D, F16, 1>, dim3((rows + 3) / 4), dim3(128), 0, s, p);
 }
 
-template <bool SCORED>
+template <int SCORE>
 cudaError_t launch_cached_score(bool e4m3, bool f16, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tks,
                                 const CUtensorMap& tvs, const CachedParams& p, cudaStream_t s) {
   const int D = p.d <= 64 ? 64 : 128;
 #define FA_CACHED_CASE(DD, EE, FF) \
-  if (D == DD && e4m3 == EE && f16 == FF) return launch_cached_d<DD, EE, FF, SCORED>(tk, tv, tks, tvs, p, s);
+  if (D == DD && e4m3 == EE && f16 == FF) return launch_cached_d<DD, EE, FF, SCORE>(tk, tv, tks, tvs, p, s);
   FA_CACHED_CASE(64, false, false)
   FA_CACHED_CASE(64, false, true)
   FA_CACHED_CASE(64, true, false)

@@ -1,0 +1,11 @@
+// The attention of the newest tokens against the cache (fa_cached.cuh), scores lowered with distance.
+#include "fa_cached.cuh"
+
+namespace fa {
+
+cudaError_t launch_cached_bias(bool e4m3, bool f16, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tks,
+                               const CUtensorMap& tvs, const CachedParams& p, cudaStream_t s) {
+  return launch_cached_score<kScoreBias>(e4m3, f16, tk, tv, tks, tvs, p, s);
+}
+
+}  // namespace fa

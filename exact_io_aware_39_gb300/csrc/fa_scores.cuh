@@ -22,6 +22,7 @@ struct ScoreParams {
   const int32_t* prefix;     // [B] or null
   float limit;               // |s| up to which the polynomial holds (kCapSmall / k), or -1: nowhere
   float a0, a1, a2, a3;      // there t2 = s (a0 + s^2 (a1 + s^2 (a2 + s^2 a3)))
+  float b0, b1, b2, b3;      // and tanh(k s) the same with these, a / c2
   float k, e2, c2;           // k; 2 k log2(e): exp(2 k s) = 2^(e2 s); c2
   int cap;
   int bounded;               // capped without a bias, at most kFreeRange
@@ -69,6 +70,10 @@ inline fa_status read_scores(const fa_scores* scores, float scale, int causal, b
     out->a1 = (float)(c2 * k * k * k * kTanh1);
     out->a2 = (float)(c2 * k * k * k * k * k * kTanh2);
     out->a3 = (float)(c2 * k * k * k * k * k * k * k * kTanh3);
+    out->b0 = (float)(k * kTanh0);
+    out->b1 = (float)(k * k * k * kTanh1);
+    out->b2 = (float)(k * k * k * k * k * kTanh2);
+    out->b3 = (float)(k * k * k * k * k * k * k * kTanh3);
   }
   return FA_OK;
 }
@@ -108,6 +113,13 @@ __device__ __forceinline__ float2 cap_small_factor2(float2 s, const ScoreParams&
 }
 __device__ __forceinline__ float2 cap_small2(float2 s, const ScoreParams& p) {
   return __fmul2_rn(s, cap_small_factor2(s, p));
+}
+// tanh(k s) of a pair of small scores
+__device__ __forceinline__ float2 tanh_small2(float2 s, const ScoreParams& p) {
+  const float2 z = __fmul2_rn(s, s);
+  float2 r = __ffma2_rn(z, make_float2(p.b3, p.b3), make_float2(p.b2, p.b2));
+  r = __ffma2_rn(z, r, make_float2(p.b1, p.b1));
+  return __fmul2_rn(s, __ffma2_rn(z, r, make_float2(p.b0, p.b0)));
 }
 // t2 of one score of any size: the polynomial where it holds
 __device__ __forceinline__ float cap_any(float s, const ScoreParams& p) {
