@@ -108,6 +108,11 @@ def _check_received(c, scale, kw, lse, past, got, lens=None):
     token hold what they held (7)."""
     r = _ref(c, scale, kw, lens, lse)
     table, Nq = c["table"].cpu().numpy(), c["q"].shape[1]
+    G = c["q"].shape[2] // got.shape[1]
+    # The rows are added to the past in blocks of 128: each block is one fp32 addition,
+    # off by at most 2^-24 of its result, past + what was received so far. The part of
+    # what was received is in tolW's Nq G + 2 roundings, that of the past is here.
+    adds = (Nq * G + 127) // 128
     got, past = _host(got), _host(past)
     page = got.shape[2]
     want, tol = np.full(got.shape, 7.0), np.zeros(got.shape)
@@ -119,7 +124,7 @@ def _check_received(c, scale, kw, lse, past, got, lens=None):
                 continue
             old = past[p, :, j % page] if past is not None and j < n - Nq else 0.0
             want[p, :, j % page] = W[:, j] + old
-            tol[p, :, j % page] = tW[:, j] + 2.0 ** -24 * np.abs(old) + 1e-37
+            tol[p, :, j % page] = tW[:, j] + adds * 2.0 ** -24 * np.abs(old) + 1e-37
     bad = np.abs(got - want) - tol
     assert bad.max() <= 0, f"off by {np.abs(got - want).max():.3g}, {bad.max():.3g} over the bound"
 
@@ -204,6 +209,55 @@ def test_received_on_streams_and_in_replayed_graphs(fa):  # noqa: F811
         _settled(fa)
         _check(c, 0.1, kw, o, lse, lens)
         _check_received(c, 0.1, kw, lse, past, w, lens)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "bf16_e4m3", "fp16_e4m3"])
+@pytest.mark.parametrize("spread", [3, 15])
+@pytest.mark.parametrize("softcap,bias", [(0.0, False), (15.0, True)])
+def test_received_by_rows_of_all_sizes(fa, softcap, bias, spread, kind):  # noqa: F811
+    """Queries of up to 2^spread times one another's size, some of them zeros."""
+    dtype = BF if kind.startswith("bf16") else FH
+    c = _case(3, 45, 8, 2, 128, 64, [700, 50, 20], dtype, kind.endswith("e4m3"))
+    g = torch.Generator().manual_seed(3)
+    size = torch.exp2(-torch.randint(0, spread + 1, (3, 45, 8, 1), generator=g).float())
+    size[:, 7] = 0.0
+    c["q"] = (c["q"].cpu() * size.to(dtype)).cuda()
+    kw = _kw(8, softcap, bias)
+    _, lse = _run(fa, c, 0.2, kw)
+    past = torch.rand(c["k"].shape[:3], device="cuda")
+    got = _received(fa, c, 0.2, kw, lse, past, torch.full(c["k"].shape[:3], 7.0, device="cuda"))
+    _settled(fa)
+    _check_received(c, 0.2, kw, lse, past, got)
+
+
+@pytest.mark.parametrize("Nq", [1, 5])
+def test_received_by_a_key_with_an_infinite_element(fa, Nq):  # noqa: F811
+    """Its scores are -inf: it receives nothing, the others what they did."""
+    c = _case(1, Nq, 4, 1, 64, 16, [40], BF, False)
+    c["q"][..., 0] = -1.0
+    page, at = int(c["table"][0, 1]), 3
+    c["k"][page, 0, at, 0] = float("inf")
+    _, lse = _run(fa, c, 0.2, {})
+    got = _received(fa, c, 0.2, {}, lse, None, torch.full(c["k"].shape[:3], 7.0, device="cuda"))
+    _settled(fa)
+    assert float(got[page, 0, at]) == 0.0
+    assert abs(float(got[got != 7.0].sum()) - 4 * Nq) < 1e-4
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_wait_of_many_rows_runs_out(fa, e4m3):  # noqa: F811
+    c = _case(2, 40, 8, 2, 128, 16, [90000, 70000], BF, e4m3)
+    _, lse = _run(fa, c, 0.1, {})
+    w = [torch.zeros(c["k"].shape[:3], device="cuda") for _ in range(2)]
+    _received(fa, c, 0.1, {}, lse, None, w[0])
+    _settled(fa)
+    _received(fa, c, 0.1, {}, lse, None, w[1], wait_limit_us=20000, test_stall=1)
+    torch.cuda.synchronize()
+    st, detail = fa.device_error()
+    assert st == 5 and 213 <= detail[1] <= 218, detail
+    _received(fa, c, 0.1, {}, lse, None, w[1])
+    _settled(fa)
+    assert torch.equal(_bits(w[0]), _bits(w[1]))
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
