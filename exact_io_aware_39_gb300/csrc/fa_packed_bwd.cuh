@@ -150,7 +150,7 @@ __device__ __forceinline__ void score_p(float (&x)[kC], uint32_t (&pk)[kC / 2], 
     // Without a bias, and all scores of the warp within the polynomial's limit: in one
     // piece, its products beside the exponentials. (One exponential and half a
     // reciprocal a score less: two sequences of 4547 and 5127 tokens, 32 / 8 heads,
-    // d = 128, with the pass over D in one piece too, 1885 -> 1669 us with gradients.)
+    // d = 128, 1885 -> 1669 us with gradients.)
     float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < kC; c += 2) top[(c >> 1) & 3] = fmax3(top[(c >> 1) & 3], fabsf(x[c]), fabsf(x[c + 1]));

@@ -345,32 +345,48 @@ fa_packed_dots_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
         const int lim = (w.causal ? min(max(row + 1, w.pre), w.len) : w.len) - kTile * e - 64 * h;
         const ScoreTile st = score_tile<SCORE>(p.score, slope2, kTile * e + 64 * h, row, e < qi ? -1 : e > qi ? 1 : 0,
                                                e == qi && (!w.causal || w.pre > kTile * e), partial, lim);
-        score_args<SCORE, false>(u, p.score, p.scale_log2, st, -lse2);
+        // Capped scores that are all within the polynomial's limit, without a bias or a mask, stay as they are
+        // until the exponential: the polynomial beside it. (Two sequences of 4547 and 5127 tokens, 32 / 8 heads,
+        // d = 128, forward and backward: 1669 -> 1640 us.)
+        bool fast = false;
+        if constexpr (SCORE == kScoreCap) {
+          const bool small = cap_vote(u, p.score, partial, lim);
+          fast = small && !partial && !st.bias;
+          if (!fast) {
+            cap_args(u[0], p.score, partial, lim, small, -lse2);
+            cap_args(u[1], p.score, partial, lim - 32, small, -lse2);
+            if (st.bias) bias_args<SCORE>(u, p.scale_log2, st, -lse2);
+          }
+        } else {
+          score_args<SCORE, false>(u, p.score, p.scale_log2, st, -lse2);
+        }
         if (!(ok = bar_wait_warp(bar(L::bPFull + t), n & 1u, ctl, 395))) break;
         tc_fence_after();
+        auto add = [&](auto polynomial) {
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < 4; ++c) {
             uint32_t v[16];
-            tmem_ld16(tP + 32u * hh + 16u * c, v);
-            if (hh + c == 2) {
+            tmem_ld16(tP + 16u * c, v);
+            if (c == 3) {
               tc_fence_before();
               mbar_arrive_warp(bar(L::bPFree + t));
             }
-            if (partial) {   // (what lies past the sequence may be NaN)
+            if (!polynomial && partial) {   // (what lies past the sequence may be NaN)
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                if (32 * hh + 16 * c + i >= lim) v[i] = 0u;
+                if (16 * c + i >= lim) v[i] = 0u;
             }
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
-              const float2 a = pair_of(u[hh], 16 * c + i);
+              float2 a = pair_of(u[c >> 1], 16 * (c & 1) + i);
+              if (polynomial) a = __ffma2_rn(a, cap_small_factor2(a, p.score), make_float2(-lse2, -lse2));
               sum[(i >> 1) & 3] = __ffma2_rn(make_float2(ex2(a.x), ex2(a.y)),
                                              make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sum[(i >> 1) & 3]);
             }
           }
-        }
+        };
+        if (fast) add(std::true_type{});
+        else add(std::false_type{});
       }
       const float2 s = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
       ex[kTile * h] = s.x + s.y;

@@ -168,6 +168,29 @@ __device__ __forceinline__ void cap_args(uint32_t (&u)[32], const ScoreParams& s
   if (partial) mask_columns(u, lim, -INFINITY);
 }
 
+// Adds the bias to 64 scores: raw ones (to which sl2 and nref go as well), or capped
+// ones, which are complete but for it.
+template <int SCORE>
+__device__ __forceinline__ void bias_args(uint32_t (&u)[2][32], float sl2, const ScoreTile& s, float nref) {
+  const float mul = SCORE == kScoreCap ? 1.f : sl2, start = SCORE == kScoreCap ? 0.f : nref;
+#pragma unroll
+  for (int hh = 0; hh < 2; ++hh) {
+    if (s.linear) {
+      BiasSteps b(s, 32 * hh, start);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2)
+        put_pair(u[hh], i, __ffma2_rn(pair_of(u[hh], i), make_float2(mul, mul), b.next((i >> 1) & 3)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float d = s.far + (float)(32 * hh + i);
+        const float2 x = __ffma2_rn(pair_of(u[hh], i), make_float2(mul, mul), make_float2(start, start));
+        put_pair(u[hh], i, make_float2(fmaf(-s.slope, fabsf(d), x.x), fmaf(-s.slope, fabsf(d + 1.f), x.y)));
+      }
+    }
+  }
+}
+
 // The arguments of the exponential, u2 + nref in log2 units, from a row's 64 raw
 // scores; -inf where masked. Returns their maximum (MAX).
 template <int SCORE, bool MAX>
@@ -181,25 +204,7 @@ __device__ __forceinline__ float score_args(uint32_t (&u)[2][32], const ScorePar
     mask_columns(u[0], s.lim, -INFINITY);
     mask_columns(u[1], s.lim - 32, -INFINITY);
   }
-  if (SCORE == kScoreBias || s.bias) {
-    const float mul = SCORE == kScoreCap ? 1.f : sl2, start = SCORE == kScoreCap ? 0.f : nref;
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      if (s.linear) {
-        BiasSteps b(s, 32 * hh, start);
-#pragma unroll
-        for (int i = 0; i < 32; i += 2)
-          put_pair(u[hh], i, __ffma2_rn(pair_of(u[hh], i), make_float2(mul, mul), b.next((i >> 1) & 3)));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float d = s.far + (float)(32 * hh + i);
-          const float2 x = __ffma2_rn(pair_of(u[hh], i), make_float2(mul, mul), make_float2(start, start));
-          put_pair(u[hh], i, make_float2(fmaf(-s.slope, fabsf(d), x.x), fmaf(-s.slope, fabsf(d + 1.f), x.y)));
-        }
-      }
-    }
-  }
+  if (SCORE == kScoreBias || s.bias) bias_args<SCORE>(u, sl2, s, nref);
   if (!MAX) return 0.f;
   float hi[4];
 #pragma unroll

@@ -94,8 +94,8 @@ fa_status flash_attn_cached_scored_fwd(const void* Q, int64_t q_token_stride, co
  *   past    : in, fp32 [num_pages, Hk, page_size], or NULL
  *   weights : out, the same; may be past itself. Places of no token are left as
  *             they were, as are those of pages outside the cache.
- *   Both 8-byte aligned. A page belongs to one sequence of the call: of two that
- *   share it, either's sums remain.
+ *   Both 8-byte aligned. A page belongs to one sequence of the call: what is left
+ *   in one that two share, or that stands twice in a table, is unspecified.
  *   No workspace. Results do not change from call to call. Of the options dtype,
  *   wait_limit_us and test_stall are used, as in flash_attn_cached_fwd.
  */
