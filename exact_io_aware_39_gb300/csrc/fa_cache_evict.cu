@@ -313,10 +313,13 @@ __global__ void __launch_bounds__(kCopyThreads, 4) evict_copy_kernel(const Evict
 
 // CTAs to a (sequence, head) of at most `tokens` tokens: more while the card has room
 // for them all at once (15 clusters of 8, 36 of 4, 76 of 2: a cluster lives within
-// one group of SMs) and each has 2048 tokens.
+// one group of SMs) and each has 2048 tokens. Eight only where four cannot hold the
+// weights: adding up eight histograms costs what the smaller shares gain. (8 heads,
+// d = 64, to a 64th, in clusters of 8, 4, 2 and 1: one sequence of 65536 tokens 39,
+// 36, 46 and 263 us, of 16384 34, 25, 26 and 30; 16 sequences of 8192 23 in all.)
 int select_cluster(long long units, long long tokens) {
   const auto most = [](int c) -> long long { return c == 8 ? 15 : c == 4 ? 36 : c == 2 ? 76 : 1ll << 40; };
-  int c = kMaxCluster;
+  int c = tokens > 4ll * kMaxKeys ? kMaxCluster : 4;
   while (c > 1 && (units > most(c) || tokens < 2048ll * c)) c /= 2;
   return c;
 }

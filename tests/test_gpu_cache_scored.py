@@ -391,6 +391,16 @@ def test_evict_of_a_long_sequence(fa):  # noqa: F811
     _check_evict(c, before, new_lens, kept, 20000, 1000)
 
 
+@pytest.mark.parametrize("lens", [[170000, 3000], [350000]])
+def test_evict_of_sequences_that_many_blocks_share(fa, lens):  # noqa: F811
+    """More weights than four blocks (eight blocks) keep in shared memory."""
+    c = _evict_case(lens, 1, 16, 256, BF, False, 20000, True, seed=7)
+    before = {n: None if x is None else x.clone() for n, x in c.items() if n != "page"}
+    new_lens, kept = _evict(fa, c, 20000, 1000)
+    _settled(fa)
+    _check_evict(c, before, new_lens, kept, 20000, 1000)
+
+
 def test_evict_offsets_past_32_bits(fa):  # noqa: F811
     """A cache of more than 2^31 elements whose last pages are read and written."""
     Hk, d, page, pages = 8, 128, 64, 36000
