@@ -12,6 +12,8 @@
 // and its place in the ring is loaded again; the weights are summed over the rows
 // in fp32 in a fixed order, and each key's sum is written by one lane, so results
 // repeat. More than 16 query rows go to a kernel of their own (below).
+// (64 sequences of 144891 tokens in all, 32 / 8 heads, d = 128, bf16, capped scores:
+// 57 us, 5.3 TB/s of 6.8.)
 //
 // The 16 bytes a lane reads of a key are 8 neighbouring dims (16 in e4m3), which
 // it spreads over two (four) K steps of the product; the queries are read in the

@@ -109,7 +109,7 @@ struct CachedLayout {
   // 64 sequences of 151070 tokens in all at d = 64 39 us so and 42 without; at d =
   // 128, with 32 keys, the step through memory costs more than it saves (the 16
   // sequences 164 and 161 us), but for scores of their own, which have more to do
-  // beside the loads (lowered with distance 176 us so and 187).
+  // beside the loads (lowered with distance, inputs not in L2, 191 us so and 196).
   static constexpr bool kByKey = E4M3 && (kKT == 64 || SCORED);
   static constexpr int kFactorBytes = kByKey ? 12 * kKT : 0;
   static constexpr int kFactors = kScale + kWarps * kStages * 2 * kScaleBytes;

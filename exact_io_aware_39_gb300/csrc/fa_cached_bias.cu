@@ -1,4 +1,5 @@
 // The attention of the newest tokens against the cache (fa_cached.cuh), scores lowered with distance.
+// (16 sequences of 485214 tokens in all, 32 / 8 heads, d = 128, e4m3: 168 us, plain scores 161.)
 #include "fa_cached.cuh"
 
 namespace fa {

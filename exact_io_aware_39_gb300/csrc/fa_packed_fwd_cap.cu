@@ -1,4 +1,5 @@
 // The packed forward (fa_packed_fwd.cuh) of scores capped by a tanh (and lowered with distance, where there are slopes).
+// (Two sequences of 4547 and 5127 tokens, 32 / 8 heads, d = 128, bf16: 321 us, 1.20 PFLOP/s; plain scores 242.)
 #include "fa_packed_fwd.cuh"
 
 namespace fa {
