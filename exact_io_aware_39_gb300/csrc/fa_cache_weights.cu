@@ -90,11 +90,10 @@ __device__ __forceinline__ void add_weights(float (&sum)[NT][2], const float (&x
       for (int c = 0; c < 2; ++c) u[n][c] = cap_any(u[n][c], sp);
   }
   if (sp.slopes != nullptr) {   // (keys past the row's place are masked)
-    const float b0 = -slope2 * far;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) u[n][c] += fmaf(slope2, (float)(8 * n + c), b0);
+      for (int c = 0; c < 2; ++c) u[n][c] = fmaf(-slope2, far - (float)(8 * n + c), u[n][c]);
   }
   if (masked) {
 #pragma unroll

@@ -578,15 +578,15 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
     // are masked below.) Their arithmetic shows beside the loads, so it is left out
     // for rows 8-15 of a unit that has none.
     const bool upper = !SCORED || p.R - rt * kRows > 8;
-    [[maybe_unused]] float bias0[2] = {0.f, 0.f};
+    [[maybe_unused]] float far[2] = {0.f, 0.f};
     if constexpr (SCORED)
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh)
-        bias0[hh] = -slope2[hh] * (float)(left - p.Nq + (rt * kRows + g + 8 * hh) / p.G - 2 * t4);
+        far[hh] = (float)(left - p.Nq + (rt * kRows + g + 8 * hh) / p.G - 2 * t4);
     // a capped product in log2 units, or one that is already, less its bias
     [[maybe_unused]] auto score2 = [&](float s, int hh, int key) -> float {
       const float u = SCORE == kScoreCap ? cap_any(s, p.score) : s;
-      return u + fmaf(slope2[hh], (float)key, bias0[hh]);
+      return fmaf(-slope2[hh], far[hh] - (float)key, u);   // (the distance is exact: near keys of steep slopes keep theirs)
     };
     // scores in log2 units; with e4m3 plus log2 of the value's scale
     float ivs[KT / 8][2];

@@ -111,7 +111,8 @@ def _check_received(c, scale, kw, lse, past, got, lens=None):
     G = c["q"].shape[2] // got.shape[1]
     # The rows are added to the past in blocks of 128: each block is one fp32 addition,
     # off by at most 2^-24 of its result, past + what was received so far. The part of
-    # what was received is in tolW's Nq G + 2 roundings, that of the past is here.
+    # what was received is in tolW's Nq G + 2 roundings, that of the past is here. Each
+    # of the Nq G weights counts as 0 below 2^-126, fp32's smallest normal number.
     adds = (Nq * G + 127) // 128
     got, past = _host(got), _host(past)
     page = got.shape[2]
@@ -124,7 +125,7 @@ def _check_received(c, scale, kw, lse, past, got, lens=None):
                 continue
             old = past[p, :, j % page] if past is not None and j < n - Nq else 0.0
             want[p, :, j % page] = W[:, j] + old
-            tol[p, :, j % page] = tW[:, j] + adds * 2.0 ** -24 * np.abs(old) + 1e-37
+            tol[p, :, j % page] = tW[:, j] + adds * 2.0 ** -24 * np.abs(old) + Nq * G * 2.0 ** -126
     bad = np.abs(got - want) - tol
     assert bad.max() <= 0, f"off by {np.abs(got - want).max():.3g}, {bad.max():.3g} over the bound"
 
@@ -148,6 +149,47 @@ def test_received_weights(fa, B, Nq, Hq, Hk, d, page, lens, softcap, bias, qmul,
     _settled(fa)
     at = got != 7.0
     assert torch.equal(again[at], got[at]) and torch.equal(again[~at], past[~at])
+
+
+@pytest.mark.parametrize("Nq", [1, 4, 20])
+@pytest.mark.parametrize("kind", ["bf16", "fp16_e4m3"])
+@pytest.mark.parametrize("softcap", [0.0, 12.0])
+def test_slopes_of_any_sign(fa, softcap, kind, Nq):  # noqa: F811
+    dtype = BF if kind == "bf16" else FH
+    for room in (0, 1 << 17):
+        c = _case(3, Nq, 4, 2, 128, 32, [2500, 900, 40], dtype, kind.endswith("e4m3"), seed=4, room=room)
+        kw = dict(softcap=softcap, slopes=torch.tensor([0.0, -0.05, 4.0, -4.0], device="cuda"))
+        o, lse = _run(fa, c, 0.1, kw)
+        _settled(fa)
+        _check(c, 0.1, kw, o, lse)
+        got = _received(fa, c, 0.1, kw, lse, None, torch.full(c["k"].shape[:3], 7.0, device="cuda"))
+        _settled(fa)
+        _check_received(c, 0.1, kw, lse, None, got)
+
+
+@pytest.mark.parametrize("Nq", [1, 9])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_pages_past_32_bits(fa, e4m3, Nq):  # noqa: F811
+    """The last pages of caches of more than 2^31 elements (e4m3: bytes), and the
+    same tokens in small caches: the same bits."""
+    c = _case(2, Nq, 16, 8, 128, 64, [300, 130], BF, e4m3, spare=0)
+    n, pages = c["k"].shape[0], 36000
+    big = dict(c)
+    for name in ("k", "v", "ks", "vs"):
+        if c[name] is not None:
+            big[name] = torch.empty((pages,) + c[name].shape[1:], dtype=c[name].dtype, device="cuda")
+            _bits(big[name]).zero_()[pages - n:] = _bits(c[name])
+    big["table"] = torch.where(c["table"] < n, c["table"] + (pages - n), c["table"])
+    kw = _kw(16, 20.0, True)
+    (o, lse), (o2, lse2) = _run(fa, c, 0.1, kw), _run(fa, big, 0.1, kw)
+    past = torch.rand(c["k"].shape[:3], device="cuda")
+    w = _received(fa, c, 0.1, kw, lse, past, torch.full(past.shape, 7.0, device="cuda"))
+    past2 = torch.zeros((pages,) + past.shape[1:], device="cuda")
+    past2[pages - n:] = past
+    w2 = _received(fa, big, 0.1, kw, lse, past2, torch.full(past2.shape, 7.0, device="cuda"))
+    _settled(fa)
+    assert torch.equal(_bits(o), _bits(o2)) and torch.equal(_bits(lse), _bits(lse2))
+    assert torch.equal(w2[pages - n:], w) and bool((w2[:pages - n] == 7.0).all())
 
 
 @pytest.mark.parametrize("e4m3", [False, True])

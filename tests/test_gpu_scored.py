@@ -238,3 +238,34 @@ def test_helpers_refuse_what_does_not_fit(fa):  # noqa: F811
     bad(prefix_lens=kw["prefix_lens"][:1])
     bad(causal=False)
     _settled(fa)
+
+
+@pytest.mark.parametrize("softcap", [0.0, 40.0])
+def test_slopes_over_long_distances(fa, softcap):  # noqa: F811
+    """A row's keys differ by thousands in either direction, so that its maximum
+    moves from tile to tile, or lies in the first one."""
+    c = _inputs([1500, 700], 4, 2, 128, FH, 12)
+    kw = dict(softcap=softcap, slopes=torch.tensor([6.0, -6.0, 0.3, -0.3], device="cuda"))
+    for causal in (True, False):
+        r = _run(fa, c, 0.09, causal, kw)
+        _settled(fa)
+        _check(c, r, 0.09, causal, kw)
+
+
+def test_offsets_past_32_bits(fa):  # noqa: F811
+    """The sequences are the last rows of tensors of more than 2^31 elements."""
+    Hq, Hk, d, T = 64, 2, 128, 263000
+    small = _inputs([150, 290], Hq, Hk, d, BF, 13)
+    n = 440
+    kw = _score_args([150, 290], Hq, 30.0, True, True)
+    big = {k: torch.zeros((T,) + small[k].shape[1:], dtype=BF, device="cuda") for k in ("q", "k", "v", "do")}
+    for k, x in big.items():
+        x[T - n:] = small[k]
+    big["cu"] = small["cu"] + (T - n)
+    out = dict(o=torch.zeros_like(big["q"]), dq=torch.zeros_like(big["q"]), dk=torch.zeros_like(big["k"]),
+               dv=torch.zeros_like(big["k"]), lse=torch.zeros(Hq, T, device="cuda"))
+    _run(fa, big, 0.09, True, kw, out=out)
+    _settled(fa)
+    got = {k: (x[:, T - n:] if k == "lse" else x[T - n:]) for k, x in out.items()}
+    _check(small, got, 0.09, True, kw)
+    assert not out["o"][:T - n].any() and not out["dq"][:T - n].any() and not out["dk"][:T - n].any()
