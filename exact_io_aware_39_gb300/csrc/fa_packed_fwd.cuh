@@ -191,7 +191,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     w.len = __shfl_sync(0xFFFFFFFFu, ring[4 * rs + 1], 0);
     w.c = __shfl_sync(0xFFFFFFFFu, ring[4 * rs + 2], 0);
     w.head = __shfl_sync(0xFFFFFFFFu, ring[4 * rs + 3], 0);
-    w.finish(p.pair_heads != 0, p.causal != 0);
+    w.finish(p.pair_heads != 0, p.causal != 0, PRE && p.score.slopes != nullptr);
     mbar_arrive_warp(bar(L::bItemEmpty + rs));
     return true;
   };
@@ -260,7 +260,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         if (PRE && direct) w.c = with_prefix(pi.c, dl.prefix);
         ring_c = w.c;
         w.head = head;
-        w.finish(p.pair_heads != 0, p.causal != 0);
+        w.finish(p.pair_heads != 0, p.causal != 0, PRE && p.score.slopes != nullptr);
       }
       if (lane == 0) {
         ring[4 * rs] = w.start;
@@ -290,7 +290,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         mbar_arrive_expect_tx_w(bar(L::bKFull + sk), L::kTileBytes);
         for (int a = 0; a < L::kHalves; ++a)
           tma_load_3d_w(sbase + L::kK + sk * L::kTileBytes + a * 16384, &tk, bar(L::bKFull + sk), 64 * a, hk,
-                        w.start + kTile * e);
+                        w.start + kTile * w.tile(e));
         ++nk;
         // the item's Q tiles behind its first K, which seldom waits; a tile's
         // buffer is free once the last S of the item before has read it
@@ -342,7 +342,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         mbar_arrive_expect_tx_w(bar(L::bVFull + sv), L::kTileBytes);
         for (int a = 0; a < L::kHalves; ++a)
           tma_load_3d_w(sbase + L::kV + sv * L::kTileBytes + a * 16384, &tv, bar(L::bVFull + sv), 64 * a, hk,
-                        w.start + kTile * e);
+                        w.start + kTile * w.tile(e));
         ++nv;
       }
     }
@@ -393,6 +393,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       more = w.c >= 0;
       const int n = more ? w.n : 0;
       const int tail = w.tail();
+      const int tail_e = w.tile(w.nT - 1);   // the entry of the sequence's last key tile (tile() is its own inverse)
       const int last[2] = {w.last(0), w.has(1) ? w.last(1) : -1};   // t is live at entries 0 .. last
       // Q_t of this item: its buffer and phase
       auto q_slot = [&](int t) -> int { return t * L::kQBuf + nq[t] % L::kQBuf; };
@@ -468,7 +469,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           pend[t] = nv;
           pfirst[t] = e == w.first(t);
           plast[t] = e == last[t];
-          ptail[t] = e == w.nT - 1 ? tail : 0;
+          ptail[t] = e == tail_e ? tail : 0;
         };
         auto on = [](int t) -> bool { return kWhich == 2 || t == kWhich; };
         if constexpr (L::kSharedS) {
@@ -550,7 +551,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     const float sl2 = p.scale_log2;
     const bool bounded = SCORE == kScoreCap && !F16 && p.score.bounded;
     // (P in fp16 ends at 2^16; moves stop all rows of a tile, so they are rare here)
-    constexpr float kMove = F16 ? 14.f : 30.f;
+    constexpr float kMove = F16 ? 14.f : 30.f, kFar = 4.f;
     volatile float* ex = reinterpret_cast<volatile float*>(smem + L::kEx) + r;   // [query tile][half][128]
     uint32_t nS = 0u, nO = 0u;               // S tiles and final O read by this group
     uint32_t nJ = 0u;                        // SPLIT: items of two groups so far
@@ -565,8 +566,9 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       const float slope2 = p.score.slopes != nullptr ? p.score.slopes[w.hq(t)] * 1.4426950408889634f : 0.f;
       float m_ref = 0.f;
       float l = 0.f;
-      for (int e = w.first(t); e <= last; e += SPLIT ? 2 : 1) {
-        const bool begin = e == w.first(t);
+      for (int i = w.first(t); i <= last; i += SPLIT ? 2 : 1) {
+        const bool begin = i == w.first(t);
+        const int e = w.tile(i);
         ok = ok && bar_wait_warp(bar(L::bSFull + t), nS & 1u, ctl, 320 + t);
         tc_fence_after();
         uint32_t u[2][32];
@@ -623,10 +625,10 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
                                                  e == qi && (!w.causal || w.pre > kTile * e), partial, lim);
           // The exponents against the row's reference as it is, which moves only where
           // one passes it by more than the threshold, and in an item's first tile. (Where
-          // the tile's largest bias lies above it, against that: from a reference that
-          // is far below, they would be rounded in its units.)
+          // the tile's largest bias lies kFar above it, against that: from a reference
+          // that is far below, they would be rounded in its units.)
           const float above = score_base(p.score, slope2, kTile * e, row, e < qi ? -1 : e > qi ? 1 : 0);
-          const float base = begin ? (above > -INFINITY ? above : 0.f) : fmaxf(m_ref, above);
+          const float base = begin ? (above > -INFINITY ? above : 0.f) : above > m_ref + kFar ? above : m_ref;
           const float mx = score_args<SCORE, true>(u, p.score, sl2, st, -base);
           if (!group_all(pair_bar, 256u, ok && !begin && base <= m_ref && mx <= kMove)) {
             // (the first group has read O_1 and what goes with it of the item before)
@@ -638,7 +640,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
             tc_fence_after();
             const float top = fmaxf(mx, ex[kTile * (2 * t + (h ^ 1))]);
             const float up = begin ? 0.f : base - m_ref;
-            const bool move = begin || top + up > kMove;
+            const bool move = begin || top + up > (up > 0.f ? 0.f : kMove);
             float alpha = 1.f, shift = up;
             if (move) {
               const float by = top > -INFINITY ? top : 0.f;   // (0: nothing to move to)
