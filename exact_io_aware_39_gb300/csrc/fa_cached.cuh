@@ -584,8 +584,8 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
       for (int hh = 0; hh < 2; ++hh)
         far[hh] = (float)(left - p.Nq + (rt * kRows + g + 8 * hh) / p.G - 2 * t4);
     // a capped product in log2 units, or one that is already, less its bias
-    [[maybe_unused]] auto score2 = [&](float s, int hh, int key) -> float {
-      const float u = SCORE == kScoreCap ? cap_any(s, p.score) : s;
+    [[maybe_unused]] auto score2 = [&](float s, int hh, int key, float mul = 1.f, float add = 0.f) -> float {
+      const float u = SCORE == kScoreCap ? cap_any(s * mul, p.score) + add : fmaf(s, mul, add);
       return fmaf(-slope2[hh], far[hh] - (float)key, u);   // (the distance is exact: near keys of steep slopes keep theirs)
     };
     // scores in log2 units; with e4m3 plus log2 of the value's scale
@@ -628,11 +628,11 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
           fa = make_float4(ks2.x * mul, ks2.y * mul, __log2f(vs2[n].x), __log2f(vs2[n].y));
         }
         if constexpr (SCORED) {
-          sc[n][0] = score2(sc[n][0] * qs[0] * fa.x, 0, 8 * n) + fa.z;
-          sc[n][1] = score2(sc[n][1] * qs[0] * fa.y, 0, 8 * n + 1) + fa.w;
+          sc[n][0] = score2(sc[n][0] * qs[0], 0, 8 * n, fa.x, fa.z);
+          sc[n][1] = score2(sc[n][1] * qs[0], 0, 8 * n + 1, fa.y, fa.w);
           if (upper) {
-            sc[n][2] = score2(sc[n][2] * qs[1] * fa.x, 1, 8 * n) + fa.z;
-            sc[n][3] = score2(sc[n][3] * qs[1] * fa.y, 1, 8 * n + 1) + fa.w;
+            sc[n][2] = score2(sc[n][2] * qs[1], 1, 8 * n, fa.x, fa.z);
+            sc[n][3] = score2(sc[n][3] * qs[1], 1, 8 * n + 1, fa.y, fa.w);
           }
           continue;
         }
@@ -648,7 +648,7 @@ fa_cached_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__
         for (int i = 0; i < 4; ++i) {
           if constexpr (!SCORED) sc[n][i] *= p.scale_log2;
           else if (i < 2 || upper)
-            sc[n][i] = score2(SCORE == kScoreCap ? sc[n][i] : sc[n][i] * p.scale_log2, i >> 1, 8 * n + (i & 1));
+            sc[n][i] = score2(sc[n][i], i >> 1, 8 * n + (i & 1), SCORE == kScoreCap ? 1.f : p.scale_log2);
         }
     }
     if (left - (p.Nq - 1) < KT) {

@@ -55,7 +55,8 @@ typedef struct {
  * layout, strides, workspace (flash_attn_packed_workspace_size), options and
  * errors as there. The backward's scores must be the forward's. It forms D_i as
  * the sum over j of P_ij dP_ij (where a row has few keys of weight, the rounding
- * of O would show in dQ and dK) and does not read O.
+ * of O would show in dQ and dK) and does not read O. (Scores without a cap, slopes
+ * and prefix_lens are plain ones: the calls of flash_attn_packed.h, which read it.)
  */
 fa_status flash_attn_packed_scored_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE,
                                        const int32_t* cu_seqlens, int B, int total, int Hq, int Hk, int d,
