@@ -253,6 +253,19 @@ def test_received_on_streams_and_in_replayed_graphs(fa):  # noqa: F811
         _check_received(c, 0.1, kw, lse, past, w, lens)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_received_of_many_sequences_and_rows(fa, e4m3):  # noqa: F811
+    """As above, with the kernel of many rows: a range has many sequences of one tile."""
+    lens = [max(0, (7 * b) % 45 - 6) for b in range(1500)]
+    c = _case(1500, 5, 8, 2, 64, 16, lens, BF, e4m3)
+    _, lse = _run(fa, c, 0.125, {})
+    got = _received(fa, c, 0.125, {}, lse, None, torch.full(c["k"].shape[:3], 7.0, device="cuda"))
+    _settled(fa)
+    _check_received(c, 0.125, {}, lse, None, got)
+    rows = 8 * sum(min(n, 5) for n in lens)   # (tokens before the first see nothing)
+    assert abs(float(got[got != 7.0].double().sum()) - rows) < 1e-5 * rows
+
+
 @pytest.mark.parametrize("kind", ["bf16", "bf16_e4m3", "fp16_e4m3"])
 @pytest.mark.parametrize("spread", [3, 15])
 @pytest.mark.parametrize("softcap,bias", [(0.0, False), (15.0, True)])
