@@ -717,7 +717,9 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           m_ref = M;
         }
       }
-      const float inv_l = 1.f / l;
+      // (bounded: the one weight of a row of one key is no 1, so its O is divided by the weight as rounded)
+      const bool alone = bounded && (w.causal ? min(max(row + 1, w.pre), w.len) : w.len) == 1;
+      const float inv_l = 1.f / (alone ? unpack2<F16>(pack2<F16>(l, l)).x : l);
       const int s4 = lane & 3;
       const int row0 = kTile * qi + 32 * (warp & 3) + (lane & ~3);   // the quad's first row
       uint16_t* op = p.o + (int64_t)(w.start + row0) * p.o_tok + w.hq(t) * p.o_head + 8 * s4;

@@ -269,3 +269,17 @@ def test_offsets_past_32_bits(fa):  # noqa: F811
     got = {k: (x[:, T - n:] if k == "lse" else x[T - n:]) for k, x in out.items()}
     _check(small, got, 0.09, True, kw)
     assert not out["o"][:T - n].any() and not out["dq"][:T - n].any() and not out["dk"][:T - n].any()
+
+
+@pytest.mark.parametrize("dtype", [BF, FH], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("softcap,bias", [(0.5, False), (30.0, False), (50.0, False), (0.0, True), (20.0, True)])
+def test_a_row_of_one_key_has_its_value(fa, softcap, bias, dtype):  # noqa: F811
+    """Its weight is one, whatever the score: O is V, bit for bit."""
+    lens = [1, 1, 5, 1, 300, 1]
+    for qmul in (1.0, 40.0):
+        c = _inputs(lens, 6, 2, 64, dtype, 14, qmul=qmul)
+        kw = _score_args(lens, 6, softcap, bias, False)
+        r = _run(fa, c, 0.125, True, kw)
+        _settled(fa)
+        first = c["cu"][:-1].long()
+        assert torch.equal(r["o"][first], c["v"][first].repeat_interleave(3, dim=1))
