@@ -150,7 +150,9 @@ __device__ __forceinline__ void score_p(float (&x)[kC], uint32_t (&pk)[kC / 2], 
     // Without a bias, and all scores of the warp within the polynomial's limit: in one
     // piece, its products beside the exponentials. (One exponential and half a
     // reciprocal a score less: two sequences of 4547 and 5127 tokens, 32 / 8 heads,
-    // d = 128, 1885 -> 1669 us with gradients.)
+    // d = 128, 1885 -> 1669 us with gradients.) A pair is two queries: a NaN score of one
+    // stays out of the other's; where the one sees the key, its LSE is NaN and brings the
+    // NaN back.
     float top[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < kC; c += 2) top[(c >> 1) & 3] = fmax3(top[(c >> 1) & 3], fabsf(x[c]), fabsf(x[c + 1]));
@@ -172,7 +174,7 @@ __device__ __forceinline__ void score_p(float (&x)[kC], uint32_t (&pk)[kC / 2], 
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < kC; c += 2) pair(c, tanh_exp2(make_float2(x[c], x[c + 1]), sp), added(c));
+      for (int c = 0; c < kC; c += 2) pair(c, tanh_exp2<true>(make_float2(x[c], x[c + 1]), sp), added(c));
     }
   } else {
 #pragma unroll

@@ -91,15 +91,18 @@ __device__ __forceinline__ float tanh_exp(float s, const ScoreParams& p) {
   return fmaf(-2.f, rcp_approx(1.f + ex2(s * p.e2)), 1.f);
 }
 // the same for a pair, whose denominators share a reciprocal: 1 / a = b / (a b).
-// The exponents are held to 60, where tanh is 1 in fp32, so that a b is finite
-// (a NaN stays one, and makes its neighbour one).
+// The exponents are held to 60, where tanh is 1 in fp32, so that a b is finite.
+// A NaN stays one, and makes its neighbour one: for a pair of one row, which has a
+// NaN then in any case. APART: for a pair of two rows; a NaN counts as 60.
 __device__ __forceinline__ float min_nan(float a, float b) {
   float y;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
+template <bool APART = false>
 __device__ __forceinline__ float2 tanh_exp2(float2 s, const ScoreParams& p) {
-  const float2 a = make_float2(ex2(min_nan(s.x * p.e2, 60.f)), ex2(min_nan(s.y * p.e2, 60.f)));
+  auto held = [](float x) -> float { return APART ? fminf(x, 60.f) : min_nan(x, 60.f); };
+  const float2 a = make_float2(ex2(held(s.x * p.e2)), ex2(held(s.y * p.e2)));
   const float2 b = __fadd2_rn(a, make_float2(1.f, 1.f));
   const float r = -2.f * rcp_approx(b.x * b.y);
   return make_float2(fmaf(r, b.y, 1.f), fmaf(r, b.x, 1.f));

@@ -1,0 +1,41 @@
+"""What one row of a capped call may do to another, and scores at the ends of the
+cap, on the GPU: a NaN stays in the rows that see it, a sequence's bits do not
+depend on what lies behind it, gradients keep their size where the cap is
+saturated, and O keeps its precision and range whatever the scores and values."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import scored as S
+from test_gpu_packed import BF, FH, _bits, _f64, _inputs, _settled, fa  # noqa: F401 (fa: the fixture)
+from test_gpu_scored import _check, _run
+
+pytestmark = pytest.mark.gpu
+
+
+def _slopes(Hq, bias):
+    return dict(slopes=torch.tensor([2.0 ** -(h + 2) for h in range(Hq)], device="cuda")) if bias else {}
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("row", [62, 63, 130])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("softcap,qmul", [(5.0, 8.0), (50.0, 1.0)])
+def test_a_nan_query_stays_in_its_row(fa, softcap, qmul, bias, row, d):  # noqa: F811
+    """Query `row` is NaN: O and dQ of all other rows, and dV of the keys it does
+    not see, are those of the formula, as in the calls of plain scores."""
+    c = _inputs([200], 2, 2, d, BF, 21, qmul=qmul)
+    kw = dict(softcap=softcap, **_slopes(2, bias))
+    val, tol = S.packed_attention(_f64(c["q"]), _f64(c["k"]), _f64(c["v"]), _f64(c["do"]), c["bounds"], 0.125, True,
+                                  2.0 ** -8, softcap, None if not bias else kw["slopes"].cpu().numpy())
+    c["q"][row] = float("nan")
+    r = _run(fa, c, 0.125, True, kw)
+    plain = _run(fa, c, 0.125, True, {})
+    _settled(fa)
+    others = np.arange(200) != row
+    unseen = np.arange(200) > row
+    for name, key, rows in (("O", "o", others), ("dQ", "dq", others), ("dV", "dv", unseen)):
+        assert torch.isfinite(plain[key]).cpu().numpy()[rows].all(), name
+        off = np.abs(_f64(r[key]) - val[name])[rows] - tol[name][rows]
+        assert off.max() <= 0, f"{name}: {off.max():.3g} over its bound"      # (a NaN fails)
+    assert torch.isnan(r["o"][row]).all() and torch.isnan(r["dq"][row]).all() and torch.isnan(r["lse"][:, row]).all()
