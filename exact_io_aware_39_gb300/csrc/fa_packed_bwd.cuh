@@ -157,9 +157,8 @@ __device__ __forceinline__ void score_p(float (&x)[kC], uint32_t (&pk)[kC / 2], 
 #pragma unroll
     for (int c = 0; c < kC; c += 2) top[(c >> 1) & 3] = fmax3(top[(c >> 1) & 3], fabsf(x[c]), fabsf(x[c + 1]));
     const bool small = __all_sync(0xFFFFFFFFu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) <= sp.limit);
-    auto pair = [&](int c, float2 th, float2 u) {
+    auto pair = [&](int c, float2 th, float2 f, float2 u) {
       u = __ffma2_rn(th, make_float2(sp.c2, sp.c2), u);
-      const float2 f = __ffma2_rn(make_float2(-th.x, -th.y), th, make_float2(1.f, 1.f));
       const float2 p = make_float2(ex2(u.x), ex2(u.y));
       pk[c / 2] = pack2<F16>(p.x, p.y);
       const float2 y = __fmul2_rn(p, f);
@@ -170,11 +169,16 @@ __device__ __forceinline__ void score_p(float (&x)[kC], uint32_t (&pk)[kC / 2], 
 #pragma unroll
       for (int c = 0; c < kC; c += 2) {
         const float2 l = *reinterpret_cast<const float2*>(lse2 + c);
-        pair(c, tanh_small2(make_float2(x[c], x[c + 1]), sp), make_float2(-l.x, -l.y));
+        const float2 th = tanh_small2(make_float2(x[c], x[c + 1]), sp);
+        pair(c, th, __ffma2_rn(make_float2(-th.x, -th.y), th, make_float2(1.f, 1.f)), make_float2(-l.x, -l.y));
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < kC; c += 2) pair(c, tanh_exp2<true>(make_float2(x[c], x[c + 1]), sp), added(c));
+      for (int c = 0; c < kC; c += 2) {
+        float2 f;
+        const float2 th = tanh_slope2(make_float2(x[c], x[c + 1]), sp, f);
+        pair(c, th, f, added(c));
+      }
     }
   } else {
 #pragma unroll

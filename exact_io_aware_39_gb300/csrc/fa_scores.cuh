@@ -90,22 +90,33 @@ __device__ __forceinline__ float rcp_approx(float x) {
 __device__ __forceinline__ float tanh_exp(float s, const ScoreParams& p) {
   return fmaf(-2.f, rcp_approx(1.f + ex2(s * p.e2)), 1.f);
 }
-// the same for a pair, whose denominators share a reciprocal: 1 / a = b / (a b).
-// The exponents are held to 60, where tanh is 1 in fp32, so that a b is finite.
-// A NaN stays one, and makes its neighbour one: for a pair of one row, which has a
-// NaN then in any case. APART: for a pair of two rows; a NaN counts as 60.
+// the same for a pair of one row, whose denominators share a reciprocal: 1 / a =
+// b / (a b). The exponents are held to 60, where tanh is 1 in fp32, so that a b is
+// finite (a NaN stays one, and makes its neighbour one, in a row that has a NaN then
+// in any case).
 __device__ __forceinline__ float min_nan(float a, float b) {
   float y;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
-template <bool APART = false>
 __device__ __forceinline__ float2 tanh_exp2(float2 s, const ScoreParams& p) {
-  auto held = [](float x) -> float { return APART ? fminf(x, 60.f) : min_nan(x, 60.f); };
-  const float2 a = make_float2(ex2(held(s.x * p.e2)), ex2(held(s.y * p.e2)));
+  const float2 a = make_float2(ex2(min_nan(s.x * p.e2, 60.f)), ex2(min_nan(s.y * p.e2, 60.f)));
   const float2 b = __fadd2_rn(a, make_float2(1.f, 1.f));
   const float r = -2.f * rcp_approx(b.x * b.y);
   return make_float2(fmaf(r, b.y, 1.f), fmaf(r, b.x, 1.f));
+}
+// tanh(k s) and its slope 1 - tanh^2 of a pair that belongs to two rows: with e =
+// exp(2 k s) and q = 1 / (1 + e), tanh is 1 - 2 q and the slope 4 e q^2, which keeps its
+// relative precision (2^-21, and 2^-23 of the exponent's argument) where 1 - tanh^2
+// would be nothing but tanh's rounding. Exponents are held to 63, scores of 21 caps,
+// where the slope is 2^-61. A NaN counts as 63 here: it stays out of its neighbour.
+__device__ __forceinline__ float2 tanh_slope2(float2 s, const ScoreParams& p, float2& slope) {
+  const float2 e = make_float2(ex2(fminf(s.x * p.e2, 63.f)), ex2(fminf(s.y * p.e2, 63.f)));
+  const float2 b = __fadd2_rn(e, make_float2(1.f, 1.f));
+  const float r = 2.f * rcp_approx(b.x * b.y);
+  const float2 q2 = __fmul2_rn(make_float2(b.y, b.x), make_float2(r, r));
+  slope = __fmul2_rn(__fmul2_rn(e, q2), q2);
+  return __fadd2_rn(make_float2(1.f, 1.f), make_float2(-q2.x, -q2.y));
 }
 // t2 = s times this, of a pair of small scores (|s| <= limit)
 __device__ __forceinline__ float2 cap_small_factor2(float2 s, const ScoreParams& p) {

@@ -44,13 +44,18 @@ def score_error(q, k, scale, softcap, slope, rows, cols, u, t, LSE):
     return e + 2.0 ** -21 * (np.abs(np.where(np.isfinite(LSE), LSE, 0.0))[:, None] + np.abs(u))
 
 
-def packed_attention(q, k, v, do, cu, scale, causal, u16, softcap=0.0, slopes=None, prefixes=None):
+def packed_attention(q, k, v, do, cu, scale, causal, u16, softcap=0.0, slopes=None, prefixes=None, relative_slope=False):
     """As oracle.packed.packed_attention (values and bounds of O, LSE, dQ, dK, dV;
     rows of no sequence are NaN), with these scores. u16: half a step of the
     16-bit type. A weight's relative error is that of its own score and the
     average of the others' (the sum it is divided by); dS has the cap's slope
     f = 1 - tanh^2, whose error is at most 0.77 of the score's over softcap plus
-    2^-18 (two roundings of tanh, and of its square)."""
+    2^-18 (two roundings of tanh, and of its square). relative_slope: at most f times
+      expm1(2 raw / softcap)     |d ln f / ds| = 2 |tanh| / softcap, raw the score's error
+      2^-21 |s| / softcap        f goes with exp(-2 |s| / softcap), whose argument has
+                                 two roundings (of the factor and of the product)
+      2^-18                      the exponential, the reciprocal, four products,
+    which holds where the cap is saturated, too."""
     q, k, v, do = (np.asarray(x, dtype=np.float64) for x in (q, k, v, do))
     T, Hq, d = q.shape
     Hk = k.shape[1]
@@ -75,10 +80,10 @@ def packed_attention(q, k, v, do, cu, scale, causal, u16, softcap=0.0, slopes=No
             hk = h // G
             slope = 0.0 if slopes is None else float(slopes[h])
             Q, K, V, dO = q[r, h], k[r, hk], v[r, hk], do[r, h]
-            U, t, _ = scores(Q, K, scale, softcap, slope, at, at)
+            U, t, raw_s = scores(Q, K, scale, softcap, slope, at, at)
             P, LSE = softmax(U, seen)
             O = P @ V
-            f = 1 - (t / softcap) ** 2 if softcap else np.ones_like(t)
+            f = 1 / np.cosh(np.clip(raw_s / softcap, -350, 350)) ** 2 if softcap else np.ones_like(t)
             dP = dO @ V.T
             D = (dO * O).sum(axis=1, keepdims=True)
             dS = P * (dP - D) * f
@@ -90,6 +95,8 @@ def packed_attention(q, k, v, do, cu, scale, causal, u16, softcap=0.0, slopes=No
             tD = (P * (eP * np.abs(dP) + dPm)).sum(axis=1, keepdims=True)   # D = rowsum(P dP) in fp32
             raw = (d + 4) * 2.0 ** -24 * scale * (np.abs(Q) @ np.abs(K).T)
             eF = 0.77 * raw / softcap + 2.0 ** -18 if softcap else 0.0
+            if softcap and relative_slope:
+                eF = f * (np.expm1(2 * raw / softcap) + 2.0 ** -21 * np.abs(raw_s) / softcap + 2.0 ** -18)
             tS = np.where(seen, (u16 + eP) * np.abs(dS) + P * f * (tD + dPm) + P * np.abs(dP - D) * eF + a
                           + z * np.abs(dP - D), 0.0)
             val["O"][r, h], val["LSE"][h, r] = O, LSE

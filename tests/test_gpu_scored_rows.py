@@ -39,3 +39,27 @@ def test_a_nan_query_stays_in_its_row(fa, softcap, qmul, bias, row, d):  # noqa:
         off = np.abs(_f64(r[key]) - val[name])[rows] - tol[name][rows]
         assert off.max() <= 0, f"{name}: {off.max():.3g} over its bound"      # (a NaN fails)
     assert torch.isnan(r["o"][row]).all() and torch.isnan(r["dq"][row]).all() and torch.isnan(r["lse"][:, row]).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("causal", [True, False])
+def test_gradients_of_a_saturated_cap(fa, causal, bias, d):  # noqa: F811
+    """All scores lie 4 to 12 caps from zero, where the cap's slope is 1e-3 to
+    1e-10: dQ and dK keep their relative precision."""
+    c = _inputs([150, 33], 2, 1, d, BF, 22)
+    g = torch.Generator().manual_seed(5)
+    sign = 1.0 - 2.0 * torch.randint(0, 2, (183, 1, 1), generator=g)
+    size = 0.5 + torch.rand(183, 2, 1, generator=g)
+    c["q"] = ((1 + torch.rand(183, 2, d, generator=g)) * size).to(BF).cuda()
+    c["k"] = ((1 + 0.75 * torch.rand(183, 1, d, generator=g)) * sign).to(BF).cuda()   # products of 1 to 3 d, of either sign
+    cap, scale = 3.0, 12.0 / d
+    kw = dict(softcap=cap, **_slopes(2, bias))
+    r = _run(fa, c, scale, causal, kw)
+    _settled(fa)
+    _check(c, r, scale, causal, kw)
+    val, tol = S.packed_attention(_f64(c["q"]), _f64(c["k"]), _f64(c["v"]), _f64(c["do"]), c["bounds"], scale, causal,
+                                  2.0 ** -8, cap, None if not bias else kw["slopes"].cpu().numpy(), relative_slope=True)
+    for name, key in (("dQ", "dq"), ("dK", "dk")):
+        off = np.abs(_f64(r[key]) - val[name]) - tol[name]
+        assert off.max() <= 0, f"{name}: {off.max():.3g} over its bound, largest value {np.abs(val[name]).max():.3g}"
