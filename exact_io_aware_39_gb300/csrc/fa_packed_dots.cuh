@@ -345,13 +345,13 @@ fa_packed_dots_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
         const bool partial = w.partial(e, qi);
         const int lim = (w.causal ? min(max(row + 1, w.pre), w.len) : w.len) - kTile * e - 64 * h;
         const ScoreTile st = score_tile<SCORE>(p.score, slope2, kTile * e + 64 * h, row, e < qi ? -1 : e > qi ? 1 : 0,
-                                               e == qi && (!w.causal || w.pre > kTile * e), partial, lim);
+                                               e == qi && (!w.causal || w.pre > kTile * e), partial, lim, live);
         // Capped scores that are all within the polynomial's limit, without a bias or a mask, stay as they are
         // until the exponential: the polynomial beside it. (Two sequences of 4547 and 5127 tokens, 32 / 8 heads,
         // d = 128, forward and backward: 1669 -> 1640 us.)
         bool fast = false;
         if constexpr (SCORE == kScoreCap) {
-          const bool small = cap_vote(u, p.score, partial, lim);
+          const bool small = cap_vote(u, p.score, partial, lim, live);
           fast = small && !partial && !st.bias;
           if (!fast) {
             cap_args(u[0], p.score, partial, lim, small, -lse2);

@@ -598,7 +598,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
         };
         if (bounded) {
           // (against a reference of 0: no maximum, and the two halves need not agree)
-          const bool small = cap_vote(u, p.score, partial, lim);
+          const bool small = cap_vote(u, p.score, partial, lim, row < w.len);
           if (small && !partial) {
             // (in one piece, so that the polynomial of some scores runs beside the
             // exponentials of others)
@@ -622,7 +622,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           if (SPLIT && t == 1 && begin && nJ > 0u) ok = ok && bar_wait_warp(bar(L::bJoined), (nJ - 1u) & 1u, ctl, 328);
         } else {
           const ScoreTile st = score_tile<SCORE>(p.score, slope2, kTile * e + 64 * h, row, e < qi ? -1 : e > qi ? 1 : 0,
-                                                 e == qi && (!w.causal || w.pre > kTile * e), partial, lim);
+                                                 e == qi && (!w.causal || w.pre > kTile * e), partial, lim, row < w.len);
           // The exponents against the row's reference as it is, which moves only where
           // one passes it by more than the threshold, and in an item's first tile. (Where
           // the tile's largest bias lies kFar above it, against that: from a reference

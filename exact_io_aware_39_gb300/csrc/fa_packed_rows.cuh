@@ -84,12 +84,13 @@ struct Pair {
 struct ScoreTile {
   float slope, far;          // slope: signed, in log2 units
   bool bias, linear, partial;
+  bool live;                 // a row of the sequence
   int lim;                   // columns from here on are no keys of the row (partial)
 };
 
 template <int SCORE>
 __device__ __forceinline__ ScoreTile score_tile(const ScoreParams& sp, float slope2, int key0, int row, int side,
-                                                bool both_sides, bool partial, int lim) {
+                                                bool both_sides, bool partial, int lim, bool live) {
   ScoreTile s;
   s.bias = sp.slopes != nullptr;
   s.linear = !both_sides;
@@ -97,6 +98,7 @@ __device__ __forceinline__ ScoreTile score_tile(const ScoreParams& sp, float slo
   s.far = (float)(key0 - row);
   s.partial = partial;
   s.lim = lim;
+  s.live = live;
   return s;
 }
 
@@ -142,9 +144,10 @@ __device__ __forceinline__ void mask_columns(uint32_t (&u)[32], int lim, float w
 }
 
 // A cap's first step on a row's 64 raw scores: whether all of them, of all rows of
-// the warp, are within the polynomial's limit. What lies in masked columns may be
+// the warp, are within the polynomial's limit. Rows past the sequence (not `live`)
+// have no say: a sequence's bits are its own. What lies in masked columns may be
 // NaN, which must not meet its neighbour in tanh_exp2: it becomes zeros.
-__device__ __forceinline__ bool cap_vote(uint32_t (&u)[2][32], const ScoreParams& sp, bool partial, int lim) {
+__device__ __forceinline__ bool cap_vote(uint32_t (&u)[2][32], const ScoreParams& sp, bool partial, int lim, bool live) {
   if (partial) {
     mask_columns(u[0], lim, 0.f);
     mask_columns(u[1], lim - 32, 0.f);
@@ -156,7 +159,7 @@ __device__ __forceinline__ bool cap_vote(uint32_t (&u)[2][32], const ScoreParams
   for (int i = 0; i < 64; i += 2)
     top[(i >> 1) & 3] = fmax3(top[(i >> 1) & 3], fabsf(__uint_as_float(u[i >> 5][i & 31])),
                               fabsf(__uint_as_float(u[i >> 5][(i & 31) + 1])));
-  return __all_sync(0xFFFFFFFFu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) <= sp.limit);
+  return __all_sync(0xFFFFFFFFu, !live || fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) <= sp.limit);
 }
 
 // The cap of 32 scores, and nref; -inf where masked (partial: from column lim on).
@@ -205,7 +208,7 @@ template <int SCORE, bool MAX>
 __device__ __forceinline__ float score_args(uint32_t (&u)[2][32], const ScoreParams& sp, float sl2, const ScoreTile& s,
                                             float nref) {
   if constexpr (SCORE == kScoreCap) {
-    const bool small = cap_vote(u, sp, s.partial, s.lim);
+    const bool small = cap_vote(u, sp, s.partial, s.lim, s.live);
     cap_args(u[0], sp, s.partial, s.lim, small, nref);
     cap_args(u[1], sp, s.partial, s.lim - 32, small, nref);
   } else if (s.partial) {

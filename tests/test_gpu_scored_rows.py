@@ -63,3 +63,31 @@ def test_gradients_of_a_saturated_cap(fa, causal, bias, d):  # noqa: F811
     for name, key in (("dQ", "dq"), ("dK", "dk")):
         off = np.abs(_f64(r[key]) - val[name]) - tol[name]
         assert off.max() <= 0, f"{name}: {off.max():.3g} over its bound, largest value {np.abs(val[name]).max():.3g}"
+
+
+
+@pytest.mark.parametrize("dtype", [BF, FH], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("Hq,Hk,d", [(4, 2, 64), (4, 2, 128), (3, 3, 64), (64, 16, 128)])
+@pytest.mark.parametrize("softcap,bias,causal", [(50.0, False, True), (50.0, False, False), (50.0, True, True), (700.0, False, True)])
+def test_bits_do_not_depend_on_what_lies_behind(fa, softcap, bias, causal, Hq, Hk, d, dtype):  # noqa: F811
+    """A sequence whose last tile is not full, before one of huge queries, before
+    one of ordinary ones, and before rows of no sequence: the same bits."""
+    n = 150
+    c = _inputs([n, 140], Hq, Hk, d, dtype, 23)
+    kw = dict(softcap=softcap, **_slopes(Hq, bias))
+    results = []
+    for behind in (1.0, 300.0):
+        c["q"][n:] = (c["q"][n:].float() * behind).to(dtype)
+        for bounds in ([0, n, n + 140], [0, n, n]):
+            c["cu"].copy_(torch.tensor(bounds, dtype=torch.int32))
+            r = _run(fa, c, d ** -0.5, causal, kw)
+            _settled(fa)
+            results.append(r)
+    for r in results[1:]:     # (two key tiles: dQ's two partial sums are the same in either order)
+        for key in ("o", "dq", "dk", "dv"):
+            assert torch.equal(_bits(r[key][:n].contiguous()), _bits(results[0][key][:n].contiguous())), key
+        assert torch.equal(_bits(r["lse"][:, :n].contiguous()), _bits(results[0]["lse"][:, :n].contiguous()))
+    if Hq <= 4:               # alone: the same kernels (with more heads, calls of few tiles share keys out)
+        o, lse = fa.attention_packed_fwd(c["q"][:n], c["k"][:n], c["v"][:n], c["cu"][:2].contiguous(), d ** -0.5, causal=causal, **kw)
+        _settled(fa)
+        assert torch.equal(_bits(o), _bits(results[0]["o"][:n])) and torch.equal(_bits(lse), _bits(results[0]["lse"][:, :n].contiguous()))
