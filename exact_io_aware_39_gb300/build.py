@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_wide.cu", "fa_noalloc.cu", "fa_cache.cu", "fa_cached_cap.cu",
            "fa_cached_bias.cu", "fa_cache_weights.cu", "fa_cache_evict.cu", "fa_packed.cu", "fa_packed_fwd.cu", "fa_packed_fwd_cap.cu",
-           "fa_packed_fwd_bias.cu", "fa_packed_bwd.cu", "fa_packed_bwd_cap.cu", "fa_packed_bwd_bias.cu", "std_attn.cu"]
+           "fa_packed_fwd_bias.cu", "fa_packed_fwd_cap_bias.cu", "fa_packed_bwd.cu", "fa_packed_bwd_cap.cu", "fa_packed_bwd_bias.cu", "std_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
           "-I", INCLUDE, "-I", CSRC]

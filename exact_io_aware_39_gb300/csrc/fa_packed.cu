@@ -246,7 +246,8 @@ fa_status packed_fwd_call(const void* Q, const void* K, const void* V, void* O, 
                          reinterpret_cast<int*>(ws + w.sorted_off), reinterpret_cast<PackedItem*>(ws + w.item_off),
                          w.cap_items, nullptr, 0, err, s) != cudaSuccess)
     return FA_ERR_CUDA;
-  const auto launch = score.cap ? launch_packed_fwd_cap : score.slopes || score.prefix ? launch_packed_fwd_bias : launch_packed_fwd;
+  const auto launch = score.cap ? (score.slopes ? launch_packed_fwd_cap_bias : launch_packed_fwd_cap)
+                      : score.slopes || score.prefix ? launch_packed_fwd_bias : launch_packed_fwd;
   return launch(o.f16, tq, tk, tv, p, s) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

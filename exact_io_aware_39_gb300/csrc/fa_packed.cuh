@@ -394,14 +394,14 @@ cudaError_t launch_packed_plan(const int32_t* cu, const int32_t* prefix, int B, 
                                bool backward, PackedPlan* plan, int* sorted, PackedItem* items, int cap_items, PackedItem* tiles, int cap_tiles,
                                unsigned int* err, cudaStream_t s);
 
-// One for each kind of score (kScorePlain, kScoreCap, kScoreBias), from a
+// One for each kind of score (kScorePlain, kScoreCap, kScoreBias; forward: kScoreCapOnly), from a
 // translation unit of its own.
 using PackedFwdLaunch = cudaError_t(bool f16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                     const PackedFwdParams& p, cudaStream_t s);
 using PackedBwdLaunch = cudaError_t(bool f16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                     const CUtensorMap& tdo, const CUtensorMap& tdq, const PackedBwdParams& p,
                                     cudaStream_t s);
-PackedFwdLaunch launch_packed_fwd, launch_packed_fwd_cap, launch_packed_fwd_bias;
+PackedFwdLaunch launch_packed_fwd, launch_packed_fwd_cap, launch_packed_fwd_bias, launch_packed_fwd_cap_bias;
 PackedBwdLaunch launch_packed_bwd, launch_packed_bwd_cap, launch_packed_bwd_bias;
 
 }  // namespace fa

@@ -351,7 +351,8 @@ fa_packed_dots_kernel(const __grid_constant__ CUtensorMap tq, const __grid_const
         // d = 128, forward and backward: 1669 -> 1640 us.)
         bool fast = false;
         if constexpr (SCORE == kScoreCap) {
-          const bool small = cap_vote(u, p.score, partial, lim, live);
+          float most;
+          const bool small = cap_vote(u, p.score, partial, lim, live, most);
           fast = small && !partial && !st.bias;
           if (!fast) {
             cap_args(u[0], p.score, partial, lim, small, -lse2);

@@ -535,7 +535,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
   } else if (PRE && warp < L::kOther) {
     // ------------------------------------------------------------ softmax groups, scores of their own
     // Thread = row and half of its columns; the two groups of a query tile share a
-    // row's reference (exchanged for every tile) and add their sums at the end. After
+    // row's reference (they agree on it for every tile) and add their sums at the end. After
     // each wait that one of them may fail they agree with group_all, so that they
     // always take the same branch and none waits where the other has left.
     if constexpr (PRE) {
@@ -549,9 +549,13 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
     const uint32_t tP = tmem + (L::kSharedS ? 128u : 256u + 2u * D) + 64u * (uint32_t)t + lane_off + 32u * (uint32_t)h;
     constexpr int kCols0 = D / 64;           // 32-column steps of O that a half rescales and writes
     const float sl2 = p.scale_log2;
-    const bool bounded = SCORE == kScoreCap && !F16 && p.score.bounded;
-    // (P in fp16 ends at 2^16; moves stop all rows of a tile, so they are rare here)
-    constexpr float kMove = F16 ? 14.f : 30.f, kFar = 4.f;
+    constexpr bool kNoBias = SCORE == kScoreCapOnly;
+    constexpr float kFar = 4.f;
+    // A move stops all rows of a query tile, so without a bias, in bf16, a reference starts up to
+    // 16 above the largest score of an item's first tile: one that moves it has to pass that by 30.
+    // (24 prompts of 16-2048 tokens, 32 / 8 heads, d = 128, a cap of 50, scores of a standard
+    // deviation of 10: 191 us, 243 with a reference that starts at the largest and moves past 20.)
+    const float head = kNoBias && !F16 ? p.score.head : 0.f;
     volatile float* ex = reinterpret_cast<volatile float*>(smem + L::kEx) + r;   // [query tile][half][128]
     uint32_t nS = 0u, nO = 0u;               // S tiles and final O read by this group
     uint32_t nJ = 0u;                        // SPLIT: items of two groups so far
@@ -563,7 +567,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
       if (!w.has(t)) continue;
       const int qi = w.qi(t), last = w.last(t);
       const int row = kTile * qi + r;        // query index within the sequence
-      const float slope2 = p.score.slopes != nullptr ? p.score.slopes[w.hq(t)] * 1.4426950408889634f : 0.f;
+      const float slope2 = !kNoBias && p.score.slopes != nullptr ? p.score.slopes[w.hq(t)] * 1.4426950408889634f : 0.f;
       float m_ref = 0.f;
       float l = 0.f;
       for (int i = w.first(t); i <= last; i += SPLIT ? 2 : 1) {
@@ -596,41 +600,52 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
             pk[hh][i] = pack2<F16>(p0, p1);
           }
         };
-        if (bounded) {
-          // (against a reference of 0: no maximum, and the two halves need not agree)
-          const bool small = cap_vote(u, p.score, partial, lim, row < w.len);
-          if (small && !partial) {
-            // (in one piece, so that the polynomial of some scores runs beside the
-            // exponentials of others)
+        // Capped scores without a bias: where no row can pass its reference by the threshold,
+        // none moves, and no maximum of the capped scores is formed. The raw ones' bounds
+        // them: their magnitude, which the choice of the tanh needs anyway, where the polynomial
+        // holds (|tanh x| <= |x|), else their maximum.
+        bool stays = false;
+        if constexpr (kNoBias) {
+          if (!begin) {
+            float most;
+            const bool small = cap_vote(u, p.score, partial, lim, row < w.len, most);
+            if (small) most *= p.score.a0;
+            else most = p.score.c2 * tanh_exp(row_max(u), p.score);
+            stays = group_all(pair_bar, 256u, ok && (row >= w.len || most <= m_ref + kRefMove));
+            if (stays && small && !partial) {
+              // (in one piece, so that the polynomial of some scores runs beside the
+              // exponentials of others)
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
+              for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 a = cap_small2(pair_of(u[hh], 2 * i), p.score);
-                const float p0 = ex2(a.x);
-                const float p1 = ex2(a.y);
-                sum4[i & 3] = __fadd2_rn(sum4[i & 3], make_float2(p0, p1));
-                pk[hh][i] = pack2<F16>(p0, p1);
+                for (int i = 0; i < 16; ++i) {
+                  const float2 x = pair_of(u[hh], 2 * i);
+                  const float2 a = __ffma2_rn(x, cap_small_factor2(x, p.score), make_float2(-m_ref, -m_ref));
+                  const float p0 = ex2(a.x);
+                  const float p1 = ex2(a.y);
+                  sum4[i & 3] = __fadd2_rn(sum4[i & 3], make_float2(p0, p1));
+                  pk[hh][i] = pack2<F16>(p0, p1);
+                }
+            } else if (stays) {
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                cap_args(u[hh], p.score, partial, lim - 32 * hh, small, -m_ref);
+                weights(hh);
               }
-          } else {
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              cap_args(u[hh], p.score, partial, lim - 32 * hh, small, 0.f);
-              weights(hh);
             }
           }
-          if (SPLIT && t == 1 && begin && nJ > 0u) ok = ok && bar_wait_warp(bar(L::bJoined), (nJ - 1u) & 1u, ctl, 328);
-        } else {
+        }
+        if (!stays) {
           const ScoreTile st = score_tile<SCORE>(p.score, slope2, kTile * e + 64 * h, row, e < qi ? -1 : e > qi ? 1 : 0,
                                                  e == qi && (!w.causal || w.pre > kTile * e), partial, lim, row < w.len);
           // The exponents against the row's reference as it is, which moves only where
           // one passes it by more than the threshold, and in an item's first tile. (Where
           // the tile's largest bias lies kFar above it, against that: from a reference
           // that is far below, they would be rounded in its units.)
-          const float above = score_base(p.score, slope2, kTile * e, row, e < qi ? -1 : e > qi ? 1 : 0);
+          const float above = kNoBias ? -INFINITY : score_base(p.score, slope2, kTile * e, row, e < qi ? -1 : e > qi ? 1 : 0);
           const float base = begin ? (above > -INFINITY ? above : 0.f) : above > m_ref + kFar ? above : m_ref;
           const float mx = score_args<SCORE, true>(u, p.score, sl2, st, -base);
-          if (!group_all(pair_bar, 256u, ok && !begin && base <= m_ref && mx <= kMove)) {
+          if (begin || kNoBias || !group_all(pair_bar, 256u, ok && base <= m_ref && mx <= kRefMove)) {
             // (the first group has read O_1 and what goes with it of the item before)
             if (SPLIT && t == 1 && begin && nJ > 0u) ok = ok && bar_wait_warp(bar(L::bJoined), (nJ - 1u) & 1u, ctl, 328);
             // the previous O_t += P_t V has completed: O_t may be rescaled
@@ -640,10 +655,10 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
             tc_fence_after();
             const float top = fmaxf(mx, ex[kTile * (2 * t + (h ^ 1))]);
             const float up = begin ? 0.f : base - m_ref;
-            const bool move = begin || top + up > (up > 0.f ? 0.f : kMove);
+            const bool move = begin || top + up > (up > 0.f ? 0.f : kRefMove);
             float alpha = 1.f, shift = up;
             if (move) {
-              const float by = top > -INFINITY ? top : 0.f;   // (0: nothing to move to)
+              const float by = (top > -INFINITY ? top : 0.f) + head;   // (0: nothing to move to)
               alpha = begin ? 0.f : ex2(m_ref - (base + by));
               shift = -by;
               m_ref = base + by;
@@ -717,9 +732,7 @@ fa_packed_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_consta
           m_ref = M;
         }
       }
-      // (bounded: the one weight of a row of one key is no 1, so its O is divided by the weight as rounded)
-      const bool alone = bounded && (w.causal ? min(max(row + 1, w.pre), w.len) : w.len) == 1;
-      const float inv_l = 1.f / (alone ? unpack2<F16>(pack2<F16>(l, l)).x : l);
+      const float inv_l = 1.f / l;
       const int s4 = lane & 3;
       const int row0 = kTile * qi + 32 * (warp & 3) + (lane & ~3);   // the quad's first row
       uint16_t* op = p.o + (int64_t)(w.start + row0) * p.o_tok + w.hq(t) * p.o_head + 8 * s4;

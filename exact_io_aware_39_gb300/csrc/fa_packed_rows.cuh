@@ -75,8 +75,10 @@ struct Pair {
 // (A thread for a whole row, as for plain scores, took 440 us for two sequences of
 // 4547 and 5127 tokens, 32 / 8 heads, d = 128, with a cap: seven more operations a
 // score in two warps of an SM's quarter. Two threads to a row 411, 64 KB of code
-// less than 93; P in columns of its own, so that the next S is computed meanwhile,
-// and weights that need no maximum 325; plain scores take 242.)
+// less than 93; P in columns of its own, so that the next S is computed meanwhile, no
+// maximum where the raw scores bound it, and a kernel without the bias 332; plain scores
+// take 242. Weights against a reference of 0, which need no bound and no agreement of a
+// row's two threads, took 320, but rounded the heaviest weight and ended at 2^30.)
 //
 // What is uniform for a row and a tile: the bias of key j is +-slope (j - i) where
 // all keys lie on one side (linear), counted up beside the scores; else, in the
@@ -143,11 +145,22 @@ __device__ __forceinline__ void mask_columns(uint32_t (&u)[32], int lim, float w
     if (i >= lim) u[i] = __float_as_uint(with);
 }
 
+__device__ __forceinline__ float row_max(const uint32_t (&u)[2][32]) {
+  float hi[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) hi[k] = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 64; i += 2)
+    hi[(i >> 1) & 3] = fmax3(hi[(i >> 1) & 3], __uint_as_float(u[i >> 5][i & 31]), __uint_as_float(u[i >> 5][(i & 31) + 1]));
+  return fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
+}
+
 // A cap's first step on a row's 64 raw scores: whether all of them, of all rows of
-// the warp, are within the polynomial's limit. Rows past the sequence (not `live`)
+// the warp, are within the polynomial's limit; `most`, the row's largest magnitude. Rows past the sequence (not `live`)
 // have no say: a sequence's bits are its own. What lies in masked columns may be
 // NaN, which must not meet its neighbour in tanh_exp2: it becomes zeros.
-__device__ __forceinline__ bool cap_vote(uint32_t (&u)[2][32], const ScoreParams& sp, bool partial, int lim, bool live) {
+__device__ __forceinline__ bool cap_vote(uint32_t (&u)[2][32], const ScoreParams& sp, bool partial, int lim, bool live,
+                                         float& most) {
   if (partial) {
     mask_columns(u[0], lim, 0.f);
     mask_columns(u[1], lim - 32, 0.f);
@@ -159,7 +172,8 @@ __device__ __forceinline__ bool cap_vote(uint32_t (&u)[2][32], const ScoreParams
   for (int i = 0; i < 64; i += 2)
     top[(i >> 1) & 3] = fmax3(top[(i >> 1) & 3], fabsf(__uint_as_float(u[i >> 5][i & 31])),
                               fabsf(__uint_as_float(u[i >> 5][(i & 31) + 1])));
-  return __all_sync(0xFFFFFFFFu, !live || fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) <= sp.limit);
+  most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  return __all_sync(0xFFFFFFFFu, !live || most <= sp.limit);
 }
 
 // The cap of 32 scores, and nref; -inf where masked (partial: from column lim on).
@@ -183,7 +197,7 @@ __device__ __forceinline__ void cap_args(uint32_t (&u)[32], const ScoreParams& s
 // ones, which are complete but for it.
 template <int SCORE>
 __device__ __forceinline__ void bias_args(uint32_t (&u)[2][32], float sl2, const ScoreTile& s, float nref) {
-  const float mul = SCORE == kScoreCap ? 1.f : sl2, start = SCORE == kScoreCap ? 0.f : nref;
+  const float mul = score_capped(SCORE) ? 1.f : sl2, start = score_capped(SCORE) ? 0.f : nref;
 #pragma unroll
   for (int hh = 0; hh < 2; ++hh) {
     if (s.linear) {
@@ -207,23 +221,17 @@ __device__ __forceinline__ void bias_args(uint32_t (&u)[2][32], float sl2, const
 template <int SCORE, bool MAX>
 __device__ __forceinline__ float score_args(uint32_t (&u)[2][32], const ScoreParams& sp, float sl2, const ScoreTile& s,
                                             float nref) {
-  if constexpr (SCORE == kScoreCap) {
-    const bool small = cap_vote(u, sp, s.partial, s.lim, s.live);
+  if constexpr (score_capped(SCORE)) {
+    float most;
+    const bool small = cap_vote(u, sp, s.partial, s.lim, s.live, most);
     cap_args(u[0], sp, s.partial, s.lim, small, nref);
     cap_args(u[1], sp, s.partial, s.lim - 32, small, nref);
   } else if (s.partial) {
     mask_columns(u[0], s.lim, -INFINITY);
     mask_columns(u[1], s.lim - 32, -INFINITY);
   }
-  if (SCORE == kScoreBias || s.bias) bias_args<SCORE>(u, sl2, s, nref);
-  if (!MAX) return 0.f;
-  float hi[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) hi[k] = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < 64; i += 2)
-    hi[(i >> 1) & 3] = fmax3(hi[(i >> 1) & 3], __uint_as_float(u[i >> 5][i & 31]), __uint_as_float(u[i >> 5][(i & 31) + 1]));
-  return fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
+  if (SCORE == kScoreBias || (SCORE == kScoreCap && s.bias)) bias_args<SCORE>(u, sl2, s, nref);
+  return MAX ? row_max(u) : 0.f;
 }
 
 }  // namespace

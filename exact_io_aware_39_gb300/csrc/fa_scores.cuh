@@ -14,8 +14,11 @@
 namespace fa {
 
 // What a packed kernel does to its scores: nothing; cap (and perhaps bias and
-// prefix); bias or prefix without a cap.
-constexpr int kScorePlain = 0, kScoreCap = 1, kScoreBias = 2;
+// prefix); bias or prefix without a cap; cap (and perhaps prefix) without a bias
+// (the forward, whose registers the bias's code cost: 24 prompts of 16-2048 tokens, 32 / 8
+// heads, d = 128, 168 us with it and 153 without).
+constexpr int kScorePlain = 0, kScoreCap = 1, kScoreBias = 2, kScoreCapOnly = 3;
+constexpr __host__ __device__ bool score_capped(int score) { return score == kScoreCap || score == kScoreCapOnly; }
 
 struct ScoreParams {
   const float* slopes;       // [Hq] or null
@@ -25,13 +28,13 @@ struct ScoreParams {
   float b0, b1, b2, b3;      // and tanh(k s) the same with these, a / c2
   float k, e2, c2;           // k; 2 k log2(e): exp(2 k s) = 2^(e2 s); c2
   int cap;
-  int bounded;               // capped without a bias, at most kFreeRange
+  float head;                // how far above the first tile's largest score a row's reference starts (bf16, no bias)
 };
 
-// P in bf16 and its fp32 sums reach 2^127 and down to 2^-126. Where a cap bounds the
-// scores by at most this in log2 units (a softcap of 55), weights are 2^u2 as it is and
-// no row needs a reference: at most 2^80 each, they leave room for values of 2^30.
-constexpr float kFreeRange = 80.f;
+// How far a row's reference may lie below its largest score, in log2 units, in the packed
+// forward: P reaches 2^kRefMove there (fp16 ends at 2^16; in bf16 P, V and the number of
+// keys share the 2^127 of an fp32 sum).
+constexpr float kRefMove = 14.f;
 
 // tanh(y) = y (C0 + C1 y^2 + C2 y^4 + C3 y^6) for |y| <= 0.4, to 9.8e-8 of the
 // value: the polynomial of least relative error (Remez exchange, in 64 bits).
@@ -62,7 +65,9 @@ inline fa_status read_scores(const fa_scores* scores, float scale, int causal, b
   out->k = (float)k;
   out->e2 = (float)(2. * 1.4426950408889634 * k);
   out->c2 = (float)c2;
-  out->bounded = s.slopes == nullptr && c2 <= kFreeRange;
+  // (an integer, at most what keeps c2 from ever passing it; 16 is a cap's 2^-20 once more)
+  const double head = std::floor(2. * c2 - kRefMove);
+  out->head = head < 0. ? 0.f : head > 16. ? 16.f : (float)head;
   // (past these k, k^7 leaves the fp32 range)
   if (k < 0x1p15 && k > 0x1p-15) {
     out->limit = (float)(kCapSmall / k);

@@ -60,6 +60,9 @@ typedef struct {
  * the sum over j of P_ij dP_ij (where a row has few keys of weight, the rounding
  * of O would show in dQ and dK) and does not read O. (Scores without a cap, slopes
  * and prefix_lens are plain ones: the calls of flash_attn_packed.h, which read it.)
+ * O is a sum in fp32 of weights of 2^14 at most: it is finite while a sequence's
+ * length times its largest |V| is below 2^112, and parts of it below 2^-109 may
+ * count as 0.
  */
 fa_status flash_attn_packed_scored_fwd(const void* Q, const void* K, const void* V, void* O, float* LSE,
                                        const int32_t* cu_seqlens, int B, int total, int Hq, int Hk, int d,

@@ -91,3 +91,47 @@ def test_bits_do_not_depend_on_what_lies_behind(fa, softcap, bias, causal, Hq, H
         o, lse = fa.attention_packed_fwd(c["q"][:n], c["k"][:n], c["v"][:n], c["cu"][:2].contiguous(), d ** -0.5, causal=causal, **kw)
         _settled(fa)
         assert torch.equal(_bits(o), _bits(results[0]["o"][:n])) and torch.equal(_bits(lse), _bits(results[0]["lse"][:, :n].contiguous()))
+
+
+
+@pytest.mark.parametrize("dtype", [BF, FH], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("softcap", [30.0, 50.0, 54.0, 80.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_row_with_one_heavy_key_has_its_value(fa, d, softcap, dtype):  # noqa: F811
+    """Sequences of 2 to 16 tokens; the first key's score is 35 to 75 before the cap,
+    the others' at most 0, so that their weights together are below 2^-30 even at a cap
+    of 30 (27 after it): O is V of the first key, bit for bit. A rounded weight and an
+    unrounded sum would be off by half a step."""
+    lens = [2, 3, 5, 9, 16, 16, 7, 2, 2, 4] * 3
+    c = _inputs(lens, 4, 2, d, dtype, 24)
+    first = c["cu"][:-1].long()
+    g = torch.Generator().manual_seed(6)
+    T = sum(lens)
+    q, k = torch.zeros(T, 4, d), torch.zeros(T, 2, d)
+    q[:, :, 0] = 5 + torch.randint(0, 64, (T, 4), generator=g) / 16.0          # 5 to 9, exact in either type
+    k[:, :, 0] = -torch.rand(T, 2, generator=g)
+    k[first.cpu(), :, 0] = 7 + torch.randint(0, 16, (len(lens), 2), generator=g) / 16.0
+    c["q"], c["k"] = q.to(dtype).cuda(), k.to(dtype).cuda()
+    kw = dict(softcap=softcap)
+    r = _run(fa, c, 1.0, True, kw)
+    _settled(fa)
+    _check(c, r, 1.0, True, kw)
+    want = c["v"][torch.repeat_interleave(first, c["cu"].diff())].repeat_interleave(2, dim=1)
+    assert torch.equal(r["o"], want)
+
+
+@pytest.mark.parametrize("softcap,bias", [(50.0, False), (55.0, False), (54.0, True), (300.0, False), (0.0, True)])
+@pytest.mark.parametrize("power", [100, 60, -60, -90])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_of_all_sizes(fa, d, power, softcap, bias):  # noqa: F811
+    """V, dO or both far from 1, beside scores up to the cap: O and the gradients
+    scale with them (the bounds do, too)."""
+    c = _inputs([300, 5, 130], 4, 2, d, BF, 25, qmul=10.0)
+    c["v"] = (c["v"].float() * 2.0 ** power).to(BF)
+    if power > 0:
+        c["do"] = (c["do"].float() * 2.0 ** -power).to(BF)
+    for causal in (True, False):
+        kw = dict(softcap=softcap, **_slopes(4, bias))
+        r = _run(fa, c, d ** -0.5, causal, kw)
+        _settled(fa)
+        _check(c, r, d ** -0.5, causal, kw)
