@@ -563,11 +563,14 @@ def _scratch(workspace, need, dev):
 
 def _scores(softcap, slopes, prefix_lens, Hq, B, dev):
     """The fa_scores of a call as bytes."""
+    cap = ctypes.c_float(softcap).value
+    if softcap and not cap:              # (0 would be none at all)
+        raise FlashAttnError(2 if softcap > 0 else 1, "softcap")
     if slopes is not None:
         _plain(slopes, "slopes", (Hq,), torch.float32, dev)
     if prefix_lens is not None:
         _plain(prefix_lens, "prefix_lens", (B,), torch.int32, dev)
-    return _pack_scores(24, softcap, 0 if slopes is None else slopes.data_ptr(),
+    return _pack_scores(24, cap, 0 if slopes is None else slopes.data_ptr(),
                         0 if prefix_lens is None else prefix_lens.data_ptr())
 
 

@@ -129,3 +129,19 @@ def test_evict_refusals(L, kw, want):
 def test_evict_options(L):
     for opts, want in ((L.fa_options(7), 2), (L.fa_options(p_drop=0.1), 2), (L.fa_options(test_stall=1), 2)):
         assert _evict(L, opts=opts) == want
+
+
+@pytest.mark.parametrize("softcap,status", [(1e-46, 2), (5e-324, 2), (-1e-46, 1)])
+def test_helpers_refuse_a_cap_that_32_bits_make_none(L, softcap, status):
+    with pytest.raises(L.FlashAttnError) as e:
+        L._scores(softcap, None, None, 8, 2, 0)
+    assert e.value.status == status
+
+
+@pytest.mark.parametrize("softcap", [0.0, 2.0 ** -10, 30.0, 0.1, 1024.0, 5000.0, 1e39, float("inf"), -1e39])
+def test_helpers_pack_the_scores_as_the_struct_does(L, softcap):
+    """Also a cap that 32 bits make infinite, which the call refuses."""
+    assert L._scores(softcap, None, None, 8, 2, 0) == bytes(L.fa_scores(softcap))
+    if not 2.0 ** -10 <= softcap <= 1024.0 and softcap:
+        for st in _calls(L, L.fa_scores(softcap)):
+            assert st in (1, 2)
