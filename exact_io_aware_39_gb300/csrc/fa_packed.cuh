@@ -175,7 +175,8 @@ __device__ __forceinline__ void report_bounds(unsigned int* err, int b) {
 // `cap` units in all (only bounds that overlap can name so many) is left out.
 // Units are listed as the plan kernel lists them: causal, by the number c of
 // units before them, descending, and for each c the sequences that have one; not
-// causal, sequence by sequence, the longest first. All lanes call the members
+// causal, sequence by sequence, the longest first (prefixes change what a unit
+// costs, but not its place). All lanes call the members
 // together. kSlots = kManySlots holds them all, 1 up to 32
 // (kernels are built for either: the claim of an item stands before its loads, and
 // with four slots for every call 24 prompts took 107 us, not 105).

@@ -16,7 +16,8 @@
 // in registers, so that the tensor core works on the next one meanwhile.
 // Bound: 4 d operations per visible pair on the tensor cores, and the scores'
 // arithmetic. (32 / 8 heads, d = 128, capped: two sequences of 4547 and 5127 tokens
-// 297 us, 1.30 PFLOP/s; 16 documents of 32-2048 tokens 81.)
+// 297 us, 1.30 PFLOP/s; 16 documents of 32-2048 tokens 81.) At 96 registers at
+// launch 28-96 bytes a thread are spilled.
 #pragma once
 
 #include "fa_packed_rows.cuh"

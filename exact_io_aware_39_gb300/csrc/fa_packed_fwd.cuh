@@ -12,7 +12,7 @@
 //     head. Calls of few query tiles take one to an item instead and share its key
 //     tiles out between the groups, whose sums are joined from TMEM (SPLIT);
 //   * the items of a call are listed on the device (the lengths are there),
-//     heaviest first: for up to 128 sequences by every producer warp for itself
+//     heaviest first (but for prefixes, which the order does not know): for up to 128 sequences by every producer warp for itself
 //     (DirectList), for more by a plan kernel. A CTA takes its own item, then,
 //     as it gets ready for one, the next of a counter that the plan kernel zeroed
 //     or, without one, a CTA of the grid that has not started, cancelled through

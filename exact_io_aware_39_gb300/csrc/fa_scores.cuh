@@ -16,7 +16,7 @@ namespace fa {
 // What a packed kernel does to its scores: nothing; cap (and perhaps bias and
 // prefix); bias or prefix without a cap; cap (and perhaps prefix) without a bias
 // (the forward, whose registers the bias's code cost: 24 prompts of 16-2048 tokens, 32 / 8
-// heads, d = 128, 168 us with it and 153 without).
+// heads, d = 128, 171 us with it and 154 without).
 constexpr int kScorePlain = 0, kScoreCap = 1, kScoreBias = 2, kScoreCapOnly = 3;
 constexpr __host__ __device__ bool score_capped(int score) { return score == kScoreCap || score == kScoreCapOnly; }
 
