@@ -32,8 +32,9 @@ extern "C" {
 /*
  *   size:        sizeof(fa_scores), set by the caller; fields past the size a
  *                caller declares are as if 0.
- *   softcap:     0 (none), or 2^-10 to 2^10 (FA_ERR_UNSUPPORTED outside;
- *                FA_ERR_INVALID_ARG when negative or not finite). t is formed in
+ *   softcap:     0 (none), or 2^-10 to 2^10, and scale / softcap from 2^-60 to
+ *                2^60 (FA_ERR_UNSUPPORTED outside; FA_ERR_INVALID_ARG when the cap
+ *                is negative or not finite). t is formed in
  *                fp32, to within 2^-21 |t| + 2^-20 softcap; the gradients' factor
  *                1 - (t / softcap)^2 to within 2^-18 of itself for scores of up to
  *                12 softcaps, 2^-17 up to 21 (past them, where it is below 2^-58, it

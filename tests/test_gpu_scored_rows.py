@@ -135,3 +135,39 @@ def test_values_of_all_sizes(fa, d, power, softcap, bias):  # noqa: F811
         r = _run(fa, c, d ** -0.5, causal, kw)
         _settled(fa)
         _check(c, r, d ** -0.5, causal, kw)
+
+
+@pytest.mark.parametrize("Hq,Hk", [(4, 2), (64, 64)], ids=["few_tiles", "many_tiles"])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (FH, 64)], ids=["bf16", "fp16"])
+def test_wait_runs_out_without_slopes(fa, dtype, d, Hq, Hk):  # noqa: F811
+    """Capped scores alone: the device stays usable, and the next call's bits are the first's."""
+    c = _inputs([700, 300], Hq, Hk, d, dtype, 5)
+    kw = dict(softcap=30.0)
+    r = _run(fa, c, 0.1, True, kw)
+    _settled(fa)
+    fa.attention_packed_fwd(c["q"], c["k"], c["v"], c["cu"], 0.1, wait_limit_us=20000, test_stall=1, **kw)
+    torch.cuda.synchronize()
+    st, detail = fa.device_error()
+    assert st == 5 and 310 <= detail[1] < 350, detail
+    r2 = _run(fa, c, 0.1, True, kw)
+    _settled(fa)
+    for key in ("o", "lse", "dk", "dv"):
+        assert torch.equal(_bits(r[key].contiguous()), _bits(r2[key].contiguous())), key
+
+
+@pytest.mark.parametrize("dtype", [BF, FH], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("order", ["rising", "falling"])
+@pytest.mark.parametrize("softcap,causal,prefix", [(50.0, True, False), (50.0, False, False), (300.0, True, True), (20.0, True, True)])
+def test_capped_scores_that_grow_along_the_keys(fa, softcap, causal, prefix, order, dtype):  # noqa: F811
+    """Scores from one end of the cap to the other along a sequence, so that rows'
+    references move from key tile to key tile, or never."""
+    c = _inputs([900, 260], 4, 2, 64, dtype, 26, qmul=4.0)
+    T = 1160
+    rise = torch.linspace(-1.5, 1.5, T, device="cuda").view(T, 1, 1) * (1 if order == "rising" else -1)
+    c["q"], c["k"] = c["q"].abs(), (c["k"].float().abs() * rise).to(dtype)
+    kw = dict(softcap=softcap)
+    if prefix:
+        kw["prefix_lens"] = torch.tensor([500, 260], dtype=torch.int32, device="cuda")
+    r = _run(fa, c, 0.2, causal, kw)
+    _settled(fa)
+    _check(c, r, 0.2, causal, kw)
