@@ -65,7 +65,8 @@ inline fa_status read_scores(const fa_scores* scores, float scale, int causal, b
   out->k = (float)k;
   out->e2 = (float)(2. * 1.4426950408889634 * k);
   out->c2 = (float)c2;
-  // (an integer, at most what keeps c2 from ever passing it; 16 is a cap's 2^-20 once more)
+  // (by how much more than the threshold a score can pass the first tile's largest, 2 c2 at
+  // most; whole, and at most 16, whose rounding in the arguments is within the cap's 2^-20)
   const double head = std::floor(2. * c2 - kRefMove);
   out->head = head < 0. ? 0.f : head > 16. ? 16.f : (float)head;
   // (past these k, k^7 leaves the fp32 range)
@@ -113,10 +114,11 @@ __device__ __forceinline__ float2 tanh_exp2(float2 s, const ScoreParams& p) {
 // tanh(k s) and its slope 1 - tanh^2 of a pair that belongs to two rows: with e =
 // exp(2 k s) and q = 1 / (1 + e), tanh is 1 - 2 q and the slope 4 e q^2, which keeps its
 // relative precision (2^-21, and 2^-23 of the exponent's argument) where 1 - tanh^2
-// would be nothing but tanh's rounding. Exponents are held to 63, scores of 21 caps,
-// where the slope is 2^-61. A NaN counts as 63 here: it stays out of its neighbour.
+// would be nothing but tanh's rounding. Exponents are held to 62, scores of 21 caps,
+// where the slope is 2^-60 and the reciprocal of a pair's 2^124 still a normal number. A
+// NaN counts as 62 here: it stays out of its neighbour.
 __device__ __forceinline__ float2 tanh_slope2(float2 s, const ScoreParams& p, float2& slope) {
-  const float2 e = make_float2(ex2(fminf(s.x * p.e2, 63.f)), ex2(fminf(s.y * p.e2, 63.f)));
+  const float2 e = make_float2(ex2(fminf(s.x * p.e2, 62.f)), ex2(fminf(s.y * p.e2, 62.f)));
   const float2 b = __fadd2_rn(e, make_float2(1.f, 1.f));
   const float r = 2.f * rcp_approx(b.x * b.y);
   const float2 q2 = __fmul2_rn(make_float2(b.y, b.x), make_float2(r, r));
@@ -129,9 +131,6 @@ __device__ __forceinline__ float2 cap_small_factor2(float2 s, const ScoreParams&
   float2 r = __ffma2_rn(z, make_float2(p.a3, p.a3), make_float2(p.a2, p.a2));
   r = __ffma2_rn(z, r, make_float2(p.a1, p.a1));
   return __ffma2_rn(z, r, make_float2(p.a0, p.a0));
-}
-__device__ __forceinline__ float2 cap_small2(float2 s, const ScoreParams& p) {
-  return __fmul2_rn(s, cap_small_factor2(s, p));
 }
 // tanh(k s) of a pair of small scores
 __device__ __forceinline__ float2 tanh_small2(float2 s, const ScoreParams& p) {

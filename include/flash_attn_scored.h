@@ -38,7 +38,7 @@ extern "C" {
  *                fp32, to within 2^-21 |t| + 2^-20 softcap; the gradients' factor
  *                1 - (t / softcap)^2 to within 2^-18 of itself for scores of up to
  *                12 softcaps, 2^-17 up to 21 (past them, where it is below 2^-58, it
- *                may count as 2^-61).
+ *                may count as 2^-60).
  *   slopes:      NULL, or fp32 [Hq] on the device (4-byte aligned), finite. They
  *                are constants of the model: no gradient of them is formed.
  *   prefix_lens: NULL, or int32 [B] on the device (4-byte aligned), clamped to
